@@ -24,6 +24,7 @@ FT_OK, FT_ERR_INVALID_ARG, FT_ERR_CUDA, FT_ERR_OOM, FT_ERR_CAPACITY, FT_ERR_STAT
     FT_ERR_CHECKED, FT_ERR_UNSUPPORTED = range(9)
 FT_W_F32, FT_W_BF16, FT_W_FP8E4M3_B128 = 0, 1, 2
 FT_FETCH_COPY_ENGINE, FT_FETCH_SM_PULL = 0, 1
+FT_KV_BF16, FT_KV_FP8E4M3 = 0, 1
 
 
 class FtError(RuntimeError):
@@ -62,6 +63,18 @@ class ft_timing(ctypes.Structure):
 class ft_plan_info(ctypes.Structure):
     _fields_ = [("event", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("n_unique", ctypes.c_int32),
                 ("n_miss", ctypes.c_int32)]
+
+
+class ft_kv_pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("kv_dtype", ctypes.c_int32)]
+
+
+class ft_kv_batch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("num_tokens", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32)]
 
 
 # ---------------------------------------------------------------- loading
@@ -105,6 +118,11 @@ def _load():
         "ft_step_graph_destroy": (st, [P]),
         "ft_moe_decode_ffn_static": (st, [I32, I32, I32, I32, I32, P, I64, P, P, P, P, I32, P, P]),
         "ft_moe_decode_ffn_static_status": (st, [P]),
+        "ft_kv_append": (st, [P, P, P, I64, I64, P, I64, I64, P]),
+        "ft_kv_read": (st, [P, P, P, I64, P, P, P]),
+        "ft_kv_attend": (st, [P, P, I32, P, I64, I64, P, I64, I64, P, ctypes.c_float, I32, I32, P, ctypes.c_uint64, P]),
+        "ft_kv_attend_workspace": (ctypes.c_uint64, [P, P, I32]),
+        "ft_kv_status": (st, [P]),
         "ft_status_str": (ctypes.c_char_p, [st]),
         "ft_last_error": (ctypes.c_char_p, []),
     }
@@ -317,6 +335,40 @@ def ft_moe_decode_ffn_static(hidden: int, inter: int, wdtype: int, num_experts: 
 def ft_moe_decode_ffn_static_status(stream: int = 0):
     """Raise FtError if an earlier static-scratch FFN call hit a bounded-wait timeout (clears it)."""
     _check(_lib.ft_moe_decode_ffn_static_status(stream or None), "ft_moe_decode_ffn_static_status")
+
+
+def ft_kv_append(pages: ft_kv_pages, batch: ft_kv_batch, k: int, k_token_stride: int, k_head_stride: int, v: int,
+                 v_token_stride: int, v_head_stride: int, stream: int = 0):
+    st = _lib.ft_kv_append(ctypes.addressof(pages), ctypes.addressof(batch), k, k_token_stride, k_head_stride, v,
+                           v_token_stride, v_head_stride, stream)
+    if st:
+        _check(st, "ft_kv_append")
+
+
+def ft_kv_read(pages: ft_kv_pages, batch: ft_kv_batch, kv_start: int, num_rows: int, k_out: int, v_out: int,
+               stream: int = 0):
+    st = _lib.ft_kv_read(ctypes.addressof(pages), ctypes.addressof(batch), kv_start, num_rows, k_out, v_out, stream)
+    if st:
+        _check(st, "ft_kv_read")
+
+
+def ft_kv_attend(pages: ft_kv_pages, batch: ft_kv_batch, num_q_heads: int, q: int, q_token_stride: int,
+                 q_head_stride: int, out: int, out_token_stride: int, out_head_stride: int, lse: int, scale: float,
+                 causal: bool, window: int, workspace: int, workspace_bytes: int, stream: int = 0):
+    st = _lib.ft_kv_attend(ctypes.addressof(pages), ctypes.addressof(batch), num_q_heads, q, q_token_stride,
+                           q_head_stride, out, out_token_stride, out_head_stride, lse, scale, causal, window, workspace,
+                           workspace_bytes, stream)
+    if st:
+        _check(st, "ft_kv_attend")
+
+
+def ft_kv_attend_workspace(pages: ft_kv_pages, batch: ft_kv_batch, num_q_heads: int) -> int:
+    return int(_lib.ft_kv_attend_workspace(ctypes.addressof(pages), ctypes.addressof(batch), num_q_heads))
+
+
+def ft_kv_status(stream: int = 0):
+    """Raise FtError if an earlier ft_kv call on this device met bad device data or a timeout (clears it)."""
+    _check(_lib.ft_kv_status(stream or None), "ft_kv_status")
 
 
 def ft_status_str(status: int) -> str:

@@ -1,0 +1,160 @@
+"""One layer's paged key/value cache as torch tensors, and the calls on it.
+
+    pages = KVPages(k, v, k_scale, v_scale)          # once, for the layer's life
+    batch = KVBatch(q_start, kv_len, block_table, num_tokens, max_q_len)   # once a step, for every layer
+    pages.append(batch, k_new, v_new)                # store the new tokens
+    pages.attend(batch, q, out)                      # softmax(q k^T / sqrt(D)) v over their sequences
+    pages.read(batch, kv_start, k_out, v_out)        # whole sequences back in bf16
+
+The caller owns every tensor.  ``KVPages.empty`` allocates a layer's pages.
+Work is enqueued on ``stream`` (default: torch's current stream of the cache's
+device); the workspace of ``attend`` is kept per device and stream and grows to
+the largest call, so make one call of a size before capturing it in a graph.
+Device-side errors are reported by ``check`` (see ft_kv_status in include/ft.h,
+which also gives the layout and the sequences' description).
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import (FT_KV_BF16, FT_KV_FP8E4M3, ft_kv_append, ft_kv_attend, ft_kv_attend_workspace, ft_kv_batch, ft_kv_pages,
+               ft_kv_read, ft_kv_status)
+
+_workspaces: dict = {}  # (device index, stream) -> uint8 tensor
+
+
+def _need(ok, text, *args):
+    if not ok:
+        raise ValueError(text % args if args else text)
+
+
+class KVBatch:
+    """One step's sequences: int32 device tensors q_start [S + 1], kv_len [S]
+    and block_table [S, pages], and the host's num_tokens and max_q_len."""
+
+    def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor, num_tokens: int,
+                 max_q_len: int):
+        S = kv_len.shape[0]
+        _need(q_start.dtype == kv_len.dtype == block_table.dtype == torch.int32,
+              "q_start, kv_len and block_table are int32 tensors")
+        _need(q_start.shape == (S + 1,) and kv_len.dim() == 1 and block_table.dim() == 2 and block_table.shape[0] == S,
+              "shapes: q_start [S + 1], kv_len [S], block_table [S, pages]")
+        _need(q_start.is_contiguous() and kv_len.is_contiguous(), "q_start and kv_len are contiguous")
+        _need(S <= 1 or (block_table.stride(1) == 1 or block_table.shape[1] == 1) and
+              block_table.stride(0) >= block_table.shape[1], "block_table's rows are contiguous")
+        _need(q_start.device == kv_len.device == block_table.device, "one device")
+        self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table  # keeps them alive
+        self.num_seqs, self.num_tokens, self.max_q_len = S, int(num_tokens), int(max_q_len)
+        self.device = kv_len.device
+        stride = block_table.stride(0) if S > 1 else block_table.shape[1]
+        self.c = ft_kv_batch(q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), stride, S, self.num_tokens,
+                             self.max_q_len)
+
+
+class KVPages:
+    """One layer's cache: k, v [pages, kv_heads, page_tokens, head_dim], bf16 or
+    float8_e4m3fn; for the latter k_scale, v_scale [pages, kv_heads,
+    page_tokens] uint8, the exponent bytes of the scales."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.is_contiguous() and v.is_contiguous(),
+              "k and v are contiguous [pages, kv_heads, page_tokens, head_dim] tensors of one type")
+        _need(k.dtype in (torch.bfloat16, torch.float8_e4m3fn), "the cache is bf16 or float8_e4m3fn, not %s", k.dtype)
+        fp8 = k.dtype == torch.float8_e4m3fn
+        _need(fp8 == (k_scale is not None) == (v_scale is not None), "scales go with a float8 cache, and only with it")
+        if fp8:
+            for t in (k_scale, v_scale):
+                _need(t.dtype == torch.uint8 and t.shape == k.shape[:3] and t.is_contiguous() and t.device == k.device,
+                      "scales are contiguous uint8 [pages, kv_heads, page_tokens]")
+        _need(k.is_cuda and v.device == k.device, "the pages are in one GPU's memory")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.num_pages, self.num_kv_heads, self.page_tokens, self.head_dim = k.shape
+        self.c = ft_kv_pages(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fp8 else None,
+                             v_scale.data_ptr() if fp8 else None, self.num_pages, self.num_kv_heads, self.head_dim,
+                             self.page_tokens, FT_KV_FP8E4M3 if fp8 else FT_KV_BF16)
+
+    @classmethod
+    def empty(cls, num_pages, num_kv_heads, page_tokens, head_dim, kv_dtype=FT_KV_BF16, device="cuda:0"):
+        """A layer's pages, contents undefined (a page is written before it is read)."""
+        shape = (num_pages, num_kv_heads, page_tokens, head_dim)
+        dt = torch.float8_e4m3fn if kv_dtype == FT_KV_FP8E4M3 else torch.bfloat16
+        kv = [torch.empty(shape, dtype=dt, device=device) for _ in range(2)]
+        sc = [torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)] if dt != torch.bfloat16 else []
+        return cls(*kv, *sc)
+
+    # ---- the calls ---------------------------------------------------------
+    def append(self, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream: torch.cuda.Stream | None = None):
+        """Store the batch's new keys and values, bf16 [num_tokens, kv_heads, head_dim] (strided views are fine)."""
+        self._rows(batch, k, self.num_kv_heads, "k")
+        self._rows(batch, v, self.num_kv_heads, "v")
+        with self._guard():
+            ft_kv_append(self.c, batch.c, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+                         v.stride(1), self._stream(stream))
+
+    def attend(self, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None = None,
+               scale: float | None = None, causal: bool = True, window: int = 0,
+               stream: torch.cuda.Stream | None = None):
+        """Attention of the batch's new tokens; q, out: bf16 [num_tokens, q_heads,
+        head_dim], lse: f32 [num_tokens, q_heads].  scale defaults to
+        1 / sqrt(head_dim); window > 0 keeps that many last tokens, the row's own
+        included."""
+        heads = q.shape[1] if q.dim() == 3 else 0
+        self._rows(batch, q, heads, "q")
+        self._rows(batch, out, heads, "out")
+        _need(lse is None or (lse.dtype == torch.float32 and lse.shape == (batch.num_tokens, heads) and
+                              lse.is_contiguous() and lse.device == self.device),
+              "lse is a contiguous float32 [num_tokens, q_heads] tensor")
+        s = self._stream(stream)
+        with self._guard():
+            need = ft_kv_attend_workspace(self.c, batch.c, heads)
+            ws = _workspaces.get((self.device.index, s))
+            if ws is None or ws.numel() < need:
+                ws = _workspaces[(self.device.index, s)] = self._new_workspace(max(need, 256), stream)
+            ft_kv_attend(self.c, batch.c, heads, q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0),
+                         out.stride(1), lse.data_ptr() if lse is not None else None,
+                         1.0 / math.sqrt(self.head_dim) if scale is None else scale, causal, window, ws.data_ptr(),
+                         ws.numel(), s)
+
+    def read(self, batch: KVBatch, kv_start: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
+             stream: torch.cuda.Stream | None = None):
+        """Whole sequences back in bf16: token p of sequence s is row kv_start[s] + p of k_out and v_out,
+        contiguous [rows, kv_heads, head_dim]."""
+        _need(kv_start.dtype == torch.int32 and kv_start.shape == (batch.num_seqs + 1,) and kv_start.is_contiguous() and
+              kv_start.device == self.device, "kv_start is a contiguous int32 [S + 1] tensor of the cache's device")
+        shape = (k_out.shape[0], self.num_kv_heads, self.head_dim)
+        for t in (k_out, v_out):
+            _need(t.dtype == torch.bfloat16 and t.shape == shape and t.is_contiguous() and t.device == self.device,
+                  "k_out and v_out are contiguous bf16 [rows, kv_heads, head_dim] tensors of the cache's device")
+        _need(batch.device == self.device, "the batch and the cache are on one device")
+        with self._guard():
+            ft_kv_read(self.c, batch.c, kv_start.data_ptr(), shape[0], k_out.data_ptr(), v_out.data_ptr(),
+                       self._stream(stream))
+
+    def check(self, stream: torch.cuda.Stream | None = None):
+        """Wait for the stream and raise FtError if a call met device data out of range or a timeout."""
+        with self._guard():
+            ft_kv_status(self._stream(stream))
+
+    # ---- helpers -------------------------------------------------------------
+    def _rows(self, batch, t, heads, name):
+        _need(t.dtype == torch.bfloat16 and t.shape == (batch.num_tokens, heads, self.head_dim) and
+              (t.stride(2) == 1 or t.numel() == 0) and
+              t.device == self.device == batch.device,
+              "%s is a bf16 [num_tokens, heads, %d] tensor of the cache's device with contiguous rows", name,
+              self.head_dim)
+
+    def _stream(self, stream):
+        return (stream or torch.cuda.current_stream(self.device)).cuda_stream
+
+    def _new_workspace(self, nbytes, stream):
+        if stream is None:
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        with torch.cuda.stream(stream):  # the allocator then reuses it in this stream's order
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+    def _guard(self):
+        return torch.cuda.device(self.device)

@@ -422,6 +422,111 @@ ft_status ft_step_graph_timing(ft_step_graph* graph, double* route_ms, double* f
 ft_status ft_step_graph_trace(ft_step_graph* graph, double* t_ms);
 ft_status ft_step_graph_destroy(ft_step_graph* graph);
 
+/*
+ * The paged key/value cache of the attention between two expert layers, and
+ * attention over it.  No handle: the caller owns every byte, describes one
+ * layer's cache with ft_kv_pages and one step's sequences with ft_kv_batch
+ * (both are host structs read during the call, and may be kept for many), and
+ * passes the stream.  Nothing is kept from one call for the next, and nothing
+ * is allocated; the calls can be captured in a CUDA graph.
+ *
+ * Layout.  A page holds page_tokens consecutive tokens of one sequence, for
+ * every key/value head: k, v [num_pages][num_kv_heads][page_tokens][head_dim].
+ * FT_KV_BF16 stores the values.  FT_KV_FP8E4M3 stores e4m3 codes and, per
+ * token and head, the exponent byte e of a power-of-two scale 2^(e - 127), in
+ * k_scale, v_scale [num_pages][num_kv_heads][page_tokens]: the smallest
+ * 2^k >= 2^-110 with max|x| <= 448 * 2^k, each x / 2^k rounded to the nearest
+ * code (ties to even; at k = 120 no further than 240, so that every stored
+ * value is a finite bf16 value).  A vector with an infinity or a NaN gets e =
+ * 255 and codes 0, and reads as NaN throughout.  A power of two makes
+ * x / scale and code * scale exact: the cache rounds each value once, and
+ * reading it back in bf16 rounds nothing.
+ *
+ * Sequences.  Sequence s has q_start[s + 1] - q_start[s] new tokens (0 is
+ * fine), rows q_start[s].. of the call's token-major tensors, and kv_len[s]
+ * tokens in all, the new ones last; token p sits in page
+ * block_table[s * table_stride + p / page_tokens], place p % page_tokens.
+ * Entries of the table past the sequence's length are not read.  A new token
+ * whose position is negative (kv_len[s] below its new tokens) is not stored
+ * and attends to nothing.
+ *
+ * Device data that is out of range (a page outside [0, num_pages), a kv_len
+ * beyond the table, a q_start outside [0, num_tokens], more new tokens than
+ * max_q_len) is never followed out of bounds: it sets a sticky word that
+ * ft_kv_status reports as FT_ERR_INVALID_ARG, and what the call gives for
+ * that sequence is then not defined.
+ */
+typedef enum ft_kv_dtype {
+  FT_KV_BF16 = 0,
+  FT_KV_FP8E4M3 = 1 /* e4m3 codes, one power-of-two scale per token and head */
+} ft_kv_dtype;
+
+typedef struct ft_kv_pages {
+  void* k;              /* device, 16-byte aligned: [num_pages][num_kv_heads][page_tokens][head_dim] */
+  void* v;
+  uint8_t* k_scale;     /* device: [num_pages][num_kv_heads][page_tokens]; FT_KV_FP8E4M3 only */
+  uint8_t* v_scale;
+  int64_t num_pages;    /* num_pages * num_kv_heads * page_tokens < 2^31 */
+  int32_t num_kv_heads; /* 1..1024 */
+  int32_t head_dim;     /* 64 or 128 */
+  int32_t page_tokens;  /* 16, 32, 64, 128 or 256 */
+  int32_t kv_dtype;     /* ft_kv_dtype */
+} ft_kv_pages;
+
+typedef struct ft_kv_batch {
+  const int32_t* q_start;     /* device [num_seqs + 1], ascending from 0 to num_tokens */
+  const int32_t* kv_len;      /* device [num_seqs] */
+  const int32_t* block_table; /* device [num_seqs][table_stride] */
+  int64_t table_stride;       /* pages a sequence has at most; table_stride * page_tokens < 2^31 */
+  int32_t num_seqs;           /* 0..4096 */
+  int32_t num_tokens;         /* new tokens of the batch */
+  int32_t max_q_len;          /* new tokens of its longest sequence, or more */
+} ft_kv_batch;
+
+/* Writes the batch's new keys and values into their pages.  k, v: device bf16
+ * [num_tokens][num_kv_heads][head_dim] with the given strides in elements
+ * (views of one projection's output are fine): 16-byte aligned, strides
+ * multiples of 8. */
+ft_status ft_kv_append(const ft_kv_pages* pages, const ft_kv_batch* batch, const void* k, int64_t k_token_stride,
+                       int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                       void* stream);
+
+/* Reads whole sequences back in bf16: rows kv_start[s] + p (p < kv_len[s]) of
+ * k_out, v_out, device [num_rows][num_kv_heads][head_dim] contiguous and
+ * 16-byte aligned, are token p of sequence s.  kv_start: device
+ * [num_seqs + 1], ascending; rows that no token maps to are written as zeros.
+ * q_start and num_tokens of the batch are not used. */
+ft_status ft_kv_read(const ft_kv_pages* pages, const ft_kv_batch* batch, const int32_t* kv_start, int64_t num_rows,
+                     void* k_out, void* v_out, void* stream);
+
+/* Attention of the batch's new tokens over their sequences, keys and values
+ * (the new tokens' own among them) read from the pages:
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k[j][h / G]) v[j][h / G],  G = num_q_heads / num_kv_heads
+ * over the tokens j < kv_len of t's sequence; with `causal`, those with
+ * j <= t's position, and with window > 0 (causal only) also
+ * j > position - window.  A row that sees nothing gives zeros (lse -inf), and
+ * so does one whose every score is -inf.  Tokens that a row does not see do
+ * not reach it, whatever they hold.
+ * q, out: device bf16 [num_tokens][num_q_heads][head_dim] with strides in
+ * elements, 16-byte aligned, strides multiples of 8.  lse: device f32
+ * [num_tokens][num_q_heads] (natural logarithm of the softmax's denominator,
+ * scores scaled), or NULL.  Softmax statistics and sums are fp32;
+ * probabilities are rounded to bf16 for the product with v.
+ * workspace: device, 256-byte aligned, ft_kv_attend_workspace bytes; its
+ * content means nothing between calls, and calls on one stream can share it. */
+ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads, const void* q,
+                       int64_t q_token_stride, int64_t q_head_stride, void* out, int64_t out_token_stride,
+                       int64_t out_head_stride, float* lse, float scale, int32_t causal, int32_t window,
+                       void* workspace, uint64_t workspace_bytes, void* stream);
+/* Bytes ft_kv_attend needs for this shape on the current device; 0 for shapes it does not take. */
+uint64_t ft_kv_attend_workspace(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads);
+
+/* Waits for `stream`, then returns what the ft_kv calls on the current device
+ * met since the last ft_kv_status: FT_ERR_INVALID_ARG (device data out of
+ * range), FT_ERR_TIMEOUT (a bounded wait ran out; the output is incomplete),
+ * else FT_OK.  Reading clears the word.  Synchronous. */
+ft_status ft_kv_status(void* stream);
+
 const char* ft_status_str(ft_status s);
 /* Message of the calling thread's last error ("" if none). */
 const char* ft_last_error(void);
