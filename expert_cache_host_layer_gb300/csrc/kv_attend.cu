@@ -1,7 +1,11 @@
-// Attention over the paged key/value cache (ft_kv_attend): the entry point and
-// the plain kernel, one warp per row (new token, query head) that walks the
-// row's visible tokens with a running maximum and sum.
-#include "kv_common.h"
+// Attention over the paged key/value cache (ft_kv_attend): the entry point,
+// the workspace, the kernel that joins partial sums, and the plain kernel, one
+// warp per row (new token, query head) that walks the row's visible tokens
+// with a running maximum and sum.
+#include <algorithm>
+
+#include "driver_api.h"
+#include "kv_attend.h"
 
 namespace ft {
 namespace kv {
@@ -84,18 +88,150 @@ __global__ void row_kernel(RowArgs a) {
   if (a.lse && lane == 0) a.lse[r] = l == 0.0f ? -INFINITY : m + logf(l);
 }
 
+// ---------------------------------------------------------------- partial sums
+
+// Block (c, y) joins rows y * R .. of what CTA c of the main kernel began and
+// others went on with: out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, in
+// the order of the tokens.  R = 8: a warp per row (few parts: the cut of a
+// batch with many sequences); R = 1: eight warps share a row's parts, and are
+// summed in order.
+constexpr int kJoinThreads = 256;
+
+template <int D, int R>
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ AttendArgs a, int rows) {
+  constexpr int N = D / 32;
+  __shared__ float s_o[R == 1 ? 8 : 1][D];
+  __shared__ float s_l[8];
+  dec::pdl_wait_primary();
+  const int4 u = __ldcg(&a.desc[blockIdx.x]);  // {s, h, row block, last CTA}
+  if (u.x < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Seq q = load_seq(a.p, a.b, u.x, a.status);
+  const int r = blockIdx.y * R + (R == 1 ? 0 : warp), row = u.z * rows + r;
+  if (row >= q.m * a.G) return;  // R = 1: all of the block; R = 8: whole warps
+  const int c0 = blockIdx.x, parts = u.w - c0 + 1;
+  // part i: CTA c0's last slot, then the first slot of each CTA after it
+  auto slot = [&](int i) { return (long long)(2 * (c0 + i) + (i == 0)) * rows + r; };
+  float m = -INFINITY;
+  for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(&a.part_ml[slot(i) * 2]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.0f : m;
+  float acc[N] = {}, l = 0.0f;
+  const int per = R == 1 ? (parts + 7) / 8 : parts, i0 = R == 1 ? warp * per : 0, i1 = min(parts, i0 + per);
+#pragma unroll 4
+  for (int i = i0; i < i1; ++i) {
+    const long long at = slot(i);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
+    const float f = exp2_approx(ml.x - base);
+    l += f * ml.y;
+    if (N == 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + lane);
+      acc[0] += f * v.x; acc[1] += f * v.y; acc[N - 2] += f * v.z; acc[N - 1] += f * v.w;
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_o + at * D) + lane);
+      acc[0] += f * v.x; acc[1] += f * v.y;
+    }
+  }
+  if (R == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s_o[R == 1 ? warp : 0][lane * N + i] = acc[i];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (warp) return;
+    l = 0.0f;
+    for (int w = 0; w < 8; ++w) l += s_l[w];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      acc[i] = 0.0f;
+      for (int w = 0; w < 8; ++w) acc[i] += s_o[R == 1 ? w : 0][lane * N + i];
+    }
+  }
+  const float inv = inverse(l);
+  __nv_bfloat16* out = a.out + out_at(a, q, u.y, row) + lane * N;
+#pragma unroll
+  for (int i = 0; i < N; i += 2)
+    *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+  if (lane == 0) write_lse(a, q, u.y, row, m, l);
+}
+
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  n = known[dev].load();
+  if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) known[dev].store(n);
+  return n;
+}
+
 }  // namespace
+
+cudaError_t launch_combine(const AttendArgs& a, int rows, int used, cudaStream_t s) {
+  const bool one = used <= 64;  // rows enough for a block each without many idle blocks
+  const dim3 grid(a.grid, one ? used : (used + 7) / 8);
+  if (a.p.head_dim == 128)
+    return one ? launch_dependent(combine_kernel<128, 1>, grid, kJoinThreads, 0, s, a, rows)
+               : launch_dependent(combine_kernel<128, 8>, grid, kJoinThreads, 0, s, a, rows);
+  return one ? launch_dependent(combine_kernel<64, 1>, grid, kJoinThreads, 0, s, a, rows)
+             : launch_dependent(combine_kernel<64, 8>, grid, kJoinThreads, 0, s, a, rows);
+}
+
+bool pages_map(CUtensorMap* m, const ft_kv_pages& p, const void* base, int box_rows) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode enc = reinterpret_cast<Encode>(driver_fn("cuTensorMapEncodeTiled"));
+  if (!enc) return false;
+  const bool fp8 = p.kv_dtype == FT_KV_FP8E4M3;
+  const cuuint64_t dims[2] = {(cuuint64_t)p.head_dim, (cuuint64_t)(p.num_pages * p.num_kv_heads * p.page_tokens)};
+  const cuuint64_t pitch[1] = {(cuuint64_t)p.head_dim * (fp8 ? 1 : 2)};
+  const cuuint32_t box[2] = {fp8 ? (cuuint32_t)p.head_dim : 64u, (cuuint32_t)box_rows};
+  const cuuint32_t step[2] = {1, 1};
+  return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+             pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             pitch[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace kv
 }  // namespace ft
 
 using namespace ft;
 using namespace ft::kv;
 
+namespace {
+
+// The workspace: [desc][part_ml][part_o], each part 256-byte aligned.
+struct Workspace {
+  uint64_t ml, o, bytes;
+};
+Workspace layout(const ft_kv_pages& p, int grid, int rows) {
+  const uint64_t parts = 2ull * grid * rows;
+  Workspace w;
+  w.ml = (grid * sizeof(int4) + 255) & ~255ull;
+  w.o = (w.ml + parts * 2 * sizeof(float) + 255) & ~255ull;
+  w.bytes = w.o + parts * p.head_dim * sizeof(float);
+  return w;
+}
+
+ft_status check_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads) {
+  ft_status st = check_pages(pages);
+  if (st == FT_OK) st = check_batch(pages, batch);
+  if (st != FT_OK) return st;
+  if (num_q_heads < 1 || num_q_heads % pages->num_kv_heads)
+    return set_error(FT_ERR_INVALID_ARG, "num_q_heads=%d is not a multiple of num_kv_heads=%d", num_q_heads,
+                     pages->num_kv_heads);
+  if (pages->kv_dtype == FT_KV_FP8E4M3 &&
+      ((reinterpret_cast<uintptr_t>(pages->k_scale) | reinterpret_cast<uintptr_t>(pages->v_scale)) & 15))
+    return set_error(FT_ERR_INVALID_ARG, "the scales are not 16-byte aligned");
+  return FT_OK;
+}
+
+}  // namespace
+
 extern "C" uint64_t ft_kv_attend_workspace(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads) {
-  if (check_pages(pages) != FT_OK || check_batch(pages, batch) != FT_OK || num_q_heads < 1 ||
-      num_q_heads % pages->num_kv_heads)
-    return 0;
-  return 256;
+  if (check_attend(pages, batch, num_q_heads) != FT_OK) return 0;
+  return layout(*pages, sm_count(), kTokenRows).bytes;
 }
 
 extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads,
@@ -103,22 +239,43 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
                                   int64_t out_token_stride, int64_t out_head_stride, float* lse, float scale,
                                   int32_t causal, int32_t window, void* workspace, uint64_t workspace_bytes,
                                   void* stream) {
-  ft_status st = check_pages(pages);
-  if (st == FT_OK) st = check_batch(pages, batch);
+  ft_status st = check_attend(pages, batch, num_q_heads);
   if (st != FT_OK) return st;
-  if (num_q_heads < 1 || num_q_heads % pages->num_kv_heads)
-    return set_error(FT_ERR_INVALID_ARG, "num_q_heads=%d is not a multiple of num_kv_heads=%d", num_q_heads,
-                     pages->num_kv_heads);
   if (window < 0 || (window > 0 && !causal))
     return set_error(FT_ERR_INVALID_ARG, "window=%d (causal=%d): a window is positive and causal", window, causal);
   if (!(scale == scale)) return set_error(FT_ERR_INVALID_ARG, "scale is NaN");
   if (batch->num_tokens == 0) return FT_OK;
   if ((st = check_rows("q", q, q_token_stride, q_head_stride)) != FT_OK) return st;
   if ((st = check_rows("out", out, out_token_stride, out_head_stride)) != FT_OK) return st;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
-      workspace_bytes < ft_kv_attend_workspace(pages, batch, num_q_heads))
-    return set_error(FT_ERR_INVALID_ARG, "workspace: %llu bytes at a 256-byte boundary are needed",
-                     (unsigned long long)ft_kv_attend_workspace(pages, batch, num_q_heads));
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return set_error(FT_ERR_INVALID_ARG, "workspace is null or not 256-byte aligned");
+  const int G = num_q_heads / pages->num_kv_heads;
+  const int grid = sm_count();
+  const Workspace ws = layout(*pages, grid, kTokenRows);
+  if (workspace_bytes < ws.bytes)
+    return set_error(FT_ERR_INVALID_ARG, "workspace of %llu bytes: %llu are needed",
+                     (unsigned long long)workspace_bytes, (unsigned long long)ws.bytes);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const long long rows = (long long)batch->max_q_len * G;  // of a (sequence, key head), at most
+  cudaError_t e;
+  if (rows <= kTokenRows) {
+    AttendArgs a{};
+    a.p = *pages; a.b = *batch;
+    a.q = static_cast<const __nv_bfloat16*>(q); a.out = static_cast<__nv_bfloat16*>(out); a.lse = lse;
+    a.qts = q_token_stride; a.qhs = q_head_stride; a.ots = out_token_stride; a.ohs = out_head_stride;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.Hq = num_q_heads; a.G = G; a.causal = causal != 0; a.window = window; a.grid = grid;
+    if ((st = status_word(&a.status)) != FT_OK) return st;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    a.desc = reinterpret_cast<int4*>(w);
+    a.part_ml = reinterpret_cast<float*>(w + ws.ml);
+    a.part_o = reinterpret_cast<float*>(w + ws.o);
+    if ((e = launch_attend_token(a, s)) != cudaSuccess)
+      return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
+    if ((e = launch_combine(a, kTokenRows, (int)rows, s)) != cudaSuccess)
+      return set_error(FT_ERR_CUDA, "attend join launch: %s", cudaGetErrorString(e));
+    return FT_OK;
+  }
   RowArgs a{};
   a.p = *pages; a.b = *batch;
   a.q = static_cast<const __nv_bfloat16*>(q); a.out = static_cast<__nv_bfloat16*>(out); a.lse = lse;
@@ -130,8 +287,7 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   const bool fp8 = pages->kv_dtype == FT_KV_FP8E4M3;
   auto* kernel = pages->head_dim == 128 ? (fp8 ? row_kernel<128, true> : row_kernel<128, false>)
                                         : (fp8 ? row_kernel<64, true> : row_kernel<64, false>);
-  kernel<<<(unsigned)blocks, 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
+  kernel<<<(unsigned)blocks, 128, 0, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
   return FT_OK;
 }

@@ -1,0 +1,247 @@
+// What the attention kernels over the paged cache share: the call's arguments,
+// visibility, the even cut of the work over the CTAs, partial sums and the
+// launch helpers.  Internal to libft.
+#pragma once
+
+#include <cuda.h>
+
+#include <atomic>
+
+#include "decode_common.h"
+#include "kv_common.h"
+
+namespace ft {
+namespace kv {
+
+constexpr int kTokenRows = 16;    // most rows of a (sequence, key head) in token_kernel
+constexpr int kTokenTile = 128;   // tokens per tile of its ring
+
+struct AttendArgs {
+  ft_kv_pages p;
+  ft_kv_batch b;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;             // or null
+  int64_t qts, qhs, ots, ohs;
+  float scale_log2;       // scale * log2(e)
+  int Hq, G, causal, window;
+  int grid;               // CTAs of the main kernel
+  int32_t* status;
+  // workspace
+  int4* desc;             // [grid] the (sequence, head, row block) that CTA c begins and does not end: {s, h, row
+                          // block, last CTA}; s = -1: none
+  float* part_o;          // [2 grid][rows][D] unnormalised sums: slot 2c of what CTA c finds begun, 2c + 1 of what it
+                          // begins and leaves
+  float* part_ml;         // [2 grid][rows][2] running maximum (log2 domain) and sum
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {  // relative error 2^-22, 2^-inf = 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Tokens [lo, hi) that new token i of a sequence sees; lo and hi grow with i.
+struct Span {
+  int lo, hi;
+};
+__device__ __forceinline__ Span visible(const AttendArgs& a, const Seq& q, int i) {
+  const int pos = q.n - q.m + i;
+  Span v;
+  v.hi = a.causal ? min(q.n, max(0, pos + 1)) : q.n;
+  v.lo = a.window ? min(v.hi, max(0, pos - a.window + 1)) : 0;
+  return v;
+}
+
+// Whole warp: wait for phase `parity` of a barrier; false if the CTA has
+// aborted or the wait ran out (which aborts the CTA).
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, int32_t* status,
+                                              volatile int* abort_flag) {
+  bool ok = dec::mbar_try_wait(bar, parity);
+  if (!ok) {
+    const unsigned long long t0 = dec::global_ns();
+    for (;;) {
+      for (int i = 0; i < 64 && !ok; ++i) ok = dec::mbar_try_wait(bar, parity);
+      if (ok || *abort_flag) break;
+      if (dec::global_ns() - t0 > dec::kWaitLimitNs) {
+        raise(status, FT_ERR_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The work laid end to end over the sequences, and the part of it that is
+// this CTA's: items [w0, w1) of `total`, sequence s's items beginning at `base`.
+struct Range {
+  long long w0, w1, base, total;
+  int s, n;  // first sequence; CTAs that have work
+};
+// CTA of item w.
+__device__ __forceinline__ int cta_of(long long w, long long total, int n) { return (int)(((w + 1) * n - 1) / total); }
+
+// Every thread of the CTA: exclusive prefix sums of count(s) over the
+// sequences into pre[0 .. S], and this CTA's even share of the total.
+template <typename Count>
+__device__ __forceinline__ Range cut(const AttendArgs& a, long long* pre, long long* scan, Count count) {
+  const int S = a.b.num_seqs, T = blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (S + T - 1) / T, s0 = min(S, (int)threadIdx.x * per), s1 = min(S, s0 + per);
+  long long mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    pre[s] = mine;
+    mine += count(s);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int w = 0; w < T / 32; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  for (int s = s0; s < s1; ++s) pre[s] += before;
+  __syncthreads();
+  Range r;
+  r.total = total;
+  r.n = (int)min((long long)gridDim.x, total);
+  r.w0 = r.w1 = r.base = 0;
+  r.s = 0;
+  if ((int)blockIdx.x < r.n) {
+    r.w0 = blockIdx.x * total / r.n;
+    r.w1 = (blockIdx.x + 1) * total / r.n;
+    int lo = 0, hi = S - 1;  // the last sequence that begins at or before w0 (ones without work begin where the next does)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= r.w0) lo = mid;
+      else hi = mid - 1;
+    }
+    r.s = lo;
+    r.base = pre[lo];
+  }
+  return r;
+}
+
+// ---------------------------------------------------------------- token_kernel's items: tiles of a (sequence, head)
+
+__device__ __forceinline__ Span token_tiles(const AttendArgs& a, const Seq& q, Span* seen) {
+  seen->lo = visible(a, q, 0).lo;
+  seen->hi = visible(a, q, max(0, q.m - 1)).hi;
+  Span t;
+  t.lo = seen->lo / kTokenTile;
+  t.hi = q.m == 0 ? t.lo : max(t.lo + 1, (seen->hi + kTokenTile - 1) / kTokenTile);  // rows that see nothing: one tile
+  return t;
+}
+__device__ __forceinline__ Range token_range(const AttendArgs& a, long long* pre, long long* scan) {
+  return cut(a, pre, scan, [&](int s) {
+    Span seen;
+    const Span t = token_tiles(a, load_seq(a.p, a.b, s, a.status), &seen);
+    return (long long)(t.hi - t.lo) * a.p.num_kv_heads;
+  });
+}
+// The (sequence, head)s of a CTA's range, one after the other.
+struct TokenWalk {
+  long long w, end, base, total;
+  int n;
+  int s, h;      // this one
+  Seq q;
+  int lo, hi;    // tokens that some row sees
+  int t0, t1;    // tiles of it that are this CTA's
+  bool begins, ends;
+  Span tiles;
+  int loaded;
+  __device__ __forceinline__ TokenWalk(const AttendArgs&, const Range& r)
+      : w(r.w0), end(r.w1), base(r.base), total(r.total), n(r.n), s(r.s), loaded(-1) {}
+  __device__ __forceinline__ bool next(const AttendArgs& a) {
+    if (w >= end) return false;
+    long long all;
+    for (;;) {
+      if (loaded != s) {
+        q = load_seq(a.p, a.b, s, a.status);
+        Span seen;
+        tiles = token_tiles(a, q, &seen);
+        lo = seen.lo;
+        hi = seen.hi;
+        loaded = s;
+      }
+      all = (long long)(tiles.hi - tiles.lo) * a.p.num_kv_heads;
+      if (w - base < all) break;
+      base += all;
+      ++s;
+    }
+    const int nt = tiles.hi - tiles.lo, rel = (int)((w - base) % nt);
+    h = (int)((w - base) / nt);
+    const int cnt = (int)min((long long)(nt - rel), end - w);
+    t0 = tiles.lo + rel;
+    t1 = t0 + cnt;
+    begins = rel == 0;
+    ends = rel + cnt == nt;
+    w += cnt;
+    return true;
+  }
+  // last CTA of this (sequence, head)
+  __device__ __forceinline__ int last_cta() const {
+    const int nt = tiles.hi - tiles.lo;
+    return cta_of(base + (long long)(h + 1) * nt - 1, total, n);
+  }
+};
+
+// ---------------------------------------------------------------- results
+
+// Row r (new token r / G, query head r % G of the group) of a (sequence, head).
+__device__ __forceinline__ long long out_at(const AttendArgs& a, const Seq& q, int h, int r) {
+  return (long long)(q.q0 + r / a.G) * a.ots + (long long)(h * a.G + r % a.G) * a.ohs;
+}
+__device__ __forceinline__ void write_lse(const AttendArgs& a, const Seq& q, int h, int r, float m, float l) {
+  if (a.lse)
+    a.lse[(long long)(q.q0 + r / a.G) * a.Hq + h * a.G + r % a.G] =
+        l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+// 1 / l; 0 for a row without weight (it sees nothing, or only scores of -inf).
+__device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+
+// ---------------------------------------------------------------- host
+
+cudaError_t launch_attend_token(const AttendArgs& a, cudaStream_t s);
+// Joins the partial sums of the (sequence, head, block of `rows` rows)s that a
+// cut divided; `used`: rows of a block that any sequence has.
+cudaError_t launch_combine(const AttendArgs& a, int rows, int used, cudaStream_t s);
+// Pages of k or v as rows of head_dim, boxes of box_rows rows x 128 bytes (or the whole row, if shorter), swizzled.
+bool pages_map(CUtensorMap* m, const ft_kv_pages& p, const void* base, int box_rows);
+
+// Raise a kernel's limit of dynamic shared memory, once per device
+// (kId: a number of its own for each kernel of one type.)
+template <int kId, typename Kernel>
+cudaError_t allow_smem(Kernel* kernel, int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+  return e;
+}
+// A launch that may begin while the kernel before it on the stream ends (the kernel waits for its end itself).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace kv
+}  // namespace ft
