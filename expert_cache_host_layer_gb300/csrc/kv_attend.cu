@@ -1,7 +1,6 @@
 // Attention over the paged key/value cache (ft_kv_attend): the entry point,
-// the workspace, the kernel that joins partial sums, and the plain kernel, one
-// warp per row (new token, query head) that walks the row's visible tokens
-// with a running maximum and sum.
+// the choice of the kernel, the workspace, and the kernel that joins partial
+// sums.
 #include <algorithm>
 
 #include "driver_api.h"
@@ -10,83 +9,6 @@
 namespace ft {
 namespace kv {
 namespace {
-
-struct RowArgs {
-  ft_kv_pages p;
-  ft_kv_batch b;
-  const __nv_bfloat16* q;
-  __nv_bfloat16* out;
-  float* lse;
-  int64_t qts, qhs, ots, ohs;
-  float scale;
-  int Hq, causal, window;
-  int32_t* status;
-};
-
-template <int D, bool kFp8>
-__device__ __forceinline__ void load_lane(const uint8_t* base, const uint8_t* scales, long long row, int lane, float* x) {
-  constexpr int N = D / 32;
-  if (kFp8) {
-    const float sc = scale_of(__ldg(scales + row));
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const __nv_fp8x2_storage_t c = __ldg(reinterpret_cast<const uint16_t*>(base + row * D + lane * N + i));
-      const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-      x[i] = f.x * sc;
-      x[i + 1] = f.y * sc;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(base + row * (2 * D) + (lane * N + i) * 2));
-      x[i] = __uint_as_float(w << 16);
-      x[i + 1] = __uint_as_float(w & 0xffff0000u);
-    }
-  }
-}
-
-template <int D, bool kFp8>
-__global__ void row_kernel(RowArgs a) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long r = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-  if (r >= (long long)a.b.num_tokens * a.Hq) return;
-  const int t = (int)(r / a.Hq), hq = (int)(r % a.Hq);
-  const int H = a.p.num_kv_heads, h = hq / (a.Hq / H), P = a.p.page_tokens;
-  const int s = find_seq(a.b.q_start, a.b.num_seqs, t);
-  const Seq q = load_seq(a.p, a.b, s, a.status);
-  const int pos = q.n - q.m + (t - q.q0);
-  const int lo = a.causal && a.window ? max(0, pos - a.window + 1) : 0;
-  const int hi = t - q.q0 >= q.m ? 0 : a.causal ? min(q.n, pos + 1) : q.n;
-  float x[N], o[N], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] = __bfloat162float(a.q[t * a.qts + hq * a.qhs + lane * N + i]);
-    o[i] = 0.0f;
-  }
-  for (int j = lo; j < hi; ++j) {
-    const int page = max(0, load_page(a.p, a.b, s, j / P, a.status));
-    const long long row = ((long long)page * H + h) * P + j % P;
-    float k[N], v[N], d = 0.0f;
-    load_lane<D, kFp8>(static_cast<const uint8_t*>(a.p.k), a.p.k_scale, row, lane, k);
-    load_lane<D, kFp8>(static_cast<const uint8_t*>(a.p.v), a.p.v_scale, row, lane, v);
-#pragma unroll
-    for (int i = 0; i < N; ++i) d = fmaf(x[i], k[i], d);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) d += __shfl_xor_sync(0xffffffffu, d, w);
-    d *= a.scale;
-    const float mn = fmaxf(m, d), base = mn == -INFINITY ? 0.0f : mn;
-    const float c = expf(m - base), p = expf(d - base);
-    l = l * c + p;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = o[i] * c + p * v[i];
-    m = mn;
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-  for (int i = 0; i < N; ++i) a.out[t * a.ots + hq * a.ohs + lane * N + i] = __float2bfloat16(o[i] * inv);
-  if (a.lse && lane == 0) a.lse[r] = l == 0.0f ? -INFINITY : m + logf(l);
-}
 
 // ---------------------------------------------------------------- partial sums
 
@@ -214,6 +136,10 @@ Workspace layout(const ft_kv_pages& p, int grid, int rows) {
   return w;
 }
 
+// Rows of a block of the kernel that takes the batch: token_kernel where every
+// (sequence, key head) fits its 16 rows, else chunk_kernel.
+int block_rows(const ft_kv_batch& b, int G) { return (long long)b.max_q_len * G <= kTokenRows ? kTokenRows : kChunkRows; }
+
 ft_status check_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads) {
   ft_status st = check_pages(pages);
   if (st == FT_OK) st = check_batch(pages, batch);
@@ -231,7 +157,7 @@ ft_status check_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32
 
 extern "C" uint64_t ft_kv_attend_workspace(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads) {
   if (check_attend(pages, batch, num_q_heads) != FT_OK) return 0;
-  return layout(*pages, sm_count(), kTokenRows).bytes;
+  return layout(*pages, sm_count(), block_rows(*batch, num_q_heads / pages->num_kv_heads)).bytes;
 }
 
 extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads,
@@ -250,44 +176,28 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return set_error(FT_ERR_INVALID_ARG, "workspace is null or not 256-byte aligned");
   const int G = num_q_heads / pages->num_kv_heads;
-  const int grid = sm_count();
-  const Workspace ws = layout(*pages, grid, kTokenRows);
+  const long long rows = (long long)batch->max_q_len * G;  // of a (sequence, key head), at most
+  if (rows > 0x7fffffffLL / 2) return set_error(FT_ERR_UNSUPPORTED, "max_q_len * (num_q_heads / num_kv_heads) is too large");
+  const int block = block_rows(*batch, G), grid = sm_count();
+  const Workspace ws = layout(*pages, grid, block);
   if (workspace_bytes < ws.bytes)
     return set_error(FT_ERR_INVALID_ARG, "workspace of %llu bytes: %llu are needed",
                      (unsigned long long)workspace_bytes, (unsigned long long)ws.bytes);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const long long rows = (long long)batch->max_q_len * G;  // of a (sequence, key head), at most
-  cudaError_t e;
-  if (rows <= kTokenRows) {
-    AttendArgs a{};
-    a.p = *pages; a.b = *batch;
-    a.q = static_cast<const __nv_bfloat16*>(q); a.out = static_cast<__nv_bfloat16*>(out); a.lse = lse;
-    a.qts = q_token_stride; a.qhs = q_head_stride; a.ots = out_token_stride; a.ohs = out_head_stride;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    a.Hq = num_q_heads; a.G = G; a.causal = causal != 0; a.window = window; a.grid = grid;
-    if ((st = status_word(&a.status)) != FT_OK) return st;
-    uint8_t* w = static_cast<uint8_t*>(workspace);
-    a.desc = reinterpret_cast<int4*>(w);
-    a.part_ml = reinterpret_cast<float*>(w + ws.ml);
-    a.part_o = reinterpret_cast<float*>(w + ws.o);
-    if ((e = launch_attend_token(a, s)) != cudaSuccess)
-      return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
-    if ((e = launch_combine(a, kTokenRows, (int)rows, s)) != cudaSuccess)
-      return set_error(FT_ERR_CUDA, "attend join launch: %s", cudaGetErrorString(e));
-    return FT_OK;
-  }
-  RowArgs a{};
+  AttendArgs a{};
   a.p = *pages; a.b = *batch;
   a.q = static_cast<const __nv_bfloat16*>(q); a.out = static_cast<__nv_bfloat16*>(out); a.lse = lse;
   a.qts = q_token_stride; a.qhs = q_head_stride; a.ots = out_token_stride; a.ohs = out_head_stride;
-  a.scale = scale; a.Hq = num_q_heads; a.causal = causal != 0; a.window = window;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.Hq = num_q_heads; a.G = G; a.causal = causal != 0; a.window = window; a.grid = grid;
   if ((st = status_word(&a.status)) != FT_OK) return st;
-  const long long blocks = ((long long)batch->num_tokens * num_q_heads + 3) / 4;
-  if (blocks > 0x7fffffffLL) return set_error(FT_ERR_UNSUPPORTED, "num_tokens * num_q_heads is too large");
-  const bool fp8 = pages->kv_dtype == FT_KV_FP8E4M3;
-  auto* kernel = pages->head_dim == 128 ? (fp8 ? row_kernel<128, true> : row_kernel<128, false>)
-                                        : (fp8 ? row_kernel<64, true> : row_kernel<64, false>);
-  kernel<<<(unsigned)blocks, 128, 0, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.desc = reinterpret_cast<int4*>(w);
+  a.part_ml = reinterpret_cast<float*>(w + ws.ml);
+  a.part_o = reinterpret_cast<float*>(w + ws.o);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = block == kTokenRows ? launch_attend_token(a, s) : launch_attend_chunk(a, s);
+  if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
+  if ((e = launch_combine(a, block, (int)std::min<long long>(rows, block), s)) != cudaSuccess)
+    return set_error(FT_ERR_CUDA, "attend join launch: %s", cudaGetErrorString(e));
   return FT_OK;
 }

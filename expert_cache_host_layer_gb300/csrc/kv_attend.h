@@ -15,6 +15,7 @@ namespace kv {
 
 constexpr int kTokenRows = 16;    // most rows of a (sequence, key head) in token_kernel
 constexpr int kTokenTile = 128;   // tokens per tile of its ring
+constexpr int kChunkRows = 256;   // rows of a block in chunk_kernel
 
 struct AttendArgs {
   ft_kv_pages p;
@@ -89,8 +90,9 @@ __device__ __forceinline__ Range cut(const AttendArgs& a, long long* pre, long l
   const int S = a.b.num_seqs, T = blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (S + T - 1) / T, s0 = min(S, (int)threadIdx.x * per), s1 = min(S, s0 + per);
   long long mine = 0;
-  for (int s = s0; s < s1; ++s) {
-    pre[s] = mine;
+  for (int k = 0; k < per; ++k) {  // whole warps together: count() may use them; count(S) = 0
+    const int s = s0 + k < s1 ? s0 + k : S;
+    if (s < S) pre[s] = mine;
     mine += count(s);
   }
   long long incl = mine;
@@ -140,6 +142,7 @@ __device__ __forceinline__ Span token_tiles(const AttendArgs& a, const Seq& q, S
 }
 __device__ __forceinline__ Range token_range(const AttendArgs& a, long long* pre, long long* scan) {
   return cut(a, pre, scan, [&](int s) {
+    if (s == a.b.num_seqs) return 0LL;
     Span seen;
     const Span t = token_tiles(a, load_seq(a.p, a.b, s, a.status), &seen);
     return (long long)(t.hi - t.lo) * a.p.num_kv_heads;
@@ -209,6 +212,7 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.
 // ---------------------------------------------------------------- host
 
 cudaError_t launch_attend_token(const AttendArgs& a, cudaStream_t s);
+cudaError_t launch_attend_chunk(const AttendArgs& a, cudaStream_t s);
 // Joins the partial sums of the (sequence, head, block of `rows` rows)s that a
 // cut divided; `used`: rows of a block that any sequence has.
 cudaError_t launch_combine(const AttendArgs& a, int rows, int used, cudaStream_t s);

@@ -1,0 +1,859 @@
+// Attention of many rows (prompt chunks, several new tokens) over the paged
+// cache on the 5th-generation tensor cores.
+//
+//   S = Q K^T,  P = 2^(x - m),  O += P V,  out = O / sum P
+//
+// with a running maximum m per row and x = scale log2(e) S.  Quantised cache:
+// the key's scale multiplies S, the value's scale P (after its share of the
+// sum), and the codes are multiplied, as in kv_token.cu.
+//
+// Item: a tile of 128 tokens for a block of 256 rows (new token x query head
+// of the group, so that a group's heads share the loaded K and V) of one
+// (sequence, key head).  The batch's items, laid end to end, are cut into
+// equal ranges, one per CTA; a row block that a cut divides leaves partial
+// sums that combine_kernel joins.  Rows of one block are two sub-tiles of 128,
+// each with its own score tile, output accumulator and softmax warpgroup:
+//
+//   warps 0-3, 4-7   softmax of sub-tile 0, 1: load Q into shared memory, and
+//                    per tile read S from TMEM (a thread per row), mask,
+//                    exponentiate, write P (16 bits) over S in TMEM; at the end
+//                    scale O and store it
+//   warp 8           producer: K and V tiles into a ring, one TMA box per page
+//                    (or half page row), 128-byte swizzled
+//   warp 9           tcgen05.mma: S_w = Q_w K^T (M 128, N 128), O_w += P_w V
+//                    with P read from TMEM and V as it lies (token-major)
+//   warps 12-15      quantised cache: expand the codes of a raw ring into tiles
+//                    of the layout that the MMA reads (exact; K in fp16, V in
+//                    bf16, whose range P needs)
+//
+// The MMA order PV_0(j-1) S_0(j) PV_1(j-1) S_1(j) keeps the tensor pipe on one
+// sub-tile while the other's softmax runs.  S_w(j)'s completion implies
+// PV_w(j-1)'s, so the softmax of tile j may rescale O_w; it does so only when
+// a row's maximum has grown by more than 2^8 since O_w's scale was set (P is
+// then at most 2^8, and the final division removes any scale).
+//
+// Bound: the tensor pipe, 4 D flops per (row, token).
+#include "kv_attend.h"
+
+namespace ft {
+namespace kv {
+namespace {
+
+constexpr int kSub = 128;
+constexpr int kTile = 128;                    // tokens per tile
+constexpr int kTmemCols = 512;                // S0 | S1 | O0 | O1, 128 columns each
+constexpr float kGrow = 8.0f;                 // log2 of the growth that O's scale may lag behind
+constexpr int kBfThreads = 384, kFpThreads = 512;
+// Registers of the warpgroups (softmax, producer and MMA, converters): within
+// what the block is launched with, 384 x 168 and 512 x 128.
+constexpr int kBfSoft = 216, kBfRest = 72, kFpSoft = 184, kFpRest = 56, kFpCvt = 88;
+static_assert(256 * kBfSoft + 128 * kBfRest <= kBfThreads * 168, "registers");
+static_assert(256 * kFpSoft + 128 * (kFpRest + kFpCvt) <= kFpThreads * 128, "registers");
+constexpr int kCvtWarps = 4;
+
+template <int D, bool kFp8>
+struct Layout {
+  static constexpr int kQBytes = 2 * kSub * D * 2;
+  static constexpr int kTileBytes = kTile * D * 2;                      // a K or V tile as the MMA reads it
+  static constexpr int kRawBytes = kFp8 ? kTile * D : 0;
+  static constexpr int kStages = (kFp8 ? 3 : 5) * (128 / D);
+  static constexpr int kRaw = kFp8 ? 3 * (128 / D) : 0;
+  static constexpr int kRingOff = kQBytes;
+  static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;          // per warpgroup, twice: 128 x {k, v}
+  static constexpr int kScaleBytes = kFp8 ? 2 * 2 * 2 * kTile * 4 : 0;
+  static constexpr int kRowOff = kScaleOff + kScaleBytes;               // Q's row scales
+  static constexpr int kRowBytes = kFp8 ? 2 * kSub * 4 : 0;
+  static constexpr int kBarOff = kRowOff + kRowBytes;
+  static constexpr int kBars = 2 * kStages + 2 * kRaw + 8 + 1;
+  static constexpr int kSmem = kBarOff + kBars * 8 + 64 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kStages * kTileBytes >= (kMaxSeqs + 1) * 8 + 1024, "the prefix sums fit the ring before it fills");
+};
+
+// ---------------------------------------------------------------- PTX wrappers
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(dec::smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bd, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(at), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 consecutive columns of this thread's TMEM lane; ld_wait() before use.
+__device__ __forceinline__ void ld32(uint32_t t, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t));
+}
+__device__ __forceinline__ void st32(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(dec::smem_addr(bar))
+      : "memory");
+}
+// Shared-memory matrix descriptor, 128-byte swizzle, rows of 128 bytes, 8-row
+// groups 1024 bytes apart.  K-major (Q, K): the leading offset is not used.
+// N-major (V: a row is a token, 64 of head_dim wide): the leading offset leads
+// to the next 64 columns, the next half of the tile.
+__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lead = 16) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16, fp32 accumulator, both operands bf16 (or fp16), B N-major or not.
+__device__ constexpr uint32_t idesc(int N, bool bf16, bool b_n_major) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_n_major ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kSub >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, bool half) {
+  if (half) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// ---------------------------------------------------------------- items
+
+// A row block: what its rows see, in tokens and tiles, whole and per sub-tile.
+struct Block {
+  int lo, hi;            // tokens that some row sees
+  int t0, t1;            // tiles of the block (at least one)
+  int s0[2], s1[2];      // tiles of each sub-tile (none: s0 = s1)
+  int all_lo, all_hi;    // tokens that every row sees
+};
+__device__ __forceinline__ Block block_of(const AttendArgs& a, const Seq& q, int rb) {
+  Block b;
+  const int rows = q.m * a.G;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int r0 = rb * kChunkRows + w * kSub, r1 = min(rows, r0 + kSub) - 1;
+    b.s0[w] = b.s1[w] = 0;
+    if (r0 > r1) continue;
+    const Span f = visible(a, q, r0 / a.G), l = visible(a, q, r1 / a.G);
+    if (l.hi > f.lo) {
+      b.s0[w] = f.lo / kTile;
+      b.s1[w] = (l.hi + kTile - 1) / kTile;
+    }
+    if (w == 0) {
+      b.lo = f.lo;
+      b.all_hi = f.hi;
+    }
+    b.hi = l.hi;
+    b.all_lo = l.lo;
+  }
+  b.t0 = b.lo / kTile;
+  b.t1 = max(b.t0 + 1, (b.hi + kTile - 1) / kTile);
+  return b;
+}
+__device__ __forceinline__ int blocks_of(const AttendArgs& a, const Seq& q) {
+  return (int)(((long long)q.m * a.G + kChunkRows - 1) / kChunkRows);
+}
+__device__ __forceinline__ int tiles_of(const AttendArgs& a, const Seq& q, int rb) {
+  const Block b = block_of(a, q, rb);
+  return b.t1 - b.t0;
+}
+// Items of one head of a sequence, summed by the whole warp.
+__device__ __forceinline__ long long head_items(const AttendArgs& a, const Seq& q, int lane) {
+  long long n = 0;
+  const int nb = blocks_of(a, q);
+  for (int rb = lane; rb < nb; rb += 32) n += tiles_of(a, q, rb);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+
+// The row blocks of a CTA's range, one after the other.  Whole warps.
+struct ChunkWalk {
+  long long w, end, base, total, at;  // at: first item of the current block
+  int n, s, h, rb, nb;
+  Seq q;
+  Block b;
+  int t0, t1;  // tiles of the block that are this CTA's
+  bool begins, ends, started;
+  __device__ __forceinline__ ChunkWalk(const Range& r)
+      : w(r.w0), end(r.w1), base(r.base), total(r.total), at(r.base), n(r.n), s(r.s), h(0), rb(0), nb(0),
+        started(false) {}
+  __device__ __forceinline__ bool next(const AttendArgs& a, int lane) {
+    if (w >= end) return false;
+    if (!started) {
+      started = true;
+      find(a, lane);
+    } else {  // the range goes on: past a whole block
+      at += b.t1 - b.t0;
+      if (++rb == nb) {
+        rb = 0;
+        if (++h == a.p.num_kv_heads) {
+          h = 0;
+          do {
+            ++s;
+            q = load_seq(a.p, a.b, s, a.status);
+          } while (q.m == 0);
+          nb = blocks_of(a, q);
+        }
+      }
+    }
+    b = block_of(a, q, rb);
+    const int nt = b.t1 - b.t0, rel = (int)(w - at), cnt = (int)min((long long)(nt - rel), end - w);
+    t0 = b.t0 + rel;
+    t1 = t0 + cnt;
+    begins = rel == 0;
+    ends = rel + cnt == nt;
+    w += cnt;
+    return true;
+  }
+  // the head and row block of item w
+  __device__ __forceinline__ void find(const AttendArgs& a, int lane) {
+    long long per;
+    for (;; ++s) {
+      q = load_seq(a.p, a.b, s, a.status);
+      per = head_items(a, q, lane);
+      if (w - base < per * a.p.num_kv_heads) break;
+      base += per * a.p.num_kv_heads;
+    }
+    nb = blocks_of(a, q);
+    h = (int)((w - base) / per);
+    at = base + h * per;
+    for (int r0 = 0;; r0 += 32) {
+      const int mine = r0 + lane < nb ? tiles_of(a, q, r0 + lane) : 0;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, at + incl > w);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        rb = r0 + l;
+        at += __shfl_sync(0xffffffffu, incl - mine, l);
+        return;
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  __device__ __forceinline__ int last_cta() const { return cta_of(at + (b.t1 - b.t0) - 1, total, n); }
+  __device__ __forceinline__ bool active(int sub, int t) const { return t >= b.s0[sub] && t < b.s1[sub]; }
+  // does sub-tile `sub` have a tile in this part?
+  __device__ __forceinline__ bool any(int sub) const { return max(t0, b.s0[sub]) < min(t1, b.s1[sub]); }
+};
+
+struct Shared {
+  uint8_t* base;
+  uint64_t *full, *empty, *rfull, *rempty, *qfull, *sfull, *pfull, *ofull, *drain;
+  uint32_t* tmem;
+  volatile int* abort_flag;
+  volatile int* poison;  // [2][2] first and last tile with values that a sub-tile adds at its block's end
+};
+
+template <int D, bool kFp8>
+__device__ __forceinline__ Shared carve(uint8_t* raw) {
+  using L = Layout<D, kFp8>;
+  Shared s;
+  s.base = raw + ((1024u - (dec::smem_addr(raw) & 1023u)) & 1023u);
+  uint64_t* b = reinterpret_cast<uint64_t*>(s.base + L::kBarOff);
+  s.full = b;
+  s.empty = b + L::kStages;
+  s.rfull = b + 2 * L::kStages;
+  s.rempty = s.rfull + L::kRaw;
+  s.qfull = s.rempty + L::kRaw;
+  s.sfull = s.qfull + 2;
+  s.pfull = s.qfull + 4;
+  s.ofull = s.qfull + 6;
+  s.drain = s.qfull + 8;
+  s.tmem = reinterpret_cast<uint32_t*>(s.drain + 1);
+  s.abort_flag = reinterpret_cast<volatile int*>(s.tmem + 1);
+  s.poison = reinterpret_cast<volatile int*>(s.tmem + 4);
+  return s;
+}
+
+// ---------------------------------------------------------------- producer
+
+// Per tile: K then V, the pages' boxes spread over the lanes.
+template <int D, bool kFp8>
+__device__ void produce(const AttendArgs& a, const Range& rg, const Shared& s, const CUtensorMap* map_k,
+                        const CUtensorMap* map_v, int lane) {
+  using L = Layout<D, kFp8>;
+  constexpr int kSlots = kFp8 ? L::kRaw : L::kStages;
+  constexpr int kHalves = kFp8 ? 1 : D / 64;
+  uint64_t* full = kFp8 ? s.rfull : s.full;
+  uint64_t* empty = kFp8 ? s.rempty : s.empty;
+  const uint32_t ring = dec::smem_addr(s.base + (kFp8 ? L::kRawOff : L::kRingOff));
+  constexpr uint32_t kBytes = kFp8 ? L::kRawBytes : L::kTileBytes;
+  const int br = min(a.p.page_tokens, kTile);  // tokens of a box
+  const int box = lane / kHalves, half = lane % kHalves;
+  constexpr int kRowBytes = kFp8 ? D : 128;
+  int it = 0;
+  bool go = true;
+  ChunkWalk w(rg);
+  while (go && w.next(a, lane)) {
+    for (int t = w.t0; t < w.t1 && go; ++t) {
+      const int j0 = t * kTile + box * br;
+      const bool mine = box * br < kTile && j0 < w.b.hi && j0 + br > w.b.lo;
+      int row = 0;
+      if (mine) {
+        const int page = max(0, load_page(a.p, a.b, w.s, j0 / a.p.page_tokens, a.status));
+        row = (page * a.p.num_kv_heads + w.h) * a.p.page_tokens + j0 % a.p.page_tokens;
+      }
+      const int live = __popc(__ballot_sync(0xffffffffu, mine));
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv, ++it) {
+        const int st = it % kSlots;
+        if (!wait_or_abort(&empty[st], ((it / kSlots) & 1) ^ 1, a.status, s.abort_flag)) {
+          go = false;
+          break;
+        }
+        if (lane == 0) dec::mbar_expect_tx(&full[st], live * br * kRowBytes);
+        __syncwarp();
+        if (mine)
+          tma_box(ring + st * kBytes + half * (kTile * 128) + box * br * kRowBytes, kv ? map_v : map_k, half * 64, row,
+                  &full[st]);
+      }
+    }
+  }
+  // no copy may still be writing this CTA's shared memory when it exits
+  for (int j = max(0, it - kSlots); j < it; ++j) dec::mbar_wait(&full[j % kSlots], (j / kSlots) & 1, a.status);
+}
+
+// ---------------------------------------------------------------- MMA
+
+// V rows (tokens) [r0, r1) of a tile to zero; whole warp.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int r1, int lane) {
+  constexpr int kPer = D / 8;
+  for (int i = r0 * kPer + lane; i < r1 * kPer; i += 32) {
+    const int r = i / kPer, ch = i % kPer;
+    *reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+  }
+}
+// Values of V rows [r0, r1) that are not finite, set to zero; whether there were any.
+template <int D>
+__device__ __forceinline__ bool take_not_finite(uint8_t* tile, int r0, int r1, int lane) {
+  constexpr int kPer = D / 8;
+  bool any = false;
+  for (int i = r0 * kPer + lane; i < r1 * kPer; i += 32) {
+    const int r = i / kPer, ch = i % kPer;
+    uint4* at = reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) << 4));
+    uint4 v = *at;
+    uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if ((x[k] & 0x7f80u) == 0x7f80u) { x[k] &= 0xffff0000u; bad = true; }
+      if ((x[k] & 0x7f800000u) == 0x7f800000u) { x[k] &= 0x0000ffffu; bad = true; }
+    }
+    if (bad) *at = v;
+    any |= bad;
+  }
+  return __any_sync(0xffffffffu, any);
+}
+
+template <int D, bool kFp8>
+__device__ void multiply(const AttendArgs& a, const Range& rg, const Shared& s, uint32_t tmem, int lane) {
+  using L = Layout<D, kFp8>;
+  const uint32_t ring = dec::smem_addr(s.base + L::kRingOff), qa = dec::smem_addr(s.base);
+  constexpr uint32_t id_s = idesc(kTile, !kFp8, false), id_o = idesc(D, true, true);
+  int it = 0;
+  uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+  bool go = true;
+  ChunkWalk w(rg);
+  while (go && w.next(a, lane)) {
+    int bad0 = 0x7fffffff, bad1 = -1;
+    bool live[2] = {false, false};  // O_w has been written in this part
+    for (int t = w.t0; t <= w.t1 && go; ++t) {
+      const int ki = it, vi = it - 1;  // ring positions of K(t) and V(t - 1)
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        if (t > w.t0) {  // O_sub += P_sub(t - 1) V(t - 1)
+          if (sub == 0) {
+            uint8_t* V = s.base + L::kRingOff + (vi % L::kStages) * L::kTileBytes;
+            if (!(go = wait_or_abort(&s.full[vi % L::kStages], (vi / L::kStages) & 1, a.status, s.abort_flag))) break;
+            if (!kFp8) {
+              const int j0 = (t - 1) * kTile, r0 = max(0, w.b.lo - j0), r1 = min(kTile, max(0, w.b.hi - j0));
+              const bool edge = r0 > 0 || r1 < kTile;
+              if (edge) {  // tokens that no row sees may hold anything
+                zero_rows<D>(V, 0, min(r0, kTile), lane);
+                zero_rows<D>(V, r1, kTile, lane);
+              }
+              // tokens that some rows see and others do not: 0 * V must not reach the others
+              bool took = false;
+              if (w.b.all_hi < j0 + r1) took |= take_not_finite<D>(V, max(r0, w.b.all_hi - j0), r1, lane);
+              if (w.b.all_lo > j0 + r0) took |= take_not_finite<D>(V, r0, min(r1, w.b.all_lo - j0), lane);
+              if (took) {
+                bad0 = min(bad0, t - 1);
+                bad1 = t - 1;
+              }
+              if (edge || took) {
+                fence_async();
+                __syncwarp();
+              }
+            }
+          }
+          if (w.active(sub, t - 1)) {
+            if (!(go = wait_or_abort(&s.pfull[sub], np[sub] & 1, a.status, s.abort_flag))) break;
+            ++np[sub];
+            fence_after();
+            if (lane == 0) {
+              const uint32_t V = ring + (vi % L::kStages) * L::kTileBytes;
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(tmem + 256 + sub * 128, tmem + sub * 128 + k * 8, desc(V + k * 2048, kTile * 128), id_o,
+                       live[sub] || k);
+            }
+            live[sub] = true;
+          }
+        }
+        if (t < w.t1) {  // S_sub = Q_sub K(t)^T
+          if (sub == 0 &&
+              !(go = wait_or_abort(&s.full[ki % L::kStages], (ki / L::kStages) & 1, a.status, s.abort_flag)))
+            break;
+          if (w.active(sub, t)) {
+            if (t == max(w.t0, w.b.s0[sub])) {
+              if (!(go = wait_or_abort(&s.qfull[sub], nq[sub] & 1, a.status, s.abort_flag))) break;
+              ++nq[sub];
+            }
+            fence_after();
+            if (lane == 0) {
+              const uint32_t K = ring + (ki % L::kStages) * L::kTileBytes, Q = qa + sub * kSub * D * 2;
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss(tmem + sub * 128, desc(Q + (k >> 2) * (kSub * 128) + (k & 3) * 32),
+                       desc(K + (k >> 2) * (kTile * 128) + (k & 3) * 32), id_s, k != 0);
+              commit(&s.sfull[sub]);
+            }
+          }
+        }
+      }
+      if (!go) break;
+      if (lane == 0) {
+        if (t > w.t0) commit(&s.empty[vi % L::kStages]);
+        if (t < w.t1) commit(&s.empty[ki % L::kStages]);
+      }
+      it += t < w.t1 ? 2 : 0;
+    }
+    if (!go) break;
+    // K and V of the last tile have been passed: `it` is at the next block's first K
+    if (lane == 0) {
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+        if (live[sub]) {  // (its warpgroup has read the block before: it has written P since)
+          s.poison[sub * 2] = bad0;
+          s.poison[sub * 2 + 1] = bad1;
+          commit(&s.ofull[sub]);
+          dec::mbar_arrive(&s.ofull[sub]);
+        }
+    }
+  }
+  // every MMA issued has completed before TMEM is freed
+  if (lane == 0) {
+    commit(s.drain);
+    dec::mbar_wait(s.drain, 0, a.status);
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------- softmax
+
+template <int D, bool kFp8>
+__device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, uint32_t tmem, int sub, int tid) {
+  using L = Layout<D, kFp8>;
+  const int lane = tid & 31, quarter = (tid >> 5) & 3;
+  const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+  const uint32_t ts = tmem + lanes + sub * 128, to = tmem + lanes + 256 + sub * 128;
+  uint8_t* Q = s.base + sub * kSub * D * 2;
+  float* scales = reinterpret_cast<float*>(s.base + L::kScaleOff) + sub * 2 * 2 * kTile;
+  float* row_scale = reinterpret_cast<float*>(s.base + L::kRowOff) + sub * kSub;
+  // the warpgroup's barrier, and whether any of its threads says so
+  auto group_any = [&](bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.pred p, %2, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(1 + sub)
+        : "memory");
+    return r != 0;
+  };
+  uint32_t ns = 0, no = 0;
+  int turn = 0;
+  int4 begun = make_int4(-1, 0, 0, 0);
+  const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // a negative scale goes into Q's signs
+  const float c0 = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);  // never 0: 0 * -inf is not -inf
+  ChunkWalk w(rg);
+  bool ok = true;
+  while (w.next(a, lane)) {
+    const int rows = w.q.m * a.G, r_base = w.rb * kChunkRows + sub * kSub;
+    const int r = r_base + tid;
+    const bool mine = r < rows;
+    const bool any = w.any(sub);
+    float m = -INFINITY, l = 0.0f, c = c0;
+    if (any) {
+      // Q: the previous block's last score tile is done, so its Q is free
+      constexpr int kPer = D / 8;
+      for (int i = tid; i < kSub * kPer; i += 128) {
+        const int rr = i / kPer, ch = i % kPer, row = r_base + rr;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < rows)
+          v = __ldg(reinterpret_cast<const uint4*>(a.q + (long long)(w.q.q0 + row / a.G) * a.qts +
+                                                   (long long)(w.h * a.G + row % a.G) * a.qhs) +
+                    ch);
+        v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+        if (kFp8) {  // to fp16, the row scaled to [1, 2)
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = max(top, max((u[k] << 16) & 0x7f800000u, u[k] & 0x7f800000u));
+#pragma unroll
+          for (int o = kPer / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = min(max((int)(top >> 23), 1), 253);
+          const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+          uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = pack2(dec::bf16_lo(u[k]) * down, dec::bf16_hi(u[k]) * down, true);
+          if (ch == 0) row_scale[rr] = __uint_as_float((uint32_t)e << 23);
+        }
+        *reinterpret_cast<uint4*>(Q + (ch >> 3) * (kSub * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) dec::mbar_arrive(&s.qfull[sub]);
+    }
+    const Span v = visible(a, w.q, mine ? r / a.G : 0);
+    const int lo = mine ? v.lo : 0, hi = mine ? v.hi : 0;
+    bool first = true;
+    for (int t = max(w.t0, w.b.s0[sub]); t < min(w.t1, w.b.s1[sub]); ++t) {
+      const int j0 = t * kTile;
+      float* sc = scales + turn * 2 * kTile;
+      bool nan_scale = false;
+      if (kFp8) {  // this thread's token's scales, for the whole warpgroup
+        float kf = 0.0f, vf = 0.0f;
+        if (j0 + tid >= w.b.lo && j0 + tid < w.b.hi) {
+          const int page = max(0, load_page(a.p, a.b, w.s, (j0 + tid) / a.p.page_tokens, a.status));
+          const long long at =
+              ((long long)page * a.p.num_kv_heads + w.h) * a.p.page_tokens + (j0 + tid) % a.p.page_tokens;
+          kf = scale_of(__ldg(a.p.k_scale + at));
+          vf = scale_of(__ldg(a.p.v_scale + at));
+        }
+        sc[tid] = kf;
+        sc[kTile + tid] = vf;
+        // two buffers: everyone has left the tile before the last
+        nan_scale = group_any(isnan(vf));
+        turn ^= 1;
+        if (first) c = c0 * row_scale[tid];
+      }
+      ok = ok && wait_or_abort(&s.sfull[sub], ns & 1, a.status, s.abort_flag);
+      ++ns;
+      if (!ok) continue;
+      fence_after();
+      float x[128];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ld32(ts + 32 * k, x + 32 * k);
+      ld_wait();
+      if (kFp8) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k) x[k] *= sc[k];
+      }
+      if (j0 < w.b.all_lo || j0 + kTile > w.b.all_hi) {  // some row does not see some of it
+        const unsigned from = (unsigned)(lo - j0), width = (unsigned)(hi - lo);
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if ((unsigned)k - from >= width) x[k] = -INFINITY;
+      }
+      float top4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int k = 4; k < 128; ++k) top4[k & 3] = fmaxf(top4[k & 3], x[k]);
+      float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+      top *= c;
+      if (first) {
+        m = top;
+        first = false;
+      } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
+        const float mn = fmaxf(m, top), f = top > m ? exp2_approx(m - mn) : 1.0f;
+        m = mn;
+        l *= f;
+        for (int k = 0; k < D; k += 32) {
+          float o[32];
+          ld32(to + k, o);
+          ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= f;
+          st32(to + k, reinterpret_cast<const uint32_t*>(o));
+        }
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      uint32_t p[64];
+#pragma unroll
+      for (int k = 0; k < 128; k += 2) {
+        float p0 = exp2_approx(fmaf(x[k], c, -base)), p1 = exp2_approx(fmaf(x[k + 1], c, -base));
+        sum[k & 3] += p0;
+        sum[(k & 3) + 1] += p1;
+        if (kFp8) {
+          if (nan_scale) {  // 0 * NaN must not reach a row that does not see the token
+            p0 = x[k] == -INFINITY ? 0.0f : p0 * sc[kTile + k];
+            p1 = x[k + 1] == -INFINITY ? 0.0f : p1 * sc[kTile + k + 1];
+          } else {
+            p0 *= sc[kTile + k];
+            p1 *= sc[kTile + k + 1];
+          }
+        }
+        p[k / 2] = pack2(p0, p1, false);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      st32(ts, p);
+      st32(ts + 32, p + 32);
+      st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) dec::mbar_arrive(&s.pfull[sub]);
+    }
+    // ------------------------------------------------------------ the block's end
+    if (any) {
+      ok = ok && wait_or_abort(&s.ofull[sub], no & 1, a.status, s.abort_flag);
+      ++no;
+      if (ok) fence_after();
+    }
+    if (w.begins && !w.ends) begun = make_int4(w.s, w.h, w.rb, w.last_cta());
+    const bool whole = w.begins && w.ends;
+    const long long slot = (2LL * blockIdx.x + w.begins) * kChunkRows + sub * kSub + tid;
+    const float inv = inverse(l);
+    const int bad0 = any && !kFp8 ? s.poison[sub * 2] : 1, bad1 = any && !kFp8 ? s.poison[sub * 2 + 1] : 0;
+    for (int k = 0; k < D; k += 32) {
+      float o[32];
+      if (any && ok) {
+        ld32(to + k, o);
+        ld_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+      }
+      if (!mine) continue;
+      if (bad0 <= bad1) {  // values that are not finite, of the tokens that this row sees in tiles bad0 .. bad1
+        for (int j = max(lo, bad0 * kTile); j < min(hi, (bad1 + 1) * kTile); ++j) {
+          // tokens that every row sees went through the product
+          if (j >= w.b.all_lo && j < w.b.all_hi) continue;
+          const int page = max(0, load_page(a.p, a.b, w.s, j / a.p.page_tokens, a.status));
+          const __nv_bfloat16* at =
+              static_cast<const __nv_bfloat16*>(a.p.v) +
+              (((long long)page * a.p.num_kv_heads + w.h) * a.p.page_tokens + j % a.p.page_tokens) * D + k;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float x = __bfloat162float(at[i]);
+            if (!isfinite(x)) o[i] += x;
+          }
+        }
+      }
+      if (whole) {
+        uint4* out = reinterpret_cast<uint4*>(a.out + out_at(a, w.q, w.h, r) + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          out[i] = make_uint4(pack2(o[8 * i] * inv, o[8 * i + 1] * inv, false),
+                              pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv, false),
+                              pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv, false),
+                              pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv, false));
+      } else {
+        float4* out = reinterpret_cast<float4*>(a.part_o + slot * D + k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      }
+    }
+    if (mine) {
+      if (whole) {
+        write_lse(a, w.q, w.h, r, m, l);
+      } else {
+        a.part_ml[slot * 2] = m;
+        a.part_ml[slot * 2 + 1] = l;
+      }
+    }
+    fence_before();  // the next block's MMAs write O after these reads
+  }
+  if (sub == 0 && tid == 0) a.desc[blockIdx.x] = begun;
+}
+
+// ---------------------------------------------------------------- e4m3 codes to 16-bit tiles
+
+template <int D>
+__device__ void expand(const AttendArgs& a, const Range& rg, const Shared& s, int tid) {
+  using L = Layout<D, true>;
+  const int lane = tid & 31;
+  int it = 0;
+  ChunkWalk w(rg);
+  while (w.next(a, lane)) {
+    for (int t = w.t0; t < w.t1; ++t)
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv, ++it) {
+        const int rs = it % L::kRaw, st = it % L::kStages;
+        if (!wait_or_abort(&s.rfull[rs], (it / L::kRaw) & 1, a.status, s.abort_flag)) return;
+        if (!wait_or_abort(&s.empty[st], ((it / L::kStages) & 1) ^ 1, a.status, s.abort_flag)) return;
+        const uint8_t* src = s.base + L::kRawOff + rs * L::kRawBytes;
+        uint8_t* dst = s.base + L::kRingOff + st * L::kTileBytes;
+        constexpr int kPer = D / 16;  // 16-byte chunks of a raw row
+        const int seen0 = w.b.lo - t * kTile, seen1 = w.b.hi - t * kTile;
+#pragma unroll 4
+        for (int i = tid; i < kTile * kPer; i += kCvtWarps * 32) {
+          const int r = i / kPer, ch = i % kPer;
+          const int phys = D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
+          uint4 c = *reinterpret_cast<const uint4*>(src + r * D + (phys << 4));
+          if (r < seen0 || r >= seen1) c = make_uint4(0, 0, 0, 0);  // tokens that no row sees may hold anything
+          const uint32_t q[4] = {c.x, c.y, c.z, c.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q[k] & 0xffffu), __NV_E4M3);
+            const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q[k] >> 16), __NV_E4M3);
+            if (kv == 0) {
+              o[2 * k] = (uint32_t)x.x | (uint32_t)x.y << 16;
+              o[2 * k + 1] = (uint32_t)y.x | (uint32_t)y.y << 16;
+            } else {
+              const float2 fx = __half22float2(__half2(x)), fy = __half22float2(__half2(y));
+              o[2 * k] = pack2(fx.x, fx.y, false);
+              o[2 * k + 1] = pack2(fy.x, fy.y, false);
+            }
+          }
+          uint8_t* row = dst + (ch >> 2) * (kTile * 128) + r * 128;
+          const int d0 = (ch & 3) * 2;
+          *reinterpret_cast<uint4*>(row + ((d0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(row + (((d0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          dec::mbar_arrive(&s.rempty[rs]);
+          dec::mbar_arrive(&s.full[st]);
+        }
+      }
+  }
+}
+
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ AttendArgs a) {
+  using L = Layout<D, kFp8>;
+  extern __shared__ uint8_t smem_raw[];
+  const Shared s = carve<D, kFp8>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      dec::mbar_init(&s.full[i], kFp8 ? kCvtWarps : 1);
+      dec::mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < L::kRaw; ++i) {
+      dec::mbar_init(&s.rfull[i], 1);
+      dec::mbar_init(&s.rempty[i], kCvtWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      dec::mbar_init(&s.qfull[i], 4);
+      dec::mbar_init(&s.sfull[i], 1);
+      dec::mbar_init(&s.pfull[i], 4);
+      dec::mbar_init(&s.ofull[i], 2);
+    }
+    dec::mbar_init(s.drain, 1);
+    *s.abort_flag = 0;
+    dec::mbar_init_fence();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dec::smem_addr(s.tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    fence_before();
+  }
+  dec::pdl_wait_primary();  // the batch, q and the pages may come from the kernel before
+  long long* pre = reinterpret_cast<long long*>(s.base + L::kRingOff);
+  long long* scan = reinterpret_cast<long long*>(s.base);
+  const Range rg = cut(a, pre, scan, [&](int seq) {
+    // (a warp's lanes are at different sequences; a long one is summed by all)
+    const Seq q = seq < a.b.num_seqs ? load_seq(a.p, a.b, seq, a.status) : Seq{0, 0, 0};
+    const int nb = blocks_of(a, q);
+    long long n = 0;
+    if (nb <= 8)
+      for (int rb = 0; rb < nb; ++rb) n += tiles_of(a, q, rb);
+    for (unsigned big = __ballot_sync(0xffffffffu, nb > 8); big; big &= big - 1) {
+      const int src = __ffs(big) - 1;
+      const Seq o{__shfl_sync(0xffffffffu, q.q0, src), __shfl_sync(0xffffffffu, q.m, src),
+                  __shfl_sync(0xffffffffu, q.n, src)};
+      const long long sum = head_items(a, o, lane);
+      if (lane == src) n = sum;
+    }
+    return n * a.p.num_kv_heads;
+  });
+  fence_async();
+  fence_before();
+  __syncthreads();  // the prefix sums are read; the ring may fill; TMEM's address is there
+  fence_after();
+  const uint32_t tmem = *s.tmem;
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8 ? kFpSoft : kBfSoft));
+    soften<D, kFp8>(a, rg, s, tmem, warp >> 2, threadIdx.x & 127);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8 ? kFpRest : kBfRest));
+    if (warp == 8) produce<D, kFp8>(a, rg, s, &map_k, &map_v, lane);
+    if (warp == 9) multiply<D, kFp8>(a, rg, s, tmem, lane);
+  } else if (kFp8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFpCvt));
+    expand<D>(a, rg, s, threadIdx.x - 384);
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+  dec::pdl_launch_dependents();
+}
+
+template <int D, bool kFp8>
+cudaError_t launch(const AttendArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  const cudaError_t e = allow_smem<4096 + D * 2 + kFp8>(chunk_kernel<D, kFp8>, Layout<D, kFp8>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(chunk_kernel<D, kFp8>, a.grid, kFp8 ? kFpThreads : kBfThreads, Layout<D, kFp8>::kSmem, s, mk,
+                          mv, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_chunk(const AttendArgs& a, cudaStream_t s) {
+  CUtensorMap mk, mv;
+  const int box = a.p.page_tokens < kTile ? a.p.page_tokens : kTile;
+  if (!pages_map(&mk, a.p, a.p.k, box) || !pages_map(&mv, a.p, a.p.v, box)) return cudaErrorInvalidValue;
+  const bool fp8 = a.p.kv_dtype == FT_KV_FP8E4M3;
+  if (a.p.head_dim == 128) return fp8 ? launch<128, true>(a, mk, mv, s) : launch<128, false>(a, mk, mv, s);
+  return fp8 ? launch<64, true>(a, mk, mv, s) : launch<64, false>(a, mk, mv, s);
+}
+
+}  // namespace kv
+}  // namespace ft

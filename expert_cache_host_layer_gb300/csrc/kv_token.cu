@@ -2,14 +2,10 @@
 // the batch has at most 16 rows (new tokens x query heads of the group), as in
 // decoding.  The work is reading K and V once: memory-bound.
 //
-// Formula, with x_j = scale log2(e) q.k_j and, for the quantised cache, v_j =
-// 2^(e_j) c_j (codes c):
+//   out = sum_j w_j v_j / sum_j w_j,   w_j = 2^(x_j - m),  x_j = scale log2(e) q.k_j,  m = max_j x_j
 //
-//   out = sum_j w_j c_j / sum_j w_j 2^(-e_j),   w_j = 2^(x_j + e_j - m),  m = max_j (x_j + e_j)
-//
-// so the value scales cost one addition per score instead of a multiplication
-// per code, and w <= 1 whatever the scales are (bf16: e = 0).  The key scale
-// multiplies the score.
+// Quantised cache: the key's scale multiplies the score and the value's scale
+// the probability (a power of two: nothing is rounded for it).
 //
 // Split: the batch's tiles of 128 tokens, laid end to end over (sequence, key
 // head, tile), are cut into equal contiguous ranges, one per CTA and one CTA
@@ -25,7 +21,9 @@
 // head).  mma.sync is enough here: a row block of 16 is an eighth of a
 // tcgen05 tile, and the path is bound by HBM, not by the tensor pipe.
 //
-// Quantised cache: codes are expanded to fp16 in registers (exact).  The
+// Quantised cache: codes are expanded in registers (exact), keys to fp16, the
+// cheaper conversion, values to bf16, whose range P needs: a probability keeps
+// its 8 bits however small it is.  The
 // contraction order over head_dim is free as long as Q uses the same, and so
 // are the order of tokens (P's columns and V's rows) and of output columns;
 // they are chosen so that each lane reads 16 consecutive bytes of a row,
@@ -77,8 +75,9 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// scores: fp16 for the quantised cache
 template <bool kFp8>
-__device__ __forceinline__ void mma16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_score(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   if (kFp8) mma_f16(c, a, b0, b1);
   else mma_bf16(c, a, b0, b1);
 }
@@ -102,6 +101,11 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t pair) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(pair & 0xffffu), __NV_E4M3);
   return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_bf162(uint32_t pair) {
+  const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(pair & 0xffffu), __NV_E4M3)));
+  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&b);
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, bool half) {
   if (half) {
@@ -193,8 +197,8 @@ struct Warp {
       for (int ks = 0; ks < kKs; ++ks) {
         uint32_t b[4];
         ldsm4(b, kb + (ks >> 2) * (kGroup * 128) + t * 128 + (((2 * (ks & 3) + ch) ^ (t & 7)) << 4));
-        mma16<kFp8>(s[0], qf[ks], b[0], b[1]);
-        mma16<kFp8>(s[1], qf[ks], b[2], b[3]);
+        mma_score<kFp8>(s[0], qf[ks], b[0], b[1]);
+        mma_score<kFp8>(s[1], qf[ks], b[2], b[3]);
       }
     } else {
 #pragma unroll
@@ -209,30 +213,28 @@ struct Warp {
                        : "r"(kb + t * D + (phys << 4)));
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            mma16<kFp8>(s[nb], qf[hf * 4 + i], e4m3x2_to_half2(w[i]), e4m3x2_to_half2(w[i] >> 16));
+            mma_score<kFp8>(s[nb], qf[hf * 4 + i], e4m3x2_to_half2(w[i]), e4m3x2_to_half2(w[i] >> 16));
         }
       }
     }
     // scores to log2 domain, scales and masks
-    float inv[4];  // 2^(-e) of this lane's four tokens (their sum's share)
+    float vs[4];  // value scales of this lane's four tokens
     float top[2] = {m[0], m[1]};
 #pragma unroll
     for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = nb * 8 + tok<D, kFp8>(2 * c + i), u = 2 * nb + i;
-        float kf = 1.0f, ve = 0.0f;
-        inv[u] = 1.0f;
+        float kf = 1.0f;
+        vs[u] = 1.0f;
         if (kFp8) {
-          const uint32_t ek = ksc[t], ev = vsc[t];
-          kf = scale_of(ek);
-          ve = ev == kNanScale ? __uint_as_float(0x7fc00000u) : (float)((int)ev - 127);
-          inv[u] = ev == kNanScale ? __uint_as_float(0x7fc00000u) : __uint_as_float((254u - ev) << 23);
+          kf = scale_of(ksc[t]);
+          vs[u] = scale_of(vsc[t]);
         }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           float x = s[nb][2 * hf + i] * sc[hf];
-          if (kFp8) x = x * kf + ve;
+          if (kFp8) x *= kf;
           if (!full && (j0 + t < lo[hf] || j0 + t >= hi[hf])) x = -INFINITY;
           s[nb][2 * hf + i] = x;
           top[hf] = fmaxf(top[hf], x);
@@ -267,11 +269,10 @@ struct Warp {
         for (int i = 0; i < 2; ++i) {
           const float x = s[nb][2 * hf + i];
           w[i] = exp2_approx(x - base);
-          // an unseen token's scale byte may be anything
-          if (kFp8) l[hf] += x == -INFINITY ? 0.0f : w[i] * inv[2 * nb + i];
-          else l[hf] += w[i];
+          l[hf] += w[i];
+          if (kFp8) w[i] = x == -INFINITY ? 0.0f : w[i] * vs[2 * nb + i];  // an unseen token's scale may be NaN
         }
-        pf[2 * nb + hf] = pack2(w[0], w[1], kFp8);
+        pf[2 * nb + hf] = pack2(w[0], w[1], false);
       }
     }
     // Tokens that no row sees hold anything (a page's unused end): their V is
@@ -324,15 +325,15 @@ struct Warp {
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb) {
         const uint32_t p = __byte_perm(w[nb][0], w[nb][1], 0x5140), q = __byte_perm(w[nb][0], w[nb][1], 0x7362);
-        b[0][nb] = e4m3x2_to_half2(p);
-        b[1][nb] = e4m3x2_to_half2(p >> 16);
-        b[2][nb] = e4m3x2_to_half2(q);
-        b[3][nb] = e4m3x2_to_half2(q >> 16);
+        b[0][nb] = e4m3x2_to_bf162(p);
+        b[1][nb] = e4m3x2_to_bf162(p >> 16);
+        b[2][nb] = e4m3x2_to_bf162(q);
+        b[3][nb] = e4m3x2_to_bf162(q >> 16);
       }
     }
   }
   __device__ __forceinline__ static bool not_finite(uint32_t b) {  // either 16-bit half an infinity or a NaN
-    const uint32_t e = kFp8 ? 0x7c00u : 0x7f80u;
+    const uint32_t e = 0x7f80u;
     return (b & e) == e || ((b >> 16) & e) == e;
   }
   __device__ __forceinline__ void accumulate(uint32_t vb, const uint32_t* pf, const uint32_t* keep, bool full,
@@ -353,7 +354,7 @@ struct Warp {
       }
       if (!split || !__any_sync(0xffffffffu, bad)) {
 #pragma unroll
-        for (int i = 0; i < kB; ++i) mma16<kFp8>(o[jb + i], pf, b[i][0], b[i][1]);
+        for (int i = 0; i < kB; ++i) mma_bf16(o[jb + i], pf, b[i][0], b[i][1]);
       } else {
         const int g = lane >> 2, c = lane & 3;
         for (int src = 0; src < 32; src += 4)  // the rows' distinct visible spans, row by row
@@ -364,7 +365,7 @@ struct Warp {
 #pragma unroll
             for (int i = 0; i < kB; ++i) {
               float t[4] = {};
-              mma16<kFp8>(t, pf, b[i][0] & k0, b[i][1] & k1);
+              mma_bf16(t, pf, b[i][0] & k0, b[i][1] & k1);
               if (g == src >> 2) {
                 o[jb + i][2 * hf] += t[2 * hf];
                 o[jb + i][2 * hf + 1] += t[2 * hf + 1];
