@@ -20,7 +20,7 @@ namespace {
 constexpr int kJoinThreads = 256;
 
 template <int D, int R>
-__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ AttendArgs a, int rows) {
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ AttendArgs a, bool chunk) {
   constexpr int N = D / 32;
   __shared__ float s_o[R == 1 ? 8 : 1][D];
   __shared__ float s_l[8];
@@ -29,8 +29,11 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
   if (u.x < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Seq q = load_seq(a.p, a.b, u.x, a.status);
-  const int r = blockIdx.y * R + (R == 1 ? 0 : warp), row = u.z * rows + r;
-  if (row >= q.m * a.G) return;  // R = 1: all of the block; R = 8: whole warps
+  const int rows = chunk ? kChunkRows : kTokenRows;
+  const int r = blockIdx.y * R + (R == 1 ? 0 : warp);
+  const int rr = chunk ? r % kSubRows : r, g = rr % a.G, ti = rr / a.G;
+  const int i_new = chunk ? (u.z * 2 + r / kSubRows) * a.tps + ti : ti;  // the row's new token
+  if (i_new >= q.m || (chunk && ti >= a.tps)) return;  // R = 1: all of the block; R = 8: whole warps
   const int c0 = blockIdx.x, parts = u.w - c0 + 1;
   // part i: CTA c0's last slot, then the first slot of each CTA after it
   auto slot = [&](int i) { return (long long)(2 * (c0 + i) + (i == 0)) * rows + r; };
@@ -70,11 +73,11 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
     }
   }
   const float inv = inverse(l);
-  __nv_bfloat16* out = a.out + out_at(a, q, u.y, row) + lane * N;
+  __nv_bfloat16* out = a.out + out_at(a, q, u.y, i_new, g) + lane * N;
 #pragma unroll
   for (int i = 0; i < N; i += 2)
     *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
-  if (lane == 0) write_lse(a, q, u.y, row, m, l);
+  if (lane == 0) write_lse(a, q, u.y, i_new, g, m, l);
 }
 
 int sm_count() {
@@ -88,21 +91,40 @@ int sm_count() {
 
 }  // namespace
 
-cudaError_t launch_combine(const AttendArgs& a, int rows, int used, cudaStream_t s) {
+cudaError_t launch_combine(const AttendArgs& a, bool chunk, int used, cudaStream_t s) {
   const bool one = used <= 64;  // rows enough for a block each without many idle blocks
   const dim3 grid(a.grid, one ? used : (used + 7) / 8);
   if (a.p.head_dim == 128)
-    return one ? launch_dependent(combine_kernel<128, 1>, grid, kJoinThreads, 0, s, a, rows)
-               : launch_dependent(combine_kernel<128, 8>, grid, kJoinThreads, 0, s, a, rows);
-  return one ? launch_dependent(combine_kernel<64, 1>, grid, kJoinThreads, 0, s, a, rows)
-             : launch_dependent(combine_kernel<64, 8>, grid, kJoinThreads, 0, s, a, rows);
+    return one ? launch_dependent(combine_kernel<128, 1>, grid, kJoinThreads, 0, s, a, chunk)
+               : launch_dependent(combine_kernel<128, 8>, grid, kJoinThreads, 0, s, a, chunk);
+  return one ? launch_dependent(combine_kernel<64, 1>, grid, kJoinThreads, 0, s, a, chunk)
+             : launch_dependent(combine_kernel<64, 8>, grid, kJoinThreads, 0, s, a, chunk);
+}
+
+namespace {
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder() {
+  static const Encode enc = reinterpret_cast<Encode>(driver_fn("cuTensorMapEncodeTiled"));
+  return enc;
+}
+}  // namespace
+
+bool queries_map(CUtensorMap* m, const AttendArgs& a, int tokens) {
+  const Encode enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.p.head_dim, (cuuint64_t)a.Hq, (cuuint64_t)a.b.num_tokens};
+  const cuuint64_t pitch[2] = {(cuuint64_t)a.qhs * 2, (cuuint64_t)a.qts * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)tokens};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(a.q), dims, pitch, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool pages_map(CUtensorMap* m, const ft_kv_pages& p, const void* base, int box_rows) {
-  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static const Encode enc = reinterpret_cast<Encode>(driver_fn("cuTensorMapEncodeTiled"));
+  const Encode enc = encoder();
   if (!enc) return false;
   const bool fp8 = p.kv_dtype == FT_KV_FP8E4M3;
   const cuuint64_t dims[2] = {(cuuint64_t)p.head_dim, (cuuint64_t)(p.num_pages * p.num_kv_heads * p.page_tokens)};
@@ -178,6 +200,10 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   const int G = num_q_heads / pages->num_kv_heads;
   const long long rows = (long long)batch->max_q_len * G;  // of a (sequence, key head), at most
   if (rows > 0x7fffffffLL / 2) return set_error(FT_ERR_UNSUPPORTED, "max_q_len * (num_q_heads / num_kv_heads) is too large");
+  if (G > kSubRows)
+    return set_error(FT_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads = %d is above %d", G, kSubRows);
+  if (q_token_stride <= 0 || q_head_stride <= 0)
+    return set_error(FT_ERR_INVALID_ARG, "q's strides must be positive");
   const int block = block_rows(*batch, G), grid = sm_count();
   const Workspace ws = layout(*pages, grid, block);
   if (workspace_bytes < ws.bytes)
@@ -188,7 +214,7 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   a.q = static_cast<const __nv_bfloat16*>(q); a.out = static_cast<__nv_bfloat16*>(out); a.lse = lse;
   a.qts = q_token_stride; a.qhs = q_head_stride; a.ots = out_token_stride; a.ohs = out_head_stride;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.Hq = num_q_heads; a.G = G; a.causal = causal != 0; a.window = window; a.grid = grid;
+  a.Hq = num_q_heads; a.G = G; a.tps = kSubRows / G; a.causal = causal != 0; a.window = window; a.grid = grid;
   if ((st = status_word(&a.status)) != FT_OK) return st;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.desc = reinterpret_cast<int4*>(w);
@@ -197,7 +223,9 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = block == kTokenRows ? launch_attend_token(a, s) : launch_attend_chunk(a, s);
   if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
-  if ((e = launch_combine(a, block, (int)std::min<long long>(rows, block), s)) != cudaSuccess)
+  // (a chunk block's rows are used without a gap only while its first sub-tile holds them all)
+  const int used = block == kTokenRows || batch->max_q_len <= a.tps ? (int)rows : kChunkRows;
+  if ((e = launch_combine(a, block == kChunkRows, used, s)) != cudaSuccess)
     return set_error(FT_ERR_CUDA, "attend join launch: %s", cudaGetErrorString(e));
   return FT_OK;
 }

@@ -15,7 +15,8 @@ namespace kv {
 
 constexpr int kTokenRows = 16;    // most rows of a (sequence, key head) in token_kernel
 constexpr int kTokenTile = 128;   // tokens per tile of its ring
-constexpr int kChunkRows = 256;   // rows of a block in chunk_kernel
+constexpr int kChunkRows = 256;   // rows of a block in chunk_kernel: two sub-tiles of 128
+constexpr int kSubRows = 128;
 
 struct AttendArgs {
   ft_kv_pages p;
@@ -26,6 +27,7 @@ struct AttendArgs {
   int64_t qts, qhs, ots, ohs;
   float scale_log2;       // scale * log2(e)
   int Hq, G, causal, window;
+  int tps;                // chunk_kernel: new tokens of a sub-tile of 128 rows, 128 / G
   int grid;               // CTAs of the main kernel
   int32_t* status;
   // workspace
@@ -197,14 +199,13 @@ struct TokenWalk {
 
 // ---------------------------------------------------------------- results
 
-// Row r (new token r / G, query head r % G of the group) of a (sequence, head).
-__device__ __forceinline__ long long out_at(const AttendArgs& a, const Seq& q, int h, int r) {
-  return (long long)(q.q0 + r / a.G) * a.ots + (long long)(h * a.G + r % a.G) * a.ohs;
+// Query head g of the group of key head h, new token i of the sequence.
+__device__ __forceinline__ long long out_at(const AttendArgs& a, const Seq& q, int h, int i, int g) {
+  return (long long)(q.q0 + i) * a.ots + (long long)(h * a.G + g) * a.ohs;
 }
-__device__ __forceinline__ void write_lse(const AttendArgs& a, const Seq& q, int h, int r, float m, float l) {
+__device__ __forceinline__ void write_lse(const AttendArgs& a, const Seq& q, int h, int i, int g, float m, float l) {
   if (a.lse)
-    a.lse[(long long)(q.q0 + r / a.G) * a.Hq + h * a.G + r % a.G] =
-        l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    a.lse[(long long)(q.q0 + i) * a.Hq + h * a.G + g] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 // 1 / l; 0 for a row without weight (it sees nothing, or only scores of -inf).
 __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
@@ -213,11 +214,14 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.
 
 cudaError_t launch_attend_token(const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_attend_chunk(const AttendArgs& a, cudaStream_t s);
-// Joins the partial sums of the (sequence, head, block of `rows` rows)s that a
-// cut divided; `used`: rows of a block that any sequence has.
-cudaError_t launch_combine(const AttendArgs& a, int rows, int used, cudaStream_t s);
+// Joins the partial sums of the (sequence, head, row block)s that a cut
+// divided; `chunk`: chunk_kernel's blocks (else token_kernel's), `used`: rows
+// of a block that any sequence has.
+cudaError_t launch_combine(const AttendArgs& a, bool chunk, int used, cudaStream_t s);
 // Pages of k or v as rows of head_dim, boxes of box_rows rows x 128 bytes (or the whole row, if shorter), swizzled.
 bool pages_map(CUtensorMap* m, const ft_kv_pages& p, const void* base, int box_rows);
+// q as [token][head][64 of head_dim], boxes of `tokens` x G heads x 128 bytes, swizzled.
+bool queries_map(CUtensorMap* m, const AttendArgs& a, int tokens);
 
 // Raise a kernel's limit of dynamic shared memory, once per device
 // (kId: a number of its own for each kernel of one type.)

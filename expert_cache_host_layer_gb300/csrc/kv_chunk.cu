@@ -7,21 +7,26 @@
 // the key's scale multiplies S, the value's scale P (after its share of the
 // sum), and the codes are multiplied, as in kv_token.cu.
 //
-// Item: a tile of 128 tokens for a block of 256 rows (new token x query head
-// of the group, so that a group's heads share the loaded K and V) of one
-// (sequence, key head).  The batch's items, laid end to end, are cut into
-// equal ranges, one per CTA; a row block that a cut divides leaves partial
-// sums that combine_kernel joins.  Rows of one block are two sub-tiles of 128,
-// each with its own score tile, output accumulator and softmax warpgroup:
+// Item: a tile of 128 tokens for a row block of one (sequence, key head).  A
+// row block is two sub-tiles of up to 128 rows, each the query heads of the
+// group of 128 / G consecutive new tokens: the heads share the loaded K and V,
+// and so do the sub-tiles.  The batch's items, laid end to end, are cut into
+// equal ranges, one per CTA; a row block that a cut divides leaves partial sums
+// that combine_kernel joins.  Each sub-tile has its own score tile, output
+// accumulator and softmax warpgroup:
 //
-//   warps 0-3, 4-7   softmax of sub-tile 0, 1: load Q into shared memory, and
-//                    per tile read S from TMEM (a thread per row), mask,
-//                    exponentiate, write P (16 bits) over S in TMEM; at the end
-//                    scale O and store it
+//   warps 0-3, 4-7   softmax of sub-tile 0, 1: per tile read S from TMEM (a
+//                    thread per row), mask, exponentiate, write P (bf16) over
+//                    S in TMEM; at the end scale O and store it, transposed
+//                    through shared memory so that a store fills its lines
 //   warp 8           producer: K and V tiles into a ring, one TMA box per page
 //                    (or half page row), 128-byte swizzled
 //   warp 9           tcgen05.mma: S_w = Q_w K^T (M 128, N 128), O_w += P_w V
 //                    with P read from TMEM and V as it lies (token-major)
+//   warps 10, 11     bf16: Q of both sub-tiles by TMA as soon as the block
+//                    before has its last score tile; V's tiles at the edge of
+//                    what the rows see (see mend).  Quantised cache: each loads
+//                    its sub-tile's Q and turns it into fp16
 //   warps 12-15      quantised cache: expand the codes of a raw ring into tiles
 //                    of the layout that the MMA reads (exact; K in fp16, V in
 //                    bf16, whose range P needs)
@@ -39,7 +44,7 @@ namespace ft {
 namespace kv {
 namespace {
 
-constexpr int kSub = 128;
+constexpr int kSub = kSubRows;
 constexpr int kTile = 128;                    // tokens per tile
 constexpr int kTmemCols = 512;                // S0 | S1 | O0 | O1, 128 columns each
 constexpr float kGrow = 8.0f;                 // log2 of the growth that O's scale may lag behind
@@ -56,17 +61,19 @@ struct Layout {
   static constexpr int kQBytes = 2 * kSub * D * 2;
   static constexpr int kTileBytes = kTile * D * 2;                      // a K or V tile as the MMA reads it
   static constexpr int kRawBytes = kFp8 ? kTile * D : 0;
-  static constexpr int kStages = (kFp8 ? 3 : 5) * (128 / D);
-  static constexpr int kRaw = kFp8 ? 3 * (128 / D) : 0;
+  static constexpr int kStages = (kFp8 ? 3 : 4) * (128 / D);
+  static constexpr int kRaw = kFp8 ? 2 * (128 / D) : 0;
   static constexpr int kRingOff = kQBytes;
   static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
   static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;          // per warpgroup, twice: 128 x {k, v}
   static constexpr int kScaleBytes = kFp8 ? 2 * 2 * 2 * kTile * 4 : 0;
   static constexpr int kRowOff = kScaleOff + kScaleBytes;               // Q's row scales
   static constexpr int kRowBytes = kFp8 ? 2 * kSub * 4 : 0;
-  static constexpr int kBarOff = kRowOff + kRowBytes;
-  static constexpr int kBars = 2 * kStages + 2 * kRaw + 8 + 1;
-  static constexpr int kSmem = kBarOff + kBars * 8 + 64 + 1024;
+  static constexpr int kLine = kFp8 ? 64 : 128;                         // bytes of a row in a softmax warp's staging
+  static constexpr int kOutOff = kRowOff + kRowBytes;
+  static constexpr int kBarOff = kOutOff + 8 * 32 * kLine;
+  static constexpr int kBars = 2 * kStages + 2 * kRaw + 12 + 3;
+  static constexpr int kSmem = kBarOff + kBars * 8 + 64 + 4 * kStages + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kStages * kTileBytes >= (kMaxSeqs + 1) * 8 + 1024, "the prefix sums fit the ring before it fills");
 };
@@ -79,18 +86,31 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(dec::smem_addr(bar))
                : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
+// One thread of the warp, chosen so that the compiler knows the branch is uniform.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// Shared-memory matrix descriptors, 128-byte swizzle, rows of 128 bytes, 8-row
+// groups 1024 bytes apart: the low word holds the address (in 16 bytes) and the
+// leading offset, the high word is a constant.  K-major (Q, K): the leading
+// offset is not used.  N-major (V: a row is a token, 64 of head_dim wide): it
+// leads to the next 64 columns, the next half of the tile.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead = 16) { return (saddr >> 4) | (lead >> 4) << 16; }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t ad, uint32_t bd, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(ad), "r"(bd), "r"(idesc), "r"((uint32_t)acc), "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bd, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint32_t bd, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(at), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(at), "r"(bd), "r"(idesc), "r"((uint32_t)acc), "r"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -117,20 +137,19 @@ __device__ __forceinline__ void st32(uint32_t t, const uint32_t* r) {
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(t)
       : "memory");
 }
+__device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(dec::smem_addr(bar))
+      : "memory");
+}
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
           "r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(dec::smem_addr(bar))
       : "memory");
-}
-// Shared-memory matrix descriptor, 128-byte swizzle, rows of 128 bytes, 8-row
-// groups 1024 bytes apart.  K-major (Q, K): the leading offset is not used.
-// N-major (V: a row is a token, 64 of head_dim wide): the leading offset leads
-// to the next 64 columns, the next half of the tile.
-__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lead = 16) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // kind::f16, fp32 accumulator, both operands bf16 (or fp16), B N-major or not.
 __device__ constexpr uint32_t idesc(int N, bool bf16, bool b_n_major) {
@@ -157,13 +176,12 @@ struct Block {
 };
 __device__ __forceinline__ Block block_of(const AttendArgs& a, const Seq& q, int rb) {
   Block b;
-  const int rows = q.m * a.G;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const int r0 = rb * kChunkRows + w * kSub, r1 = min(rows, r0 + kSub) - 1;
+    const int i0 = (rb * 2 + w) * a.tps, i1 = min(q.m, i0 + a.tps) - 1;
     b.s0[w] = b.s1[w] = 0;
-    if (r0 > r1) continue;
-    const Span f = visible(a, q, r0 / a.G), l = visible(a, q, r1 / a.G);
+    if (i0 > i1) continue;
+    const Span f = visible(a, q, i0), l = visible(a, q, i1);
     if (l.hi > f.lo) {
       b.s0[w] = f.lo / kTile;
       b.s1[w] = (l.hi + kTile - 1) / kTile;
@@ -179,9 +197,7 @@ __device__ __forceinline__ Block block_of(const AttendArgs& a, const Seq& q, int
   b.t1 = max(b.t0 + 1, (b.hi + kTile - 1) / kTile);
   return b;
 }
-__device__ __forceinline__ int blocks_of(const AttendArgs& a, const Seq& q) {
-  return (int)(((long long)q.m * a.G + kChunkRows - 1) / kChunkRows);
-}
+__device__ __forceinline__ int blocks_of(const AttendArgs& a, const Seq& q) { return (q.m + 2 * a.tps - 1) / (2 * a.tps); }
 __device__ __forceinline__ int tiles_of(const AttendArgs& a, const Seq& q, int rb) {
   const Block b = block_of(a, q, rb);
   return b.t1 - b.t0;
@@ -204,6 +220,23 @@ struct ChunkWalk {
   Block b;
   int t0, t1;  // tiles of the block that are this CTA's
   bool begins, ends, started;
+  // V's tile t as the rows see it: tokens [r0, r1) of the tile are seen by some
+  // row, [p0, p1) and [p2, p3) of them not by all
+  struct Edge {
+    int r0, r1, p0, p1, p2, p3;
+    __device__ __forceinline__ bool any() const { return (r0 & 15) || (r1 & 15) || p0 < p1 || p2 < p3; }
+  };
+  __device__ __forceinline__ Edge edge(int t) const {
+    Edge e;
+    const int j0 = t * kTile;
+    e.r0 = min(kTile, max(0, b.lo - j0));
+    e.r1 = max(e.r0, min(kTile, b.hi - j0));
+    e.p0 = e.r0;
+    e.p1 = min(e.r1, b.all_lo - j0);
+    e.p2 = max(e.r0, b.all_hi - j0);
+    e.p3 = e.r1;
+    return e;
+  }
   __device__ __forceinline__ ChunkWalk(const Range& r)
       : w(r.w0), end(r.w1), base(r.base), total(r.total), at(r.base), n(r.n), s(r.s), h(0), rb(0), nb(0),
         started(false) {}
@@ -273,9 +306,10 @@ struct ChunkWalk {
 
 struct Shared {
   uint8_t* base;
-  uint64_t *full, *empty, *rfull, *rempty, *qfull, *sfull, *pfull, *ofull, *drain;
+  uint64_t *full, *empty, *rfull, *rempty, *qfull, *qempty, *sfull, *pfull, *ofull, *landed, *drain, *mended, *asked;
   uint32_t* tmem;
   volatile int* abort_flag;
+  volatile int* took;    // [stages] V's tile had values that are not finite where not every row sees them
   volatile int* poison;  // [2][2] first and last tile with values that a sub-tile adds at its block's end
 };
 
@@ -290,13 +324,18 @@ __device__ __forceinline__ Shared carve(uint8_t* raw) {
   s.rfull = b + 2 * L::kStages;
   s.rempty = s.rfull + L::kRaw;
   s.qfull = s.rempty + L::kRaw;
-  s.sfull = s.qfull + 2;
-  s.pfull = s.qfull + 4;
-  s.ofull = s.qfull + 6;
-  s.drain = s.qfull + 8;
-  s.tmem = reinterpret_cast<uint32_t*>(s.drain + 1);
+  s.qempty = s.qfull + 2;
+  s.sfull = s.qfull + 4;
+  s.pfull = s.qfull + 6;
+  s.ofull = s.qfull + 8;
+  s.landed = s.qfull + 10;
+  s.drain = s.qfull + 12;
+  s.mended = s.drain + 1;
+  s.asked = s.drain + 2;
+  s.tmem = reinterpret_cast<uint32_t*>(s.drain + 3);
   s.abort_flag = reinterpret_cast<volatile int*>(s.tmem + 1);
   s.poison = reinterpret_cast<volatile int*>(s.tmem + 4);
+  s.took = s.poison + 4;
   return s;
 }
 
@@ -348,7 +387,7 @@ __device__ void produce(const AttendArgs& a, const Range& rg, const Shared& s, c
   for (int j = max(0, it - kSlots); j < it; ++j) dec::mbar_wait(&full[j % kSlots], (j / kSlots) & 1, a.status);
 }
 
-// ---------------------------------------------------------------- MMA
+// ---------------------------------------------------------------- V at the edge
 
 // V rows (tokens) [r0, r1) of a tile to zero; whole warp.
 template <int D>
@@ -362,24 +401,67 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int r1, int lan
 // Values of V rows [r0, r1) that are not finite, set to zero; whether there were any.
 template <int D>
 __device__ __forceinline__ bool take_not_finite(uint8_t* tile, int r0, int r1, int lane) {
-  constexpr int kPer = D / 8;
+  constexpr int kPer = D / 8, kBatch = 8;
   bool any = false;
-  for (int i = r0 * kPer + lane; i < r1 * kPer; i += 32) {
-    const int r = i / kPer, ch = i % kPer;
-    uint4* at = reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) << 4));
-    uint4 v = *at;
-    uint32_t* x = reinterpret_cast<uint32_t*>(&v);
-    bool bad = false;
+  for (int i0 = r0 * kPer + lane; i0 < r1 * kPer; i0 += 32 * kBatch) {
+    uint4 v[kBatch];
+    auto at = [&](int k) {
+      const int i = i0 + 32 * k, r = i / kPer, ch = i % kPer;
+      return reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) << 4));
+    };
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if ((x[k] & 0x7f80u) == 0x7f80u) { x[k] &= 0xffff0000u; bad = true; }
-      if ((x[k] & 0x7f800000u) == 0x7f800000u) { x[k] &= 0x0000ffffu; bad = true; }
+    for (int k = 0; k < kBatch; ++k) v[k] = i0 + 32 * k < r1 * kPer ? *at(k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      uint32_t y[4];
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool lo = (x[j] & 0x7f80u) == 0x7f80u, hi = (x[j] & 0x7f800000u) == 0x7f800000u;
+        y[j] = x[j] & (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+        bad |= lo | hi;
+      }
+      if (bad) *at(k) = make_uint4(y[0], y[1], y[2], y[3]);
+      any |= bad;
     }
-    if (bad) *at = v;
-    any |= bad;
   }
   return __any_sync(0xffffffffu, any);
 }
+
+// One warp, while the tile's softmax runs.  Tokens of a bf16 tile that no row sees hold
+// anything (a page's unused end, an evicted page): those within the MMA's
+// 16-token steps are set to zero.  Of tokens that some rows see and others do
+// not, values that are not finite are set to zero too, lest 0 * V reach the
+// others; the rows that see them add them at the block's end.
+template <int D>
+__device__ void mend(const AttendArgs& a, const Range& rg, const Shared& s, int lane) {
+  using L = Layout<D, false>;
+  int it = 1;  // V of the walk's first tile
+  uint32_t n = 0;
+  ChunkWalk w(rg);
+  while (w.next(a, lane))
+    for (int t = w.t0; t < w.t1; ++t, it += 2) {
+      const ChunkWalk::Edge e = w.edge(t);
+      if (!e.any()) continue;
+      // asked by the MMA warp, which has not used this V yet: the ring cannot be a turn ahead or behind
+      if (!wait_or_abort(s.asked, n++ & 1, a.status, s.abort_flag)) return;
+      const int st = it % L::kStages;
+      if (!wait_or_abort(&s.full[st], (it / L::kStages) & 1, a.status, s.abort_flag)) return;
+      uint8_t* V = s.base + L::kRingOff + st * L::kTileBytes;
+      zero_rows<D>(V, e.r0 & ~15, e.r0, lane);
+      zero_rows<D>(V, e.r1, (e.r1 + 15) & ~15, lane);
+      bool took = false;
+      if (e.p0 < e.p1) took |= take_not_finite<D>(V, e.p0, e.p1, lane);
+      if (e.p2 < e.p3) took |= take_not_finite<D>(V, e.p2, e.p3, lane);
+      s.took[st] = took;
+      fence_async();
+      __syncwarp();
+      if (lane == 0) dec::mbar_arrive(s.mended);
+    }
+}
+
+// ---------------------------------------------------------------- MMA
 
 template <int D, bool kFp8>
 __device__ void multiply(const AttendArgs& a, const Range& rg, const Shared& s, uint32_t tmem, int lane) {
@@ -387,7 +469,7 @@ __device__ void multiply(const AttendArgs& a, const Range& rg, const Shared& s, 
   const uint32_t ring = dec::smem_addr(s.base + L::kRingOff), qa = dec::smem_addr(s.base);
   constexpr uint32_t id_s = idesc(kTile, !kFp8, false), id_o = idesc(D, true, true);
   int it = 0;
-  uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+  uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, mended = 0;
   bool go = true;
   ChunkWalk w(rg);
   while (go && w.next(a, lane)) {
@@ -395,78 +477,76 @@ __device__ void multiply(const AttendArgs& a, const Range& rg, const Shared& s, 
     bool live[2] = {false, false};  // O_w has been written in this part
     for (int t = w.t0; t <= w.t1 && go; ++t) {
       const int ki = it, vi = it - 1;  // ring positions of K(t) and V(t - 1)
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        if (t > w.t0) {  // O_sub += P_sub(t - 1) V(t - 1)
-          if (sub == 0) {
-            uint8_t* V = s.base + L::kRingOff + (vi % L::kStages) * L::kTileBytes;
-            if (!(go = wait_or_abort(&s.full[vi % L::kStages], (vi / L::kStages) & 1, a.status, s.abort_flag))) break;
-            if (!kFp8) {
-              const int j0 = (t - 1) * kTile, r0 = max(0, w.b.lo - j0), r1 = min(kTile, max(0, w.b.hi - j0));
-              const bool edge = r0 > 0 || r1 < kTile;
-              if (edge) {  // tokens that no row sees may hold anything
-                zero_rows<D>(V, 0, min(r0, kTile), lane);
-                zero_rows<D>(V, r1, kTile, lane);
-              }
-              // tokens that some rows see and others do not: 0 * V must not reach the others
-              bool took = false;
-              if (w.b.all_hi < j0 + r1) took |= take_not_finite<D>(V, max(r0, w.b.all_hi - j0), r1, lane);
-              if (w.b.all_lo > j0 + r0) took |= take_not_finite<D>(V, r0, min(r1, w.b.all_lo - j0), lane);
-              if (took) {
-                bad0 = min(bad0, t - 1);
-                bad1 = t - 1;
-              }
-              if (edge || took) {
-                fence_async();
-                __syncwarp();
-              }
-            }
-          }
-          if (w.active(sub, t - 1)) {
-            if (!(go = wait_or_abort(&s.pfull[sub], np[sub] & 1, a.status, s.abort_flag))) break;
-            ++np[sub];
-            fence_after();
-            if (lane == 0) {
-              const uint32_t V = ring + (vi % L::kStages) * L::kTileBytes;
-#pragma unroll
-              for (int k = 0; k < kTile / 16; ++k)
-                mma_ts(tmem + 256 + sub * 128, tmem + sub * 128 + k * 8, desc(V + k * 2048, kTile * 128), id_o,
-                       live[sub] || k);
-            }
-            live[sub] = true;
+      const int ks = ki % L::kStages, vs = t > w.t0 ? vi % L::kStages : 0;
+      const uint32_t kd = desc_lo(ring + ks * L::kTileBytes), vd = desc_lo(ring + vs * L::kTileBytes, kTile * 128);
+      int k0 = 0, k1 = kTile / 16;  // 16-token steps of V(t - 1) with tokens that some row sees
+      if (t > w.t0) {
+        if (!(go = wait_or_abort(&s.full[vs], (vi / L::kStages) & 1, a.status, s.abort_flag))) break;
+        const ChunkWalk::Edge e = w.edge(t - 1);
+        k0 = e.r0 >> 4;
+        k1 = (e.r1 + 15) >> 4;
+        if (!kFp8 && e.any()) {
+          if (!(go = wait_or_abort(s.mended, mended & 1, a.status, s.abort_flag))) break;
+          ++mended;
+          if (s.took[vs]) {
+            bad0 = min(bad0, t - 1);
+            bad1 = t - 1;
           }
         }
+      }
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const uint32_t S = tmem + sub * 128, O = tmem + 256 + sub * 128;
+        if (t > w.t0 && w.active(sub, t - 1)) {  // O_sub += P_sub(t - 1) V(t - 1)
+          if (!(go = wait_or_abort(&s.pfull[sub], np[sub] & 1, a.status, s.abort_flag))) break;
+          ++np[sub];
+          fence_after();
+          if (elect()) {
+            if (k0 == 0 && k1 == kTile / 16) {
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k) mma_ts(O, S + k * 8, vd + k * 128, id_o, k != 0 || live[sub]);
+            } else {
+              for (int k = k0; k < k1; ++k) mma_ts(O, S + k * 8, vd + k * 128, id_o, k != k0 || live[sub]);
+            }
+          }
+          __syncwarp();
+          live[sub] = true;
+        }
         if (t < w.t1) {  // S_sub = Q_sub K(t)^T
-          if (sub == 0 &&
-              !(go = wait_or_abort(&s.full[ki % L::kStages], (ki / L::kStages) & 1, a.status, s.abort_flag)))
-            break;
+          if (sub == 0) {
+            if (!kFp8 && w.edge(t).any() && lane == 0) dec::mbar_arrive(s.asked);
+            if (!(go = wait_or_abort(&s.full[ks], (ki / L::kStages) & 1, a.status, s.abort_flag))) break;
+          }
           if (w.active(sub, t)) {
             if (t == max(w.t0, w.b.s0[sub])) {
               if (!(go = wait_or_abort(&s.qfull[sub], nq[sub] & 1, a.status, s.abort_flag))) break;
               ++nq[sub];
             }
             fence_after();
-            if (lane == 0) {
-              const uint32_t K = ring + (ki % L::kStages) * L::kTileBytes, Q = qa + sub * kSub * D * 2;
+            const uint32_t qd = desc_lo(qa + sub * kSub * D * 2);
+            if (elect()) {
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
-                mma_ss(tmem + sub * 128, desc(Q + (k >> 2) * (kSub * 128) + (k & 3) * 32),
-                       desc(K + (k >> 2) * (kTile * 128) + (k & 3) * 32), id_s, k != 0);
+                mma_ss(S, qd + (k >> 2) * (kSub * 8) + (k & 3) * 2, kd + (k >> 2) * (kTile * 8) + (k & 3) * 2, id_s,
+                       k != 0);
               commit(&s.sfull[sub]);
+              if (t + 1 == min(w.t1, w.b.s1[sub])) commit(&s.qempty[sub]);
             }
+            __syncwarp();
           }
         }
       }
       if (!go) break;
-      if (lane == 0) {
-        if (t > w.t0) commit(&s.empty[vi % L::kStages]);
-        if (t < w.t1) commit(&s.empty[ki % L::kStages]);
+      if (elect()) {
+        if (t > w.t0) commit(&s.empty[vs]);
+        if (t < w.t1) commit(&s.empty[ks]);
       }
+      __syncwarp();
       it += t < w.t1 ? 2 : 0;
     }
     if (!go) break;
     // K and V of the last tile have been passed: `it` is at the next block's first K
-    if (lane == 0) {
+    if (elect()) {
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub)
         if (live[sub]) {  // (its warpgroup has read the block before: it has written P since)
@@ -476,16 +556,128 @@ __device__ void multiply(const AttendArgs& a, const Range& rg, const Shared& s, 
           dec::mbar_arrive(&s.ofull[sub]);
         }
     }
+    __syncwarp();
   }
   // every MMA issued has completed before TMEM is freed
-  if (lane == 0) {
+  if (elect()) {
     commit(s.drain);
     dec::mbar_wait(s.drain, 0, a.status);
   }
   __syncwarp();
 }
 
+// ---------------------------------------------------------------- Q
+
+// Q of the sub-tiles [sub0, sub1) of every block, by TMA: a box of the group's
+// heads x 128 / G tokens is the K-major tile.  (Rows past the sequence's end
+// are the next one's, or zeros; rows past the box keep what they held.  Both
+// are never stored.)  Quantised cache: to fp16, each row scaled by a power of
+// two to [1, 2), in place; a thread takes a row.  A negative softmax scale goes
+// into Q's signs.
+template <int D, bool kFp8>
+__device__ void load_q(const AttendArgs& a, const Range& rg, const Shared& s, const CUtensorMap* map, int sub0, int sub1,
+                       int lane) {
+  using L = Layout<D, kFp8>;
+  const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+  uint32_t n[2] = {0, 0};
+  ChunkWalk w(rg);
+  while (w.next(a, lane))
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      if (sub < sub0 || sub >= sub1 || !w.any(sub)) continue;
+      if (!wait_or_abort(&s.qempty[sub], (n[sub] & 1) ^ 1, a.status, s.abort_flag)) return;
+      ++n[sub];
+      uint8_t* Q = s.base + sub * kSub * D * 2;
+      const bool rework = kFp8 || flip;  // then it arrives on `landed` first
+      uint64_t* bar = rework ? &s.landed[sub] : &s.qfull[sub];
+      if (lane == 0) {
+        dec::mbar_expect_tx(bar, a.tps * a.G * D * 2);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_box3(dec::smem_addr(Q + c * kSub * 128), map, c * 64, w.h * a.G, w.q.q0 + (w.rb * 2 + sub) * a.tps, bar);
+      }
+      if (!rework) continue;
+      if (!wait_or_abort(bar, (n[sub] & 1) ^ 1, a.status, s.abort_flag)) return;
+      for (int r = lane; r < a.tps * a.G; r += 32) {
+        auto chunk = [&](int ch) {
+          return reinterpret_cast<uint4*>(Q + (ch >> 3) * (kSub * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+        };
+        float down = 1.0f;
+        if (kFp8) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int ch = 0; ch < D / 8; ++ch) {
+            const uint4 v = *chunk(ch);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = max(top, max((u[j] << 16) & 0x7f800000u, u[j] & 0x7f800000u));
+          }
+          const int e = min(max((int)(top >> 23), 1), 253);  // infinities and NaN stay what they are
+          down = __uint_as_float((uint32_t)(254 - e) << 23);
+          reinterpret_cast<float*>(s.base + L::kRowOff)[sub * kSub + r] = __uint_as_float((uint32_t)e << 23);
+        }
+#pragma unroll 4
+        for (int ch = 0; ch < D / 8; ++ch) {
+          uint4 v = *chunk(ch);
+          v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+          if (kFp8) {
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = pack2(dec::bf16_lo(u[j]) * down, dec::bf16_hi(u[j]) * down, true);
+          }
+          *chunk(ch) = v;
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) dec::mbar_arrive(&s.qfull[sub]);
+    }
+}
+
 // ---------------------------------------------------------------- softmax
+
+// A warp's 32 rows of kChunks 16-byte chunks in shared memory, swizzled so that
+// neither a lane per row nor neighbouring lanes in a row collide.
+template <int kChunks>
+__device__ __forceinline__ uint4* stage_at(uint8_t* stage, int r, int c) {
+  const int x = kChunks == 8 ? r & 7 : (r >> 1) & 3;
+  return reinterpret_cast<uint4*>(stage + r * (kChunks * 16) + ((c ^ x) << 4));
+}
+template <int kChunks>
+__device__ __forceinline__ void stage_put(uint8_t* stage, int r, int c, uint4 v) {
+  *stage_at<kChunks>(stage, r, c) = v;
+}
+// Out to column `col` of the rows; at: element offset of this lane's row (-1: none).
+template <int kChunks>
+__device__ __forceinline__ void stage_out(uint8_t* stage, int lane, long long at, uint8_t* base, int esz, int col) {
+  __syncwarp();
+  constexpr int kRows = 32 / kChunks;
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += kRows) {
+    const int r = r0 + lane / kChunks, c = lane % kChunks;
+    const long long to = __shfl_sync(0xffffffffu, at, r);
+    if (to >= 0) *reinterpret_cast<uint4*>(base + (to + col) * esz + c * 16) = *stage_at<kChunks>(stage, r, c);
+  }
+  __syncwarp();
+}
+// Adds to a row's columns k .. k + 31 the values that are not finite of tokens
+// [from, to), those that every row sees left out: they went through the product.
+template <int D>
+__device__ __noinline__ void add_not_finite(const AttendArgs& a, int s, int h, int all_lo, int all_hi, int from, int to,
+                                            int k, float* o) {
+  for (int j = from; j < to; ++j) {
+    if (j >= all_lo && j < all_hi) continue;
+    const int page = max(0, load_page(a.p, a.b, s, j / a.p.page_tokens, a.status));
+    const __nv_bfloat16* at =
+        static_cast<const __nv_bfloat16*>(a.p.v) +
+        (((long long)page * a.p.num_kv_heads + h) * a.p.page_tokens + j % a.p.page_tokens) * D + k;
+    for (int i = 0; i < 32; ++i) {
+      const float x = __bfloat162float(at[i]);
+      if (!isfinite(x)) o[i] += x;
+    }
+  }
+}
 
 template <int D, bool kFp8>
 __device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, uint32_t tmem, int sub, int tid) {
@@ -493,9 +685,8 @@ __device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, ui
   const int lane = tid & 31, quarter = (tid >> 5) & 3;
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
   const uint32_t ts = tmem + lanes + sub * 128, to = tmem + lanes + 256 + sub * 128;
-  uint8_t* Q = s.base + sub * kSub * D * 2;
   float* scales = reinterpret_cast<float*>(s.base + L::kScaleOff) + sub * 2 * 2 * kTile;
-  float* row_scale = reinterpret_cast<float*>(s.base + L::kRowOff) + sub * kSub;
+  const float* row_scale = reinterpret_cast<const float*>(s.base + L::kRowOff) + sub * kSub;
   // the warpgroup's barrier, and whether any of its threads says so
   auto group_any = [&](bool x) {
     uint32_t r;
@@ -510,48 +701,21 @@ __device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, ui
   uint32_t ns = 0, no = 0;
   int turn = 0;
   int4 begun = make_int4(-1, 0, 0, 0);
-  const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // a negative scale goes into Q's signs
   const float c0 = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);  // never 0: 0 * -inf is not -inf
+  const int my_token = tid / a.G, my_head = tid % a.G;
+  uint8_t* stage = s.base + L::kOutOff + (sub * 4 + quarter) * 32 * L::kLine;
   ChunkWalk w(rg);
   bool ok = true;
   while (w.next(a, lane)) {
-    const int rows = w.q.m * a.G, r_base = w.rb * kChunkRows + sub * kSub;
-    const int r = r_base + tid;
-    const bool mine = r < rows;
+    const int i_new = (w.rb * 2 + sub) * a.tps + my_token;  // this row's new token
+    const bool mine = my_token < a.tps && i_new < w.q.m;
     const bool any = w.any(sub);
     float m = -INFINITY, l = 0.0f, c = c0;
-    if (any) {
-      // Q: the previous block's last score tile is done, so its Q is free
-      constexpr int kPer = D / 8;
-      for (int i = tid; i < kSub * kPer; i += 128) {
-        const int rr = i / kPer, ch = i % kPer, row = r_base + rr;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < rows)
-          v = __ldg(reinterpret_cast<const uint4*>(a.q + (long long)(w.q.q0 + row / a.G) * a.qts +
-                                                   (long long)(w.h * a.G + row % a.G) * a.qhs) +
-                    ch);
-        v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-        if (kFp8) {  // to fp16, the row scaled to [1, 2)
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-          uint32_t top = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top = max(top, max((u[k] << 16) & 0x7f800000u, u[k] & 0x7f800000u));
-#pragma unroll
-          for (int o = kPer / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int e = min(max((int)(top >> 23), 1), 253);
-          const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-          uint32_t* x = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = pack2(dec::bf16_lo(u[k]) * down, dec::bf16_hi(u[k]) * down, true);
-          if (ch == 0) row_scale[rr] = __uint_as_float((uint32_t)e << 23);
-        }
-        *reinterpret_cast<uint4*>(Q + (ch >> 3) * (kSub * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) dec::mbar_arrive(&s.qfull[sub]);
+    if (any && kFp8) {
+      ok = ok && wait_or_abort(&s.qfull[sub], no & 1, a.status, s.abort_flag);
+      if (ok) c = c0 * row_scale[tid];
     }
-    const Span v = visible(a, w.q, mine ? r / a.G : 0);
+    const Span v = visible(a, w.q, mine ? i_new : 0);
     const int lo = mine ? v.lo : 0, hi = mine ? v.hi : 0;
     bool first = true;
     for (int t = max(w.t0, w.b.s0[sub]); t < min(w.t1, w.b.s1[sub]); ++t) {
@@ -572,7 +736,6 @@ __device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, ui
         // two buffers: everyone has left the tile before the last
         nan_scale = group_any(isnan(vf));
         turn ^= 1;
-        if (first) c = c0 * row_scale[tid];
       }
       ok = ok && wait_or_abort(&s.sfull[sub], ns & 1, a.status, s.abort_flag);
       ++ns;
@@ -648,9 +811,11 @@ __device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, ui
     }
     if (w.begins && !w.ends) begun = make_int4(w.s, w.h, w.rb, w.last_cta());
     const bool whole = w.begins && w.ends;
-    const long long slot = (2LL * blockIdx.x + w.begins) * kChunkRows + sub * kSub + tid;
+    const long long slot = (2LL * blockIdx.x + w.begins) * kChunkRows + sub * kSub + quarter * 32;
     const float inv = inverse(l);
     const int bad0 = any && !kFp8 ? s.poison[sub * 2] : 1, bad1 = any && !kFp8 ? s.poison[sub * 2 + 1] : 0;
+    // where this warp's rows go, in elements (-1: no row)
+    const long long at = !mine ? -1 : whole ? out_at(a, w.q, w.h, i_new, my_head) : (slot + lane) * D;
     for (int k = 0; k < D; k += 32) {
       float o[32];
       if (any && ok) {
@@ -660,42 +825,43 @@ __device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, ui
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = 0.0f;
       }
-      if (!mine) continue;
-      if (bad0 <= bad1) {  // values that are not finite, of the tokens that this row sees in tiles bad0 .. bad1
-        for (int j = max(lo, bad0 * kTile); j < min(hi, (bad1 + 1) * kTile); ++j) {
-          // tokens that every row sees went through the product
-          if (j >= w.b.all_lo && j < w.b.all_hi) continue;
-          const int page = max(0, load_page(a.p, a.b, w.s, j / a.p.page_tokens, a.status));
-          const __nv_bfloat16* at =
-              static_cast<const __nv_bfloat16*>(a.p.v) +
-              (((long long)page * a.p.num_kv_heads + w.h) * a.p.page_tokens + j % a.p.page_tokens) * D + k;
+      if (bad0 <= bad1 && mine) {
+        float add[32] = {};
+        add_not_finite<D>(a, w.s, w.h, w.b.all_lo, w.b.all_hi, max(lo, bad0 * kTile), min(hi, (bad1 + 1) * kTile), k, add);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float x = __bfloat162float(at[i]);
-            if (!isfinite(x)) o[i] += x;
-          }
-        }
+        for (int i = 0; i < 32; ++i) o[i] += add[i];
       }
+      // rows through shared memory, so that neighbouring lanes store neighbouring bytes
+      constexpr int kChunks = L::kLine / 16;
       if (whole) {
-        uint4* out = reinterpret_cast<uint4*>(a.out + out_at(a, w.q, w.h, r) + k);
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = pack2(o[2 * i] * inv, o[2 * i + 1] * inv, false);
+        constexpr int kHalf = L::kLine / 64;  // chunks of 32 columns in a line
+        const int c0 = kHalf == 2 ? (k >> 5 & 1) * 4 : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          out[i] = make_uint4(pack2(o[8 * i] * inv, o[8 * i + 1] * inv, false),
-                              pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv, false),
-                              pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv, false),
-                              pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv, false));
+          stage_put<kChunks>(stage, lane, c0 + i, make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]));
+        if (kHalf == 2 && (k >> 5 & 1) == 0) continue;
+        stage_out<kChunks>(stage, lane, at, reinterpret_cast<uint8_t*>(a.out), 2, k & ~(kHalf * 32 - 1));
       } else {
-        float4* out = reinterpret_cast<float4*>(a.part_o + slot * D + k);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        for (int k2 = 0; k2 < 32; k2 += L::kLine / 4) {
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i)
+            stage_put<kChunks>(stage, lane, i,
+                               make_uint4(__float_as_uint(o[k2 + 4 * i]), __float_as_uint(o[k2 + 4 * i + 1]),
+                                          __float_as_uint(o[k2 + 4 * i + 2]), __float_as_uint(o[k2 + 4 * i + 3])));
+          stage_out<kChunks>(stage, lane, at, reinterpret_cast<uint8_t*>(a.part_o), 4, k + k2);
+        }
       }
     }
     if (mine) {
       if (whole) {
-        write_lse(a, w.q, w.h, r, m, l);
+        write_lse(a, w.q, w.h, i_new, my_head, m, l);
       } else {
-        a.part_ml[slot * 2] = m;
-        a.part_ml[slot * 2 + 1] = l;
+        a.part_ml[(slot + lane) * 2] = m;
+        a.part_ml[(slot + lane) * 2 + 1] = l;
       }
     }
     fence_before();  // the next block's MMAs write O after these reads
@@ -761,7 +927,7 @@ __device__ void expand(const AttendArgs& a, const Range& rg, const Shared& s, in
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                 const __grid_constant__ AttendArgs a) {
+                 const __grid_constant__ CUtensorMap map_q, const __grid_constant__ AttendArgs a) {
   using L = Layout<D, kFp8>;
   extern __shared__ uint8_t smem_raw[];
   const Shared s = carve<D, kFp8>(smem_raw);
@@ -776,12 +942,16 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
       dec::mbar_init(&s.rempty[i], kCvtWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      dec::mbar_init(&s.qfull[i], 4);
+      dec::mbar_init(&s.qfull[i], 1);
+      dec::mbar_init(&s.qempty[i], 1);
+      dec::mbar_init(&s.landed[i], 1);
       dec::mbar_init(&s.sfull[i], 1);
       dec::mbar_init(&s.pfull[i], 4);
       dec::mbar_init(&s.ofull[i], 2);
     }
     dec::mbar_init(s.drain, 1);
+    dec::mbar_init(s.mended, 1);
+    dec::mbar_init(s.asked, 1);
     *s.abort_flag = 0;
     dec::mbar_init_fence();
   }
@@ -823,6 +993,9 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8 ? kFpRest : kBfRest));
     if (warp == 8) produce<D, kFp8>(a, rg, s, &map_k, &map_v, lane);
     if (warp == 9) multiply<D, kFp8>(a, rg, s, tmem, lane);
+    if (kFp8 && warp >= 10) load_q<D, kFp8>(a, rg, s, &map_q, warp - 10, warp - 9, lane);
+    if (!kFp8 && warp == 10) load_q<D, kFp8>(a, rg, s, &map_q, 0, 2, lane);
+    if (!kFp8 && warp == 11) mend<D>(a, rg, s, lane);
   } else if (kFp8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFpCvt));
     expand<D>(a, rg, s, threadIdx.x - 384);
@@ -837,22 +1010,24 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
 }
 
 template <int D, bool kFp8>
-cudaError_t launch(const AttendArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+cudaError_t launch(const AttendArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq,
+                   cudaStream_t s) {
   const cudaError_t e = allow_smem<4096 + D * 2 + kFp8>(chunk_kernel<D, kFp8>, Layout<D, kFp8>::kSmem);
   if (e != cudaSuccess) return e;
   return launch_dependent(chunk_kernel<D, kFp8>, a.grid, kFp8 ? kFpThreads : kBfThreads, Layout<D, kFp8>::kSmem, s, mk,
-                          mv, a);
+                          mv, mq, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attend_chunk(const AttendArgs& a, cudaStream_t s) {
-  CUtensorMap mk, mv;
+  CUtensorMap mk, mv, mq;
   const int box = a.p.page_tokens < kTile ? a.p.page_tokens : kTile;
-  if (!pages_map(&mk, a.p, a.p.k, box) || !pages_map(&mv, a.p, a.p.v, box)) return cudaErrorInvalidValue;
+  if (!pages_map(&mk, a.p, a.p.k, box) || !pages_map(&mv, a.p, a.p.v, box) || !queries_map(&mq, a, a.tps))
+    return cudaErrorInvalidValue;
   const bool fp8 = a.p.kv_dtype == FT_KV_FP8E4M3;
-  if (a.p.head_dim == 128) return fp8 ? launch<128, true>(a, mk, mv, s) : launch<128, false>(a, mk, mv, s);
-  return fp8 ? launch<64, true>(a, mk, mv, s) : launch<64, false>(a, mk, mv, s);
+  if (a.p.head_dim == 128) return fp8 ? launch<128, true>(a, mk, mv, mq, s) : launch<128, false>(a, mk, mv, mq, s);
+  return fp8 ? launch<64, true>(a, mk, mv, mq, s) : launch<64, false>(a, mk, mv, mq, s);
 }
 
 }  // namespace kv

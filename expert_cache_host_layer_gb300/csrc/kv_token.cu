@@ -520,8 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mx != -INFINITY) l += ml[(x * 16 + r) * 2 + 1] * exp2_approx(mx - mm);
           }
           if (whole) {
-            a.out[out_at(a, w.q, w.h, r) + d] = __float2bfloat16(sum * inverse(l));
-            if (d == 0) write_lse(a, w.q, w.h, r, mm, l);
+            a.out[out_at(a, w.q, w.h, r / a.G, r % a.G) + d] = __float2bfloat16(sum * inverse(l));
+            if (d == 0) write_lse(a, w.q, w.h, r / a.G, r % a.G, mm, l);
           } else {
             a.part_o[(slot * kTokenRows + r) * D + d] = sum;
             if (d == 0) {

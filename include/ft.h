@@ -508,7 +508,8 @@ ft_status ft_kv_read(const ft_kv_pages* pages, const ft_kv_batch* batch, const i
  * so does one whose every score is -inf.  Tokens that a row does not see do
  * not reach it, whatever they hold.
  * q, out: device bf16 [num_tokens][num_q_heads][head_dim] with strides in
- * elements, 16-byte aligned, strides multiples of 8.  lse: device f32
+ * elements, 16-byte aligned, strides positive multiples of 8; at most 128
+ * query heads to a key head; the scales 16-byte aligned.  lse: device f32
  * [num_tokens][num_q_heads] (natural logarithm of the softmax's denominator,
  * scores scaled), or NULL.  Softmax statistics and sums are fp32;
  * probabilities are rounded to bf16 for the product with v.
