@@ -224,9 +224,10 @@ bool pages_map(CUtensorMap* m, const ft_kv_pages& p, const void* base, int box_r
 bool queries_map(CUtensorMap* m, const AttendArgs& a, int tokens);
 
 // Raise a kernel's limit of dynamic shared memory, once per device
-// (kId: a number of its own for each kernel of one type.)
+// (kId: a number of its own for each kernel of one type.  Static: a process may
+// load two builds of the library, whose kernels are not the same.)
 template <int kId, typename Kernel>
-cudaError_t allow_smem(Kernel* kernel, int bytes) {
+static cudaError_t allow_smem(Kernel* kernel, int bytes) {
   static std::atomic<unsigned long long> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -237,7 +238,7 @@ cudaError_t allow_smem(Kernel* kernel, int bytes) {
 }
 // A launch that may begin while the kernel before it on the stream ends (the kernel waits for its end itself).
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, const A&... args) {
+static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);

@@ -19,8 +19,9 @@
 //                    thread per row), mask, exponentiate, write P (bf16) over
 //                    S in TMEM; at the end scale O and store it, transposed
 //                    through shared memory so that a store fills its lines
-//   warp 8           producer: K and V tiles into a ring, one TMA box per page
-//                    (or half page row), 128-byte swizzled
+//   warp 8           walks the CTA's row blocks, tells the other warps of each
+//                    through a small ring, and loads K and V tiles into another,
+//                    one TMA box per page (or half page row), 128-byte swizzled
 //   warp 9           tcgen05.mma: S_w = Q_w K^T (M 128, N 128), O_w += P_w V
 //                    with P read from TMEM and V as it lies (token-major)
 //   warps 10, 11     bf16: Q of both sub-tiles by TMA as soon as the block
@@ -29,10 +30,11 @@
 //                    its sub-tile's Q and turns it into fp16
 //   warps 12-15      quantised cache: expand the codes of a raw ring into tiles
 //                    of the layout that the MMA reads (exact; K in fp16, V in
-//                    bf16, whose range P needs)
+//                    bf16, whose range P needs), and the scales to floats
 //
 // The MMA order PV_0(j-1) S_0(j) PV_1(j-1) S_1(j) keeps the tensor pipe on one
-// sub-tile while the other's softmax runs.  S_w(j)'s completion implies
+// sub-tile while the other's softmax runs; P comes in two halves, so that PV
+// starts on the first while the second is made.  S_w(j)'s completion implies
 // PV_w(j-1)'s, so the softmax of tile j may rescale O_w; it does so only when
 // a row's maximum has grown by more than 2^8 since O_w's scale was set (P is
 // then at most 2^8, and the final division removes any scale).
@@ -47,11 +49,13 @@ namespace {
 constexpr int kSub = kSubRows;
 constexpr int kTile = 128;                    // tokens per tile
 constexpr int kTmemCols = 512;                // S0 | S1 | O0 | O1, 128 columns each
+constexpr int kUnits = 4;                     // ring of row blocks
+constexpr int kBlockItems = 4;                // a block's fixed cost, in tiles, for the cut
 constexpr float kGrow = 8.0f;                 // log2 of the growth that O's scale may lag behind
 constexpr int kBfThreads = 384, kFpThreads = 512;
 // Registers of the warpgroups (softmax, producer and MMA, converters): within
 // what the block is launched with, 384 x 168 and 512 x 128.
-constexpr int kBfSoft = 216, kBfRest = 72, kFpSoft = 184, kFpRest = 56, kFpCvt = 88;
+constexpr int kBfSoft = 216, kBfRest = 72, kFpSoft = 200, kFpRest = 48, kFpCvt = 64;
 static_assert(256 * kBfSoft + 128 * kBfRest <= kBfThreads * 168, "registers");
 static_assert(256 * kFpSoft + 128 * (kFpRest + kFpCvt) <= kFpThreads * 128, "registers");
 constexpr int kCvtWarps = 4;
@@ -65,15 +69,21 @@ struct Layout {
   static constexpr int kRaw = kFp8 ? 2 * (128 / D) : 0;
   static constexpr int kRingOff = kQBytes;
   static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
-  static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;          // per warpgroup, twice: 128 x {k, v}
-  static constexpr int kScaleBytes = kFp8 ? 2 * 2 * 2 * kTile * 4 : 0;
+  // The scales of kScaleTurns tiles: k [128], v [128], flags [4].  Two would do:
+  // expanding K(j + 2) takes the place of V(j), which both softmaxes have used.
+  static constexpr int kScaleTurns = 3;
+  static constexpr int kScaleWords = 2 * kTile + 4;
+  static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;
+  static constexpr int kScaleBytes = kFp8 ? kScaleTurns * kScaleWords * 4 : 0;
   static constexpr int kRowOff = kScaleOff + kScaleBytes;               // Q's row scales
   static constexpr int kRowBytes = kFp8 ? 2 * kSub * 4 : 0;
   static constexpr int kLine = kFp8 ? 64 : 128;                         // bytes of a row in a softmax warp's staging
   static constexpr int kOutOff = kRowOff + kRowBytes;
   static constexpr int kBarOff = kOutOff + 8 * 32 * kLine;
-  static constexpr int kBars = 2 * kStages + 2 * kRaw + 12 + 3;
-  static constexpr int kSmem = kBarOff + kBars * 8 + 64 + 4 * kStages + 1024;
+  static constexpr int kBars = 2 * kStages + 2 * kRaw + 2 * kUnits + 14 + 3;
+  static constexpr int kUnitOff = kBarOff + (kBars * 8 + 15) / 16 * 16;
+  static constexpr int kMiscOff = kUnitOff + kUnits * 96;
+  static constexpr int kSmem = kMiscOff + 48 + 4 * kStages + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kStages * kTileBytes >= (kMaxSeqs + 1) * 8 + 1024, "the prefix sums fit the ring before it fills");
 };
@@ -202,24 +212,31 @@ __device__ __forceinline__ int tiles_of(const AttendArgs& a, const Seq& q, int r
   const Block b = block_of(a, q, rb);
   return b.t1 - b.t0;
 }
+// Items of a block: its tiles, after kBlockItems that stand for its fixed cost.
+__device__ __forceinline__ int items_of(const AttendArgs& a, const Seq& q, int rb) {
+  return tiles_of(a, q, rb) + kBlockItems;
+}
 // Items of one head of a sequence, summed by the whole warp.
 __device__ __forceinline__ long long head_items(const AttendArgs& a, const Seq& q, int lane) {
   long long n = 0;
   const int nb = blocks_of(a, q);
-  for (int rb = lane; rb < nb; rb += 32) n += tiles_of(a, q, rb);
+  for (int rb = lane; rb < nb; rb += 32) n += items_of(a, q, rb);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n;
 }
 
-// The row blocks of a CTA's range, one after the other.  Whole warps.
-struct ChunkWalk {
-  long long w, end, base, total, at;  // at: first item of the current block
-  int n, s, h, rb, nb;
-  Seq q;
-  Block b;
-  int t0, t1;  // tiles of the block that are this CTA's
-  bool begins, ends, started;
+// A CTA's part of a row block, as the other warps get it.
+struct Unit {
+  int s, h, rb;       // s < 0: no more
+  int q0, m, n;
+  int t0, t1;         // its tiles
+  int f0[2], f1[2];   // those of them that each sub-tile has (none: f0 >= f1)
+  int lo, hi, all_lo, all_hi;
+  int begins, ends, last;
+  int pad[5];
+  __device__ __forceinline__ Seq seq() const { return Seq{q0, m, n}; }
+  __device__ __forceinline__ bool any(int sub) const { return f0[sub] < f1[sub]; }
   // V's tile t as the rows see it: tokens [r0, r1) of the tile are seen by some
   // row, [p0, p1) and [p2, p3) of them not by all
   struct Edge {
@@ -229,44 +246,68 @@ struct ChunkWalk {
   __device__ __forceinline__ Edge edge(int t) const {
     Edge e;
     const int j0 = t * kTile;
-    e.r0 = min(kTile, max(0, b.lo - j0));
-    e.r1 = max(e.r0, min(kTile, b.hi - j0));
+    e.r0 = min(kTile, max(0, lo - j0));
+    e.r1 = max(e.r0, min(kTile, hi - j0));
     e.p0 = e.r0;
-    e.p1 = min(e.r1, b.all_lo - j0);
-    e.p2 = max(e.r0, b.all_hi - j0);
+    e.p1 = min(e.r1, all_lo - j0);
+    e.p2 = max(e.r0, all_hi - j0);
     e.p3 = e.r1;
     return e;
   }
-  __device__ __forceinline__ ChunkWalk(const Range& r)
-      : w(r.w0), end(r.w1), base(r.base), total(r.total), at(r.base), n(r.n), s(r.s), h(0), rb(0), nb(0),
-        started(false) {}
-  __device__ __forceinline__ bool next(const AttendArgs& a, int lane) {
-    if (w >= end) return false;
-    if (!started) {
-      started = true;
-      find(a, lane);
-    } else {  // the range goes on: past a whole block
-      at += b.t1 - b.t0;
-      if (++rb == nb) {
-        rb = 0;
-        if (++h == a.p.num_kv_heads) {
-          h = 0;
-          do {
-            ++s;
-            q = load_seq(a.p, a.b, s, a.status);
-          } while (q.m == 0);
-          nb = blocks_of(a, q);
+};
+static_assert(sizeof(Unit) == 96, "Layout");
+
+// The parts of row blocks in a CTA's range, one after the other (whole warp).
+struct ChunkWalk {
+  long long w, end, base, total, at;  // at: first item of the current block
+  int n, s, h, rb, nb, items;
+  Seq q;
+  bool started;
+  __device__ __forceinline__ ChunkWalk(const AttendArgs& a, const Range& r, int lane)
+      : w(r.w0), end(r.w1), base(r.base), total(r.total), at(r.base), n(r.n), s(r.s), h(0), rb(0), nb(0), items(0),
+        started(false) {
+    if (w < end) find(a, lane);
+  }
+  __device__ __forceinline__ bool next(const AttendArgs& a, Unit& u) {
+    for (;;) {
+      if (w >= end) return false;
+      if (!started) {
+        started = true;
+      } else {  // the range goes on: past a whole block
+        at += items;
+        if (++rb == nb) {
+          rb = 0;
+          if (++h == a.p.num_kv_heads) {
+            h = 0;
+            do {
+              ++s;
+              q = load_seq(a.p, a.b, s, a.status);
+            } while (q.m == 0);
+            nb = blocks_of(a, q);
+          }
         }
       }
+      const Block b = block_of(a, q, rb);
+      const int nt = b.t1 - b.t0;
+      items = nt + kBlockItems;
+      const int rel = (int)(w - at), cnt = (int)min((long long)(items - rel), end - w);
+      const int r0 = max(0, rel - kBlockItems), r1 = max(0, rel + cnt - kBlockItems);
+      w += cnt;
+      if (r0 == r1) continue;  // only of the fixed cost
+      u.s = s; u.h = h; u.rb = rb;
+      u.q0 = q.q0; u.m = q.m; u.n = q.n;
+      u.t0 = b.t0 + r0; u.t1 = b.t0 + r1;
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        u.f0[sub] = max(u.t0, b.s0[sub]);
+        u.f1[sub] = min(u.t1, b.s1[sub]);
+      }
+      u.lo = b.lo; u.hi = b.hi; u.all_lo = b.all_lo; u.all_hi = b.all_hi;
+      u.begins = r0 == 0;
+      u.ends = r1 == nt;
+      u.last = cta_of(at + items - 1, total, n);
+      return true;
     }
-    b = block_of(a, q, rb);
-    const int nt = b.t1 - b.t0, rel = (int)(w - at), cnt = (int)min((long long)(nt - rel), end - w);
-    t0 = b.t0 + rel;
-    t1 = t0 + cnt;
-    begins = rel == 0;
-    ends = rel + cnt == nt;
-    w += cnt;
-    return true;
   }
   // the head and row block of item w
   __device__ __forceinline__ void find(const AttendArgs& a, int lane) {
@@ -281,7 +322,7 @@ struct ChunkWalk {
     h = (int)((w - base) / per);
     at = base + h * per;
     for (int r0 = 0;; r0 += 32) {
-      const int mine = r0 + lane < nb ? tiles_of(a, q, r0 + lane) : 0;
+      const int mine = r0 + lane < nb ? items_of(a, q, r0 + lane) : 0;
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -298,19 +339,18 @@ struct ChunkWalk {
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  __device__ __forceinline__ int last_cta() const { return cta_of(at + (b.t1 - b.t0) - 1, total, n); }
-  __device__ __forceinline__ bool active(int sub, int t) const { return t >= b.s0[sub] && t < b.s1[sub]; }
-  // does sub-tile `sub` have a tile in this part?
-  __device__ __forceinline__ bool any(int sub) const { return max(t0, b.s0[sub]) < min(t1, b.s1[sub]); }
 };
 
 struct Shared {
   uint8_t* base;
-  uint64_t *full, *empty, *rfull, *rempty, *qfull, *qempty, *sfull, *pfull, *ofull, *landed, *drain, *mended, *asked;
+  uint64_t *full, *empty, *rfull, *rempty, *ufull, *uempty;
+  uint64_t *qfull, *qempty, *landed, *sfull, *pfull, *pfull2, *ofull;  // per sub-tile
+  uint64_t *drain, *mended, *asked;
+  Unit* unit;
   uint32_t* tmem;
   volatile int* abort_flag;
-  volatile int* took;    // [stages] V's tile had values that are not finite where not every row sees them
   volatile int* poison;  // [2][2] first and last tile with values that a sub-tile adds at its block's end
+  volatile int* took;    // [stages] V's tile had values that are not finite where not every row sees them
 };
 
 template <int D, bool kFp8>
@@ -319,29 +359,67 @@ __device__ __forceinline__ Shared carve(uint8_t* raw) {
   Shared s;
   s.base = raw + ((1024u - (dec::smem_addr(raw) & 1023u)) & 1023u);
   uint64_t* b = reinterpret_cast<uint64_t*>(s.base + L::kBarOff);
-  s.full = b;
-  s.empty = b + L::kStages;
-  s.rfull = b + 2 * L::kStages;
-  s.rempty = s.rfull + L::kRaw;
-  s.qfull = s.rempty + L::kRaw;
-  s.qempty = s.qfull + 2;
-  s.sfull = s.qfull + 4;
-  s.pfull = s.qfull + 6;
-  s.ofull = s.qfull + 8;
-  s.landed = s.qfull + 10;
-  s.drain = s.qfull + 12;
-  s.mended = s.drain + 1;
-  s.asked = s.drain + 2;
-  s.tmem = reinterpret_cast<uint32_t*>(s.drain + 3);
+  auto take = [&](int n) {
+    uint64_t* r = b;
+    b += n;
+    return r;
+  };
+  s.full = take(L::kStages);
+  s.empty = take(L::kStages);
+  s.rfull = take(L::kRaw);
+  s.rempty = take(L::kRaw);
+  s.ufull = take(kUnits);
+  s.uempty = take(kUnits);
+  s.qfull = take(2);
+  s.qempty = take(2);
+  s.landed = take(2);
+  s.sfull = take(2);
+  s.pfull = take(2);
+  s.pfull2 = take(2);
+  s.ofull = take(2);
+  s.drain = take(1);
+  s.mended = take(1);
+  s.asked = take(1);
+  s.unit = reinterpret_cast<Unit*>(s.base + L::kUnitOff);
+  s.tmem = reinterpret_cast<uint32_t*>(s.base + L::kMiscOff);
   s.abort_flag = reinterpret_cast<volatile int*>(s.tmem + 1);
   s.poison = reinterpret_cast<volatile int*>(s.tmem + 4);
   s.took = s.poison + 4;
   return s;
 }
 
+// A place in a ring of barriers and the parity of its turn.
+template <int kN>
+struct Turn {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == kN) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// A warp's view of the ring of row blocks.
+struct Units {
+  Turn<kUnits> at;
+  // the next block, or null: no more (or the CTA has aborted)
+  __device__ __forceinline__ const Unit* next(const AttendArgs& a, const Shared& s) {
+    if (!wait_or_abort(&s.ufull[at.st], at.ph, a.status, s.abort_flag)) return nullptr;
+    const Unit* u = &s.unit[at.st];
+    return u->s < 0 ? nullptr : u;
+  }
+  __device__ __forceinline__ void done(const Shared& s, int lane) {
+    __syncwarp();
+    if (lane == 0) dec::mbar_arrive(&s.uempty[at.st]);
+    at.next();
+  }
+};
+
 // ---------------------------------------------------------------- producer
 
-// Per tile: K then V, the pages' boxes spread over the lanes.
+// The row blocks, and per tile K then V, the pages' boxes spread over the lanes.
 template <int D, bool kFp8>
 __device__ void produce(const AttendArgs& a, const Range& rg, const Shared& s, const CUtensorMap* map_k,
                         const CUtensorMap* map_v, int lane) {
@@ -355,31 +433,44 @@ __device__ void produce(const AttendArgs& a, const Range& rg, const Shared& s, c
   const int br = min(a.p.page_tokens, kTile);  // tokens of a box
   const int box = lane / kHalves, half = lane % kHalves;
   constexpr int kRowBytes = kFp8 ? D : 128;
+  Turn<kSlots> at;
+  Turn<kUnits> ut;
   int it = 0;
   bool go = true;
-  ChunkWalk w(rg);
-  while (go && w.next(a, lane)) {
-    for (int t = w.t0; t < w.t1 && go; ++t) {
+  ChunkWalk w(a, rg, lane);
+  Unit u;
+  while (go) {
+    const bool more = w.next(a, u);
+    if (!more) u.s = -1;
+    if (!wait_or_abort(&s.uempty[ut.st], ut.ph ^ 1, a.status, s.abort_flag)) break;
+    if (lane == 0) {
+      s.unit[ut.st] = u;
+      dec::mbar_arrive(&s.ufull[ut.st]);
+    }
+    ut.next();
+    if (!more) break;
+    for (int t = u.t0; t < u.t1 && go; ++t) {
       const int j0 = t * kTile + box * br;
-      const bool mine = box * br < kTile && j0 < w.b.hi && j0 + br > w.b.lo;
+      const bool mine = box * br < kTile && j0 < u.hi && j0 + br > u.lo;
       int row = 0;
       if (mine) {
-        const int page = max(0, load_page(a.p, a.b, w.s, j0 / a.p.page_tokens, a.status));
-        row = (page * a.p.num_kv_heads + w.h) * a.p.page_tokens + j0 % a.p.page_tokens;
+        const int page = max(0, load_page(a.p, a.b, u.s, j0 / a.p.page_tokens, a.status));
+        row = (page * a.p.num_kv_heads + u.h) * a.p.page_tokens + j0 % a.p.page_tokens;
       }
       const int live = __popc(__ballot_sync(0xffffffffu, mine));
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++it) {
-        const int st = it % kSlots;
-        if (!wait_or_abort(&empty[st], ((it / kSlots) & 1) ^ 1, a.status, s.abort_flag)) {
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!wait_or_abort(&empty[at.st], at.ph ^ 1, a.status, s.abort_flag)) {
           go = false;
           break;
         }
-        if (lane == 0) dec::mbar_expect_tx(&full[st], live * br * kRowBytes);
+        if (lane == 0) dec::mbar_expect_tx(&full[at.st], live * br * kRowBytes);
         __syncwarp();
         if (mine)
-          tma_box(ring + st * kBytes + half * (kTile * 128) + box * br * kRowBytes, kv ? map_v : map_k, half * 64, row,
-                  &full[st]);
+          tma_box(ring + at.st * kBytes + half * (kTile * 128) + box * br * kRowBytes, kv ? map_v : map_k, half * 64,
+                  row, &full[at.st]);
+        at.next();
+        ++it;
       }
     }
   }
@@ -435,129 +526,158 @@ __device__ __forceinline__ bool take_not_finite(uint8_t* tile, int r0, int r1, i
 // not, values that are not finite are set to zero too, lest 0 * V reach the
 // others; the rows that see them add them at the block's end.
 template <int D>
-__device__ void mend(const AttendArgs& a, const Range& rg, const Shared& s, int lane) {
+__device__ void mend(const AttendArgs& a, const Shared& s, int lane) {
   using L = Layout<D, false>;
-  int it = 1;  // V of the walk's first tile
+  Turn<L::kStages> vt;  // the next V
+  vt.next();
   uint32_t n = 0;
-  ChunkWalk w(rg);
-  while (w.next(a, lane))
-    for (int t = w.t0; t < w.t1; ++t, it += 2) {
-      const ChunkWalk::Edge e = w.edge(t);
+  Units units;
+  while (const Unit* u = units.next(a, s)) {
+    for (int t = u->t0; t < u->t1; ++t, vt.next(), vt.next()) {
+      const Unit::Edge e = u->edge(t);
       if (!e.any()) continue;
       // asked by the MMA warp, which has not used this V yet: the ring cannot be a turn ahead or behind
       if (!wait_or_abort(s.asked, n++ & 1, a.status, s.abort_flag)) return;
-      const int st = it % L::kStages;
-      if (!wait_or_abort(&s.full[st], (it / L::kStages) & 1, a.status, s.abort_flag)) return;
-      uint8_t* V = s.base + L::kRingOff + st * L::kTileBytes;
+      if (!wait_or_abort(&s.full[vt.st], vt.ph, a.status, s.abort_flag)) return;
+      uint8_t* V = s.base + L::kRingOff + vt.st * L::kTileBytes;
       zero_rows<D>(V, e.r0 & ~15, e.r0, lane);
       zero_rows<D>(V, e.r1, (e.r1 + 15) & ~15, lane);
       bool took = false;
       if (e.p0 < e.p1) took |= take_not_finite<D>(V, e.p0, e.p1, lane);
       if (e.p2 < e.p3) took |= take_not_finite<D>(V, e.p2, e.p3, lane);
-      s.took[st] = took;
+      s.took[vt.st] = took;
       fence_async();
       __syncwarp();
       if (lane == 0) dec::mbar_arrive(s.mended);
     }
+    units.done(s, lane);
+  }
 }
 
 // ---------------------------------------------------------------- MMA
 
+// The warp runs together and elects the issuing thread at each step: issued
+// from a branch that one lane is in throughout, the MMAs came 10% slower.
 template <int D, bool kFp8>
-__device__ void multiply(const AttendArgs& a, const Range& rg, const Shared& s, uint32_t tmem, int lane) {
+__device__ void multiply(const AttendArgs& a, const Shared& s, uint32_t tmem, int lane) {
   using L = Layout<D, kFp8>;
-  const uint32_t ring = dec::smem_addr(s.base + L::kRingOff), qa = dec::smem_addr(s.base);
+  const uint32_t ring = desc_lo(dec::smem_addr(s.base + L::kRingOff)), qd = desc_lo(dec::smem_addr(s.base));
   constexpr uint32_t id_s = idesc(kTile, !kFp8, false), id_o = idesc(D, true, true);
-  int it = 0;
-  uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, mended = 0;
-  bool go = true;
-  ChunkWalk w(rg);
-  while (go && w.next(a, lane)) {
+  constexpr uint32_t kVLead = ((kTile * 128 - 16) >> 4) << 16;  // a V descriptor's leading offset, from a K one's
+  constexpr int kSteps = kTile / 16;
+  Turn<L::kStages> kt, vt;  // places of the next K and V
+  vt.next();
+  uint32_t pq[2] = {0, 0}, pp[2] = {0, 0}, pm = 0;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_or_abort(bar, parity, a.status, s.abort_flag); };
+  Units units;
+  while (const Unit* u = units.next(a, s)) {
     int bad0 = 0x7fffffff, bad1 = -1;
     bool live[2] = {false, false};  // O_w has been written in this part
-    for (int t = w.t0; t <= w.t1 && go; ++t) {
-      const int ki = it, vi = it - 1;  // ring positions of K(t) and V(t - 1)
-      const int ks = ki % L::kStages, vs = t > w.t0 ? vi % L::kStages : 0;
-      const uint32_t kd = desc_lo(ring + ks * L::kTileBytes), vd = desc_lo(ring + vs * L::kTileBytes, kTile * 128);
-      int k0 = 0, k1 = kTile / 16;  // 16-token steps of V(t - 1) with tokens that some row sees
-      if (t > w.t0) {
-        if (!(go = wait_or_abort(&s.full[vs], (vi / L::kStages) & 1, a.status, s.abort_flag))) break;
-        const ChunkWalk::Edge e = w.edge(t - 1);
-        k0 = e.r0 >> 4;
-        k1 = (e.r1 + 15) >> 4;
-        if (!kFp8 && e.any()) {
-          if (!(go = wait_or_abort(s.mended, mended & 1, a.status, s.abort_flag))) break;
-          ++mended;
-          if (s.took[vs]) {
-            bad0 = min(bad0, t - 1);
-            bad1 = t - 1;
+    const int t0 = u->t0, t1 = u->t1;
+    const int f0[2] = {u->f0[0], u->f0[1]}, f1[2] = {u->f1[0], u->f1[1]};
+    // tiles [e0, e1) are seen whole by every row
+    const int e0 = (max(u->lo, u->all_lo) + kTile - 1) / kTile, e1 = u->all_hi / kTile;
+    for (int t = t0; t <= t1; ++t) {
+      int k0 = 0, k1 = kSteps;  // 16-token steps of V(t - 1) with tokens that some row sees
+      if (t > t0) {
+        if (!wait(&s.full[vt.st], vt.ph)) goto out;
+        if (t - 1 < e0 || t > e1) {
+          const Unit::Edge e = u->edge(t - 1);
+          k0 = e.r0 >> 4;
+          k1 = (e.r1 + 15) >> 4;
+          if (!kFp8 && e.any()) {
+            if (!wait(s.mended, pm)) goto out;
+            pm ^= 1;
+            if (s.took[vt.st]) {
+              bad0 = min(bad0, t - 1);
+              bad1 = t - 1;
+            }
           }
         }
       }
+      const uint32_t kd = ring + kt.st * (L::kTileBytes >> 4), vd = ring + vt.st * (L::kTileBytes >> 4) + kVLead;
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
         const uint32_t S = tmem + sub * 128, O = tmem + 256 + sub * 128;
-        if (t > w.t0 && w.active(sub, t - 1)) {  // O_sub += P_sub(t - 1) V(t - 1)
-          if (!(go = wait_or_abort(&s.pfull[sub], np[sub] & 1, a.status, s.abort_flag))) break;
-          ++np[sub];
+        if (t > f0[sub] && t <= f1[sub]) {  // O_sub += P_sub(t - 1) V(t - 1)
+          if (!wait(&s.pfull[sub], pp[sub])) goto out;
           fence_after();
-          if (elect()) {
-            if (k0 == 0 && k1 == kTile / 16) {
+          if (k0 == 0 && k1 == kSteps) {
+            if (elect()) {
 #pragma unroll
-              for (int k = 0; k < kTile / 16; ++k) mma_ts(O, S + k * 8, vd + k * 128, id_o, k != 0 || live[sub]);
-            } else {
-              for (int k = k0; k < k1; ++k) mma_ts(O, S + k * 8, vd + k * 128, id_o, k != k0 || live[sub]);
+              for (int k = 0; k < kSteps / 2; ++k) mma_ts(O, S + k * 8, vd + k * 128, id_o, k != 0 || live[sub]);
             }
+            __syncwarp();
+            if (!wait(&s.pfull2[sub], pp[sub])) goto out;
+            fence_after();
+            if (elect()) {
+#pragma unroll
+              for (int k = kSteps / 2; k < kSteps; ++k) mma_ts(O, S + k * 8, vd + k * 128, id_o, true);
+            }
+          } else {
+            if (!wait(&s.pfull2[sub], pp[sub])) goto out;
+            fence_after();
+            if (elect())
+              for (int k = k0; k < k1; ++k) mma_ts(O, S + k * 8, vd + k * 128, id_o, k != k0 || live[sub]);
           }
           __syncwarp();
+          pp[sub] ^= 1;
           live[sub] = true;
         }
-        if (t < w.t1) {  // S_sub = Q_sub K(t)^T
+        if (t < t1) {  // S_sub = Q_sub K(t)^T
           if (sub == 0) {
-            if (!kFp8 && w.edge(t).any() && lane == 0) dec::mbar_arrive(s.asked);
-            if (!(go = wait_or_abort(&s.full[ks], (ki / L::kStages) & 1, a.status, s.abort_flag))) break;
+            if (!kFp8 && (t < e0 || t >= e1) && u->edge(t).any() && lane == 0) dec::mbar_arrive(s.asked);
+            if (!wait(&s.full[kt.st], kt.ph)) goto out;
           }
-          if (w.active(sub, t)) {
-            if (t == max(w.t0, w.b.s0[sub])) {
-              if (!(go = wait_or_abort(&s.qfull[sub], nq[sub] & 1, a.status, s.abort_flag))) break;
-              ++nq[sub];
+          if (t >= f0[sub] && t < f1[sub]) {
+            if (t == f0[sub]) {
+              if (!wait(&s.qfull[sub], pq[sub])) goto out;
+              pq[sub] ^= 1;
             }
             fence_after();
-            const uint32_t qd = desc_lo(qa + sub * kSub * D * 2);
             if (elect()) {
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
-                mma_ss(S, qd + (k >> 2) * (kSub * 8) + (k & 3) * 2, kd + (k >> 2) * (kTile * 8) + (k & 3) * 2, id_s,
-                       k != 0);
+                mma_ss(S, qd + sub * (kSub * D / 8) + (k >> 2) * (kSub * 8) + (k & 3) * 2,
+                       kd + (k >> 2) * (kTile * 8) + (k & 3) * 2, id_s, k != 0);
               commit(&s.sfull[sub]);
-              if (t + 1 == min(w.t1, w.b.s1[sub])) commit(&s.qempty[sub]);
+              if (t + 1 == f1[sub]) commit(&s.qempty[sub]);
             }
             __syncwarp();
           }
         }
       }
-      if (!go) break;
       if (elect()) {
-        if (t > w.t0) commit(&s.empty[vs]);
-        if (t < w.t1) commit(&s.empty[ks]);
+        if (t > t0) commit(&s.empty[vt.st]);
+        if (t < t1) commit(&s.empty[kt.st]);
       }
       __syncwarp();
-      it += t < w.t1 ? 2 : 0;
+      if (t > t0) {
+        vt.next();
+        vt.next();
+      }
+      if (t < t1) {
+        kt.next();
+        kt.next();
+      }
     }
-    if (!go) break;
-    // K and V of the last tile have been passed: `it` is at the next block's first K
-    if (elect()) {
+    if (lane == 0) {
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub)
         if (live[sub]) {  // (its warpgroup has read the block before: it has written P since)
           s.poison[sub * 2] = bad0;
           s.poison[sub * 2 + 1] = bad1;
-          commit(&s.ofull[sub]);
           dec::mbar_arrive(&s.ofull[sub]);
         }
     }
     __syncwarp();
+    if (elect()) {
+      if (live[0]) commit(&s.ofull[0]);
+      if (live[1]) commit(&s.ofull[1]);
+    }
+    units.done(s, lane);
   }
+out:
   // every MMA issued has completed before TMEM is freed
   if (elect()) {
     commit(s.drain);
@@ -575,16 +695,15 @@ __device__ void multiply(const AttendArgs& a, const Range& rg, const Shared& s, 
 // two to [1, 2), in place; a thread takes a row.  A negative softmax scale goes
 // into Q's signs.
 template <int D, bool kFp8>
-__device__ void load_q(const AttendArgs& a, const Range& rg, const Shared& s, const CUtensorMap* map, int sub0, int sub1,
-                       int lane) {
+__device__ void load_q(const AttendArgs& a, const Shared& s, const CUtensorMap* map, int sub0, int sub1, int lane) {
   using L = Layout<D, kFp8>;
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
   uint32_t n[2] = {0, 0};
-  ChunkWalk w(rg);
-  while (w.next(a, lane))
+  Units units;
+  while (const Unit* u = units.next(a, s)) {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
-      if (sub < sub0 || sub >= sub1 || !w.any(sub)) continue;
+      if (sub < sub0 || sub >= sub1 || !u->any(sub)) continue;
       if (!wait_or_abort(&s.qempty[sub], (n[sub] & 1) ^ 1, a.status, s.abort_flag)) return;
       ++n[sub];
       uint8_t* Q = s.base + sub * kSub * D * 2;
@@ -594,7 +713,7 @@ __device__ void load_q(const AttendArgs& a, const Range& rg, const Shared& s, co
         dec::mbar_expect_tx(bar, a.tps * a.G * D * 2);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
-          tma_box3(dec::smem_addr(Q + c * kSub * 128), map, c * 64, w.h * a.G, w.q.q0 + (w.rb * 2 + sub) * a.tps, bar);
+          tma_box3(dec::smem_addr(Q + c * kSub * 128), map, c * 64, u->h * a.G, u->q0 + (u->rb * 2 + sub) * a.tps, bar);
       }
       if (!rework) continue;
       if (!wait_or_abort(bar, (n[sub] & 1) ^ 1, a.status, s.abort_flag)) return;
@@ -633,6 +752,8 @@ __device__ void load_q(const AttendArgs& a, const Range& rg, const Shared& s, co
       __syncwarp();
       if (lane == 0) dec::mbar_arrive(&s.qfull[sub]);
     }
+    units.done(s, lane);
+  }
 }
 
 // ---------------------------------------------------------------- softmax
@@ -679,87 +800,137 @@ __device__ __noinline__ void add_not_finite(const AttendArgs& a, int s, int h, i
   }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Probabilities of 64 of a row's scores, as bf16 pairs, and their sum.  vs: the
+// value scales (quantised cache); a scale may be NaN (nan_scale): then 0 * NaN
+// must not reach a row that does not see the token.
+template <bool kFp8>
+__device__ __forceinline__ float2 probabilities(const float* x, float c, float base, const float* vs, bool nan_scale,
+                                                uint32_t* p) {
+  const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+  float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+  for (int k = 0; k < 64; k += 2) {
+    const float2 y = fma2(make_float2(x[k], x[k + 1]), c2, b2);
+    float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+    if (k & 2) sum1 = add2(sum1, e);
+    else sum0 = add2(sum0, e);
+    if (kFp8) {
+      const float2 v = *reinterpret_cast<const float2*>(vs + k);
+      if (nan_scale) {
+        e.x = x[k] == -INFINITY ? 0.0f : e.x * v.x;
+        e.y = x[k + 1] == -INFINITY ? 0.0f : e.y * v.y;
+      } else {
+        e = mul2(e, v);
+      }
+    }
+    p[k / 2] = pack2(e.x, e.y, false);
+  }
+  return add2(sum0, sum1);
+}
+
 template <int D, bool kFp8>
-__device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, uint32_t tmem, int sub, int tid) {
+__device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int sub, int tid) {
   using L = Layout<D, kFp8>;
   const int lane = tid & 31, quarter = (tid >> 5) & 3;
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
   const uint32_t ts = tmem + lanes + sub * 128, to = tmem + lanes + 256 + sub * 128;
-  float* scales = reinterpret_cast<float*>(s.base + L::kScaleOff) + sub * 2 * 2 * kTile;
-  const float* row_scale = reinterpret_cast<const float*>(s.base + L::kRowOff) + sub * kSub;
-  // the warpgroup's barrier, and whether any of its threads says so
-  auto group_any = [&](bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.pred p, %2, 128, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x), "r"(1 + sub)
-        : "memory");
-    return r != 0;
-  };
-  uint32_t ns = 0, no = 0;
-  int turn = 0;
-  int4 begun = make_int4(-1, 0, 0, 0);
+  const float* scales = reinterpret_cast<const float*>(s.base + L::kScaleOff);
   const float c0 = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);  // never 0: 0 * -inf is not -inf
-  const int my_token = tid / a.G, my_head = tid % a.G;
+  const int my_token = tid / a.G;
   uint8_t* stage = s.base + L::kOutOff + (sub * 4 + quarter) * 32 * L::kLine;
-  ChunkWalk w(rg);
-  bool ok = true;
-  while (w.next(a, lane)) {
-    const int i_new = (w.rb * 2 + sub) * a.tps + my_token;  // this row's new token
-    const bool mine = my_token < a.tps && i_new < w.q.m;
-    const bool any = w.any(sub);
+  uint32_t ns = 0, no = 0;
+  Turn<L::kScaleTurns> turn;
+  int4 begun = make_int4(-1, 0, 0, 0);
+  Units units;
+  while (const Unit* u = units.next(a, s)) {
+    const int i_new = (u->rb * 2 + sub) * a.tps + my_token;  // this row's new token
+    const bool mine = my_token < a.tps && i_new < u->m;
+    const bool any = u->any(sub);
+    const Span v = visible(a, u->seq(), mine ? i_new : 0);
+    const int lo = mine ? v.lo : 0, hi = mine ? v.hi : 0;
     float m = -INFINITY, l = 0.0f, c = c0;
     if (any && kFp8) {
-      ok = ok && wait_or_abort(&s.qfull[sub], no & 1, a.status, s.abort_flag);
-      if (ok) c = c0 * row_scale[tid];
+      if (!wait_or_abort(&s.qfull[sub], no, a.status, s.abort_flag)) return;
+      c = c0 * reinterpret_cast<const float*>(s.base + L::kRowOff)[sub * kSub + tid];
     }
-    const Span v = visible(a, w.q, mine ? i_new : 0);
-    const int lo = mine ? v.lo : 0, hi = mine ? v.hi : 0;
+    const int t_end = any ? u->f1[sub] : u->t0, all_lo = u->all_lo, all_hi = u->all_hi;
     bool first = true;
-    for (int t = max(w.t0, w.b.s0[sub]); t < min(w.t1, w.b.s1[sub]); ++t) {
+    int t = u->t0;
+    if (any)
+      for (; t < u->f0[sub]; ++t) turn.next();  // (every tile has its turn of scales)
+    for (; t < t_end; ++t) {
       const int j0 = t * kTile;
-      float* sc = scales + turn * 2 * kTile;
-      bool nan_scale = false;
-      if (kFp8) {  // this thread's token's scales, for the whole warpgroup
-        float kf = 0.0f, vf = 0.0f;
-        if (j0 + tid >= w.b.lo && j0 + tid < w.b.hi) {
-          const int page = max(0, load_page(a.p, a.b, w.s, (j0 + tid) / a.p.page_tokens, a.status));
-          const long long at =
-              ((long long)page * a.p.num_kv_heads + w.h) * a.p.page_tokens + (j0 + tid) % a.p.page_tokens;
-          kf = scale_of(__ldg(a.p.k_scale + at));
-          vf = scale_of(__ldg(a.p.v_scale + at));
-        }
-        sc[tid] = kf;
-        sc[kTile + tid] = vf;
-        // two buffers: everyone has left the tile before the last
-        nan_scale = group_any(isnan(vf));
-        turn ^= 1;
-      }
-      ok = ok && wait_or_abort(&s.sfull[sub], ns & 1, a.status, s.abort_flag);
-      ++ns;
-      if (!ok) continue;
+      const float* sc = scales + turn.st * L::kScaleWords;
+      turn.next();
+      if (!wait_or_abort(&s.sfull[sub], ns, a.status, s.abort_flag)) return;
+      ns ^= 1;
       fence_after();
       float x[128];
 #pragma unroll
       for (int k = 0; k < 4; ++k) ld32(ts + 32 * k, x + 32 * k);
       ld_wait();
+      bool nan_scale = false;
       if (kFp8) {
+        const int4 f = *reinterpret_cast<const int4*>(sc + 2 * kTile);
+        nan_scale = (f.x | f.y | f.z | f.w) != 0;
 #pragma unroll
-        for (int k = 0; k < 128; ++k) x[k] *= sc[k];
+        for (int k = 0; k < 128; k += 2) {
+          const float2 y = mul2(make_float2(x[k], x[k + 1]), *reinterpret_cast<const float2*>(sc + k));
+          x[k] = y.x;
+          x[k + 1] = y.y;
+        }
       }
-      if (j0 < w.b.all_lo || j0 + kTile > w.b.all_hi) {  // some row does not see some of it
-        const unsigned from = (unsigned)(lo - j0), width = (unsigned)(hi - lo);
+      if (j0 + kTile > all_hi) {  // some row does not see the last of it
+        const int end = hi - j0;
 #pragma unroll
         for (int k = 0; k < 128; ++k)
-          if ((unsigned)k - from >= width) x[k] = -INFINITY;
+          if (k >= end) x[k] = -INFINITY;
       }
-      float top4[4] = {x[0], x[1], x[2], x[3]};
+      if (j0 < all_lo) {  // or the first
+        const int from = lo - j0;
 #pragma unroll
-      for (int k = 4; k < 128; ++k) top4[k & 3] = fmaxf(top4[k & 3], x[k]);
-      float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-      top *= c;
+        for (int k = 0; k < 128; ++k)
+          if (k < from) x[k] = -INFINITY;
+      }
+      float top4[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top4[k] = fmaxf(x[k], x[k + 4]);
+#pragma unroll
+      for (int k = 8; k < 128; k += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top4[i] = max3(top4[i], x[k + i], x[k + 4 + i]);
+      const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * c;
       if (first) {
         m = top;
         first = false;
@@ -777,48 +948,48 @@ __device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, ui
         }
       }
       const float base = m == -INFINITY ? 0.0f : m;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      uint32_t p[64];
-#pragma unroll
-      for (int k = 0; k < 128; k += 2) {
-        float p0 = exp2_approx(fmaf(x[k], c, -base)), p1 = exp2_approx(fmaf(x[k + 1], c, -base));
-        sum[k & 3] += p0;
-        sum[(k & 3) + 1] += p1;
-        if (kFp8) {
-          if (nan_scale) {  // 0 * NaN must not reach a row that does not see the token
-            p0 = x[k] == -INFINITY ? 0.0f : p0 * sc[kTile + k];
-            p1 = x[k + 1] == -INFINITY ? 0.0f : p1 * sc[kTile + k + 1];
-          } else {
-            p0 *= sc[kTile + k];
-            p1 *= sc[kTile + k + 1];
-          }
-        }
-        p[k / 2] = pack2(p0, p1, false);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      uint32_t p[32];
+      float2 sum = probabilities<kFp8>(x, c, base, sc + kTile, nan_scale, p);
       st32(ts, p);
-      st32(ts + 32, p + 32);
       st_wait();
       fence_before();
       __syncwarp();
       if (lane == 0) dec::mbar_arrive(&s.pfull[sub]);
+      const float2 more = probabilities<kFp8>(x + 64, c, base, sc + kTile + 64, nan_scale, p);
+      st32(ts + 32, p);
+      st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) dec::mbar_arrive(&s.pfull2[sub]);
+      sum = add2(sum, more);
+      l += sum.x + sum.y;
     }
+    for (; t < u->t1; ++t) turn.next();
     // ------------------------------------------------------------ the block's end
-    if (any) {
-      ok = ok && wait_or_abort(&s.ofull[sub], no & 1, a.status, s.abort_flag);
-      ++no;
-      if (ok) fence_after();
+    const bool whole = u->begins && u->ends;
+    const int my_head = tid - my_token * a.G;
+    if (u->begins && !u->ends) begun = make_int4(u->s, u->h, u->rb, u->last);
+    const long long slot = (2LL * blockIdx.x + u->begins) * kChunkRows + sub * kSub + quarter * 32;
+    // where this lane's row goes, in elements (-1: no row)
+    const long long at = !mine ? -1 : whole ? out_at(a, u->seq(), u->h, i_new, my_head) : (slot + lane) * D;
+    if (mine) {
+      if (whole) {
+        write_lse(a, u->seq(), u->h, i_new, my_head, m, l);
+      } else {
+        a.part_ml[(slot + lane) * 2] = m;
+        a.part_ml[(slot + lane) * 2 + 1] = l;
+      }
     }
-    if (w.begins && !w.ends) begun = make_int4(w.s, w.h, w.rb, w.last_cta());
-    const bool whole = w.begins && w.ends;
-    const long long slot = (2LL * blockIdx.x + w.begins) * kChunkRows + sub * kSub + quarter * 32;
     const float inv = inverse(l);
+    if (any) {
+      if (!wait_or_abort(&s.ofull[sub], no, a.status, s.abort_flag)) return;
+      no ^= 1;
+      fence_after();
+    }
     const int bad0 = any && !kFp8 ? s.poison[sub * 2] : 1, bad1 = any && !kFp8 ? s.poison[sub * 2 + 1] : 0;
-    // where this warp's rows go, in elements (-1: no row)
-    const long long at = !mine ? -1 : whole ? out_at(a, w.q, w.h, i_new, my_head) : (slot + lane) * D;
     for (int k = 0; k < D; k += 32) {
       float o[32];
-      if (any && ok) {
+      if (any) {
         ld32(to + k, o);
         ld_wait();
       } else {
@@ -827,23 +998,24 @@ __device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, ui
       }
       if (bad0 <= bad1 && mine) {
         float add[32] = {};
-        add_not_finite<D>(a, w.s, w.h, w.b.all_lo, w.b.all_hi, max(lo, bad0 * kTile), min(hi, (bad1 + 1) * kTile), k, add);
+        add_not_finite<D>(a, u->s, u->h, all_lo, all_hi, max(lo, bad0 * kTile), min(hi, (bad1 + 1) * kTile), k, add);
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] += add[i];
       }
       // rows through shared memory, so that neighbouring lanes store neighbouring bytes
       constexpr int kChunks = L::kLine / 16;
       if (whole) {
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = pack2(o[2 * i] * inv, o[2 * i + 1] * inv, false);
-        constexpr int kHalf = L::kLine / 64;  // chunks of 32 columns in a line
-        const int c0 = kHalf == 2 ? (k >> 5 & 1) * 4 : 0;
+        constexpr int kHalf = L::kLine / 64;  // runs of 32 columns in a line
+        const int run = kHalf == 2 ? k >> 5 & 1 : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          stage_put<kChunks>(stage, lane, c0 + i, make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]));
-        if (kHalf == 2 && (k >> 5 & 1) == 0) continue;
-        stage_out<kChunks>(stage, lane, at, reinterpret_cast<uint8_t*>(a.out), 2, k & ~(kHalf * 32 - 1));
+          stage_put<kChunks>(stage, lane, run * 4 + i,
+                             make_uint4(pack2(o[8 * i] * inv, o[8 * i + 1] * inv, false),
+                                        pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv, false),
+                                        pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv, false),
+                                        pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv, false)));
+        if (run == kHalf - 1)
+          stage_out<kChunks>(stage, lane, at, reinterpret_cast<uint8_t*>(a.out), 2, k & ~(kHalf * 32 - 1));
       } else {
 #pragma unroll
         for (int k2 = 0; k2 < 32; k2 += L::kLine / 4) {
@@ -856,15 +1028,8 @@ __device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, ui
         }
       }
     }
-    if (mine) {
-      if (whole) {
-        write_lse(a, w.q, w.h, i_new, my_head, m, l);
-      } else {
-        a.part_ml[(slot + lane) * 2] = m;
-        a.part_ml[(slot + lane) * 2 + 1] = l;
-      }
-    }
     fence_before();  // the next block's MMAs write O after these reads
+    units.done(s, lane);
   }
   if (sub == 0 && tid == 0) a.desc[blockIdx.x] = begun;
 }
@@ -872,22 +1037,33 @@ __device__ void soften(const AttendArgs& a, const Range& rg, const Shared& s, ui
 // ---------------------------------------------------------------- e4m3 codes to 16-bit tiles
 
 template <int D>
-__device__ void expand(const AttendArgs& a, const Range& rg, const Shared& s, int tid) {
+__device__ void expand(const AttendArgs& a, const Shared& s, int tid) {
   using L = Layout<D, true>;
   const int lane = tid & 31;
-  int it = 0;
-  ChunkWalk w(rg);
-  while (w.next(a, lane)) {
-    for (int t = w.t0; t < w.t1; ++t)
+  Turn<L::kRaw> rt;
+  Turn<L::kStages> st;
+  Turn<L::kScaleTurns> turn;
+  Units units;
+  while (const Unit* u = units.next(a, s)) {
+    const int lo = u->lo, hi = u->hi, t1 = u->t1;
+    for (int t = u->t0; t < t1; ++t) {
+      // this thread's token's scales, on their way while K is expanded
+      uint32_t ek = 0, ev = 0;
+      const int j = t * kTile + tid;
+      if (j >= lo && j < hi) {
+        const int page = max(0, load_page(a.p, a.b, u->s, j / a.p.page_tokens, a.status));
+        const long long at = ((long long)page * a.p.num_kv_heads + u->h) * a.p.page_tokens + j % a.p.page_tokens;
+        ek = __ldg(a.p.k_scale + at);
+        ev = __ldg(a.p.v_scale + at);
+      }
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++it) {
-        const int rs = it % L::kRaw, st = it % L::kStages;
-        if (!wait_or_abort(&s.rfull[rs], (it / L::kRaw) & 1, a.status, s.abort_flag)) return;
-        if (!wait_or_abort(&s.empty[st], ((it / L::kStages) & 1) ^ 1, a.status, s.abort_flag)) return;
-        const uint8_t* src = s.base + L::kRawOff + rs * L::kRawBytes;
-        uint8_t* dst = s.base + L::kRingOff + st * L::kTileBytes;
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!wait_or_abort(&s.rfull[rt.st], rt.ph, a.status, s.abort_flag)) return;
+        if (!wait_or_abort(&s.empty[st.st], st.ph ^ 1, a.status, s.abort_flag)) return;
+        const uint8_t* src = s.base + L::kRawOff + rt.st * L::kRawBytes;
+        uint8_t* dst = s.base + L::kRingOff + st.st * L::kTileBytes;
         constexpr int kPer = D / 16;  // 16-byte chunks of a raw row
-        const int seen0 = w.b.lo - t * kTile, seen1 = w.b.hi - t * kTile;
+        const int seen0 = lo - t * kTile, seen1 = hi - t * kTile;
 #pragma unroll 4
         for (int i = tid; i < kTile * kPer; i += kCvtWarps * 32) {
           const int r = i / kPer, ch = i % kPer;
@@ -914,13 +1090,25 @@ __device__ void expand(const AttendArgs& a, const Range& rg, const Shared& s, in
           *reinterpret_cast<uint4*>(row + ((d0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4*>(row + (((d0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
+        if (kv == 0) {
+          float* sc = reinterpret_cast<float*>(s.base + L::kScaleOff) + turn.st * L::kScaleWords;
+          sc[tid] = scale_of(ek);
+          sc[kTile + tid] = scale_of(ev);
+          const bool nan = __any_sync(0xffffffffu, ev == kNanScale);
+          if (lane == 0) reinterpret_cast<int*>(sc)[2 * kTile + (tid >> 5)] = nan;
+          turn.next();
+        }
         fence_async();
         __syncwarp();
         if (lane == 0) {
-          dec::mbar_arrive(&s.rempty[rs]);
-          dec::mbar_arrive(&s.full[st]);
+          dec::mbar_arrive(&s.rempty[rt.st]);
+          dec::mbar_arrive(&s.full[st.st]);
         }
+        rt.next();
+        st.next();
       }
+    }
+    units.done(s, lane);
   }
 }
 
@@ -941,12 +1129,17 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
       dec::mbar_init(&s.rfull[i], 1);
       dec::mbar_init(&s.rempty[i], kCvtWarps);
     }
+    for (int i = 0; i < kUnits; ++i) {
+      dec::mbar_init(&s.ufull[i], 1);
+      dec::mbar_init(&s.uempty[i], 8 + 1 + 2 + (kFp8 ? kCvtWarps : 0));  // softmax, MMA, warps 10 and 11, expanding
+    }
     for (int i = 0; i < 2; ++i) {
       dec::mbar_init(&s.qfull[i], 1);
       dec::mbar_init(&s.qempty[i], 1);
       dec::mbar_init(&s.landed[i], 1);
       dec::mbar_init(&s.sfull[i], 1);
       dec::mbar_init(&s.pfull[i], 4);
+      dec::mbar_init(&s.pfull2[i], 4);
       dec::mbar_init(&s.ofull[i], 2);
     }
     dec::mbar_init(s.drain, 1);
@@ -971,7 +1164,7 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
     const int nb = blocks_of(a, q);
     long long n = 0;
     if (nb <= 8)
-      for (int rb = 0; rb < nb; ++rb) n += tiles_of(a, q, rb);
+      for (int rb = 0; rb < nb; ++rb) n += items_of(a, q, rb);
     for (unsigned big = __ballot_sync(0xffffffffu, nb > 8); big; big &= big - 1) {
       const int src = __ffs(big) - 1;
       const Seq o{__shfl_sync(0xffffffffu, q.q0, src), __shfl_sync(0xffffffffu, q.m, src),
@@ -988,17 +1181,17 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
   const uint32_t tmem = *s.tmem;
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8 ? kFpSoft : kBfSoft));
-    soften<D, kFp8>(a, rg, s, tmem, warp >> 2, threadIdx.x & 127);
+    soften<D, kFp8>(a, s, tmem, warp >> 2, threadIdx.x & 127);
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8 ? kFpRest : kBfRest));
     if (warp == 8) produce<D, kFp8>(a, rg, s, &map_k, &map_v, lane);
-    if (warp == 9) multiply<D, kFp8>(a, rg, s, tmem, lane);
-    if (kFp8 && warp >= 10) load_q<D, kFp8>(a, rg, s, &map_q, warp - 10, warp - 9, lane);
-    if (!kFp8 && warp == 10) load_q<D, kFp8>(a, rg, s, &map_q, 0, 2, lane);
-    if (!kFp8 && warp == 11) mend<D>(a, rg, s, lane);
+    if (warp == 9) multiply<D, kFp8>(a, s, tmem, lane);
+    if (kFp8 && warp >= 10) load_q<D, kFp8>(a, s, &map_q, warp - 10, warp - 9, lane);
+    if (!kFp8 && warp == 10) load_q<D, kFp8>(a, s, &map_q, 0, 2, lane);
+    if (!kFp8 && warp == 11) mend<D>(a, s, lane);
   } else if (kFp8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFpCvt));
-    expand<D>(a, rg, s, threadIdx.x - 384);
+    expand<D>(a, s, threadIdx.x - 384);
   }
   fence_before();
   __syncthreads();
