@@ -3,9 +3,9 @@
 //
 //   S = Q K^T,  P = 2^(x - m),  O += P V,  out = O / sum P
 //
-// with a running maximum m per row and x = scale log2(e) S.  Quantised cache:
-// the key's scale multiplies S, the value's scale P (after its share of the
-// sum), and the codes are multiplied, as in kv_token.cu.
+// with a running maximum m per row and x = scale log2(e) S.  Quantised cache: a
+// code times its power-of-two scale is a bf16 value, so its tiles are expanded
+// to exactly that and the rest is the same.
 //
 // Item: a tile of 128 tokens for a row block of one (sequence, key head).  A
 // row block is two sub-tiles of up to 128 rows, each the query heads of the
@@ -24,13 +24,12 @@
 //                    one TMA box per page (or half page row), 128-byte swizzled
 //   warp 9           tcgen05.mma: S_w = Q_w K^T (M 128, N 128), O_w += P_w V
 //                    with P read from TMEM and V as it lies (token-major)
-//   warps 10, 11     bf16: Q of both sub-tiles by TMA as soon as the block
-//                    before has its last score tile; V's tiles at the edge of
-//                    what the rows see (see mend).  Quantised cache: each loads
-//                    its sub-tile's Q and turns it into fp16
-//   warps 12-15      quantised cache: expand the codes of a raw ring into tiles
-//                    of the layout that the MMA reads (exact; K in fp16, V in
-//                    bf16, whose range P needs), and the scales to floats
+//   warp 10          Q of both sub-tiles by TMA as soon as the block before has
+//                    its last score tile
+//   warp 11          bf16 cache: V's tiles at the edge of what the rows see (see
+//                    mend)
+//   warps 12-19      quantised cache: expand the codes of a raw ring, times their
+//                    scales, into bf16 tiles of the layout that the MMA reads
 //
 // The MMA order PV_0(j-1) S_0(j) PV_1(j-1) S_1(j) keeps the tensor pipe on one
 // sub-tile while the other's softmax runs; P comes in two halves, so that PV
@@ -52,13 +51,13 @@ constexpr int kTmemCols = 512;                // S0 | S1 | O0 | O1, 128 columns 
 constexpr int kUnits = 4;                     // ring of row blocks
 constexpr int kBlockItems = 4;                // a block's fixed cost, in tiles, for the cut
 constexpr float kGrow = 8.0f;                 // log2 of the growth that O's scale may lag behind
-constexpr int kBfThreads = 384, kFpThreads = 512;
+constexpr int kBfThreads = 384, kFpThreads = 640;
 // Registers of the warpgroups (softmax, producer and MMA, converters): within
-// what the block is launched with, 384 x 168 and 512 x 128.
-constexpr int kBfSoft = 216, kBfRest = 72, kFpSoft = 200, kFpRest = 48, kFpCvt = 64;
+// what the block is launched with, 384 x 168 and 640 x 96.
+constexpr int kBfSoft = 216, kBfRest = 72, kFpSoft = 160, kFpRest = 48, kFpCvt = 56;
 static_assert(256 * kBfSoft + 128 * kBfRest <= kBfThreads * 168, "registers");
-static_assert(256 * kFpSoft + 128 * (kFpRest + kFpCvt) <= kFpThreads * 128, "registers");
-constexpr int kCvtWarps = 4;
+static_assert(256 * (kFpSoft + kFpCvt) + 128 * kFpRest <= kFpThreads * 96, "registers");
+constexpr int kCvtWarps = 8;
 
 template <int D, bool kFp8>
 struct Layout {
@@ -69,16 +68,8 @@ struct Layout {
   static constexpr int kRaw = kFp8 ? 2 * (128 / D) : 0;
   static constexpr int kRingOff = kQBytes;
   static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
-  // The scales of kScaleTurns tiles: k [128], v [128], flags [4].  Two would do:
-  // expanding K(j + 2) takes the place of V(j), which both softmaxes have used.
-  static constexpr int kScaleTurns = 3;
-  static constexpr int kScaleWords = 2 * kTile + 4;
-  static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;
-  static constexpr int kScaleBytes = kFp8 ? kScaleTurns * kScaleWords * 4 : 0;
-  static constexpr int kRowOff = kScaleOff + kScaleBytes;               // Q's row scales
-  static constexpr int kRowBytes = kFp8 ? 2 * kSub * 4 : 0;
   static constexpr int kLine = kFp8 ? 64 : 128;                         // bytes of a row in a softmax warp's staging
-  static constexpr int kOutOff = kRowOff + kRowBytes;
+  static constexpr int kOutOff = kRawOff + kRaw * kRawBytes;
   static constexpr int kBarOff = kOutOff + 8 * 32 * kLine;
   static constexpr int kBars = 2 * kStages + 2 * kRaw + 2 * kUnits + 14 + 3;
   static constexpr int kUnitOff = kBarOff + (kBars * 8 + 15) / 16 * 16;
@@ -161,16 +152,12 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(dec::smem_addr(bar))
       : "memory");
 }
-// kind::f16, fp32 accumulator, both operands bf16 (or fp16), B N-major or not.
-__device__ constexpr uint32_t idesc(int N, bool bf16, bool b_n_major) {
-  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_n_major ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kSub >> 4) << 24);
+// kind::f16, fp32 accumulator, both operands bf16, B N-major or not.
+__device__ constexpr uint32_t idesc(int N, bool b_n_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_n_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(kSub >> 4) << 24);
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, bool half) {
-  if (half) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
@@ -234,7 +221,8 @@ struct Unit {
   int f0[2], f1[2];   // those of them that each sub-tile has (none: f0 >= f1)
   int lo, hi, all_lo, all_hi;
   int begins, ends, last;
-  int pad[5];
+  int nan_v;          // quantised cache: some value of the part is NaN (see expand)
+  int pad[4];
   __device__ __forceinline__ Seq seq() const { return Seq{q0, m, n}; }
   __device__ __forceinline__ bool any(int sub) const { return f0[sub] < f1[sub]; }
   // V's tile t as the rows see it: tokens [r0, r1) of the tile are seen by some
@@ -306,6 +294,7 @@ struct ChunkWalk {
       u.begins = r0 == 0;
       u.ends = r1 == nt;
       u.last = cta_of(at + items - 1, total, n);
+      u.nan_v = 0;
       return true;
     }
   }
@@ -405,9 +394,9 @@ struct Turn {
 struct Units {
   Turn<kUnits> at;
   // the next block, or null: no more (or the CTA has aborted)
-  __device__ __forceinline__ const Unit* next(const AttendArgs& a, const Shared& s) {
+  __device__ __forceinline__ Unit* next(const AttendArgs& a, const Shared& s) {
     if (!wait_or_abort(&s.ufull[at.st], at.ph, a.status, s.abort_flag)) return nullptr;
-    const Unit* u = &s.unit[at.st];
+    Unit* u = &s.unit[at.st];
     return u->s < 0 ? nullptr : u;
   }
   __device__ __forceinline__ void done(const Shared& s, int lane) {
@@ -562,7 +551,7 @@ template <int D, bool kFp8>
 __device__ void multiply(const AttendArgs& a, const Shared& s, uint32_t tmem, int lane) {
   using L = Layout<D, kFp8>;
   const uint32_t ring = desc_lo(dec::smem_addr(s.base + L::kRingOff)), qd = desc_lo(dec::smem_addr(s.base));
-  constexpr uint32_t id_s = idesc(kTile, !kFp8, false), id_o = idesc(D, true, true);
+  constexpr uint32_t id_s = idesc(kTile, false), id_o = idesc(D, true);
   constexpr uint32_t kVLead = ((kTile * 128 - 16) >> 4) << 16;  // a V descriptor's leading offset, from a K one's
   constexpr int kSteps = kTile / 16;
   Turn<L::kStages> kt, vt;  // places of the next K and V
@@ -688,69 +677,42 @@ out:
 
 // ---------------------------------------------------------------- Q
 
-// Q of the sub-tiles [sub0, sub1) of every block, by TMA: a box of the group's
-// heads x 128 / G tokens is the K-major tile.  (Rows past the sequence's end
-// are the next one's, or zeros; rows past the box keep what they held.  Both
-// are never stored.)  Quantised cache: to fp16, each row scaled by a power of
-// two to [1, 2), in place; a thread takes a row.  A negative softmax scale goes
-// into Q's signs.
-template <int D, bool kFp8>
-__device__ void load_q(const AttendArgs& a, const Shared& s, const CUtensorMap* map, int sub0, int sub1, int lane) {
-  using L = Layout<D, kFp8>;
-  const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-  uint32_t n[2] = {0, 0};
+// Q of every block by TMA: a box of the group's heads x 128 / G tokens is the
+// K-major tile.  (Rows past the sequence's end are the next one's, or zeros;
+// rows past the box keep what they held.  Both are never stored.)  A negative
+// softmax scale goes into Q's signs.
+template <int D>
+__device__ void load_q(const AttendArgs& a, const Shared& s, const CUtensorMap* map, int lane) {
+  const bool flip = a.scale_log2 < 0.0f;  // then Q arrives on `landed` first
+  uint32_t ph[2] = {0, 0};
   Units units;
   while (const Unit* u = units.next(a, s)) {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
-      if (sub < sub0 || sub >= sub1 || !u->any(sub)) continue;
-      if (!wait_or_abort(&s.qempty[sub], (n[sub] & 1) ^ 1, a.status, s.abort_flag)) return;
-      ++n[sub];
+      if (!u->any(sub)) continue;
+      if (!wait_or_abort(&s.qempty[sub], ph[sub] ^ 1, a.status, s.abort_flag)) return;
       uint8_t* Q = s.base + sub * kSub * D * 2;
-      const bool rework = kFp8 || flip;  // then it arrives on `landed` first
-      uint64_t* bar = rework ? &s.landed[sub] : &s.qfull[sub];
+      uint64_t* bar = flip ? &s.landed[sub] : &s.qfull[sub];
       if (lane == 0) {
         dec::mbar_expect_tx(bar, a.tps * a.G * D * 2);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
           tma_box3(dec::smem_addr(Q + c * kSub * 128), map, c * 64, u->h * a.G, u->q0 + (u->rb * 2 + sub) * a.tps, bar);
       }
-      if (!rework) continue;
-      if (!wait_or_abort(bar, (n[sub] & 1) ^ 1, a.status, s.abort_flag)) return;
-      for (int r = lane; r < a.tps * a.G; r += 32) {
-        auto chunk = [&](int ch) {
-          return reinterpret_cast<uint4*>(Q + (ch >> 3) * (kSub * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-        };
-        float down = 1.0f;
-        if (kFp8) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int ch = 0; ch < D / 8; ++ch) {
-            const uint4 v = *chunk(ch);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max((u[j] << 16) & 0x7f800000u, u[j] & 0x7f800000u));
-          }
-          const int e = min(max((int)(top >> 23), 1), 253);  // infinities and NaN stay what they are
-          down = __uint_as_float((uint32_t)(254 - e) << 23);
-          reinterpret_cast<float*>(s.base + L::kRowOff)[sub * kSub + r] = __uint_as_float((uint32_t)e << 23);
-        }
+      if (flip) {
+        if (!wait_or_abort(bar, ph[sub], a.status, s.abort_flag)) return;
 #pragma unroll 4
-        for (int ch = 0; ch < D / 8; ++ch) {
-          uint4 v = *chunk(ch);
-          v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-          if (kFp8) {
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-            uint32_t* x = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = pack2(dec::bf16_lo(u[j]) * down, dec::bf16_hi(u[j]) * down, true);
-          }
-          *chunk(ch) = v;
+        for (int i = lane; i < kSub * D / 8; i += 32) {
+          uint4* at = reinterpret_cast<uint4*>(Q) + i;
+          uint4 v = *at;
+          v.x ^= 0x80008000u; v.y ^= 0x80008000u; v.z ^= 0x80008000u; v.w ^= 0x80008000u;
+          *at = v;
         }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) dec::mbar_arrive(&s.qfull[sub]);
       }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) dec::mbar_arrive(&s.qfull[sub]);
+      ph[sub] ^= 1;
     }
     units.done(s, lane);
   }
@@ -822,41 +784,29 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
-      "mov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
-// Probabilities of 64 of a row's scores, as bf16 pairs, and their sum.  vs: the
-// value scales (quantised cache); a scale may be NaN (nan_scale): then 0 * NaN
-// must not reach a row that does not see the token.
-template <bool kFp8>
-__device__ __forceinline__ float2 probabilities(const float* x, float c, float base, const float* vs, bool nan_scale,
-                                                uint32_t* p) {
+// Probabilities of 64 of a row's scores, as bf16 pairs, and their sum.
+__device__ __forceinline__ float2 probabilities(const float* x, float c, float base, uint32_t* p) {
   const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
   float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
   for (int k = 0; k < 64; k += 2) {
     const float2 y = fma2(make_float2(x[k], x[k + 1]), c2, b2);
-    float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+    const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
     if (k & 2) sum1 = add2(sum1, e);
     else sum0 = add2(sum0, e);
-    if (kFp8) {
-      const float2 v = *reinterpret_cast<const float2*>(vs + k);
-      if (nan_scale) {
-        e.x = x[k] == -INFINITY ? 0.0f : e.x * v.x;
-        e.y = x[k + 1] == -INFINITY ? 0.0f : e.y * v.y;
-      } else {
-        e = mul2(e, v);
-      }
-    }
-    p[k / 2] = pack2(e.x, e.y, false);
+    p[k / 2] = pack2(e.x, e.y);
   }
   return add2(sum0, sum1);
+}
+
+// Does any of tokens [from, to) have a value of NaN (quantised cache)?
+__device__ __noinline__ bool any_nan_value(const AttendArgs& a, int s, int h, int from, int to) {
+  for (int j = from; j < to; ++j) {
+    const int page = max(0, load_page(a.p, a.b, s, j / a.p.page_tokens, a.status));
+    if (a.p.v_scale[((long long)page * a.p.num_kv_heads + h) * a.p.page_tokens + j % a.p.page_tokens] == kNanScale)
+      return true;
+  }
+  return false;
 }
 
 template <int D, bool kFp8>
@@ -865,12 +815,10 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
   const int lane = tid & 31, quarter = (tid >> 5) & 3;
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
   const uint32_t ts = tmem + lanes + sub * 128, to = tmem + lanes + 256 + sub * 128;
-  const float* scales = reinterpret_cast<const float*>(s.base + L::kScaleOff);
-  const float c0 = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);  // never 0: 0 * -inf is not -inf
+  const float c = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);  // never 0: 0 * -inf is not -inf
   const int my_token = tid / a.G;
   uint8_t* stage = s.base + L::kOutOff + (sub * 4 + quarter) * 32 * L::kLine;
   uint32_t ns = 0, no = 0;
-  Turn<L::kScaleTurns> turn;
   int4 begun = make_int4(-1, 0, 0, 0);
   Units units;
   while (const Unit* u = units.next(a, s)) {
@@ -879,58 +827,49 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
     const bool any = u->any(sub);
     const Span v = visible(a, u->seq(), mine ? i_new : 0);
     const int lo = mine ? v.lo : 0, hi = mine ? v.hi : 0;
-    float m = -INFINITY, l = 0.0f, c = c0;
-    if (any && kFp8) {
-      if (!wait_or_abort(&s.qfull[sub], no, a.status, s.abort_flag)) return;
-      c = c0 * reinterpret_cast<const float*>(s.base + L::kRowOff)[sub * kSub + tid];
-    }
-    const int t_end = any ? u->f1[sub] : u->t0, all_lo = u->all_lo, all_hi = u->all_hi;
+    float m = -INFINITY, l = 0.0f;
+    const int t_end = any ? u->f1[sub] : 0, all_lo = u->all_lo, all_hi = u->all_hi;
     bool first = true;
-    int t = u->t0;
-    if (any)
-      for (; t < u->f0[sub]; ++t) turn.next();  // (every tile has its turn of scales)
-    for (; t < t_end; ++t) {
+    for (int t = u->f0[sub]; t < t_end; ++t) {
       const int j0 = t * kTile;
-      const float* sc = scales + turn.st * L::kScaleWords;
-      turn.next();
       if (!wait_or_abort(&s.sfull[sub], ns, a.status, s.abort_flag)) return;
       ns ^= 1;
       fence_after();
-      float x[128];
+      // Quantised cache: the registers are needed for the expanding warps, so a
+      // row's scores are read by halves, once for the maximum and once more.
+      constexpr int kHeld = kFp8 ? 64 : 128;
+      float x[kHeld];
+      auto load = [&](int col) {  // kHeld scores from column col, the unseen ones -inf
 #pragma unroll
-      for (int k = 0; k < 4; ++k) ld32(ts + 32 * k, x + 32 * k);
-      ld_wait();
-      bool nan_scale = false;
-      if (kFp8) {
-        const int4 f = *reinterpret_cast<const int4*>(sc + 2 * kTile);
-        nan_scale = (f.x | f.y | f.z | f.w) != 0;
+        for (int k = 0; k < kHeld; k += 32) ld32(ts + col + k, x + k);
+        ld_wait();
+        if (j0 + kTile > all_hi) {  // some row does not see the last of the tile
+          const int end = hi - j0 - col;
 #pragma unroll
-        for (int k = 0; k < 128; k += 2) {
-          const float2 y = mul2(make_float2(x[k], x[k + 1]), *reinterpret_cast<const float2*>(sc + k));
-          x[k] = y.x;
-          x[k + 1] = y.y;
+          for (int k = 0; k < kHeld; ++k)
+            if (k >= end) x[k] = -INFINITY;
         }
+        if (j0 < all_lo) {  // or the first
+          const int from = lo - j0 - col;
+#pragma unroll
+          for (int k = 0; k < kHeld; ++k)
+            if (k < from) x[k] = -INFINITY;
+        }
+      };
+      float top = -INFINITY;
+#pragma unroll
+      for (int col = 128 - kHeld; col >= 0; col -= kHeld) {
+        load(col);
+        float top4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top4[k] = fmaxf(x[k], x[k + 4]);
+#pragma unroll
+        for (int k = 8; k < kHeld; k += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top4[i] = max3(top4[i], x[k + i], x[k + 4 + i]);
+        top = max3(top, max3(top4[0], top4[1], top4[2]), top4[3]);
       }
-      if (j0 + kTile > all_hi) {  // some row does not see the last of it
-        const int end = hi - j0;
-#pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (k >= end) x[k] = -INFINITY;
-      }
-      if (j0 < all_lo) {  // or the first
-        const int from = lo - j0;
-#pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (k < from) x[k] = -INFINITY;
-      }
-      float top4[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) top4[k] = fmaxf(x[k], x[k + 4]);
-#pragma unroll
-      for (int k = 8; k < 128; k += 8)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top4[i] = max3(top4[i], x[k + i], x[k + 4 + i]);
-      const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * c;
+      top *= c;
       if (first) {
         m = top;
         first = false;
@@ -949,13 +888,14 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
       }
       const float base = m == -INFINITY ? 0.0f : m;
       uint32_t p[32];
-      float2 sum = probabilities<kFp8>(x, c, base, sc + kTile, nan_scale, p);
+      float2 sum = probabilities(x, c, base, p);
       st32(ts, p);
       st_wait();
       fence_before();
       __syncwarp();
       if (lane == 0) dec::mbar_arrive(&s.pfull[sub]);
-      const float2 more = probabilities<kFp8>(x + 64, c, base, sc + kTile + 64, nan_scale, p);
+      if (kFp8) load(64);
+      const float2 more = probabilities(x + kHeld - 64, c, base, p);
       st32(ts + 32, p);
       st_wait();
       fence_before();
@@ -964,7 +904,6 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
       sum = add2(sum, more);
       l += sum.x + sum.y;
     }
-    for (; t < u->t1; ++t) turn.next();
     // ------------------------------------------------------------ the block's end
     const bool whole = u->begins && u->ends;
     const int my_head = tid - my_token * a.G;
@@ -986,6 +925,10 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
       no ^= 1;
       fence_after();
     }
+    bool poisoned = false;
+    if (kFp8 && any && *const_cast<const volatile int*>(&u->nan_v) && mine &&
+        any_nan_value(a, u->s, u->h, max(lo, u->t0 * kTile), min(hi, u->t1 * kTile)))
+      poisoned = true;
     const int bad0 = any && !kFp8 ? s.poison[sub * 2] : 1, bad1 = any && !kFp8 ? s.poison[sub * 2 + 1] : 0;
     for (int k = 0; k < D; k += 32) {
       float o[32];
@@ -1002,6 +945,10 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] += add[i];
       }
+      if (kFp8 && poisoned) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(0x7fc00000u);
+      }
       // rows through shared memory, so that neighbouring lanes store neighbouring bytes
       constexpr int kChunks = L::kLine / 16;
       if (whole) {
@@ -1010,10 +957,10 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           stage_put<kChunks>(stage, lane, run * 4 + i,
-                             make_uint4(pack2(o[8 * i] * inv, o[8 * i + 1] * inv, false),
-                                        pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv, false),
-                                        pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv, false),
-                                        pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv, false)));
+                             make_uint4(pack2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                        pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                        pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                        pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv)));
         if (run == kHalf - 1)
           stage_out<kChunks>(stage, lane, at, reinterpret_cast<uint8_t*>(a.out), 2, k & ~(kHalf * 32 - 1));
       } else {
@@ -1034,69 +981,84 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
   if (sub == 0 && tid == 0) a.desc[blockIdx.x] = begun;
 }
 
-// ---------------------------------------------------------------- e4m3 codes to 16-bit tiles
+// ---------------------------------------------------------------- e4m3 codes to bf16 tiles
 
+// Tokens that no row sees become zeros: they may hold anything.  So do the
+// values of a token whose scale is NaN, lest 0 * NaN reach a row that does not
+// see it; the block's end makes the rows that do NaN.  (A key of NaN may stay:
+// its scores are hidden, not multiplied.)
 template <int D>
 __device__ void expand(const AttendArgs& a, const Shared& s, int tid) {
   using L = Layout<D, true>;
   const int lane = tid & 31;
   Turn<L::kRaw> rt;
   Turn<L::kStages> st;
-  Turn<L::kScaleTurns> turn;
+  // A warp takes eight rows at a time, 64 codes of each (half a row of 128): a
+  // lane 16 codes, four lanes a row.  The lanes of a quarter-warp are at rows r
+  // and r ^ 5, whose chunks the swizzles put into different banks, where they
+  // are read and where the two bf16 chunks are written.
+  constexpr int kHalves = D / 64, kGroups = kCvtWarps / kHalves, kN = kTile / 8 / kGroups;
+  const int half = (tid >> 5) % kHalves, ch = half * 4 + (lane & 3);
+  const int r0 = (tid >> 5) / kHalves * 8 + ((lane >> 3) ^ (lane & 4 ? 5 : 0));  // then every kGroups * 8 rows
+  constexpr int kRows = kGroups * 8;
   Units units;
-  while (const Unit* u = units.next(a, s)) {
+  while (Unit* u = units.next(a, s)) {
     const int lo = u->lo, hi = u->hi, t1 = u->t1;
+    // the scale bytes of tokens 4 lane .. + 3 of tile t (a page's tokens come in sixteens)
+    auto scales = [&](int t, uint32_t* e) {
+      const int j = t * kTile + 4 * lane;
+      e[0] = e[1] = 0;
+      if (t >= t1 || j + 3 < lo || j >= hi) return;
+      const int page = max(0, load_page(a.p, a.b, u->s, j / a.p.page_tokens, a.status));
+      const long long at = ((long long)page * a.p.num_kv_heads + u->h) * a.p.page_tokens + j % a.p.page_tokens;
+      e[0] = __ldg(reinterpret_cast<const uint32_t*>(a.p.k_scale + at));
+      e[1] = __ldg(reinterpret_cast<const uint32_t*>(a.p.v_scale + at));
+    };
+    uint32_t e[2];
+    scales(u->t0, e);
     for (int t = u->t0; t < t1; ++t) {
-      // this thread's token's scales, on their way while K is expanded
-      uint32_t ek = 0, ev = 0;
-      const int j = t * kTile + tid;
-      if (j >= lo && j < hi) {
-        const int page = max(0, load_page(a.p, a.b, u->s, j / a.p.page_tokens, a.status));
-        const long long at = ((long long)page * a.p.num_kv_heads + u->h) * a.p.page_tokens + j % a.p.page_tokens;
-        ek = __ldg(a.p.k_scale + at);
-        ev = __ldg(a.p.v_scale + at);
-      }
+      const int seen0 = lo - t * kTile, seen1 = hi - t * kTile;
+      const bool edge = seen0 > 0 || seen1 < kTile;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         if (!wait_or_abort(&s.rfull[rt.st], rt.ph, a.status, s.abort_flag)) return;
-        if (!wait_or_abort(&s.empty[st.st], st.ph ^ 1, a.status, s.abort_flag)) return;
         const uint8_t* src = s.base + L::kRawOff + rt.st * L::kRawBytes;
-        uint8_t* dst = s.base + L::kRingOff + st.st * L::kTileBytes;
-        constexpr int kPer = D / 16;  // 16-byte chunks of a raw row
-        const int seen0 = lo - t * kTile, seen1 = hi - t * kTile;
-#pragma unroll 4
-        for (int i = tid; i < kTile * kPer; i += kCvtWarps * 32) {
-          const int r = i / kPer, ch = i % kPer;
-          const int phys = D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
-          uint4 c = *reinterpret_cast<const uint4*>(src + r * D + (phys << 4));
-          if (r < seen0 || r >= seen1) c = make_uint4(0, 0, 0, 0);  // tokens that no row sees may hold anything
-          const uint32_t q[4] = {c.x, c.y, c.z, c.w};
+        uint4 c[kN];
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          const int r = r0 + k * kRows, phys = D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
+          c[k] = *reinterpret_cast<const uint4*>(src + r * D + (phys << 4));
+        }
+        const uint32_t mine = e[kv];
+        if (kv == 1) scales(t + 1, e);  // on their way while V is expanded
+        if (!wait_or_abort(&s.empty[st.st], st.ph ^ 1, a.status, s.abort_flag)) return;
+        uint8_t* dst = s.base + L::kRingOff + st.st * L::kTileBytes + (ch >> 2) * (kTile * 128);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          const int r = r0 + k * kRows;
+          const uint32_t b = __shfl_sync(0xffffffffu, mine, r >> 2) >> ((r & 3) * 8) & 0xffu;
+          bool drop = edge && (r < seen0 || r >= seen1);
+          if (kv == 1 && b == kNanScale && !drop) {
+            drop = true;
+            *reinterpret_cast<volatile int*>(&u->nan_v) = 1;
+          }
+          if (drop) c[k] = make_uint4(0, 0, 0, 0);
+          // 2^(b - 127) as bf16 (byte 0 or 255, unseen or dropped: times codes 0)
+          const uint32_t sc = b == kNanScale ? (kv ? 0u : 0x7fc07fc0u) : drop ? 0u : b << 7 | b << 23;
+          const __nv_bfloat162 sc2 = *reinterpret_cast<const __nv_bfloat162*>(&sc);
+          const uint32_t q[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
           uint32_t o[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q[k] & 0xffffu), __NV_E4M3);
-            const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q[k] >> 16), __NV_E4M3);
-            if (kv == 0) {
-              o[2 * k] = (uint32_t)x.x | (uint32_t)x.y << 16;
-              o[2 * k + 1] = (uint32_t)y.x | (uint32_t)y.y << 16;
-            } else {
-              const float2 fx = __half22float2(__half2(x)), fy = __half22float2(__half2(y));
-              o[2 * k] = pack2(fx.x, fx.y, false);
-              o[2 * k + 1] = pack2(fy.x, fy.y, false);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t pair = i & 1 ? q[i >> 1] >> 16 : q[i >> 1] & 0xffffu;
+            const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3)));
+            const __nv_bfloat162 v = __hmul2(__floats2bfloat162_rn(f.x, f.y), sc2);  // exact
+            o[i] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          uint8_t* row = dst + (ch >> 2) * (kTile * 128) + r * 128;
+          uint8_t* row = dst + r * 128;
           const int d0 = (ch & 3) * 2;
           *reinterpret_cast<uint4*>(row + ((d0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4*>(row + (((d0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-        if (kv == 0) {
-          float* sc = reinterpret_cast<float*>(s.base + L::kScaleOff) + turn.st * L::kScaleWords;
-          sc[tid] = scale_of(ek);
-          sc[kTile + tid] = scale_of(ev);
-          const bool nan = __any_sync(0xffffffffu, ev == kNanScale);
-          if (lane == 0) reinterpret_cast<int*>(sc)[2 * kTile + (tid >> 5)] = nan;
-          turn.next();
         }
         fence_async();
         __syncwarp();
@@ -1131,7 +1093,7 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
     }
     for (int i = 0; i < kUnits; ++i) {
       dec::mbar_init(&s.ufull[i], 1);
-      dec::mbar_init(&s.uempty[i], 8 + 1 + 2 + (kFp8 ? kCvtWarps : 0));  // softmax, MMA, warps 10 and 11, expanding
+      dec::mbar_init(&s.uempty[i], 8 + 2 + (kFp8 ? kCvtWarps : 1));  // softmax, MMA, Q, expanding or mending
     }
     for (int i = 0; i < 2; ++i) {
       dec::mbar_init(&s.qfull[i], 1);
@@ -1186,8 +1148,7 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8 ? kFpRest : kBfRest));
     if (warp == 8) produce<D, kFp8>(a, rg, s, &map_k, &map_v, lane);
     if (warp == 9) multiply<D, kFp8>(a, s, tmem, lane);
-    if (kFp8 && warp >= 10) load_q<D, kFp8>(a, s, &map_q, warp - 10, warp - 9, lane);
-    if (!kFp8 && warp == 10) load_q<D, kFp8>(a, s, &map_q, 0, 2, lane);
+    if (warp == 10) load_q<D>(a, s, &map_q, lane);
     if (!kFp8 && warp == 11) mend<D>(a, s, lane);
   } else if (kFp8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFpCvt));
