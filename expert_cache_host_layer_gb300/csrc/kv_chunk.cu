@@ -54,7 +54,7 @@ constexpr float kGrow = 8.0f;                 // log2 of the growth that O's sca
 constexpr int kBfThreads = 384, kFpThreads = 640;
 // Registers of the warpgroups (softmax, producer and MMA, converters): within
 // what the block is launched with, 384 x 168 and 640 x 96.
-constexpr int kBfSoft = 216, kBfRest = 72, kFpSoft = 160, kFpRest = 48, kFpCvt = 56;
+constexpr int kBfSoft = 200, kBfRest = 104, kFpSoft = 136, kFpRest = 80, kFpCvt = 64;
 static_assert(256 * kBfSoft + 128 * kBfRest <= kBfThreads * 168, "registers");
 static_assert(256 * (kFpSoft + kFpCvt) + 128 * kFpRest <= kFpThreads * 96, "registers");
 constexpr int kCvtWarps = 8;
@@ -784,12 +784,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-// Probabilities of 64 of a row's scores, as bf16 pairs, and their sum.
+// Probabilities of kN of a row's scores, as bf16 pairs, and their sum.
+template <int kN>
 __device__ __forceinline__ float2 probabilities(const float* x, float c, float base, uint32_t* p) {
   const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
   float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
-  for (int k = 0; k < 64; k += 2) {
+  for (int k = 0; k < kN; k += 2) {
     const float2 y = fma2(make_float2(x[k], x[k + 1]), c2, b2);
     const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
     if (k & 2) sum1 = add2(sum1, e);
@@ -835,9 +836,11 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
       if (!wait_or_abort(&s.sfull[sub], ns, a.status, s.abort_flag)) return;
       ns ^= 1;
       fence_after();
-      // Quantised cache: the registers are needed for the expanding warps, so a
-      // row's scores are read by halves, once for the maximum and once more.
-      constexpr int kHeld = kFp8 ? 64 : 128;
+      // A row's scores come by kHeld, once for the maximum and once more for P:
+      // short loops, which with the other warps' fit the instruction cache
+      // (unrolled over the row, the quantised cache's kernel took 1.35 times as
+      // long, its warps waiting for instructions).
+      constexpr int kHeld = 64;
       float x[kHeld];
       auto load = [&](int col) {  // kHeld scores from column col, the unseen ones -inf
 #pragma unroll
@@ -857,8 +860,8 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
         }
       };
       float top = -INFINITY;
-#pragma unroll
-      for (int col = 128 - kHeld; col >= 0; col -= kHeld) {
+#pragma unroll 1
+      for (int col = 0; col < 128; col += kHeld) {
         load(col);
         float top4[4];
 #pragma unroll
@@ -887,21 +890,20 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
         }
       }
       const float base = m == -INFINITY ? 0.0f : m;
-      uint32_t p[32];
-      float2 sum = probabilities(x, c, base, p);
-      st32(ts, p);
-      st_wait();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) dec::mbar_arrive(&s.pfull[sub]);
-      if (kFp8) load(64);
-      const float2 more = probabilities(x + kHeld - 64, c, base, p);
-      st32(ts + 32, p);
-      st_wait();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) dec::mbar_arrive(&s.pfull2[sub]);
-      sum = add2(sum, more);
+      float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+      for (int col = 0; col < 128; col += kHeld) {
+        uint32_t p[kHeld / 2];
+        load(col);
+        sum = add2(sum, probabilities<kHeld>(x, c, base, p));
+        st32(ts + col / 2, p);
+        if ((col + kHeld) % 64 == 0) {  // half of P
+          st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) dec::mbar_arrive(col >= 64 ? &s.pfull2[sub] : &s.pfull[sub]);
+        }
+      }
       l += sum.x + sum.y;
     }
     // ------------------------------------------------------------ the block's end
@@ -997,7 +999,7 @@ __device__ void expand(const AttendArgs& a, const Shared& s, int tid) {
   // lane 16 codes, four lanes a row.  The lanes of a quarter-warp are at rows r
   // and r ^ 5, whose chunks the swizzles put into different banks, where they
   // are read and where the two bf16 chunks are written.
-  constexpr int kHalves = D / 64, kGroups = kCvtWarps / kHalves, kN = kTile / 8 / kGroups;
+  constexpr int kHalves = D / 64, kGroups = kCvtWarps / kHalves;
   const int half = (tid >> 5) % kHalves, ch = half * 4 + (lane & 3);
   const int r0 = (tid >> 5) / kHalves * 8 + ((lane >> 3) ^ (lane & 4 ? 5 : 0));  // then every kGroups * 8 rows
   constexpr int kRows = kGroups * 8;
@@ -1019,34 +1021,29 @@ __device__ void expand(const AttendArgs& a, const Shared& s, int tid) {
     for (int t = u->t0; t < t1; ++t) {
       const int seen0 = lo - t * kTile, seen1 = hi - t * kTile;
       const bool edge = seen0 > 0 || seen1 < kTile;
-#pragma unroll
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         if (!wait_or_abort(&s.rfull[rt.st], rt.ph, a.status, s.abort_flag)) return;
         const uint8_t* src = s.base + L::kRawOff + rt.st * L::kRawBytes;
-        uint4 c[kN];
-#pragma unroll
-        for (int k = 0; k < kN; ++k) {
-          const int r = r0 + k * kRows, phys = D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
-          c[k] = *reinterpret_cast<const uint4*>(src + r * D + (phys << 4));
-        }
-        const uint32_t mine = e[kv];
+        const uint32_t mine = kv ? e[1] : e[0];
         if (kv == 1) scales(t + 1, e);  // on their way while V is expanded
         if (!wait_or_abort(&s.empty[st.st], st.ph ^ 1, a.status, s.abort_flag)) return;
         uint8_t* dst = s.base + L::kRingOff + st.st * L::kTileBytes + (ch >> 2) * (kTile * 128);
-#pragma unroll
-        for (int k = 0; k < kN; ++k) {
-          const int r = r0 + k * kRows;
+#pragma unroll 1
+        for (int r = r0; r < kTile; r += kRows) {
+          const int phys = D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
+          uint4 c = *reinterpret_cast<const uint4*>(src + r * D + (phys << 4));
           const uint32_t b = __shfl_sync(0xffffffffu, mine, r >> 2) >> ((r & 3) * 8) & 0xffu;
           bool drop = edge && (r < seen0 || r >= seen1);
           if (kv == 1 && b == kNanScale && !drop) {
             drop = true;
             *reinterpret_cast<volatile int*>(&u->nan_v) = 1;
           }
-          if (drop) c[k] = make_uint4(0, 0, 0, 0);
+          if (drop) c = make_uint4(0, 0, 0, 0);
           // 2^(b - 127) as bf16 (byte 0 or 255, unseen or dropped: times codes 0)
           const uint32_t sc = b == kNanScale ? (kv ? 0u : 0x7fc07fc0u) : drop ? 0u : b << 7 | b << 23;
           const __nv_bfloat162 sc2 = *reinterpret_cast<const __nv_bfloat162*>(&sc);
-          const uint32_t q[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+          const uint32_t q[4] = {c.x, c.y, c.z, c.w};
           uint32_t o[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
