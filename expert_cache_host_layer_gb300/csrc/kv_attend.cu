@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
   if (lane == 0) write_lse(a, q, u.y, i_new, g, m, l);
 }
 
+}  // namespace
+
 int sm_count() {
   static std::atomic<int> known[64];
   int dev = 0, n = 0;
@@ -88,8 +90,6 @@ int sm_count() {
   if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) known[dev].store(n);
   return n;
 }
-
-}  // namespace
 
 cudaError_t launch_combine(const AttendArgs& a, bool chunk, int used, cudaStream_t s) {
   const bool one = used <= 64;  // rows enough for a block each without many idle blocks

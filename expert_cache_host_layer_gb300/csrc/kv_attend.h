@@ -212,6 +212,7 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.
 
 // ---------------------------------------------------------------- host
 
+int sm_count();  // of the current device
 cudaError_t launch_attend_token(const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_attend_chunk(const AttendArgs& a, cudaStream_t s);
 // Joins the partial sums of the (sequence, head, row block)s that a cut

@@ -4,7 +4,7 @@
 #include <mutex>
 
 #include "driver_api.h"
-#include "kv_common.h"
+#include "kv_attend.h"
 
 namespace ft {
 namespace kv {
@@ -80,140 +80,189 @@ ft_status check_rows(const char* name, const void* ptr, int64_t token_stride, in
 
 namespace {
 
-// ---------------------------------------------------------------- append
+// Both directions move vectors (a token's key or value of one head) between a
+// token-major tensor and the pages; they are bound by HBM.  A block takes
+// `per` consecutive tokens.  Its first threads look their places up (sequence,
+// position, page: a chain of dependent loads that costs more than moving a
+// vector, so it is done once per token and not once per vector), and leave the
+// rows in shared memory.  Then a group of D / 8 lanes takes a vector at a time,
+// kBatch vectors in flight; append has its first batch on the way while the
+// places are looked up.
+constexpr int kMoveThreads = 256;
+constexpr int kMostTokens = 32;  // of a block
+constexpr int kBatch = 2;
 
-struct AppendArgs {
+struct MoveArgs {
   ft_kv_pages p;
   ft_kv_batch b;
-  const __nv_bfloat16* x[2];  // k, v
+  const int32_t* start;             // read: [num_seqs + 1]
+  int rows, per;                    // tokens in all, and of a block
+  uint32_t by_h;                    // floor(2^32 / H) + 1, 0 for H = 1: v / H = (v * by_h) >> 32 for v < 2^17, H <= 2^10
+  const __nv_bfloat16* x[2];        // append: k, v
   int64_t ts[2], hs[2];
+  __nv_bfloat16* out[2];            // read
   int32_t* status;
 };
 
-// Scale exponent of a vector: the smallest k >= -110 with amax <= 448 * 2^k.
-// amax = (1 + f) 2^E and 448 = 1.75 * 2^8, so k = E - 8, one more if 1 + f > 1.75.
+// Page row of token `t` at head 0 (head h: + h * page_tokens), or -1.
+template <bool kAppend>
+__device__ __forceinline__ int place_of(const MoveArgs& a, int t) {
+  const int s = find_seq(kAppend ? a.b.q_start : a.start, a.b.num_seqs, t);
+  int pos;
+  if (kAppend) {
+    const Seq q = load_seq(a.p, a.b, s, a.status);
+    pos = q.n - q.m + (t - q.q0);
+    if (t - q.q0 >= q.m || pos < 0) return -1;
+  } else {
+    const int n = __ldg(&a.b.kv_len[s]);
+    pos = t - __ldg(&a.start[s]);
+    if (n > a.b.table_stride * a.p.page_tokens) {
+      raise(a.status, FT_ERR_INVALID_ARG);
+      return -1;
+    }
+    if (pos < 0 || pos >= n) return -1;
+  }
+  const int page = load_page(a.p, a.b, s, pos / a.p.page_tokens, a.status);
+  if (page < 0) return -1;
+  return page * a.p.num_kv_heads * a.p.page_tokens + pos % a.p.page_tokens;  // rows are below 2^31
+}
+
+// Scale exponent of a vector: the smallest k >= -110 with amax <= 448 * 2^k,
+// 121 if amax is not finite.  amax = (1 + f) 2^E and 448 = 1.75 * 2^8, so k = E - 8,
+// one more if 1 + f > 1.75.
 __device__ __forceinline__ int scale_exp(float amax) {
   const uint32_t u = __float_as_uint(amax);
+  if (u >= 0x7f800000u) return 121;
   const int k = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u);
   return max(k, kMinScaleExp);
 }
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
-
-// One group of D / 8 lanes per vector (token, k or v, head): a 16-byte load per
-// lane, the largest magnitude by shuffles within the group, an 8-byte (fp8) or
-// 16-byte (bf16) store.
-template <int D, bool kFp8>
-__global__ void append_kernel(AppendArgs a) {
-  constexpr int kLanes = D / 8;
-  const int H = a.p.num_kv_heads;
-  const long long g = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / kLanes;
-  const int sub = threadIdx.x % kLanes;
-  if (g >= 2LL * a.b.num_tokens * H) return;  // whole groups leave together
-  const int h = (int)(g % H);
-  const long long r = g / H;
-  const int which = (int)(r & 1), t = (int)(r >> 1);
-  const int s = find_seq(a.b.q_start, a.b.num_seqs, t);
-  const Seq q = load_seq(a.p, a.b, s, a.status);
-  const int pos = q.n - q.m + (t - q.q0);
-  if (t - q.q0 >= q.m || pos < 0) return;
-  const int page = load_page(a.p, a.b, s, pos / a.p.page_tokens, a.status);
-  if (page < 0) return;
-  const uint4 raw = __ldg(reinterpret_cast<const uint4*>(a.x[which] + t * a.ts[which] + h * a.hs[which]) + sub);
-  const long long row = ((long long)page * H + h) * a.p.page_tokens + pos % a.p.page_tokens;
-  if (!kFp8) {
-    reinterpret_cast<uint4*>(static_cast<uint8_t*>(which ? a.p.v : a.p.k) + row * (2 * D))[sub] = raw;
-    return;
-  }
+// Eight values of a vector, a lane of its group of kLanes: codes and exponent byte.
+template <int kLanes>
+__device__ __forceinline__ uint2 quantise(uint4 raw, uint32_t* e) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  // largest magnitude, as bits: bf16 magnitudes order like integers, NaN above infinity
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top = max(top & 0xffff0000u, top << 16);
+  const int k = scale_exp(__uint_as_float(top));
+  const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
   float x[8];
-  uint32_t top = 0;  // largest magnitude, as bits: bf16 magnitudes order like integers, NaN above infinity
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    top = max(top, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+    x[2 * i] = __uint_as_float(w[i] << 16) * inv;
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * inv;
   }
-  const uint32_t mask = (kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes));
+  if (k >= 120) {  // 256 * 2^120 would not be a bf16 value; k = 121: not finite
 #pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
-  uint2 codes = make_uint2(0u, 0u);
-  uint32_t e = kNanScale;
-  if (top < 0x7f800000u) {
-    const int k = scale_exp(__uint_as_float(top));
-    e = (uint32_t)(k + 127);
-    const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
-    const float lim = k == 120 ? 240.0f : 448.0f;  // 256 * 2^120 would not be a bf16 value
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = pack_e4m3(fminf(fmaxf(x[2 * i] * inv, -lim), lim), fminf(fmaxf(x[2 * i + 1] * inv, -lim), lim));
-    codes = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    for (int i = 0; i < 8; ++i) x[i] = k > 120 ? 0.0f : fminf(fmaxf(x[i], -240.0f), 240.0f);
   }
-  reinterpret_cast<uint2*>(static_cast<uint8_t*>(which ? a.p.v : a.p.k) + row * D)[sub] = codes;
-  if (sub == 0) (which ? a.p.v_scale : a.p.k_scale)[row] = (uint8_t)e;
+  *e = k > 120 ? (uint32_t)kNanScale : (uint32_t)(k + 127);
+  return make_uint2(pack_e4m3(x[0], x[1]) | pack_e4m3(x[2], x[3]) << 16,
+                    pack_e4m3(x[4], x[5]) | pack_e4m3(x[6], x[7]) << 16);
+}
+// Eight codes times their scale: exact, 4 significant bits.
+__device__ __forceinline__ uint4 dequantise(uint2 c, float scale) {
+  const uint32_t w[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[i], __NV_E4M3)));
+    const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * scale, f.y * scale);
+    v[i] = *reinterpret_cast<const uint32_t*>(&b2);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// ---------------------------------------------------------------- read
-
-struct ReadArgs {
-  ft_kv_pages p;
-  ft_kv_batch b;
-  const int32_t* start;
-  long long rows;
-  __nv_bfloat16* out[2];
-  int32_t* status;
-};
-
-template <int D, bool kFp8>
-__global__ void read_kernel(ReadArgs a) {
-  constexpr int kLanes = D / 8;
-  const int H = a.p.num_kv_heads;
-  const long long g = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / kLanes;
+template <int D, bool kFp8, bool kAppend>
+__global__ void __launch_bounds__(kMoveThreads, 8) move_kernel(const __grid_constant__ MoveArgs a) {
+  constexpr int kLanes = D / 8, kGroups = kMoveThreads / kLanes;
+  __shared__ int s_row[kMostTokens];
+  const int H = a.p.num_kv_heads, P = a.p.page_tokens, which = blockIdx.y;  // k or v
+  const int t0 = blockIdx.x * a.per, tokens = min(a.per, a.rows - t0), vectors = tokens * H;
   const int sub = threadIdx.x % kLanes;
-  if (g >= 2 * a.rows * H) return;
-  const int h = (int)(g % H);
-  const long long r2 = g / H;
-  const int which = (int)(r2 & 1);
-  const long long r = r2 >> 1;
-  const int s = find_seq(a.start, a.b.num_seqs, (int)r);
-  const int pos = (int)r - __ldg(&a.start[s]);
-  const int n = __ldg(&a.b.kv_len[s]);
-  uint4 o = make_uint4(0u, 0u, 0u, 0u);
-  const bool over = n > a.b.table_stride * a.p.page_tokens;
-  if (over) raise(a.status, FT_ERR_INVALID_ARG);
-  int page = -1;
-  if (!over && pos >= 0 && pos < n) page = load_page(a.p, a.b, s, pos / a.p.page_tokens, a.status);
-  if (page >= 0) {
-    const long long row = ((long long)page * H + h) * a.p.page_tokens + pos % a.p.page_tokens;
-    const uint8_t* src = static_cast<const uint8_t*>(which ? a.p.v : a.p.k);
-    if (!kFp8) {
-      o = __ldg(reinterpret_cast<const uint4*>(src + row * (2 * D)) + sub);
-    } else {
-      const uint2 c = __ldg(reinterpret_cast<const uint2*>(src + row * D) + sub);
-      const float sc = scale_of(__ldg((which ? a.p.v_scale : a.p.k_scale) + row));
-      const uint32_t w[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
-      uint32_t v[4];
+  uint8_t* pages = static_cast<uint8_t*>(which ? a.p.v : a.p.k);
+  uint8_t* scales = which ? a.p.v_scale : a.p.k_scale;
+  const int64_t ts = kAppend ? a.ts[which] : (int64_t)H * D, hs = kAppend ? a.hs[which] : D;  // of the token-major side
+  uint4* dense = reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(kAppend ? a.x[which] : a.out[which]) + t0 * ts) + sub;
+  // vector v of the block: token v / H, head v % H
+  auto token_of = [&](int v) { return a.by_h ? (int)__umulhi((uint32_t)v, a.by_h) : v; };
+  auto dense_at = [&](int v) {
+    const int t = token_of(v);
+    return dense + (t * ts + (v - t * H) * hs) / 8;
+  };
+  uint4 x[kBatch];
+  dec::pdl_wait_primary();
+  int v0 = threadIdx.x / kLanes;
+  if (kAppend) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[i], __NV_E4M3);
-        const float2 f = __half22float2(__half2(hr));
-        const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * sc, f.y * sc);  // exact: 4 significant bits
-        v[i] = *reinterpret_cast<const uint32_t*>(&b2);
+    for (int i = 0; i < kBatch; ++i)
+      x[i] = v0 + i * kGroups < vectors ? __ldg(dense_at(v0 + i * kGroups)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (threadIdx.x < tokens) s_row[threadIdx.x] = place_of<kAppend>(a, t0 + threadIdx.x);
+  __syncthreads();
+  for (; v0 - threadIdx.x / kLanes < vectors; v0 += kBatch * kGroups) {  // whole warps together
+    int row[kBatch];
+    uint2 c[kBatch];
+    float sc[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int v = v0 + i * kGroups, t = token_of(v);
+      row[i] = v < vectors ? s_row[t] : -1;
+      if (row[i] < 0) continue;
+      row[i] += (v - t * H) * P;
+      if (kAppend) continue;
+      if (kFp8) {
+        c[i] = __ldg(reinterpret_cast<const uint2*>(pages + (long long)row[i] * D) + sub);
+        sc[i] = scale_of(__ldg(scales + row[i]));
+      } else {
+        x[i] = __ldg(reinterpret_cast<const uint4*>(pages + (long long)row[i] * (2 * D)) + sub);
       }
-      o = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int v = v0 + i * kGroups;
+      if (kAppend) {
+        if (kFp8) {
+          uint32_t e;
+          const uint2 codes = quantise<kLanes>(x[i], &e);
+          if (row[i] >= 0) {
+            reinterpret_cast<uint2*>(pages + (long long)row[i] * D)[sub] = codes;
+            if (sub == 0) scales[row[i]] = (uint8_t)e;
+          }
+        } else if (row[i] >= 0) {
+          reinterpret_cast<uint4*>(pages + (long long)row[i] * (2 * D))[sub] = x[i];
+        }
+        if (v + kBatch * kGroups < vectors) x[i] = __ldg(dense_at(v + kBatch * kGroups));
+      } else if (v < vectors) {
+        *dense_at(v) = row[i] < 0 ? make_uint4(0u, 0u, 0u, 0u) : kFp8 ? dequantise(c[i], sc[i]) : x[i];
+      }
     }
   }
-  reinterpret_cast<uint4*>(a.out[which] + (r * H + h) * D)[sub] = o;
+  dec::pdl_launch_dependents();
 }
 
-template <typename Args>
-cudaError_t launch_groups(void (*kernel)(Args), const Args& a, long long groups, int lanes, cudaStream_t s) {
-  const long long blocks = (groups * lanes + 255) / 256;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  kernel<<<(unsigned)blocks, 256, 0, s>>>(a);
-  return cudaGetLastError();
+template <bool kAppend>
+ft_status launch_move(MoveArgs& a, const char* name, cudaStream_t s) {
+  const ft_status st = status_word(&a.status);
+  if (st != FT_OK) return st;
+  // one wave of eight blocks an SM, while that leaves a block no more than kMostTokens
+  const int blocks = 4 * sm_count();  // for k, and as many for v
+  a.per = (int)(((long long)a.rows + blocks - 1) / blocks);
+  a.per = a.per > kMostTokens ? kMostTokens : a.per;
+  a.by_h = a.p.num_kv_heads == 1 ? 0 : (uint32_t)((1ull << 32) / a.p.num_kv_heads) + 1;
+  const dim3 grid((unsigned)(((long long)a.rows + a.per - 1) / a.per), 2);
+  const bool fp8 = a.p.kv_dtype == FT_KV_FP8E4M3;
+  auto* kernel = a.p.head_dim == 128 ? (fp8 ? move_kernel<128, true, kAppend> : move_kernel<128, false, kAppend>)
+                                     : (fp8 ? move_kernel<64, true, kAppend> : move_kernel<64, false, kAppend>);
+  const cudaError_t e = launch_dependent(kernel, grid, kMoveThreads, 0, s, a);
+  if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(e));
+  return FT_OK;
 }
 
 }  // namespace
@@ -231,20 +280,12 @@ extern "C" ft_status ft_kv_append(const ft_kv_pages* pages, const ft_kv_batch* b
   if (st != FT_OK || batch->num_tokens == 0) return st;
   if ((st = check_rows("k", k, k_token_stride, k_head_stride)) != FT_OK) return st;
   if ((st = check_rows("v", v, v_token_stride, v_head_stride)) != FT_OK) return st;
-  AppendArgs a{};
-  a.p = *pages; a.b = *batch;
+  MoveArgs a{};
+  a.p = *pages; a.b = *batch; a.rows = batch->num_tokens;
   a.x[0] = static_cast<const __nv_bfloat16*>(k); a.x[1] = static_cast<const __nv_bfloat16*>(v);
   a.ts[0] = k_token_stride; a.ts[1] = v_token_stride;
   a.hs[0] = k_head_stride; a.hs[1] = v_head_stride;
-  if ((st = status_word(&a.status)) != FT_OK) return st;
-  const long long groups = 2LL * batch->num_tokens * pages->num_kv_heads;
-  const bool fp8 = pages->kv_dtype == FT_KV_FP8E4M3;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      pages->head_dim == 128 ? launch_groups(fp8 ? append_kernel<128, true> : append_kernel<128, false>, a, groups, 16, s)
-                             : launch_groups(fp8 ? append_kernel<64, true> : append_kernel<64, false>, a, groups, 8, s);
-  if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
-  return FT_OK;
+  return launch_move<true>(a, "append", static_cast<cudaStream_t>(stream));
 }
 
 extern "C" ft_status ft_kv_read(const ft_kv_pages* pages, const ft_kv_batch* batch, const int32_t* kv_start,
@@ -258,18 +299,10 @@ extern "C" ft_status ft_kv_read(const ft_kv_pages* pages, const ft_kv_batch* bat
   if (!kv_start) return set_error(FT_ERR_INVALID_ARG, "kv_start is null");
   if ((st = check_rows("k_out", k_out, 0, 0)) != FT_OK) return st;
   if ((st = check_rows("v_out", v_out, 0, 0)) != FT_OK) return st;
-  ReadArgs a{};
-  a.p = *pages; a.b = *batch; a.start = kv_start; a.rows = num_rows;
+  MoveArgs a{};
+  a.p = *pages; a.b = *batch; a.start = kv_start; a.rows = (int)num_rows;
   a.out[0] = static_cast<__nv_bfloat16*>(k_out); a.out[1] = static_cast<__nv_bfloat16*>(v_out);
-  if ((st = status_word(&a.status)) != FT_OK) return st;
-  const long long groups = 2LL * num_rows * pages->num_kv_heads;
-  const bool fp8 = pages->kv_dtype == FT_KV_FP8E4M3;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      pages->head_dim == 128 ? launch_groups(fp8 ? read_kernel<128, true> : read_kernel<128, false>, a, groups, 16, s)
-                             : launch_groups(fp8 ? read_kernel<64, true> : read_kernel<64, false>, a, groups, 8, s);
-  if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "read launch: %s", cudaGetErrorString(e));
-  return FT_OK;
+  return launch_move<false>(a, "read", static_cast<cudaStream_t>(stream));
 }
 
 extern "C" ft_status ft_kv_status(void* stream) {
