@@ -14,7 +14,7 @@ namespace ft {
 namespace kv {
 
 constexpr int kTokenRows = 16;    // most rows of a (sequence, key head) in token_kernel
-constexpr int kTokenTile = 128;   // tokens per tile of its ring
+constexpr int kTokenTile = 64;    // tokens per tile of its ring
 constexpr int kChunkRows = 256;   // rows of a block in chunk_kernel: two sub-tiles of 128
 constexpr int kSubRows = 128;
 
@@ -82,8 +82,15 @@ struct Range {
   long long w0, w1, base, total;
   int s, n;  // first sequence; CTAs that have work
 };
+// x / y, x >= 0, y > 0: in 32 bits where they do (64 take some 100 instructions).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (long long)((uint32_t)x / (uint32_t)y);
+  return x / y;
+}
 // CTA of item w.
-__device__ __forceinline__ int cta_of(long long w, long long total, int n) { return (int)(((w + 1) * n - 1) / total); }
+__device__ __forceinline__ int cta_of(long long w, long long total, int n) {
+  return (int)quotient((w + 1) * n - 1, total);
+}
 
 // Every thread of the CTA: exclusive prefix sums of count(s) over the
 // sequences into pre[0 .. S], and this CTA's even share of the total.
@@ -118,8 +125,8 @@ __device__ __forceinline__ Range cut(const AttendArgs& a, long long* pre, long l
   r.w0 = r.w1 = r.base = 0;
   r.s = 0;
   if ((int)blockIdx.x < r.n) {
-    r.w0 = blockIdx.x * total / r.n;
-    r.w1 = (blockIdx.x + 1) * total / r.n;
+    r.w0 = quotient(blockIdx.x * total, r.n);
+    r.w1 = quotient((blockIdx.x + 1) * total, r.n);
     int lo = 0, hi = S - 1;  // the last sequence that begins at or before w0 (ones without work begin where the next does)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -134,6 +141,8 @@ __device__ __forceinline__ Range cut(const AttendArgs& a, long long* pre, long l
 
 // ---------------------------------------------------------------- token_kernel's items: tiles of a (sequence, head)
 
+constexpr int kPairItems = 4;  // a (sequence, head)'s fixed cost (its rows of q, joining the warps), in tiles
+
 __device__ __forceinline__ Span token_tiles(const AttendArgs& a, const Seq& q, Span* seen) {
   seen->lo = visible(a, q, 0).lo;
   seen->hi = visible(a, q, max(0, q.m - 1)).hi;
@@ -142,15 +151,16 @@ __device__ __forceinline__ Span token_tiles(const AttendArgs& a, const Seq& q, S
   t.hi = q.m == 0 ? t.lo : max(t.lo + 1, (seen->hi + kTokenTile - 1) / kTokenTile);  // rows that see nothing: one tile
   return t;
 }
+// Items of one head of a sequence: its tiles, after kPairItems.
+__device__ __forceinline__ int token_items(const Span& t) { return t.hi > t.lo ? t.hi - t.lo + kPairItems : 0; }
 __device__ __forceinline__ Range token_range(const AttendArgs& a, long long* pre, long long* scan) {
   return cut(a, pre, scan, [&](int s) {
     if (s == a.b.num_seqs) return 0LL;
     Span seen;
-    const Span t = token_tiles(a, load_seq(a.p, a.b, s, a.status), &seen);
-    return (long long)(t.hi - t.lo) * a.p.num_kv_heads;
+    return (long long)token_items(token_tiles(a, load_seq(a.p, a.b, s, a.status), &seen)) * a.p.num_kv_heads;
   });
 }
-// The (sequence, head)s of a CTA's range, one after the other.
+// The parts of (sequence, head)s in a CTA's range, one after the other.
 struct TokenWalk {
   long long w, end, base, total;
   int n;
@@ -164,9 +174,8 @@ struct TokenWalk {
   __device__ __forceinline__ TokenWalk(const AttendArgs&, const Range& r)
       : w(r.w0), end(r.w1), base(r.base), total(r.total), n(r.n), s(r.s), loaded(-1) {}
   __device__ __forceinline__ bool next(const AttendArgs& a) {
-    if (w >= end) return false;
-    long long all;
     for (;;) {
+      if (w >= end) return false;
       if (loaded != s) {
         q = load_seq(a.p, a.b, s, a.status);
         Span seen;
@@ -175,25 +184,27 @@ struct TokenWalk {
         hi = seen.hi;
         loaded = s;
       }
-      all = (long long)(tiles.hi - tiles.lo) * a.p.num_kv_heads;
-      if (w - base < all) break;
-      base += all;
-      ++s;
+      const int items = token_items(tiles);
+      const long long all = (long long)items * a.p.num_kv_heads;
+      if (w - base >= all) {
+        base += all;
+        ++s;
+        continue;
+      }
+      h = (int)quotient(w - base, items);
+      const int rel = (int)(w - base - (long long)h * items), cnt = (int)min((long long)(items - rel), end - w);
+      w += cnt;
+      t0 = tiles.lo + max(0, rel - kPairItems);
+      t1 = tiles.lo + max(0, rel + cnt - kPairItems);
+      if (t0 == t1) continue;  // only of the fixed cost
+      begins = t0 == tiles.lo;
+      ends = t1 == tiles.hi;
+      return true;
     }
-    const int nt = tiles.hi - tiles.lo, rel = (int)((w - base) % nt);
-    h = (int)((w - base) / nt);
-    const int cnt = (int)min((long long)(nt - rel), end - w);
-    t0 = tiles.lo + rel;
-    t1 = t0 + cnt;
-    begins = rel == 0;
-    ends = rel + cnt == nt;
-    w += cnt;
-    return true;
   }
   // last CTA of this (sequence, head)
   __device__ __forceinline__ int last_cta() const {
-    const int nt = tiles.hi - tiles.lo;
-    return cta_of(base + (long long)(h + 1) * nt - 1, total, n);
+    return cta_of(base + (long long)(h + 1) * token_items(tiles) - 1, total, n);
   }
 };
 

@@ -2,35 +2,38 @@
 // the batch has at most 16 rows (new tokens x query heads of the group), as in
 // decoding.  The work is reading K and V once: memory-bound.
 //
-//   out = sum_j w_j v_j / sum_j w_j,   w_j = 2^(x_j - m),  x_j = scale log2(e) q.k_j,  m = max_j x_j
+//   out = sum_j w_j v_j / sum_j w_j,   w_j = 2^(x_j - m),  x_j = scale log2(e) q.k_j,  m >= max_j x_j - 8
 //
 // Quantised cache: the key's scale multiplies the score and the value's scale
 // the probability (a power of two: nothing is rounded for it).
 //
-// Split: the batch's tiles of 128 tokens, laid end to end over (sequence, key
+// Split: the batch's tiles of 64 tokens, laid end to end over (sequence, key
 // head, tile), are cut into equal contiguous ranges, one per CTA and one CTA
 // per SM, whatever the lengths are.  A (sequence, head) that a cut divides
 // leaves partial sums (unnormalised out, m, l) in the workspace, which
 // combine_kernel joins in tile order.
 //
-// CTA: one producer warp, eight consumer warps.  The producer's lanes 0..7
-// load one group of 16 tokens each (a group never crosses a page) as swizzled
-// TMA boxes into a ring of stages; consumer warp w takes group w of every
-// tile: S = Q K^T as m16n8k16 (16 rows, the invalid ones zero), its own
-// running m, l and O, O += P V.  Warps meet only at the end of a (sequence,
-// head).  mma.sync is enough here: a row block of 16 is an eighth of a
-// tcgen05 tile, and the path is bound by HBM, not by the tensor pipe.
+// CTA: two producer warps (K, V) and kWarps consumer warps in sets of four.  The
+// producers load a tile as swizzled TMA boxes of as many tokens as a page holds
+// (64 at most: issuing a copy costs some 50 ns, and boxes of 16 tokens kept the
+// consumers waiting) into a ring; the sets take the tiles in turn, a warp a
+// group of 16 tokens.  S^T = K Q^T and O^T += V^T P^T as m16n8k16: tokens
+// (then head_dim) are the 16 rows, so that 8 attention rows cost one block of
+// columns and not a half-empty block of 16 rows.  Every warp has its own m, l
+// and O; warps meet only at the end of a (sequence, head).  mma.sync is enough
+// here: the path is bound by HBM and by what a code's expansion costs, not by
+// the tensor pipe, and S^T's fragments become P^T's by one transposition of 8 x
+// 8 registers.
 //
 // Quantised cache: codes are expanded in registers (exact), keys to fp16, the
 // cheaper conversion, values to bf16, whose range P needs: a probability keeps
-// its 8 bits however small it is.  The
-// contraction order over head_dim is free as long as Q uses the same, and so
-// are the order of tokens (P's columns and V's rows) and of output columns;
-// they are chosen so that each lane reads 16 consecutive bytes of a row,
-// without bank conflicts, and needs no transposition.  Q is scaled per row by
-// a power of two to [1, 2) before it is rounded to fp16, so that no value
-// leaves fp16's range: q elements below 2^-14 of the row's largest lose bits
-// that weigh less than 2^-25 of it.
+// its 8 bits however small it is.  The contraction order over head_dim is free
+// as long as Q uses the same, and so are the order of tokens and of output
+// columns; they are chosen so that each lane reads 16 consecutive bytes of a
+// row, without bank conflicts.  Q is scaled per row by a power of two to [1, 2)
+// before it is rounded to fp16, so that no value leaves fp16's range: q
+// elements below 2^-14 of the row's largest lose bits that weigh less than
+// 2^-25 of it.
 #include <cuda.h>
 
 #include "decode_common.h"
@@ -40,25 +43,33 @@ namespace ft {
 namespace kv {
 namespace {
 
-constexpr int kConsumers = 8;
-constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kGroup = 16;
-static_assert(kTokenTile == kConsumers * kGroup, "a group per consumer warp");
-constexpr int kRedRows = 4;  // rows joined across the warps at a time
+constexpr int kSet = 4;  // warps of a set, groups of a tile
+static_assert(kTokenTile == kSet * kGroup, "a group per warp of a set");
+constexpr float kGrow = 8.0f;  // log2 of the growth of a row's maximum that its sums' scale may lag behind
 
-template <int D, bool kFp8>
+// NB: blocks of 8 rows.  The expansion of the codes wants more warps; bf16 is
+// content with eight, and 16 rows' registers leave room for no more.
+template <int D, bool kFp8, int NB>
 struct Layout {
-  static constexpr int kEsz = kFp8 ? 1 : 2;
-  static constexpr int kGroupBytes = kGroup * D * kEsz;  // K of a group; V follows
-  static constexpr int kStageBytes = 2 * kConsumers * kGroupBytes;
-  static constexpr int kStages = kStageBytes >= 65536 ? 3 : kStageBytes >= 32768 ? 6 : 8;
+  static constexpr int kWarps = kFp8 && NB == 1 ? 12 : 8;
+  static constexpr int kSets = kWarps / kSet;
+  static constexpr int kThreads = (kWarps + 2) * 32;
+  static constexpr int kLine = kFp8 ? D : 128;                     // bytes of a token's row in a box
+  static constexpr int kBoxes = kFp8 ? 1 : D / 64;                 // boxes side by side: 64 bf16 of a row each
+  static constexpr int kHalfBytes = kTokenTile * kLine * kBoxes;   // a tile's K; its V follows
+  static constexpr int kStageBytes = 2 * kHalfBytes;
+  static constexpr int kStages = kStageBytes >= 32768 ? 6 : 12;    // a multiple of kSets: a stage is one set's
+  static constexpr int kRedRows = 4;                               // rows joined across the warps at a time
   static constexpr int kRowFloats = D + 4;
   static constexpr int kScaleOff = kStages * kStageBytes;
   static constexpr int kScaleBytes = kFp8 ? kStages * 2 * kTokenTile : 0;
   static constexpr int kRedOff = kScaleOff + kScaleBytes;
-  static constexpr int kMlOff = kRedOff + kConsumers * kRedRows * kRowFloats * 4;
-  static constexpr int kBarOff = kMlOff + kConsumers * 16 * 2 * 4;
+  static constexpr int kMlOff = kRedOff + kWarps * kRedRows * kRowFloats * 4;
+  static constexpr int kTotOff = kMlOff + kWarps * 8 * NB * 2 * 4;  // a row's maximum and 1 / sum, of all warps
+  static constexpr int kBarOff = kTotOff + 8 * NB * 2 * 4;
   static constexpr int kSmem = kBarOff + 2 * kStages * 8 + 16 + 1024;
+  static_assert(kStages % kSets == 0, "a set that skipped a turn of a barrier would take it for the next");
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kStages * kStageBytes >= (kMaxSeqs + 1) * 8 + 1024, "the prefix sums fit the ring before it fills");
 };
@@ -75,12 +86,6 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// scores: fp16 for the quantised cache
-template <bool kFp8>
-__device__ __forceinline__ void mma_score(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if (kFp8) mma_f16(c, a, b0, b1);
-  else mma_bf16(c, a, b0, b1);
-}
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -91,6 +96,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
@@ -98,290 +108,300 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(dec::smem_addr(bar))
       : "memory");
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t pair) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(pair & 0xffffu), __NV_E4M3);
-  return (uint32_t)h.x | (uint32_t)h.y << 16;
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ uint32_t bits(__nv_bfloat162 b) { return *reinterpret_cast<const uint32_t*>(&b); }
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t pair) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3));
 }
 __device__ __forceinline__ uint32_t e4m3x2_to_bf162(uint32_t pair) {
-  const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(pair & 0xffffu), __NV_E4M3)));
-  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t*>(&b);
+  const float2 f = __half22float2(e4m3x2_to_half2(pair));
+  return bits(__floats2bfloat162_rn(f.x, f.y));
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, bool half) {
-  if (half) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-__device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory"); }
 
-// Order of a group's tokens in S's columns (and P's): column n of an 8-column
-// block is token tok(n) of the block.  fp8 rows of 128 bytes: neighbouring
+// Token of row n of an 8-row block of S^T.  fp8 rows of 128 bytes: neighbouring
 // rows of a quarter-warp differ in bit 2, which the swizzle turns into other
 // banks.
 template <int D, bool kFp8>
 __device__ __forceinline__ int tok(int n) {
   return kFp8 && D == 128 ? (n >> 1) | ((n & 1) << 2) : n;
 }
-// Output column of accumulator block j, fragment column 2c + i.
+// Output column of row g + 8 i of block mb of O^T.
 template <int D, bool kFp8>
-__device__ __forceinline__ int out_col(int j, int c, int i) {
-  return !kFp8 ? 8 * j + 2 * c + i : D == 128 ? 16 * c + 64 * i + j : 16 * c + 8 * i + j;
+__device__ __forceinline__ int out_col(int mb, int g, int i) {
+  return !kFp8 ? 16 * mb + 8 * i + g : (D == 128 ? 16 * ((g >> 1) | ((g & 1) << 2)) : 8 * g) + 2 * mb + i;
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, int NB>
 struct Warp {
-  static constexpr int kKs = D / 16, kNb = D / 8;
-  uint32_t qf[kKs][4];
-  float o[kNb][4];
-  float m[2], l[2], sc[2];  // rows lane / 4 and + 8: running maximum, this lane's sum, score factor
-  int lo[2], hi[2];         // visible tokens [lo, hi) of those rows
+  static constexpr int kKs = D / 16, kMb = D / 16;
+  uint32_t qf[NB][kKs][2];
+  float o[NB][kMb][4];
+  float m[NB][2], l[NB][2], sc[NB][2];  // rows 8 nb + 2c, + 1: running maximum, this lane's sum, score factor
+  int lo[NB][2], hi[NB][2];             // visible tokens [lo, hi) of those rows
+  bool started;
 
   __device__ __forceinline__ void begin(const AttendArgs& a, const Seq& q, int h, int lane) {
     const int g = lane >> 2, c = lane & 3;
+    started = false;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = g + 8 * half, i = r / a.G;
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = 8 * nb + g, i = r / a.G;
       const bool ok = i < q.m;
       const __nv_bfloat16* row = a.q + (long long)(q.q0 + i) * a.qts + (long long)(h * a.G + r % a.G) * a.qhs;
-      const Span v = visible(a, q, ok ? i : 0);
-      lo[half] = v.lo;
-      hi[half] = ok ? v.hi : 0;
-      m[half] = -INFINITY;
-      l[half] = 0.0f;
-      sc[half] = a.scale_log2;
+      uint32_t top = 0;
 #pragma unroll
       for (int ks = 0; ks < kKs; ++ks)
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int d = !kFp8 ? 16 * ks + 8 * w + 2 * c : (ks < 4 ? 0 : 64) + 16 * c + 4 * (ks & 3) + 2 * w;
-          qf[ks][2 * w + half] = ok ? __ldg(reinterpret_cast<const uint32_t*>(row + d)) : 0u;
+          const uint32_t u = ok ? __ldg(reinterpret_cast<const uint32_t*>(row + d)) : 0u;
+          qf[nb][ks][w] = u;
+          top = max(top, max((u << 16) & 0x7f800000u, u & 0x7f800000u));
         }
+      float up = 1.0f;
       if (kFp8) {  // to fp16, the row scaled to [1, 2)
-        uint32_t top = 0;
-#pragma unroll
-        for (int ks = 0; ks < kKs; ++ks)
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t u = qf[ks][2 * w + half];
-            top = max(top, max((u << 16) & 0x7f800000u, u & 0x7f800000u));
-          }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = min(max((int)(top >> 23), 1), 253);  // infinities and NaN stay what they are
         const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-        sc[half] *= __uint_as_float((uint32_t)e << 23);
+        up = __uint_as_float((uint32_t)e << 23);
 #pragma unroll
         for (int ks = 0; ks < kKs; ++ks)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const uint32_t u = qf[ks][2 * w + half];
-            qf[ks][2 * w + half] = pack2(dec::bf16_lo(u) * down, dec::bf16_hi(u) * down, true);
+            const uint32_t u = qf[nb][ks][w];
+            qf[nb][ks][w] = bits(__floats2half2_rn(dec::bf16_lo(u) * down, dec::bf16_hi(u) * down));
           }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kNb; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+      for (int j = 0; j < 2; ++j) {
+        const int rj = 8 * nb + 2 * c + j, ij = rj / a.G;
+        const Span v = visible(a, q, ij < q.m ? ij : 0);
+        lo[nb][j] = v.lo;
+        hi[nb][j] = ij < q.m ? v.hi : 0;
+        m[nb][j] = -INFINITY;
+        l[nb][j] = 0.0f;
+        sc[nb][j] = a.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * c + j) * 4);
+      }
+#pragma unroll
+      for (int mb = 0; mb < kMb; ++mb) o[nb][mb][0] = o[nb][mb][1] = o[nb][mb][2] = o[nb][mb][3] = 0.0f;
+    }
   }
 
-  // One group: tokens j0 .. j0 + 15 at shared addresses kb, vb; ksc, vsc their scale bytes.
+  // One group: tokens j0 .. j0 + 15 at shared addresses kb, vb; ksc, vsc their
+  // scale bytes.  full: every row sees all of them.
   __device__ __forceinline__ void group(uint32_t kb, uint32_t vb, const uint8_t* ksc, const uint8_t* vsc, int j0,
                                         bool full, int m_new, int lane) {
     const int g = lane >> 2, c = lane & 3;
-    float s[2][4] = {};
+    float s[NB][4] = {};
     if (!kFp8) {
-      const int t = ((lane >> 4) << 3) + (lane & 7), ch = (lane >> 3) & 1;
+      const int t = lane & 15, ch = lane >> 4;
 #pragma unroll
       for (int ks = 0; ks < kKs; ++ks) {
-        uint32_t b[4];
-        ldsm4(b, kb + (ks >> 2) * (kGroup * 128) + t * 128 + (((2 * (ks & 3) + ch) ^ (t & 7)) << 4));
-        mma_score<kFp8>(s[0], qf[ks], b[0], b[1]);
-        mma_score<kFp8>(s[1], qf[ks], b[2], b[3]);
+        uint32_t k[4];
+        ldsm4(k, kb + (ks >> 2) * (kTokenTile * 128) + t * 128 + (((2 * (ks & 3) + ch) ^ (t & 7)) << 4));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma_bf16(s[nb], k, qf[nb][ks][0], qf[nb][ks][1]);
       }
     } else {
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        const int t = nb * 8 + tok<D, kFp8>(g);
-#pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf) {
-          const int phys = D == 128 ? (c + 4 * hf) ^ (t & 7) : c ^ ((t >> 1) & 3);
-          uint32_t w[4];
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(kb + t * D + (phys << 4)));
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_score<kFp8>(s[nb], qf[hf * 4 + i], e4m3x2_to_half2(w[i]), e4m3x2_to_half2(w[i] >> 16));
-        }
-      }
-    }
-    // scores to log2 domain, scales and masks
-    float vs[4];  // value scales of this lane's four tokens
-    float top[2] = {m[0], m[1]};
-#pragma unroll
-    for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = nb * 8 + tok<D, kFp8>(2 * c + i), u = 2 * nb + i;
-        float kf = 1.0f;
-        vs[u] = 1.0f;
-        if (kFp8) {
-          kf = scale_of(ksc[t]);
-          vs[u] = scale_of(vsc[t]);
-        }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float x = s[nb][2 * hf + i] * sc[hf];
-          if (kFp8) x *= kf;
-          if (!full && (j0 + t < lo[hf] || j0 + t >= hi[hf])) x = -INFINITY;
-          s[nb][2 * hf + i] = x;
-          top[hf] = fmaxf(top[hf], x);
-        }
-      }
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xffffffffu, top[hf], 1));
-      top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xffffffffu, top[hf], 2));
-    }
-    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float f = top[hf] > m[hf] ? exp2_approx(m[hf] - top[hf]) : 1.0f;
-        l[hf] *= f;
-        m[hf] = top[hf];
-#pragma unroll
-        for (int j = 0; j < kNb; ++j) {
-          o[j][2 * hf] *= f;
-          o[j][2 * hf + 1] *= f;
-        }
-      }
-    }
-    uint32_t pf[4];
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const float base = m[hf] == -INFINITY ? 0.0f : m[hf];
-#pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        float w[2];
+      for (int hf = 0; hf < D / 64; ++hf) {
+        uint32_t w[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float x = s[nb][2 * hf + i];
-          w[i] = exp2_approx(x - base);
-          l[hf] += w[i];
-          if (kFp8) w[i] = x == -INFINITY ? 0.0f : w[i] * vs[2 * nb + i];  // an unseen token's scale may be NaN
+          const int t = 8 * i + tok<D, kFp8>(g);
+          const int phys = D == 128 ? (c + 4 * hf) ^ (t & 7) : c ^ ((t >> 1) & 3);
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                       : "r"(kb + t * D + (phys << 4)));
         }
-        pf[2 * nb + hf] = pack2(w[0], w[1], false);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t f[4] = {bits(e4m3x2_to_half2(w[0][k] & 0xffffu)), bits(e4m3x2_to_half2(w[1][k] & 0xffffu)),
+                                 bits(e4m3x2_to_half2(w[0][k] >> 16)), bits(e4m3x2_to_half2(w[1][k] >> 16))};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma_f16(s[nb], f, qf[nb][hf * 4 + k][0], qf[nb][hf * 4 + k][1]);
+        }
       }
     }
-    // Tokens that no row sees hold anything (a page's unused end): their V is
-    // taken as zero.  Where some rows see a token and others do not
-    // (m_new > 1) and its V is not finite, 0 * V must not reach the others:
-    // one product per new token, over the V that it sees, added to its rows.
-    uint32_t keep[2] = {~0u, ~0u};
-    bool split = false;
-    if (!full) {
-      const int any_lo = __shfl_sync(0xffffffffu, lo[0], 0);  // row 0 belongs to the first new token
-      const int any_hi = max(hi[0], hi[1]);
-      const int w_hi = max(any_hi, __shfl_xor_sync(0xffffffffu, any_hi, 4));
-      const int x_hi = max(w_hi, __shfl_xor_sync(0xffffffffu, w_hi, 8));
-      const int t_hi = max(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 16));
-#pragma unroll
-      for (int nb = 0; nb < 2; ++nb) keep[nb] = keep_mask(nb, c, j0, any_lo, t_hi);
-      split = m_new > 1;
-    }
-    accumulate(vb, pf, keep, full, split, j0, m_new, lane);
-  }
-  __device__ __forceinline__ uint32_t keep_mask(int nb, int c, int j0, int from, int to) const {
-    uint32_t k = 0;
+    // scores in the log2 domain; s[nb][2 i + j]: token tok(g) + 8 i, row 8 nb + 2c + j
+    float vs[2] = {1.0f, 1.0f};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int j = j0 + nb * 8 + tok<D, kFp8>(2 * c + i);
-      if (j >= from && j < to) k |= 0xffffu << (16 * i);
+      const int t = 8 * i + tok<D, kFp8>(g);
+      float kf = 1.0f;
+      if (kFp8) {
+        kf = scale_of(ksc[t]);
+        vs[i] = scale_of(vsc[t]);
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x = s[nb][2 * i + j] * sc[nb][j];
+          if (kFp8) x *= kf;
+          if (!full && (j0 + t < lo[nb][j] || j0 + t >= hi[nb][j])) x = -INFINITY;
+          s[nb][2 * i + j] = x;
+        }
+    }
+    bool grown = !started;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) grown |= fmaxf(s[nb][j], s[nb][2 + j]) > m[nb][j] + kGrow;
+    if (__any_sync(0xffffffffu, grown)) {
+      started = true;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float top = fmaxf(m[nb][j], fmaxf(s[nb][j], s[nb][2 + j]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const float f = top > m[nb][j] ? exp2_approx(m[nb][j] - top) : 1.0f;
+          m[nb][j] = top;
+          l[nb][j] *= f;
+#pragma unroll
+          for (int mb = 0; mb < kMb; ++mb) {
+            o[nb][mb][j] *= f;
+            o[nb][mb][2 + j] *= f;
+          }
+        }
+    }
+    uint32_t pf[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float x = s[nb][2 * i + j], base = m[nb][j] == -INFINITY ? 0.0f : m[nb][j];
+          w[j] = exp2_approx(x - base);
+          l[nb][j] += w[j];
+          if (kFp8) w[j] = x == -INFINITY ? 0.0f : w[j] * vs[i];  // an unseen token's scale may be NaN
+        }
+        pf[nb][i] = transpose8(bits(__floats2bfloat162_rn(w[0], w[1])));
+      }
+    // Tokens that no row sees hold anything (a page's unused end): their V is
+    // taken as zero.  Where some rows see a token and others do not (m_new > 1)
+    // and its V is not finite, 0 * V must not reach the others: one product per
+    // row, over the V that it sees, added to it alone.
+    uint32_t keep[2] = {~0u, ~0u};
+    if (!full) {
+      int from = lo[0][0], to = 0;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) to = max(to, hi[nb][j]);
+      from = __shfl_sync(0xffffffffu, from, 0);  // row 0 belongs to the first new token
+      to = max(to, __shfl_xor_sync(0xffffffffu, to, 1));
+      to = max(to, __shfl_xor_sync(0xffffffffu, to, 2));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) keep[i] = keep_mask(i, c, j0, from, to);
+    }
+    if (full) accumulate<true>(vb, pf, keep, false, j0, lane);
+    else accumulate<false>(vb, pf, keep, m_new > 1, j0, lane);
+  }
+  // Bit mask of the pair of tokens 8 i + tok(2c), tok(2c + 1) within [from, to).
+  __device__ __forceinline__ uint32_t keep_mask(int i, int c, int j0, int from, int to) const {
+    uint32_t k = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int t = j0 + 8 * i + tok<D, kFp8>(2 * c + j);
+      if (t >= from && t < to) k |= 0xffffu << (16 * j);
     }
     return k;
   }
-  // fragments (b0, b1) of kB consecutive blocks starting at block jb
-  static constexpr int kB = kFp8 ? 4 : 2;
-  __device__ __forceinline__ void v_frags(uint32_t vb, int jb, int lane, uint32_t (*b)[2]) const {
-    const int g = lane >> 2, c = lane & 3;
-    if (!kFp8) {
-      const int t = (lane & 7) + (((lane >> 3) & 1) << 3), ch = jb + (lane >> 4);
-      uint32_t r[4];
-      ldsm4t(r, vb + (ch >> 3) * (kGroup * 128) + t * 128 + (((ch & 7) ^ (t & 7)) << 4));
-      b[0][0] = r[0]; b[0][1] = r[1]; b[1][0] = r[2]; b[1][1] = r[3];
-    } else {
-      uint32_t w[2][2];
+  __device__ __forceinline__ static bool not_finite(uint32_t b) {  // either bf16 half an infinity or a NaN
+    return (b & 0x7f80u) == 0x7f80u || (b & 0x7f800000u) == 0x7f800000u;
+  }
+  // O^T block mb += V^T block (fragment v) P^T
+  template <bool kFull>
+  __device__ __forceinline__ void product(int mb, uint32_t* v, const uint32_t (*pf)[2], const uint32_t* keep, bool split,
+                                          int j0, int lane) {
+    bool bad = false;
+    if (!kFull) {
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = nb * 8 + tok<D, kFp8>(2 * c + i);
-          const int ch = D == 128 ? ((g >> 1) | ((g & 1) << 2)) ^ (t & 7) : (g >> 1) ^ ((t >> 1) & 3);
-          const uint32_t at = vb + t * D + (ch << 4) + (D == 128 ? jb : (g & 1) * 8 + jb);
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[nb][i]) : "r"(at));
-        }
-#pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        const uint32_t p = __byte_perm(w[nb][0], w[nb][1], 0x5140), q = __byte_perm(w[nb][0], w[nb][1], 0x7362);
-        b[0][nb] = e4m3x2_to_bf162(p);
-        b[1][nb] = e4m3x2_to_bf162(p >> 16);
-        b[2][nb] = e4m3x2_to_bf162(q);
-        b[3][nb] = e4m3x2_to_bf162(q >> 16);
+      for (int i = 0; i < 4; ++i) {
+        v[i] &= keep[i >> 1];
+        bad |= not_finite(v[i]);
       }
     }
-  }
-  __device__ __forceinline__ static bool not_finite(uint32_t b) {  // either 16-bit half an infinity or a NaN
-    const uint32_t e = 0x7f80u;
-    return (b & e) == e || ((b >> 16) & e) == e;
-  }
-  __device__ __forceinline__ void accumulate(uint32_t vb, const uint32_t* pf, const uint32_t* keep, bool full,
-                                             bool split, int j0, int m_new, int lane) {
+    if (kFull || !split || !__any_sync(0xffffffffu, bad)) {
 #pragma unroll
-    for (int jb = 0; jb < kNb; jb += kB) {
-      uint32_t b[kB][2];
-      v_frags(vb, jb, lane, b);
-      bool bad = false;
-      if (!full) {
+      for (int nb = 0; nb < NB; ++nb) mma_bf16(o[nb][mb], v, pf[nb][0], pf[nb][1]);
+      return;
+    }
+    const int c = lane & 3;
 #pragma unroll
-        for (int i = 0; i < kB; ++i)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb) {
-            b[i][nb] &= keep[nb];
-            bad |= not_finite(b[i][nb]);
+      for (int j = 0; j < 2; ++j)
+        for (int src = 0; src < 4; ++src) {  // row 8 nb + 2 src + j
+          const int from = __shfl_sync(0xffffffffu, lo[nb][j], src), to = __shfl_sync(0xffffffffu, hi[nb][j], src);
+          const uint32_t k0 = keep_mask(0, c, j0, from, to), k1 = keep_mask(1, c, j0, from, to);
+          const uint32_t seen[4] = {v[0] & k0, v[1] & k0, v[2] & k1, v[3] & k1};
+          float t[4] = {};
+          mma_bf16(t, seen, pf[nb][0], pf[nb][1]);
+          if (c == src) {
+            o[nb][mb][j] += t[j];
+            o[nb][mb][2 + j] += t[2 + j];
           }
-      }
-      if (!split || !__any_sync(0xffffffffu, bad)) {
+        }
+  }
+  template <bool kFull>
+  __device__ __forceinline__ void accumulate(uint32_t vb, const uint32_t (*pf)[2], const uint32_t* keep, bool split,
+                                             int j0, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    if (!kFp8) {
+      const int t = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
 #pragma unroll
-        for (int i = 0; i < kB; ++i) mma_bf16(o[jb + i], pf, b[i][0], b[i][1]);
+      for (int mb = 0; mb < kMb; ++mb) {
+        uint32_t v[4];
+        ldsm4t(v, vb + (mb >> 2) * (kTokenTile * 128) + t * 128 + (((2 * (mb & 3) + ch) ^ (t & 7)) << 4));
+        product<kFull>(mb, v, pf, keep, split, j0, lane);
+      }
+      return;
+    }
+    // this lane's 16 (8) codes of the four tokens of its fragments
+    constexpr int kW = D / 32;
+    uint32_t w[4][kW];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 8 * (i >> 1) + tok<D, kFp8>(2 * c + (i & 1));
+      if (D == 128) {
+        const uint32_t at = vb + t * D + ((((g >> 1) | ((g & 1) << 2)) ^ (t & 7)) << 4);
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][kW - 2]), "=r"(w[i][kW - 1])
+                     : "r"(at));
       } else {
-        const int g = lane >> 2, c = lane & 3;
-        for (int src = 0; src < 32; src += 4)  // the rows' distinct visible spans, row by row
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const int from = __shfl_sync(0xffffffffu, lo[hf], src), to = __shfl_sync(0xffffffffu, hi[hf], src);
-            const uint32_t k0 = keep_mask(0, c, j0, from, to), k1 = keep_mask(1, c, j0, from, to);
-#pragma unroll
-            for (int i = 0; i < kB; ++i) {
-              float t[4] = {};
-              mma_bf16(t, pf, b[i][0] & k0, b[i][1] & k1);
-              if (g == src >> 2) {
-                o[jb + i][2 * hf] += t[2 * hf];
-                o[jb + i][2 * hf + 1] += t[2 * hf + 1];
-              }
-            }
-          }
+        const uint32_t at = vb + t * D + (((g >> 1) ^ ((t >> 1) & 3)) << 4) + (g & 1) * 8;
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(at));
       }
+    }
+#pragma unroll
+    for (int k = 0; k < kW; ++k) {
+      // bytes 0..3 of the word, each of a pair of tokens
+      const uint32_t a0 = __byte_perm(w[0][k], w[1][k], 0x5140), a1 = __byte_perm(w[0][k], w[1][k], 0x7362);
+      const uint32_t b0 = __byte_perm(w[2][k], w[3][k], 0x5140), b1 = __byte_perm(w[2][k], w[3][k], 0x7362);
+      uint32_t v[4] = {e4m3x2_to_bf162(a0 & 0xffffu), e4m3x2_to_bf162(a0 >> 16), e4m3x2_to_bf162(b0 & 0xffffu),
+                       e4m3x2_to_bf162(b0 >> 16)};
+      product<kFull>(2 * k, v, pf, keep, split, j0, lane);
+      uint32_t u[4] = {e4m3x2_to_bf162(a1 & 0xffffu), e4m3x2_to_bf162(a1 >> 16), e4m3x2_to_bf162(b1 & 0xffffu),
+                       e4m3x2_to_bf162(b1 >> 16)};
+      product<kFull>(2 * k + 1, u, pf, keep, split, j0, lane);
     }
   }
 };
 
-template <int D, bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool kFp8, int NB>
+__global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
     token_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ AttendArgs a) {
-  using L = Layout<D, kFp8>;
+  using L = Layout<D, kFp8, NB>;
+  constexpr int kRows = 8 * NB, kConsumers = L::kWarps * 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (dec::smem_addr(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -392,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
-      dec::mbar_init(&full[i], 1);
-      dec::mbar_init(&empty[i], kConsumers);
+      dec::mbar_init(&full[i], 2);
+      dec::mbar_init(&empty[i], kSet);
     }
     *abort_flag = 0;
     dec::mbar_init_fence();
@@ -403,40 +423,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();  // the prefix sums are read; the ring may fill
 
-  if (warp == kConsumers) {
-    // ------------------------------------------------------------ producer
+  if (warp >= L::kWarps) {
+    // ------------------------------------------------------------ producers
+    // Lane l has the page row of box l of the next 32 boxes, and issues its copies.
+    const bool v = warp > L::kWarps;
+    const CUtensorMap* map = v ? &map_v : &map_k;
+    const uint8_t* scales = v ? a.p.v_scale : a.p.k_scale;
+    const int br = min(a.p.page_tokens, kTokenTile), per = kTokenTile / br;  // tokens of a box, boxes of a tile
     int it = 0;
     bool go = true;
     TokenWalk w(a, rg);
     while (go && w.next(a)) {
-      const int hi = w.hi, lo = w.lo;
-      for (int t = w.t0; t < w.t1; ++t, ++it) {
-        const int st = it % L::kStages, j0 = t * kTokenTile + lane * kGroup;
-        const bool mine = lane < kConsumers && j0 < hi && j0 + kGroup > lo;
-        int row = 0;
-        if (mine) {
-          const int page = max(0, load_page(a.p, a.b, w.s, j0 / a.p.page_tokens, a.status));
-          row = (page * a.p.num_kv_heads + w.h) * a.p.page_tokens + j0 % a.p.page_tokens;
-        }
-        if (!wait_or_abort(&empty[st], ((it / L::kStages) & 1) ^ 1, a.status, abort_flag)) {
-          go = false;
-          break;
-        }
-        const int live = __popc(__ballot_sync(0xffffffffu, mine));
-        if (lane == 0) dec::mbar_expect_tx(&full[st], live * (2 * L::kGroupBytes + (kFp8 ? 2 * kGroup : 0)));
-        __syncwarp();
-        if (mine) {
-          const uint32_t kb = dec::smem_addr(smem + st * L::kStageBytes) + lane * (2 * L::kGroupBytes);
-          const uint32_t vb = kb + L::kGroupBytes;
-#pragma unroll
-          for (int c = 0; c < (kFp8 ? 1 : D / 64); ++c) {
-            tma_box(kb + c * kGroup * 128, &map_k, c * 64, row, &full[st]);
-            tma_box(vb + c * kGroup * 128, &map_v, c * 64, row, &full[st]);
+      const int hi = w.hi, lo = w.lo, t1 = w.t1;
+      auto row_of = [&](int t) {  // of this lane's box, from tile t on; -1: no row sees a token of it
+        const int j0 = t * kTokenTile + lane * br;
+        if (j0 >= t1 * kTokenTile || j0 >= hi || j0 + br <= lo) return -1;
+        const int page = max(0, load_page(a.p, a.b, w.s, j0 / a.p.page_tokens, a.status));
+        return (page * a.p.num_kv_heads + w.h) * a.p.page_tokens + j0 % a.p.page_tokens;
+      };
+      int ahead = row_of(w.t0);
+      for (int tb = w.t0; tb < t1 && go; tb += 32 / per) {
+        const int row = ahead, te = min(t1, tb + 32 / per);
+        ahead = row_of(te);  // on its way while these are issued
+        const unsigned live = __ballot_sync(0xffffffffu, row >= 0);
+        for (int t = tb; t < te; ++t, ++it) {
+          const int st = it % L::kStages, l0 = (t - tb) * per;
+          if (!wait_or_abort(&empty[st], ((it / L::kStages) & 1) ^ 1, a.status, abort_flag)) {
+            go = false;
+            break;
           }
-          if (kFp8) {
-            uint8_t* sc = smem + L::kScaleOff + st * 2 * kTokenTile + lane * kGroup;
-            dec::bulk_g2s(sc, a.p.k_scale + row, kGroup, &full[st]);
-            dec::bulk_g2s(sc + kTokenTile, a.p.v_scale + row, kGroup, &full[st]);
+          if (lane == 0)
+            dec::mbar_expect_tx(&full[st],
+                                __popc(live >> l0 & ((1u << per) - 1u)) * br * (L::kLine * L::kBoxes + (kFp8 ? 1 : 0)));
+          __syncwarp();
+          if (lane >= l0 && lane < l0 + per && row >= 0) {
+            const int at = (lane - l0) * br;
+            const uint32_t dst = dec::smem_addr(smem + st * L::kStageBytes) + v * L::kHalfBytes + at * L::kLine;
+#pragma unroll
+            for (int c = 0; c < L::kBoxes; ++c) tma_box(dst + c * kTokenTile * 128, map, c * 64, row, &full[st]);
+            if (kFp8)
+              dec::bulk_g2s(smem + L::kScaleOff + (2 * st + v) * kTokenTile + at, scales + row, br, &full[st]);
           }
         }
       }
@@ -447,90 +473,112 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ consumers
     float* red = reinterpret_cast<float*>(smem + L::kRedOff);
-    float* ml = reinterpret_cast<float*>(smem + L::kMlOff);
+    float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
+    float2* tot = reinterpret_cast<float2*>(smem + L::kTotOff);
+    auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); };
+    const int set = warp / kSet, grp = warp % kSet;
     int it = 0;
     int4 begun = make_int4(-1, 0, 0, 0);
     TokenWalk w(a, rg);
-    Warp<D, kFp8> ws;
+    Warp<D, kFp8, NB> ws;
     while (w.next(a)) {
       ws.begin(a, w.q, w.h, lane);
       const int hi = w.hi, lo = w.lo;
-      // every row sees [all_lo, all_hi): the first new token's end, the last one's start
+      // every row sees [last.lo, first.hi): from the last new token's start to the first one's end
       const Span first = visible(a, w.q, 0), last = visible(a, w.q, max(0, w.q.m - 1));
       for (int t = w.t0; t < w.t1; ++t, ++it) {
-        const int st = it % L::kStages, j0 = t * kTokenTile + warp * kGroup;
+        if (it % L::kSets != set) continue;
+        const int st = it % L::kStages, j0 = t * kTokenTile + grp * kGroup;
         const bool live = wait_or_abort(&full[st], (it / L::kStages) & 1, a.status, abort_flag);
         if (live && j0 < hi && j0 + kGroup > lo) {
-          const uint32_t kb = dec::smem_addr(smem + st * L::kStageBytes) + warp * (2 * L::kGroupBytes);
-          const uint8_t* sc = smem + L::kScaleOff + st * 2 * kTokenTile + warp * kGroup;
-          ws.group(kb, kb + L::kGroupBytes, sc, sc + kTokenTile, j0, j0 >= last.lo && j0 + kGroup <= first.hi, w.q.m,
+          const uint32_t kb = dec::smem_addr(smem + st * L::kStageBytes) + grp * kGroup * L::kLine;
+          const uint8_t* sc = smem + L::kScaleOff + st * 2 * kTokenTile + grp * kGroup;
+          ws.group(kb, kb + L::kHalfBytes, sc, sc + kTokenTile, j0, j0 >= last.lo && j0 + kGroup <= first.hi, w.q.m,
                    lane);
         }
         __syncwarp();
         if (lane == 0) dec::mbar_arrive(&empty[st]);
       }
-      // join the eight warps, four rows at a time
+      // join the warps, kRedRows rows at a time
       const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float l = ws.l[hf];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (c == 0) {
-          ml[(warp * 16 + g + 8 * hf) * 2] = ws.m[hf];
-          ml[(warp * 16 + g + 8 * hf) * 2 + 1] = l;
-        }
-      }
-      bar_consumers();
-      float top[2], f[2];
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        top[hf] = -INFINITY;
-        for (int x = 0; x < kConsumers; ++x) top[hf] = fmaxf(top[hf], ml[(x * 16 + g + 8 * hf) * 2]);
-        f[hf] = ws.m[hf] == -INFINITY ? 0.0f : exp2_approx(ws.m[hf] - top[hf]);
-      }
-      const int rows = min(16, w.q.m * a.G);
+        for (int j = 0; j < 2; ++j) {
+          float l = ws.l[nb][j];
+          l += __shfl_xor_sync(0xffffffffu, l, 4);
+          l += __shfl_xor_sync(0xffffffffu, l, 8);
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          if (g == 0) {
+            const int r = 8 * nb + 2 * c + j;
+            ml[warp * kRows + r] = make_float2(ws.m[nb][j], l);
+          }
+        }
+      sync();
+      const int rows = min(kRows, w.q.m * a.G);
       const bool whole = w.begins && w.ends;
       const long long slot = 2LL * blockIdx.x + w.begins;
       if (w.begins && !w.ends) begun = make_int4(w.s, w.h, 0, w.last_cta());
-      for (int r0 = 0; r0 < rows; r0 += kRedRows) {
-        const int hf = r0 >> 3;
-        if ((g & ~(kRedRows - 1)) == (r0 & 7)) {
-          float* dst = red + (warp * kRedRows + (g & (kRedRows - 1))) * L::kRowFloats;
-          const float fx = hf ? f[1] : f[0];
+      if (threadIdx.x < rows) {  // (read after the next barrier)
+        const int r = threadIdx.x;
+        float mm = -INFINITY, l = 0.0f;
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j)
+        for (int x = 0; x < L::kWarps; ++x) mm = fmaxf(mm, ml[x * kRows + r].x);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              dst[out_col<D, kFp8>(j, c, i)] = (hf ? ws.o[j][2 + i] : ws.o[j][i]) * fx;
+        for (int x = 0; x < L::kWarps; ++x) {
+          const float2 y = ml[x * kRows + r];
+          if (y.x != -INFINITY) l += y.y * exp2_approx(y.x - mm);
         }
-        bar_consumers();
-        for (int e = threadIdx.x; e < kRedRows * D; e += kConsumers * 32) {
-          const int rr = e / D, d = e % D, r = r0 + rr;
-          if (r >= rows) continue;
-          float sum = 0.0f, l = 0.0f, mm = -INFINITY;
+        tot[r] = make_float2(mm, inverse(l));
+        if (whole) {
+          write_lse(a, w.q, w.h, r / a.G, r % a.G, mm, l);
+        } else {
+          a.part_ml[(slot * kTokenRows + r) * 2] = mm;
+          a.part_ml[(slot * kTokenRows + r) * 2 + 1] = l;
+        }
+      }
 #pragma unroll
-          for (int x = 0; x < kConsumers; ++x) {
-            sum += red[(x * kRedRows + rr) * L::kRowFloats + d];
-            mm = fmaxf(mm, ml[(x * 16 + r) * 2]);
-          }
+      for (int nb = 0; nb < NB; ++nb) {
+        float f[2];
 #pragma unroll
-          for (int x = 0; x < kConsumers; ++x) {
-            const float mx = ml[(x * 16 + r) * 2];
-            if (mx != -INFINITY) l += ml[(x * 16 + r) * 2 + 1] * exp2_approx(mx - mm);
-          }
-          if (whole) {
-            a.out[out_at(a, w.q, w.h, r / a.G, r % a.G) + d] = __float2bfloat16(sum * inverse(l));
-            if (d == 0) write_lse(a, w.q, w.h, r / a.G, r % a.G, mm, l);
-          } else {
-            a.part_o[(slot * kTokenRows + r) * D + d] = sum;
-            if (d == 0) {
-              a.part_ml[(slot * kTokenRows + r) * 2] = mm;
-              a.part_ml[(slot * kTokenRows + r) * 2 + 1] = l;
+        for (int j = 0; j < 2; ++j) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < L::kWarps; ++x) top = fmaxf(top, ml[x * kRows + 8 * nb + 2 * c + j].x);
+          f[j] = ws.m[nb][j] == -INFINITY ? 0.0f : exp2_approx(ws.m[nb][j] - top);
+        }
+        for (int r0 = 8 * nb; r0 < min(rows, 8 * nb + 8); r0 += L::kRedRows) {
+          if ((2 * c & ~(L::kRedRows - 1)) == (r0 & 7)) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float* dst = red + (warp * L::kRedRows + ((2 * c + j) & (L::kRedRows - 1))) * L::kRowFloats;
+#pragma unroll
+              for (int mb = 0; mb < D / 16; ++mb)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) dst[out_col<D, kFp8>(mb, g, i)] = ws.o[nb][mb][2 * i + j] * f[j];
             }
           }
+          sync();
+          for (int e = threadIdx.x * 2; e < L::kRedRows * D; e += kConsumers * 2) {
+            const int rr = e / D, d = e % D, r = r0 + rr;
+            if (r >= rows) continue;
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int x = 0; x < L::kWarps; ++x) {
+              const float2 y = *reinterpret_cast<const float2*>(&red[(x * L::kRedRows + rr) * L::kRowFloats + d]);
+              sum.x += y.x;
+              sum.y += y.y;
+            }
+            if (whole) {
+              const float inv = tot[r].y;
+              *reinterpret_cast<__nv_bfloat162*>(a.out + out_at(a, w.q, w.h, r / a.G, r % a.G) + d) =
+                  __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
+            } else {
+              *reinterpret_cast<float2*>(a.part_o + (slot * kTokenRows + r) * D + d) = sum;
+            }
+          }
+          sync();
         }
-        bar_consumers();
       }
     }
     if (threadIdx.x == 0) a.desc[blockIdx.x] = begun;
@@ -538,21 +586,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   dec::pdl_launch_dependents();
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, int NB>
 cudaError_t launch(const AttendArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-  const cudaError_t e = allow_smem<D * 2 + kFp8>(token_kernel<D, kFp8>, Layout<D, kFp8>::kSmem);
+  using L = Layout<D, kFp8, NB>;
+  const cudaError_t e = allow_smem<(D * 2 + kFp8) * 2 + NB - 1>(token_kernel<D, kFp8, NB>, L::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(token_kernel<D, kFp8>, a.grid, kThreads, Layout<D, kFp8>::kSmem, s, mk, mv, a);
+  return launch_dependent(token_kernel<D, kFp8, NB>, a.grid, L::kThreads, L::kSmem, s, mk, mv, a);
+}
+template <int D, bool kFp8>
+cudaError_t launch_rows(const AttendArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  return a.b.max_q_len * a.G <= 8 ? launch<D, kFp8, 1>(a, mk, mv, s) : launch<D, kFp8, 2>(a, mk, mv, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attend_token(const AttendArgs& a, cudaStream_t s) {
   CUtensorMap mk, mv;
-  if (!pages_map(&mk, a.p, a.p.k, kGroup) || !pages_map(&mv, a.p, a.p.v, kGroup)) return cudaErrorInvalidValue;
+  const int box = a.p.page_tokens < kTokenTile ? a.p.page_tokens : kTokenTile;
+  if (!pages_map(&mk, a.p, a.p.k, box) || !pages_map(&mv, a.p, a.p.v, box)) return cudaErrorInvalidValue;
   const bool fp8 = a.p.kv_dtype == FT_KV_FP8E4M3;
-  if (a.p.head_dim == 128) return fp8 ? launch<128, true>(a, mk, mv, s) : launch<128, false>(a, mk, mv, s);
-  return fp8 ? launch<64, true>(a, mk, mv, s) : launch<64, false>(a, mk, mv, s);
+  if (a.p.head_dim == 128) return fp8 ? launch_rows<128, true>(a, mk, mv, s) : launch_rows<128, false>(a, mk, mv, s);
+  return fp8 ? launch_rows<64, true>(a, mk, mv, s) : launch_rows<64, false>(a, mk, mv, s);
 }
 
 }  // namespace kv
