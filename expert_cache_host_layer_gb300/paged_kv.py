@@ -15,13 +15,17 @@ which also gives the layout and the sequences' description).
 """
 from __future__ import annotations
 
-import math
+import ctypes
 
 import torch
 
-from . import (FT_KV_BF16, FT_KV_FP8E4M3, ft_kv_append, ft_kv_attend, ft_kv_attend_workspace, ft_kv_batch, ft_kv_pages,
-               ft_kv_read, ft_kv_status)
+from . import (FT_KV_BF16, FT_KV_FP8E4M3, _check, ft_kv_attend_workspace, ft_kv_batch, ft_kv_pages, ft_kv_status,
+               library)
 
+# The three calls are made once per layer and step, so they go to the library
+# directly: at a decode step's sizes the binding's own functions, a device guard
+# and a stream object would cost as much as the GPU's work.
+_lib = library()
 _workspaces: dict = {}  # (device index, stream) -> uint8 tensor
 
 
@@ -48,9 +52,11 @@ class KVBatch:
         self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table  # keeps them alive
         self.num_seqs, self.num_tokens, self.max_q_len = S, int(num_tokens), int(max_q_len)
         self.device = kv_len.device
+        self.index = kv_len.get_device()
         stride = block_table.stride(0) if S > 1 else block_table.shape[1]
         self.c = ft_kv_batch(q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), stride, S, self.num_tokens,
                              self.max_q_len)
+        self.address = ctypes.addressof(self.c)
 
 
 class KVPages:
@@ -76,6 +82,9 @@ class KVPages:
         self.c = ft_kv_pages(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fp8 else None,
                              v_scale.data_ptr() if fp8 else None, self.num_pages, self.num_kv_heads, self.head_dim,
                              self.page_tokens, FT_KV_FP8E4M3 if fp8 else FT_KV_BF16)
+        self.address = ctypes.addressof(self.c)
+        self.index = k.get_device()
+        self._needs: dict = {}  # (q_heads, max_q_len) -> workspace bytes
 
     @classmethod
     def empty(cls, num_pages, num_kv_heads, page_tokens, head_dim, kv_dtype=FT_KV_BF16, device="cuda:0"):
@@ -89,11 +98,8 @@ class KVPages:
     # ---- the calls ---------------------------------------------------------
     def append(self, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream: torch.cuda.Stream | None = None):
         """Store the batch's new keys and values, bf16 [num_tokens, kv_heads, head_dim] (strided views are fine)."""
-        self._rows(batch, k, self.num_kv_heads, "k")
-        self._rows(batch, v, self.num_kv_heads, "v")
-        with self._guard():
-            ft_kv_append(self.c, batch.c, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                         v.stride(1), self._stream(stream))
+        rows = (*self._rows(batch, k, self.num_kv_heads, "k"), *self._rows(batch, v, self.num_kv_heads, "v"))
+        self._call("ft_kv_append", self.address, batch.address, *rows, self._stream(stream))
 
     def attend(self, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None = None,
                scale: float | None = None, causal: bool = True, window: int = 0,
@@ -103,58 +109,68 @@ class KVPages:
         1 / sqrt(head_dim); window > 0 keeps that many last tokens, the row's own
         included."""
         heads = q.shape[1] if q.dim() == 3 else 0
-        self._rows(batch, q, heads, "q")
-        self._rows(batch, out, heads, "out")
-        _need(lse is None or (lse.dtype == torch.float32 and lse.shape == (batch.num_tokens, heads) and
-                              lse.is_contiguous() and lse.device == self.device),
-              "lse is a contiguous float32 [num_tokens, q_heads] tensor")
+        rows = (*self._rows(batch, q, heads, "q"), *self._rows(batch, out, heads, "out"))
+        if lse is not None:
+            _need(lse.dtype == torch.float32 and lse.shape == (batch.num_tokens, heads) and lse.is_contiguous() and
+                  lse.get_device() == self.index, "lse is a contiguous float32 [num_tokens, q_heads] tensor")
         s = self._stream(stream)
-        with self._guard():
-            need = ft_kv_attend_workspace(self.c, batch.c, heads)
-            ws = _workspaces.get((self.device.index, s))
-            if ws is None or ws.numel() < need:
-                ws = _workspaces[(self.device.index, s)] = self._new_workspace(max(need, 256), stream)
-            ft_kv_attend(self.c, batch.c, heads, q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0),
-                         out.stride(1), lse.data_ptr() if lse is not None else None,
-                         1.0 / math.sqrt(self.head_dim) if scale is None else scale, causal, window, ws.data_ptr(),
-                         ws.numel(), s)
+        ws = _workspaces.get((self.index, s))
+        if ws is None or ws.numel() < self._need_bytes(batch, heads):
+            ws = self._new_workspace(s, self._need_bytes(batch, heads), stream)
+        self._call("ft_kv_attend", self.address, batch.address, heads, *rows,
+                   lse.data_ptr() if lse is not None else None, self.head_dim ** -0.5 if scale is None else scale, causal,
+                   window, ws.data_ptr(), ws.numel(), s)
 
     def read(self, batch: KVBatch, kv_start: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
              stream: torch.cuda.Stream | None = None):
         """Whole sequences back in bf16: token p of sequence s is row kv_start[s] + p of k_out and v_out,
         contiguous [rows, kv_heads, head_dim]."""
         _need(kv_start.dtype == torch.int32 and kv_start.shape == (batch.num_seqs + 1,) and kv_start.is_contiguous() and
-              kv_start.device == self.device, "kv_start is a contiguous int32 [S + 1] tensor of the cache's device")
+              kv_start.get_device() == self.index, "kv_start is a contiguous int32 [S + 1] tensor of the cache's device")
         shape = (k_out.shape[0], self.num_kv_heads, self.head_dim)
         for t in (k_out, v_out):
-            _need(t.dtype == torch.bfloat16 and t.shape == shape and t.is_contiguous() and t.device == self.device,
+            _need(t.dtype == torch.bfloat16 and t.shape == shape and t.is_contiguous() and t.get_device() == self.index,
                   "k_out and v_out are contiguous bf16 [rows, kv_heads, head_dim] tensors of the cache's device")
-        _need(batch.device == self.device, "the batch and the cache are on one device")
-        with self._guard():
-            ft_kv_read(self.c, batch.c, kv_start.data_ptr(), shape[0], k_out.data_ptr(), v_out.data_ptr(),
-                       self._stream(stream))
+        _need(batch.index == self.index, "the batch and the cache are on one device")
+        self._call("ft_kv_read", self.address, batch.address, kv_start.data_ptr(), shape[0], k_out.data_ptr(),
+                   v_out.data_ptr(), self._stream(stream))
 
     def check(self, stream: torch.cuda.Stream | None = None):
         """Wait for the stream and raise FtError if a call met device data out of range or a timeout."""
-        with self._guard():
+        with torch.cuda.device(self.device):
             ft_kv_status(self._stream(stream))
 
     # ---- helpers -------------------------------------------------------------
     def _rows(self, batch, t, heads, name):
-        _need(t.dtype == torch.bfloat16 and t.shape == (batch.num_tokens, heads, self.head_dim) and
-              (t.stride(2) == 1 or t.numel() == 0) and
-              t.device == self.device == batch.device,
-              "%s is a bf16 [num_tokens, heads, %d] tensor of the cache's device with contiguous rows", name,
-              self.head_dim)
+        """Address and strides of a [num_tokens, heads, head_dim] tensor."""
+        if (t.dtype != torch.bfloat16 or t.shape != (batch.num_tokens, heads, self.head_dim) or
+                t.get_device() != self.index or batch.index != self.index):
+            raise ValueError(f"{name} is a bf16 [num_tokens, heads, {self.head_dim}] tensor of the cache's device")
+        s0, s1, s2 = t.stride()
+        _need(s2 == 1 or t.numel() == 0, "%s's rows are contiguous", name)
+        return t.data_ptr(), s0, s1
+
+    def _call(self, name, *args):
+        if torch.cuda.current_device() == self.index:
+            st = getattr(_lib, name)(*args)
+        else:
+            with torch.cuda.device(self.device):
+                st = getattr(_lib, name)(*args)
+        if st:
+            _check(st, name)
 
     def _stream(self, stream):
-        return (stream or torch.cuda.current_stream(self.device)).cuda_stream
+        # (a Stream object of the current stream takes 2 us to make)
+        return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.index)
 
-    def _new_workspace(self, nbytes, stream):
-        if stream is None:
-            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        with torch.cuda.stream(stream):  # the allocator then reuses it in this stream's order
-            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+    def _need_bytes(self, batch, heads):
+        key = (heads, batch.max_q_len)
+        if key not in self._needs:
+            with torch.cuda.device(self.device):
+                self._needs[key] = max(256, ft_kv_attend_workspace(self.c, batch.c, heads))
+        return self._needs[key]
 
-    def _guard(self):
-        return torch.cuda.device(self.device)
+    def _new_workspace(self, s, nbytes, stream):
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):  # reused in this stream's order
+            ws = _workspaces[(self.index, s)] = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        return ws
