@@ -2,6 +2,7 @@
 // the choice of the kernel, the workspace, and the kernel that joins partial
 // sums.
 #include <algorithm>
+#include <type_traits>
 
 #include "driver_api.h"
 #include "kv_attend.h"
@@ -12,72 +13,97 @@ namespace {
 
 // ---------------------------------------------------------------- partial sums
 
-// Block (c, y) joins rows y * R .. of what CTA c of the main kernel began and
+// Block (c, y) joins rows of the row block that CTA c of chunk_kernel began and
 // others went on with: out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, in
-// the order of the tokens.  R = 8: a warp per row (few parts: the cut of a
-// batch with many sequences); R = 1: eight warps share a row's parts, and are
-// summed in order.
-constexpr int kJoinThreads = 256;
+// the order of the tokens.  kOne: a block per row, its eight warps share the
+// parts (few rows of a long sequence, which many CTAs worked on); else a block
+// takes kJoinRows rows, a warp kPer of them at once (many rows, a few parts).
+constexpr int kJoinThreads = 256, kPer = 4, kJoinRows = 8 * kPer;
 
-template <int D, int R>
-__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ AttendArgs a, bool chunk) {
-  constexpr int N = D / 32;
-  __shared__ float s_o[R == 1 ? 8 : 1][D];
+template <int D, bool kOne>
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int N = D / 32, R = kOne ? 1 : kPer;
+  using Vec = typename std::conditional<N == 4, float4, float2>::type;
+  __shared__ float s_o[kOne ? 8 : 1][D];
   __shared__ float s_l[8];
   dec::pdl_wait_primary();
   const int4 u = __ldcg(&a.desc[blockIdx.x]);  // {s, h, row block, last CTA}
   if (u.x < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Seq q = load_seq(a.p, a.b, u.x, a.status);
-  const int rows = chunk ? kChunkRows : kTokenRows;
-  const int r = blockIdx.y * R + (R == 1 ? 0 : warp);
-  const int rr = chunk ? r % kSubRows : r, g = rr % a.G, ti = rr / a.G;
-  const int i_new = chunk ? (u.z * 2 + r / kSubRows) * a.tps + ti : ti;  // the row's new token
-  if (i_new >= q.m || (chunk && ti >= a.tps)) return;  // R = 1: all of the block; R = 8: whole warps
   const int c0 = blockIdx.x, parts = u.w - c0 + 1;
-  // part i: CTA c0's last slot, then the first slot of each CTA after it
-  auto slot = [&](int i) { return (long long)(2 * (c0 + i) + (i == 0)) * rows + r; };
-  float m = -INFINITY;
-  for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(&a.part_ml[slot(i) * 2]));
+  // part i of row r: CTA c0's last slot, then the first slot of each CTA after it
+  auto slot = [&](int i, int r) { return (long long)(2 * (c0 + i) + (i == 0)) * kChunkRows + r; };
+  int row[R], token[R], head[R];
+  float m[R], l[R], acc[R][N];
+  bool any = false;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float base = m == -INFINITY ? 0.0f : m;
-  float acc[N] = {}, l = 0.0f;
-  const int per = R == 1 ? (parts + 7) / 8 : parts, i0 = R == 1 ? warp * per : 0, i1 = min(parts, i0 + per);
-#pragma unroll 4
+  for (int k = 0; k < R; ++k) {
+    row[k] = kOne ? blockIdx.y : blockIdx.y * kJoinRows + k * 8 + warp;
+    const int rr = row[k] % kSubRows, ti = rr / a.G;
+    head[k] = rr - ti * a.G;
+    token[k] = (u.z * 2 + row[k] / kSubRows) * a.tps + ti;
+    if (ti >= a.tps || token[k] >= q.m) token[k] = -1;
+    any |= token[k] >= 0;
+    m[k] = -INFINITY;
+    l[k] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[k][i] = 0.0f;
+  }
+  if (!any) return;  // kOne: all of the block; else whole warps
+  for (int i = lane; i < parts; i += 32)
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (token[k] >= 0) m[k] = fmaxf(m[k], __ldcg(&a.part_ml[slot(i, row[k]) * 2]));
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
+  const int per = kOne ? (parts + 7) / 8 : parts, i0 = kOne ? warp * per : 0, i1 = min(parts, i0 + per);
+#pragma unroll 2
   for (int i = i0; i < i1; ++i) {
-    const long long at = slot(i);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
-    const float f = exp2_approx(ml.x - base);
-    l += f * ml.y;
-    if (N == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + lane);
-      acc[0] += f * v.x; acc[1] += f * v.y; acc[N - 2] += f * v.z; acc[N - 1] += f * v.w;
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_o + at * D) + lane);
-      acc[0] += f * v.x; acc[1] += f * v.y;
+    float2 ml[R];
+    float v[R][N];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      if (token[k] < 0) continue;
+      ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot(i, row[k]));
+      *reinterpret_cast<Vec*>(v[k]) = __ldcg(reinterpret_cast<const Vec*>(a.part_o + slot(i, row[k]) * D) + lane);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (token[k] < 0) continue;
+      const float f = exp2_approx(ml[k].x - (m[k] == -INFINITY ? 0.0f : m[k]));
+      l[k] += f * ml[k].y;
+#pragma unroll
+      for (int n = 0; n < N; ++n) acc[k][n] += f * v[k][n];
     }
   }
-  if (R == 1) {
+  if (kOne) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s_o[R == 1 ? warp : 0][lane * N + i] = acc[i];
-    if (lane == 0) s_l[warp] = l;
+    for (int i = 0; i < N; ++i) s_o[kOne ? warp : 0][lane * N + i] = acc[0][i];
+    if (lane == 0) s_l[warp] = l[0];
     __syncthreads();
     if (warp) return;
-    l = 0.0f;
-    for (int w = 0; w < 8; ++w) l += s_l[w];
+    l[0] = 0.0f;
+    for (int w = 0; w < 8; ++w) l[0] += s_l[w];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      acc[i] = 0.0f;
-      for (int w = 0; w < 8; ++w) acc[i] += s_o[R == 1 ? w : 0][lane * N + i];
+      acc[0][i] = 0.0f;
+      for (int w = 0; w < 8; ++w) acc[0][i] += s_o[kOne ? w : 0][lane * N + i];
     }
   }
-  const float inv = inverse(l);
-  __nv_bfloat16* out = a.out + out_at(a, q, u.y, i_new, g) + lane * N;
 #pragma unroll
-  for (int i = 0; i < N; i += 2)
-    *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
-  if (lane == 0) write_lse(a, q, u.y, i_new, g, m, l);
+  for (int k = 0; k < R; ++k) {
+    if (token[k] < 0) continue;
+    const float inv = inverse(l[k]);
+    __nv_bfloat16* out = a.out + out_at(a, q, u.y, token[k], head[k]) + lane * N;
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[k][i] * inv, acc[k][i + 1] * inv);
+    if (lane == 0) write_lse(a, q, u.y, token[k], head[k], m[k], l[k]);
+  }
 }
 
 }  // namespace
@@ -91,14 +117,14 @@ int sm_count() {
   return n;
 }
 
-cudaError_t launch_combine(const AttendArgs& a, bool chunk, int used, cudaStream_t s) {
+cudaError_t launch_combine(const AttendArgs& a, int used, cudaStream_t s) {
   const bool one = used <= 64;  // rows enough for a block each without many idle blocks
-  const dim3 grid(a.grid, one ? used : (used + 7) / 8);
+  const dim3 grid(a.grid, one ? used : (used + kJoinRows - 1) / kJoinRows);
   if (a.p.head_dim == 128)
-    return one ? launch_dependent(combine_kernel<128, 1>, grid, kJoinThreads, 0, s, a, chunk)
-               : launch_dependent(combine_kernel<128, 8>, grid, kJoinThreads, 0, s, a, chunk);
-  return one ? launch_dependent(combine_kernel<64, 1>, grid, kJoinThreads, 0, s, a, chunk)
-             : launch_dependent(combine_kernel<64, 8>, grid, kJoinThreads, 0, s, a, chunk);
+    return one ? launch_dependent(combine_kernel<128, true>, grid, kJoinThreads, 0, s, a)
+               : launch_dependent(combine_kernel<128, false>, grid, kJoinThreads, 0, s, a);
+  return one ? launch_dependent(combine_kernel<64, true>, grid, kJoinThreads, 0, s, a)
+             : launch_dependent(combine_kernel<64, false>, grid, kJoinThreads, 0, s, a);
 }
 
 namespace {
@@ -145,14 +171,16 @@ using namespace ft::kv;
 
 namespace {
 
-// The workspace: [desc][part_ml][part_o], each part 256-byte aligned.
+// The workspace: [counter][desc][part_ml][part_o], each 256-byte aligned, the
+// counters in one place for every shape.
 struct Workspace {
-  uint64_t ml, o, bytes;
+  uint64_t desc, ml, o, bytes;
 };
 Workspace layout(const ft_kv_pages& p, int grid, int rows) {
   const uint64_t parts = 2ull * grid * rows;
   Workspace w;
-  w.ml = (grid * sizeof(int4) + 255) & ~255ull;
+  w.desc = (kMostCtas * sizeof(unsigned) + 255) & ~255ull;
+  w.ml = (w.desc + grid * sizeof(int4) + 255) & ~255ull;
   w.o = (w.ml + parts * 2 * sizeof(float) + 255) & ~255ull;
   w.bytes = w.o + parts * p.head_dim * sizeof(float);
   return w;
@@ -179,7 +207,7 @@ ft_status check_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32
 
 extern "C" uint64_t ft_kv_attend_workspace(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads) {
   if (check_attend(pages, batch, num_q_heads) != FT_OK) return 0;
-  return layout(*pages, sm_count(), block_rows(*batch, num_q_heads / pages->num_kv_heads)).bytes;
+  return layout(*pages, std::min(sm_count(), kMostCtas), block_rows(*batch, num_q_heads / pages->num_kv_heads)).bytes;
 }
 
 extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads,
@@ -204,7 +232,7 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
     return set_error(FT_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads = %d is above %d", G, kSubRows);
   if (q_token_stride <= 0 || q_head_stride <= 0)
     return set_error(FT_ERR_INVALID_ARG, "q's strides must be positive");
-  const int block = block_rows(*batch, G), grid = sm_count();
+  const int block = block_rows(*batch, G), grid = std::min(sm_count(), kMostCtas);
   const Workspace ws = layout(*pages, grid, block);
   if (workspace_bytes < ws.bytes)
     return set_error(FT_ERR_INVALID_ARG, "workspace of %llu bytes: %llu are needed",
@@ -217,15 +245,21 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   a.Hq = num_q_heads; a.G = G; a.tps = kSubRows / G; a.causal = causal != 0; a.window = window; a.grid = grid;
   if ((st = status_word(&a.status)) != FT_OK) return st;
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  a.desc = reinterpret_cast<int4*>(w);
+  a.counter = reinterpret_cast<unsigned*>(w);
+  a.desc = reinterpret_cast<int4*>(w + ws.desc);
   a.part_ml = reinterpret_cast<float*>(w + ws.ml);
   a.part_o = reinterpret_cast<float*>(w + ws.o);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = block == kTokenRows ? launch_attend_token(a, s) : launch_attend_chunk(a, s);
-  if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
-  // (a chunk block's rows are used without a gap only while its first sub-tile holds them all)
-  const int used = block == kTokenRows || batch->max_q_len <= a.tps ? (int)rows : kChunkRows;
-  if ((e = launch_combine(a, block == kChunkRows, used, s)) != cudaSuccess)
+  cudaError_t e;
+  if (block == kTokenRows) {
+    if ((e = launch_attend_token(a, s)) != cudaSuccess)
+      return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
+    return FT_OK;
+  }
+  if ((e = launch_attend_chunk(a, s)) != cudaSuccess)
+    return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
+  // (a block's rows are used without a gap only while its first sub-tile holds them all)
+  if ((e = launch_combine(a, batch->max_q_len <= a.tps ? (int)rows : kChunkRows, s)) != cudaSuccess)
     return set_error(FT_ERR_CUDA, "attend join launch: %s", cudaGetErrorString(e));
   return FT_OK;
 }

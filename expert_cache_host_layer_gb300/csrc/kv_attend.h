@@ -14,6 +14,7 @@ namespace ft {
 namespace kv {
 
 constexpr int kTokenRows = 16;    // most rows of a (sequence, key head) in token_kernel
+constexpr int kMostCtas = 160;    // of a main kernel's grid, one per SM
 constexpr int kTokenTile = 64;    // tokens per tile of its ring
 constexpr int kChunkRows = 256;   // rows of a block in chunk_kernel: two sub-tiles of 128
 constexpr int kSubRows = 128;
@@ -31,7 +32,8 @@ struct AttendArgs {
   int grid;               // CTAs of the main kernel
   int32_t* status;
   // workspace
-  int4* desc;             // [grid] the (sequence, head, row block) that CTA c begins and does not end: {s, h, row
+  unsigned* counter;      // [grid] token_kernel: parts done of what CTA c begins and does not end; 0 between calls
+  int4* desc;             // [grid] chunk_kernel: the (sequence, head, row block) that CTA c begins and does not end: {s, h, row
                           // block, last CTA}; s = -1: none
   float* part_o;          // [2 grid][rows][D] unnormalised sums: slot 2c of what CTA c finds begun, 2c + 1 of what it
                           // begins and leaves
@@ -202,7 +204,10 @@ struct TokenWalk {
       return true;
     }
   }
-  // last CTA of this (sequence, head)
+  // first and last CTA of this (sequence, head)
+  __device__ __forceinline__ int first_cta() const {
+    return cta_of(base + (long long)h * token_items(tiles) + kPairItems, total, n);
+  }
   __device__ __forceinline__ int last_cta() const {
     return cta_of(base + (long long)(h + 1) * token_items(tiles) - 1, total, n);
   }
@@ -226,10 +231,9 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.
 int sm_count();  // of the current device
 cudaError_t launch_attend_token(const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_attend_chunk(const AttendArgs& a, cudaStream_t s);
-// Joins the partial sums of the (sequence, head, row block)s that a cut
-// divided; `chunk`: chunk_kernel's blocks (else token_kernel's), `used`: rows
-// of a block that any sequence has.
-cudaError_t launch_combine(const AttendArgs& a, bool chunk, int used, cudaStream_t s);
+// Joins the partial sums of chunk_kernel's row blocks that a cut divided;
+// `used`: rows of a block that any sequence has.
+cudaError_t launch_combine(const AttendArgs& a, int used, cudaStream_t s);
 // Pages of k or v as rows of head_dim, boxes of box_rows rows x 128 bytes (or the whole row, if shorter), swizzled.
 bool pages_map(CUtensorMap* m, const ft_kv_pages& p, const void* base, int box_rows);
 // q as [token][head][64 of head_dim], boxes of `tokens` x G heads x 128 bytes, swizzled.

@@ -10,8 +10,10 @@
 // Split: the batch's tiles of 64 tokens, laid end to end over (sequence, key
 // head, tile), are cut into equal contiguous ranges, one per CTA and one CTA
 // per SM, whatever the lengths are.  A (sequence, head) that a cut divides
-// leaves partial sums (unnormalised out, m, l) in the workspace, which
-// combine_kernel joins in tile order.
+// leaves partial sums (unnormalised out, m, l) in the workspace; the CTA that
+// finishes the last part joins them, in tile order.  (A kernel of its own for
+// that took 5 us and a launch; with every part from another CTA, 152 of them,
+// one CTA reads 0.6 MB, some 5 us.)
 //
 // CTA: two producer warps (K, V) and kWarps consumer warps in sets of four.  The
 // producers load a tile as swizzled TMA boxes of as many tokens as a page holds
@@ -65,7 +67,8 @@ struct Layout {
   static constexpr int kScaleOff = kStages * kStageBytes;
   static constexpr int kScaleBytes = kFp8 ? kStages * 2 * kTokenTile : 0;
   static constexpr int kRedOff = kScaleOff + kScaleBytes;
-  static constexpr int kMlOff = kRedOff + kWarps * kRedRows * kRowFloats * 4;
+  static constexpr int kRedBytes = kWarps * kRedRows * kRowFloats * 4, kFacBytes = kMostCtas * 8 * NB * 4;
+  static constexpr int kMlOff = kRedOff + (kRedBytes > kFacBytes ? kRedBytes : kFacBytes);
   static constexpr int kTotOff = kMlOff + kWarps * 8 * NB * 2 * 4;  // a row's maximum and 1 / sum, of all warps
   static constexpr int kBarOff = kTotOff + 8 * NB * 2 * 4;
   static constexpr int kSmem = kBarOff + 2 * kStages * 8 + 16 + 1024;
@@ -478,7 +481,6 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
     auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); };
     const int set = warp / kSet, grp = warp % kSet;
     int it = 0;
-    int4 begun = make_int4(-1, 0, 0, 0);
     TokenWalk w(a, rg);
     Warp<D, kFp8, NB> ws;
     while (w.next(a)) {
@@ -486,10 +488,13 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
       const int hi = w.hi, lo = w.lo;
       // every row sees [last.lo, first.hi): from the last new token's start to the first one's end
       const Span first = visible(a, w.q, 0), last = visible(a, w.q, max(0, w.q.m - 1));
-      for (int t = w.t0; t < w.t1; ++t, ++it) {
-        if (it % L::kSets != set) continue;
-        const int st = it % L::kStages, j0 = t * kTokenTile + grp * kGroup;
-        const bool live = wait_or_abort(&full[st], (it / L::kStages) & 1, a.status, abort_flag);
+      // this set's tiles: those whose place in the CTA's sequence of tiles is set modulo kSets
+      const int first_turn = (set + L::kSets - it % L::kSets) % L::kSets;
+      int st = (it + first_turn) % L::kStages;
+      uint32_t ph = (it + first_turn) / L::kStages & 1;
+      for (int t = w.t0 + first_turn; t < w.t1; t += L::kSets) {
+        const int j0 = t * kTokenTile + grp * kGroup;
+        const bool live = wait_or_abort(&full[st], ph, a.status, abort_flag);
         if (live && j0 < hi && j0 + kGroup > lo) {
           const uint32_t kb = dec::smem_addr(smem + st * L::kStageBytes) + grp * kGroup * L::kLine;
           const uint8_t* sc = smem + L::kScaleOff + st * 2 * kTokenTile + grp * kGroup;
@@ -498,7 +503,13 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) dec::mbar_arrive(&empty[st]);
+        st += L::kSets;
+        if (st >= L::kStages) {
+          st -= L::kStages;
+          ph ^= 1;
+        }
       }
+      it += w.t1 - w.t0;
       // join the warps, kRedRows rows at a time
       const int g = lane >> 2, c = lane & 3;
 #pragma unroll
@@ -518,7 +529,6 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
       const int rows = min(kRows, w.q.m * a.G);
       const bool whole = w.begins && w.ends;
       const long long slot = 2LL * blockIdx.x + w.begins;
-      if (w.begins && !w.ends) begun = make_int4(w.s, w.h, 0, w.last_cta());
       if (threadIdx.x < rows) {  // (read after the next barrier)
         const int r = threadIdx.x;
         float mm = -INFINITY, l = 0.0f;
@@ -580,8 +590,64 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
           sync();
         }
       }
+      if (whole) continue;
+      // the last of the parts joins them
+      const int c0 = w.first_cta(), parts = w.last_cta() - c0 + 1;
+      __threadfence();
+      sync();
+      if (threadIdx.x == 0) {
+        const bool all = atomicAdd(&a.counter[c0], 1u) + 1u == (unsigned)parts;
+        if (all) a.counter[c0] = 0u;
+        tot[0].x = all ? 1.0f : 0.0f;
+      }
+      sync();
+      const bool join = tot[0].x != 0.0f;
+      sync();
+      if (!join) continue;
+      __threadfence();
+      // part i: CTA c0's last slot, then the first slot of each CTA after it
+      auto part = [&](int i, int r) { return (long long)(2 * (c0 + i) + (i == 0)) * kTokenRows + r; };
+      float* fac = red;  // [parts][kRows] 2^(m_i - m)
+      for (int r = warp; r < rows; r += L::kWarps) {
+        float mm = -INFINITY, l = 0.0f;
+        for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, __ldcg(&a.part_ml[part(i, r) * 2]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        for (int i = lane; i < parts; i += 32) {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + part(i, r));
+          const float f = y.x == -INFINITY ? 0.0f : exp2_approx(y.x - mm);
+          fac[i * kRows + r] = f;
+          l += f * y.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0) {
+          tot[r] = make_float2(mm, inverse(l));
+          write_lse(a, w.q, w.h, r / a.G, r % a.G, mm, l);
+        }
+      }
+      sync();
+      for (int e = threadIdx.x * 4; e < rows * D; e += kConsumers * 4) {
+        const int r = e / D, d = e % D;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float4* at = reinterpret_cast<const float4*>(a.part_o + ((2LL * c0 + 1) * kTokenRows + r) * D + d);
+#pragma unroll 8
+        for (int i = 0; i < parts; ++i) {
+          const float4 y = __ldcg(at + (i ? (2 * i - 1) * (kTokenRows * D / 4) : 0));
+          const float f = fac[i * kRows + r];
+          sum.x += f * y.x;
+          sum.y += f * y.y;
+          sum.z += f * y.z;
+          sum.w += f * y.w;
+        }
+        const float inv = tot[r].y;
+        __nv_bfloat162* out =
+            reinterpret_cast<__nv_bfloat162*>(a.out + out_at(a, w.q, w.h, r / a.G, r % a.G) + d);
+        out[0] = __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
+        out[1] = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
+      }
+      sync();
     }
-    if (threadIdx.x == 0) a.desc[blockIdx.x] = begun;
   }
   dec::pdl_launch_dependents();
 }

@@ -172,5 +172,5 @@ class KVPages:
 
     def _new_workspace(self, s, nbytes, stream):
         with torch.cuda.device(self.device), torch.cuda.stream(stream):  # reused in this stream's order
-            ws = _workspaces[(self.index, s)] = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            ws = _workspaces[(self.index, s)] = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         return ws

@@ -427,7 +427,7 @@ ft_status ft_step_graph_destroy(ft_step_graph* graph);
  * attention over it.  No handle: the caller owns every byte, describes one
  * layer's cache with ft_kv_pages and one step's sequences with ft_kv_batch
  * (both are host structs read during the call, and may be kept for many), and
- * passes the stream.  Nothing is kept from one call for the next, and nothing
+ * passes the stream.  No result is kept from one call for the next, and nothing
  * is allocated; the calls can be captured in a CUDA graph.
  *
  * Layout.  A page holds page_tokens consecutive tokens of one sequence, for
@@ -513,8 +513,9 @@ ft_status ft_kv_read(const ft_kv_pages* pages, const ft_kv_batch* batch, const i
  * [num_tokens][num_q_heads] (natural logarithm of the softmax's denominator,
  * scores scaled), or NULL.  Softmax statistics and sums are fp32;
  * probabilities are rounded to bf16 for the product with v.
- * workspace: device, 256-byte aligned, ft_kv_attend_workspace bytes; its
- * content means nothing between calls, and calls on one stream can share it. */
+ * workspace: device, 256-byte aligned, ft_kv_attend_workspace bytes, zero
+ * before its first use (each call leaves its counters zero again); calls that
+ * follow one another on a stream, of any shape, can share it. */
 ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads, const void* q,
                        int64_t q_token_stride, int64_t q_head_stride, void* out, int64_t out_token_stride,
                        int64_t out_head_stride, float* lse, float scale, int32_t causal, int32_t window,
