@@ -186,9 +186,22 @@ Workspace layout(const ft_kv_pages& p, int grid, int rows) {
   return w;
 }
 
-// Rows of a block of the kernel that takes the batch: token_kernel where every
-// (sequence, key head) fits its 16 rows, else chunk_kernel.
-int block_rows(const ft_kv_batch& b, int G) { return (long long)b.max_q_len * G <= kTokenRows ? kTokenRows : kChunkRows; }
+// Which kernel takes what.  A (sequence, key head) of up to 16 rows is
+// token_kernel's, one of more chunk_kernel's: its tiles have 128 rows whether
+// they are used or not (a batch of 32 decoding sequences beside a chunk, e4m3:
+// 96 us in chunk_kernel alone).  A batch that may hold both gets both, one
+// after the other; there token_kernel takes up to 8 rows, its faster form,
+// unless a single token has more.
+struct Split {
+  int small;  // rows of the largest sequence that is token_kernel's
+  bool token, chunk;
+};
+Split split(const ft_kv_batch& b, int G) {
+  const long long most = (long long)b.max_q_len * G;
+  if (most <= kTokenRows) return {most <= 8 ? 8 : kTokenRows, true, false};
+  if ((long long)b.num_seqs * b.max_q_len <= b.num_tokens || G > kTokenRows) return {0, false, true};  // all as long, or no single token fits
+  return {G <= 8 ? 8 : kTokenRows, true, true};
+}
 
 ft_status check_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads) {
   ft_status st = check_pages(pages);
@@ -207,7 +220,8 @@ ft_status check_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32
 
 extern "C" uint64_t ft_kv_attend_workspace(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads) {
   if (check_attend(pages, batch, num_q_heads) != FT_OK) return 0;
-  return layout(*pages, std::min(sm_count(), kMostCtas), block_rows(*batch, num_q_heads / pages->num_kv_heads)).bytes;
+  const Split sp = split(*batch, num_q_heads / pages->num_kv_heads);
+  return layout(*pages, std::min(sm_count(), kMostCtas), sp.chunk ? kChunkRows : kTokenRows).bytes;
 }
 
 extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads,
@@ -232,8 +246,9 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
     return set_error(FT_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads = %d is above %d", G, kSubRows);
   if (q_token_stride <= 0 || q_head_stride <= 0)
     return set_error(FT_ERR_INVALID_ARG, "q's strides must be positive");
-  const int block = block_rows(*batch, G), grid = std::min(sm_count(), kMostCtas);
-  const Workspace ws = layout(*pages, grid, block);
+  const Split sp = split(*batch, G);
+  const int grid = std::min(sm_count(), kMostCtas);
+  const Workspace ws = layout(*pages, grid, sp.chunk ? kChunkRows : kTokenRows);
   if (workspace_bytes < ws.bytes)
     return set_error(FT_ERR_INVALID_ARG, "workspace of %llu bytes: %llu are needed",
                      (unsigned long long)workspace_bytes, (unsigned long long)ws.bytes);
@@ -242,7 +257,7 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   a.q = static_cast<const __nv_bfloat16*>(q); a.out = static_cast<__nv_bfloat16*>(out); a.lse = lse;
   a.qts = q_token_stride; a.qhs = q_head_stride; a.ots = out_token_stride; a.ohs = out_head_stride;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.Hq = num_q_heads; a.G = G; a.tps = kSubRows / G; a.causal = causal != 0; a.window = window; a.grid = grid;
+  a.Hq = num_q_heads; a.G = G; a.tps = kSubRows / G; a.causal = causal != 0; a.window = window; a.grid = grid; a.small = sp.small;
   if ((st = status_word(&a.status)) != FT_OK) return st;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.counter = reinterpret_cast<unsigned*>(w);
@@ -250,16 +265,11 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   a.part_ml = reinterpret_cast<float*>(w + ws.ml);
   a.part_o = reinterpret_cast<float*>(w + ws.o);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (block == kTokenRows) {
-    if ((e = launch_attend_token(a, s)) != cudaSuccess)
-      return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
-    return FT_OK;
-  }
-  if ((e = launch_attend_chunk(a, s)) != cudaSuccess)
-    return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
+  cudaError_t e = cudaSuccess;
+  if (sp.token) e = launch_attend_token(a, s);
+  if (e == cudaSuccess && sp.chunk) e = launch_attend_chunk(a, s);
   // (a block's rows are used without a gap only while its first sub-tile holds them all)
-  if ((e = launch_combine(a, batch->max_q_len <= a.tps ? (int)rows : kChunkRows, s)) != cudaSuccess)
-    return set_error(FT_ERR_CUDA, "attend join launch: %s", cudaGetErrorString(e));
+  if (e == cudaSuccess && sp.chunk) e = launch_combine(a, batch->max_q_len <= a.tps ? (int)rows : kChunkRows, s);
+  if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "attend launch: %s", cudaGetErrorString(e));
   return FT_OK;
 }

@@ -29,6 +29,7 @@ struct AttendArgs {
   float scale_log2;       // scale * log2(e)
   int Hq, G, causal, window;
   int tps;                // chunk_kernel: new tokens of a sub-tile of 128 rows, 128 / G
+  int small;              // sequences of up to so many rows a head are token_kernel's, the others chunk_kernel's
   int grid;               // CTAs of the main kernel
   int32_t* status;
   // workspace
@@ -56,6 +57,14 @@ __device__ __forceinline__ Span visible(const AttendArgs& a, const Seq& q, int i
   v.hi = a.causal ? min(q.n, max(0, pos + 1)) : q.n;
   v.lo = a.window ? min(v.hi, max(0, pos - a.window + 1)) : 0;
   return v;
+}
+
+// Sequence s as token_kernel (or chunk_kernel) sees it: without new tokens if it is the other's.
+template <bool kToken>
+__device__ __forceinline__ Seq own_seq(const AttendArgs& a, int s) {
+  Seq q = load_seq(a.p, a.b, s, a.status);
+  if ((q.m * a.G <= a.small) != kToken) q.m = 0;
+  return q;
 }
 
 // Whole warp: wait for phase `parity` of a barrier; false if the CTA has
@@ -159,7 +168,7 @@ __device__ __forceinline__ Range token_range(const AttendArgs& a, long long* pre
   return cut(a, pre, scan, [&](int s) {
     if (s == a.b.num_seqs) return 0LL;
     Span seen;
-    return (long long)token_items(token_tiles(a, load_seq(a.p, a.b, s, a.status), &seen)) * a.p.num_kv_heads;
+    return (long long)token_items(token_tiles(a, own_seq<true>(a, s), &seen)) * a.p.num_kv_heads;
   });
 }
 // The parts of (sequence, head)s in a CTA's range, one after the other.
@@ -179,7 +188,7 @@ struct TokenWalk {
     for (;;) {
       if (w >= end) return false;
       if (loaded != s) {
-        q = load_seq(a.p, a.b, s, a.status);
+        q = own_seq<true>(a, s);
         Span seen;
         tiles = token_tiles(a, q, &seen);
         lo = seen.lo;

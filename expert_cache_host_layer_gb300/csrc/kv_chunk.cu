@@ -269,7 +269,7 @@ struct ChunkWalk {
             h = 0;
             do {
               ++s;
-              q = load_seq(a.p, a.b, s, a.status);
+              q = own_seq<false>(a, s);
             } while (q.m == 0);
             nb = blocks_of(a, q);
           }
@@ -302,7 +302,7 @@ struct ChunkWalk {
   __device__ __forceinline__ void find(const AttendArgs& a, int lane) {
     long long per;
     for (;; ++s) {
-      q = load_seq(a.p, a.b, s, a.status);
+      q = own_seq<false>(a, s);
       per = head_items(a, q, lane);
       if (w - base < per * a.p.num_kv_heads) break;
       base += per * a.p.num_kv_heads;
@@ -1119,7 +1119,7 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
   long long* scan = reinterpret_cast<long long*>(s.base);
   const Range rg = cut(a, pre, scan, [&](int seq) {
     // (a warp's lanes are at different sequences; a long one is summed by all)
-    const Seq q = seq < a.b.num_seqs ? load_seq(a.p, a.b, seq, a.status) : Seq{0, 0, 0};
+    const Seq q = seq < a.b.num_seqs ? own_seq<false>(a, seq) : Seq{0, 0, 0};
     const int nb = blocks_of(a, q);
     long long n = 0;
     if (nb <= 8)

@@ -661,7 +661,7 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap& mk, const CUtensorMap
 }
 template <int D, bool kFp8>
 cudaError_t launch_rows(const AttendArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-  return a.b.max_q_len * a.G <= 8 ? launch<D, kFp8, 1>(a, mk, mv, s) : launch<D, kFp8, 2>(a, mk, mv, s);
+  return a.small <= 8 ? launch<D, kFp8, 1>(a, mk, mv, s) : launch<D, kFp8, 2>(a, mk, mv, s);
 }
 
 }  // namespace
