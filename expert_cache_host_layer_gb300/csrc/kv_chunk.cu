@@ -26,8 +26,6 @@
 //                    with P read from TMEM and V as it lies (token-major)
 //   warp 10          Q of both sub-tiles by TMA as soon as the block before has
 //                    its last score tile
-//   warp 11          bf16 cache: V's tiles at the edge of what the rows see (see
-//                    mend)
 //   warps 12-19      quantised cache: expand the codes of a raw ring, times their
 //                    scales, into bf16 tiles of the layout that the MMA reads
 //
@@ -71,10 +69,10 @@ struct Layout {
   static constexpr int kLine = kFp8 ? 64 : 128;                         // bytes of a row in a softmax warp's staging
   static constexpr int kOutOff = kRawOff + kRaw * kRawBytes;
   static constexpr int kBarOff = kOutOff + 8 * 32 * kLine;
-  static constexpr int kBars = 2 * kStages + 2 * kRaw + 2 * kUnits + 14 + 3;
+  static constexpr int kBars = 2 * kStages + 2 * kRaw + 2 * kUnits + 14 + 1;
   static constexpr int kUnitOff = kBarOff + (kBars * 8 + 15) / 16 * 16;
   static constexpr int kMiscOff = kUnitOff + kUnits * 96;
-  static constexpr int kSmem = kMiscOff + 48 + 4 * kStages + 1024;
+  static constexpr int kSmem = kMiscOff + 16 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kStages * kTileBytes >= (kMaxSeqs + 1) * 8 + 1024, "the prefix sums fit the ring before it fills");
 };
@@ -221,7 +219,7 @@ struct Unit {
   int f0[2], f1[2];   // those of them that each sub-tile has (none: f0 >= f1)
   int lo, hi, all_lo, all_hi;
   int begins, ends, last;
-  int nan_v;          // quantised cache: some value of the part is NaN (see expand)
+  int odd;            // some value of the part is not finite (see mend, expand)
   int pad[4];
   __device__ __forceinline__ Seq seq() const { return Seq{q0, m, n}; }
   __device__ __forceinline__ bool any(int sub) const { return f0[sub] < f1[sub]; }
@@ -229,7 +227,6 @@ struct Unit {
   // row, [p0, p1) and [p2, p3) of them not by all
   struct Edge {
     int r0, r1, p0, p1, p2, p3;
-    __device__ __forceinline__ bool any() const { return (r0 & 15) || (r1 & 15) || p0 < p1 || p2 < p3; }
   };
   __device__ __forceinline__ Edge edge(int t) const {
     Edge e;
@@ -294,7 +291,7 @@ struct ChunkWalk {
       u.begins = r0 == 0;
       u.ends = r1 == nt;
       u.last = cta_of(at + items - 1, total, n);
-      u.nan_v = 0;
+      u.odd = 0;
       return true;
     }
   }
@@ -334,12 +331,10 @@ struct Shared {
   uint8_t* base;
   uint64_t *full, *empty, *rfull, *rempty, *ufull, *uempty;
   uint64_t *qfull, *qempty, *landed, *sfull, *pfull, *pfull2, *ofull;  // per sub-tile
-  uint64_t *drain, *mended, *asked;
+  uint64_t* drain;
   Unit* unit;
   uint32_t* tmem;
   volatile int* abort_flag;
-  volatile int* poison;  // [2][2] first and last tile with values that a sub-tile adds at its block's end
-  volatile int* took;    // [stages] V's tile had values that are not finite where not every row sees them
 };
 
 template <int D, bool kFp8>
@@ -367,13 +362,9 @@ __device__ __forceinline__ Shared carve(uint8_t* raw) {
   s.pfull2 = take(2);
   s.ofull = take(2);
   s.drain = take(1);
-  s.mended = take(1);
-  s.asked = take(1);
   s.unit = reinterpret_cast<Unit*>(s.base + L::kUnitOff);
   s.tmem = reinterpret_cast<uint32_t*>(s.base + L::kMiscOff);
   s.abort_flag = reinterpret_cast<volatile int*>(s.tmem + 1);
-  s.poison = reinterpret_cast<volatile int*>(s.tmem + 4);
-  s.took = s.poison + 4;
   return s;
 }
 
@@ -469,78 +460,48 @@ __device__ void produce(const AttendArgs& a, const Range& rg, const Shared& s, c
 
 // ---------------------------------------------------------------- V at the edge
 
-// V rows (tokens) [r0, r1) of a tile to zero; whole warp.
+// A bf16 tile at the edge of what the rows see, by the warpgroup whose P goes to
+// it first.  Tokens that no row sees hold anything (a page's unused end, an
+// evicted page): those within the MMA's 16-token steps are set to zero.  Of
+// tokens that some rows see and others do not, values that are not finite are
+// set to zero too, lest 0 * V reach the others; the rows that see them add them
+// at the block's end.  Returns whether there were any (any thread's).
 template <int D>
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int r1, int lane) {
+__device__ __forceinline__ bool mend(uint8_t* tile, const Unit::Edge& e, int tid) {
   constexpr int kPer = D / 8;
-  for (int i = r0 * kPer + lane; i < r1 * kPer; i += 32) {
+  // 16-byte chunk i of the tile (rows are mended whole, or chunk by chunk in place: the swizzle does not matter)
+  auto chunk = [&](int i) {
     const int r = i / kPer, ch = i % kPer;
-    *reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
-  }
-}
-// Values of V rows [r0, r1) that are not finite, set to zero; whether there were any.
-template <int D>
-__device__ __forceinline__ bool take_not_finite(uint8_t* tile, int r0, int r1, int lane) {
-  constexpr int kPer = D / 8, kBatch = 8;
-  bool any = false;
-  for (int i0 = r0 * kPer + lane; i0 < r1 * kPer; i0 += 32 * kBatch) {
-    uint4 v[kBatch];
-    auto at = [&](int k) {
-      const int i = i0 + 32 * k, r = i / kPer, ch = i % kPer;
-      return reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) << 4));
-    };
+    return reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) << 4));
+  };
+  auto zero = [&](int r0, int r1) {
+    for (int i = r0 * kPer + tid; i < r1 * kPer; i += 128) *chunk(i) = make_uint4(0, 0, 0, 0);
+  };
+  bool odd = false;
+  auto take = [&](int r0, int r1) {
+#pragma unroll 4
+    for (int i = r0 * kPer + tid; i < r1 * kPer; i += 128) {
+      uint4 v = *chunk(i);
+      uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+      // an exponent of all ones carries into the sign's place
+      uint32_t hit = 0;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) v[k] = i0 + 32 * k < r1 * kPer ? *at(k) : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < 4; ++k) hit |= (x[k] & 0x7f807f80u) + 0x00800080u;
+      if (!(hit & 0x80008000u)) continue;
+      odd = true;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-      uint32_t y[4];
-      bool bad = false;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool lo = (x[j] & 0x7f80u) == 0x7f80u, hi = (x[j] & 0x7f800000u) == 0x7f800000u;
-        y[j] = x[j] & (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
-        bad |= lo | hi;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t bad = ((x[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        x[k] &= ~((bad & 0x8000u ? 0xffffu : 0u) | (bad & 0x80000000u ? 0xffff0000u : 0u));
       }
-      if (bad) *at(k) = make_uint4(y[0], y[1], y[2], y[3]);
-      any |= bad;
+      *chunk(i) = v;
     }
-  }
-  return __any_sync(0xffffffffu, any);
-}
-
-// One warp, while the tile's softmax runs.  Tokens of a bf16 tile that no row sees hold
-// anything (a page's unused end, an evicted page): those within the MMA's
-// 16-token steps are set to zero.  Of tokens that some rows see and others do
-// not, values that are not finite are set to zero too, lest 0 * V reach the
-// others; the rows that see them add them at the block's end.
-template <int D>
-__device__ void mend(const AttendArgs& a, const Shared& s, int lane) {
-  using L = Layout<D, false>;
-  Turn<L::kStages> vt;  // the next V
-  vt.next();
-  uint32_t n = 0;
-  Units units;
-  while (const Unit* u = units.next(a, s)) {
-    for (int t = u->t0; t < u->t1; ++t, vt.next(), vt.next()) {
-      const Unit::Edge e = u->edge(t);
-      if (!e.any()) continue;
-      // asked by the MMA warp, which has not used this V yet: the ring cannot be a turn ahead or behind
-      if (!wait_or_abort(s.asked, n++ & 1, a.status, s.abort_flag)) return;
-      if (!wait_or_abort(&s.full[vt.st], vt.ph, a.status, s.abort_flag)) return;
-      uint8_t* V = s.base + L::kRingOff + vt.st * L::kTileBytes;
-      zero_rows<D>(V, e.r0 & ~15, e.r0, lane);
-      zero_rows<D>(V, e.r1, (e.r1 + 15) & ~15, lane);
-      bool took = false;
-      if (e.p0 < e.p1) took |= take_not_finite<D>(V, e.p0, e.p1, lane);
-      if (e.p2 < e.p3) took |= take_not_finite<D>(V, e.p2, e.p3, lane);
-      s.took[vt.st] = took;
-      fence_async();
-      __syncwarp();
-      if (lane == 0) dec::mbar_arrive(s.mended);
-    }
-    units.done(s, lane);
-  }
+  };
+  zero(e.r0 & ~15, e.r0);
+  zero(e.r1, (e.r1 + 15) & ~15);
+  if (e.p0 < e.p1) take(e.p0, e.p1);
+  if (e.p2 < e.p3) take(e.p2, e.p3);
+  return odd;
 }
 
 // ---------------------------------------------------------------- MMA
@@ -556,11 +517,10 @@ __device__ void multiply(const AttendArgs& a, const Shared& s, uint32_t tmem, in
   constexpr int kSteps = kTile / 16;
   Turn<L::kStages> kt, vt;  // places of the next K and V
   vt.next();
-  uint32_t pq[2] = {0, 0}, pp[2] = {0, 0}, pm = 0;
+  uint32_t pq[2] = {0, 0}, pp[2] = {0, 0};
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_or_abort(bar, parity, a.status, s.abort_flag); };
   Units units;
   while (const Unit* u = units.next(a, s)) {
-    int bad0 = 0x7fffffff, bad1 = -1;
     bool live[2] = {false, false};  // O_w has been written in this part
     const int t0 = u->t0, t1 = u->t1;
     const int f0[2] = {u->f0[0], u->f0[1]}, f1[2] = {u->f1[0], u->f1[1]};
@@ -574,14 +534,6 @@ __device__ void multiply(const AttendArgs& a, const Shared& s, uint32_t tmem, in
           const Unit::Edge e = u->edge(t - 1);
           k0 = e.r0 >> 4;
           k1 = (e.r1 + 15) >> 4;
-          if (!kFp8 && e.any()) {
-            if (!wait(s.mended, pm)) goto out;
-            pm ^= 1;
-            if (s.took[vt.st]) {
-              bad0 = min(bad0, t - 1);
-              bad1 = t - 1;
-            }
-          }
         }
       }
       const uint32_t kd = ring + kt.st * (L::kTileBytes >> 4), vd = ring + vt.st * (L::kTileBytes >> 4) + kVLead;
@@ -614,10 +566,7 @@ __device__ void multiply(const AttendArgs& a, const Shared& s, uint32_t tmem, in
           live[sub] = true;
         }
         if (t < t1) {  // S_sub = Q_sub K(t)^T
-          if (sub == 0) {
-            if (!kFp8 && (t < e0 || t >= e1) && u->edge(t).any() && lane == 0) dec::mbar_arrive(s.asked);
-            if (!wait(&s.full[kt.st], kt.ph)) goto out;
-          }
+          if (sub == 0 && !wait(&s.full[kt.st], kt.ph)) goto out;
           if (t >= f0[sub] && t < f1[sub]) {
             if (t == f0[sub]) {
               if (!wait(&s.qfull[sub], pq[sub])) goto out;
@@ -650,16 +599,6 @@ __device__ void multiply(const AttendArgs& a, const Shared& s, uint32_t tmem, in
         kt.next();
       }
     }
-    if (lane == 0) {
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
-        if (live[sub]) {  // (its warpgroup has read the block before: it has written P since)
-          s.poison[sub * 2] = bad0;
-          s.poison[sub * 2 + 1] = bad1;
-          dec::mbar_arrive(&s.ofull[sub]);
-        }
-    }
-    __syncwarp();
     if (elect()) {
       if (live[0]) commit(&s.ofull[0]);
       if (live[1]) commit(&s.ofull[1]);
@@ -744,13 +683,10 @@ __device__ __forceinline__ void stage_out(uint8_t* stage, int lane, long long at
   }
   __syncwarp();
 }
-// Adds to a row's columns k .. k + 31 the values that are not finite of tokens
-// [from, to), those that every row sees left out: they went through the product.
+// Adds to a row's columns k .. k + 31 the values of tokens [from, to) that are not finite.
 template <int D>
-__device__ __noinline__ void add_not_finite(const AttendArgs& a, int s, int h, int all_lo, int all_hi, int from, int to,
-                                            int k, float* o) {
+__device__ __noinline__ void add_not_finite(const AttendArgs& a, int s, int h, int from, int to, int k, float* o) {
   for (int j = from; j < to; ++j) {
-    if (j >= all_lo && j < all_hi) continue;
     const int page = max(0, load_page(a.p, a.b, s, j / a.p.page_tokens, a.status));
     const __nv_bfloat16* at =
         static_cast<const __nv_bfloat16*>(a.p.v) +
@@ -820,9 +756,10 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
   const int my_token = tid / a.G;
   uint8_t* stage = s.base + L::kOutOff + (sub * 4 + quarter) * 32 * L::kLine;
   uint32_t ns = 0, no = 0;
+  int tiles = 0;  // of the blocks before
   int4 begun = make_int4(-1, 0, 0, 0);
   Units units;
-  while (const Unit* u = units.next(a, s)) {
+  while (Unit* u = units.next(a, s)) {
     const int i_new = (u->rb * 2 + sub) * a.tps + my_token;  // this row's new token
     const bool mine = my_token < a.tps && i_new < u->m;
     const bool any = u->any(sub);
@@ -842,21 +779,26 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
       // long, its warps waiting for instructions).
       constexpr int kHeld = 64;
       float x[kHeld];
+      const bool edge = j0 < all_lo || j0 + kTile > all_hi;  // some row does not see all of the tile
+      const int from = lo - j0, end = hi - j0;
       auto load = [&](int col) {  // kHeld scores from column col, the unseen ones -inf
 #pragma unroll
         for (int k = 0; k < kHeld; k += 32) ld32(ts + col + k, x + k);
         ld_wait();
-        if (j0 + kTile > all_hi) {  // some row does not see the last of the tile
-          const int end = hi - j0 - col;
+        if (edge) {
 #pragma unroll
-          for (int k = 0; k < kHeld; ++k)
-            if (k >= end) x[k] = -INFINITY;
-        }
-        if (j0 < all_lo) {  // or the first
-          const int from = lo - j0 - col;
+          for (int k0 = 0; k0 < kHeld; k0 += 32) {  // 32 columns that some row of the warp does not see all of
+            if (__any_sync(0xffffffffu, end < col + k0 + 32)) {
 #pragma unroll
-          for (int k = 0; k < kHeld; ++k)
-            if (k < from) x[k] = -INFINITY;
+              for (int k = k0; k < k0 + 32; ++k)
+                if (k >= end - col) x[k] = -INFINITY;
+            }
+            if (__any_sync(0xffffffffu, from > col + k0)) {
+#pragma unroll
+              for (int k = k0; k < k0 + 32; ++k)
+                if (k < from - col) x[k] = -INFINITY;
+            }
+          }
         }
       };
       float top = -INFINITY;
@@ -891,6 +833,14 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
       }
       const float base = m == -INFINITY ? 0.0f : m;
       float2 sum = make_float2(0.0f, 0.0f);
+      // (sub-tile 0's P goes to V first, unless only the other has the tile)
+      if (!kFp8 && edge && (sub == 0 || t < u->f0[0] || t >= u->f1[0])) {
+        const int i = 2 * (tiles + t - u->t0) + 1;  // V's place among the ring's tiles
+        if (!wait_or_abort(&s.full[i % L::kStages], i / L::kStages & 1, a.status, s.abort_flag)) return;
+        if (mend<D>(s.base + L::kRingOff + i % L::kStages * L::kTileBytes, u->edge(t), tid))
+          *reinterpret_cast<volatile int*>(&u->odd) = 1;
+        fence_async();
+      }
 #pragma unroll 1
       for (int col = 0; col < 128; col += kHeld) {
         uint32_t p[kHeld / 2];
@@ -927,11 +877,9 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
       no ^= 1;
       fence_after();
     }
-    bool poisoned = false;
-    if (kFp8 && any && *const_cast<const volatile int*>(&u->nan_v) && mine &&
-        any_nan_value(a, u->s, u->h, max(lo, u->t0 * kTile), min(hi, u->t1 * kTile)))
-      poisoned = true;
-    const int bad0 = any && !kFp8 ? s.poison[sub * 2] : 1, bad1 = any && !kFp8 ? s.poison[sub * 2 + 1] : 0;
+    const bool odd = any && *const_cast<const volatile int*>(&u->odd) && mine;
+    const int first_tok = max(lo, u->t0 * kTile), last_tok = min(hi, u->t1 * kTile);
+    const bool poisoned = kFp8 && odd && any_nan_value(a, u->s, u->h, first_tok, last_tok);
     for (int k = 0; k < D; k += 32) {
       float o[32];
       if (any) {
@@ -941,9 +889,10 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = 0.0f;
       }
-      if (bad0 <= bad1 && mine) {
+      if (!kFp8 && odd) {  // (tokens that every row sees went through the product)
         float add[32] = {};
-        add_not_finite<D>(a, u->s, u->h, all_lo, all_hi, max(lo, bad0 * kTile), min(hi, (bad1 + 1) * kTile), k, add);
+        add_not_finite<D>(a, u->s, u->h, first_tok, min(last_tok, all_lo), k, add);
+        add_not_finite<D>(a, u->s, u->h, max(first_tok, max(all_lo, all_hi)), last_tok, k, add);
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] += add[i];
       }
@@ -977,6 +926,7 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
         }
       }
     }
+    tiles += u->t1 - u->t0;
     fence_before();  // the next block's MMAs write O after these reads
     units.done(s, lane);
   }
@@ -1037,7 +987,7 @@ __device__ void expand(const AttendArgs& a, const Shared& s, int tid) {
           bool drop = edge && (r < seen0 || r >= seen1);
           if (kv == 1 && b == kNanScale && !drop) {
             drop = true;
-            *reinterpret_cast<volatile int*>(&u->nan_v) = 1;
+            *reinterpret_cast<volatile int*>(&u->odd) = 1;
           }
           if (drop) c = make_uint4(0, 0, 0, 0);
           // 2^(b - 127) as bf16 (byte 0 or 255, unseen or dropped: times codes 0)
@@ -1090,7 +1040,7 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
     }
     for (int i = 0; i < kUnits; ++i) {
       dec::mbar_init(&s.ufull[i], 1);
-      dec::mbar_init(&s.uempty[i], 8 + 2 + (kFp8 ? kCvtWarps : 1));  // softmax, MMA, Q, expanding or mending
+      dec::mbar_init(&s.uempty[i], 8 + 2 + (kFp8 ? kCvtWarps : 0));  // softmax, MMA, Q, expanding
     }
     for (int i = 0; i < 2; ++i) {
       dec::mbar_init(&s.qfull[i], 1);
@@ -1099,11 +1049,9 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
       dec::mbar_init(&s.sfull[i], 1);
       dec::mbar_init(&s.pfull[i], 4);
       dec::mbar_init(&s.pfull2[i], 4);
-      dec::mbar_init(&s.ofull[i], 2);
+      dec::mbar_init(&s.ofull[i], 1);
     }
     dec::mbar_init(s.drain, 1);
-    dec::mbar_init(s.mended, 1);
-    dec::mbar_init(s.asked, 1);
     *s.abort_flag = 0;
     dec::mbar_init_fence();
   }
@@ -1146,7 +1094,6 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
     if (warp == 8) produce<D, kFp8>(a, rg, s, &map_k, &map_v, lane);
     if (warp == 9) multiply<D, kFp8>(a, s, tmem, lane);
     if (warp == 10) load_q<D>(a, s, &map_q, lane);
-    if (!kFp8 && warp == 11) mend<D>(a, s, lane);
   } else if (kFp8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFpCvt));
     expand<D>(a, s, threadIdx.x - 384);
