@@ -352,3 +352,62 @@ def test_bad_device_data_is_reported(what):
             c.pages.check()
         assert e.value.status == FT_ERR_INVALID_ARG
         c.pages.check()  # reported once
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kv_heads,group,dim,page", [(2, 4, 128, 64), (3, 1, 64, 16), (1, 12, 128, 32), (2, 6, 64, 128)])
+def test_long_and_short_sequences_in_one_batch(fp8, kv_heads, group, dim, page):
+    """Chunks, single tokens, a few tokens and idle sequences side by side: each
+    kernel takes its own, and nobody's rows are left out."""
+    c = make([150, 1, 0, 2, 1, 40, 3, 1], [400, 900, 5, 31, 1, 40, 1200, 64], kv_heads, group, dim, page, fp8, sharp=2.0)
+    out, lse = c.attend()
+    assert not (out == 7.0).all(-1).any()  # every row has been written
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("q_len,kv_len,at", [(40, 100, 80), (200, 300, 290), (1, 300, 17), (2, 40, 39)])
+def test_a_value_of_nan_in_the_quantised_cache(q_len, kv_len, at):
+    """Rows that see the token are NaN, with a finite lse; the others do not notice."""
+    c = make([q_len], [kv_len], 2, 4, 128, 16, fp8=True)
+    clean, lse_clean = c.attend()
+    page, slot = int(c.table[0, at // 16]), at % 16
+    c.pages.v_scale[page, :, slot] = 255
+    out, lse = c.attend()
+    sees = max(0, at - (kv_len - q_len))
+    assert torch.equal(out[:sees], clean[:sees])
+    assert torch.isnan(out[sees:]).all()
+    assert torch.equal(lse, lse_clean)
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0])
+@pytest.mark.parametrize("q_len", [1, 30])
+def test_scales_that_are_not_positive(scale, q_len):
+    for fp8 in (False, True):
+        c = make([q_len], [70], 2, 4, 64, 16, fp8=fp8)
+        c.check(*c.attend(scale=scale), scale=scale)
+
+
+def test_many_query_heads_to_a_key_head():
+    c = make([3, 1], [100, 50], 1, 100, 64, 16)
+    c.check(*c.attend())
+
+
+def test_large_batches_of_single_tokens_with_a_window():
+    rng = np.random.default_rng(6)
+    n = rng.integers(1, 3000, 200).tolist()
+    c = make([1] * 200, n, 1, 8, 128, 16, fp8=True)
+    c.check(*c.attend(window=200), window=200)
+
+
+def test_the_workspace_is_left_as_it_was_found():
+    """Counters are zero again after every call: calls of all shapes share a workspace."""
+    from expert_cache_host_layer_gb300 import paged_kv
+    shapes = [([1], [30000]), ([1] * 9, [700] * 9), ([64], [9000]), ([1, 300], [5000, 400])]
+    cases = [make(q, n, 2, 8, 128, 64) for q, n in shapes]
+    first = [c.attend()[0] for c in cases]
+    for _ in range(3):
+        for c, want in zip(reversed(cases), reversed(first)):
+            assert torch.equal(c.attend()[0], want)
+    torch.cuda.synchronize()
+    ws = paged_kv._workspaces[(0, torch.cuda.current_stream().cuda_stream)]
+    assert (ws[:640] == 0).all()

@@ -105,3 +105,13 @@ def test_the_torch_wrapper_refuses_wrong_tensors():
     with pytest.raises(ValueError, match="bf16 or float8"):
         KVPages(x.float(), x.float())
     assert ctypes.sizeof(ft.ft_kv_pages) == 56 and ctypes.sizeof(ft.ft_kv_batch) == 48
+
+
+def test_attend_refuses_what_its_kernels_do_not_take():
+    with pytest.raises(ft.FtError, match="above 128") as e:
+        attend(pages(num_kv_heads=1), batch(), heads=129)
+    assert e.value.status == ft.FT_ERR_UNSUPPORTED
+    with pytest.raises(ft.FtError, match="positive"):
+        attend(pages(), batch(), qt=0)
+    with pytest.raises(ft.FtError, match="scales are not"):
+        attend(pages(k_scale=(1 << 22) + 8), batch())
