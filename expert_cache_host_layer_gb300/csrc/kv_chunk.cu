@@ -47,13 +47,12 @@ constexpr int kSub = kSubRows;
 constexpr int kTile = 128;                    // tokens per tile
 constexpr int kTmemCols = 512;                // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kUnits = 4;                     // ring of row blocks
-constexpr int kBlockItems = 4;                // a block's fixed cost, in tiles, for the cut
+constexpr int kBlockItems = 3;                // a block's fixed cost, in tiles, for the cut
 constexpr float kGrow = 8.0f;                 // log2 of the growth that O's scale may lag behind
 constexpr int kBfThreads = 384, kFpThreads = 640;
-// Registers of the warpgroups (softmax, producer and MMA, converters): within
-// what the block is launched with, 384 x 168 and 640 x 96.
-constexpr int kBfSoft = 200, kBfRest = 104, kFpSoft = 136, kFpRest = 80, kFpCvt = 64;
-static_assert(256 * kBfSoft + 128 * kBfRest <= kBfThreads * 168, "registers");
+// Registers of the quantised cache's warps (softmax, walker to Q, expanding),
+// within what the block is launched with, 640 x 96.
+constexpr int kFpSoft = 136, kFpRest = 80, kFpCvt = 64;
 static_assert(256 * (kFpSoft + kFpCvt) + 128 * kFpRest <= kFpThreads * 96, "registers");
 constexpr int kCvtWarps = 8;
 
@@ -780,26 +779,25 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
       constexpr int kHeld = 64;
       float x[kHeld];
       const bool edge = j0 < all_lo || j0 + kTile > all_hi;  // some row does not see all of the tile
-      const int from = lo - j0, end = hi - j0;
-      auto load = [&](int col) {  // kHeld scores from column col, the unseen ones -inf
+      if (edge) {  // unseen scores become -inf in place, so that the loops below are short
+        const int from = lo - j0, end = hi - j0;
+#pragma unroll 1
+        for (int col = 0; col < 128; col += 32) {
+          if (__all_sync(0xffffffffu, from <= col && end >= col + 32)) continue;
+          float y[32];
+          ld32(ts + col, y);
+          ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (k < from - col || k >= end - col) y[k] = -INFINITY;
+          st32(ts + col, reinterpret_cast<const uint32_t*>(y));
+        }
+        st_wait();
+      }
+      auto load = [&](int col) {  // kHeld scores from column col
 #pragma unroll
         for (int k = 0; k < kHeld; k += 32) ld32(ts + col + k, x + k);
         ld_wait();
-        if (edge) {
-#pragma unroll
-          for (int k0 = 0; k0 < kHeld; k0 += 32) {  // 32 columns that some row of the warp does not see all of
-            if (__any_sync(0xffffffffu, end < col + k0 + 32)) {
-#pragma unroll
-              for (int k = k0; k < k0 + 32; ++k)
-                if (k >= end - col) x[k] = -INFINITY;
-            }
-            if (__any_sync(0xffffffffu, from > col + k0)) {
-#pragma unroll
-              for (int k = k0; k < k0 + 32; ++k)
-                if (k < from - col) x[k] = -INFINITY;
-            }
-          }
-        }
       };
       float top = -INFINITY;
 #pragma unroll 1
@@ -970,13 +968,14 @@ __device__ void expand(const AttendArgs& a, const Shared& s, int tid) {
     scales(u->t0, e);
     for (int t = u->t0; t < t1; ++t) {
       const int seen0 = lo - t * kTile, seen1 = hi - t * kTile;
-      const bool edge = seen0 > 0 || seen1 < kTile;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         if (!wait_or_abort(&s.rfull[rt.st], rt.ph, a.status, s.abort_flag)) return;
         const uint8_t* src = s.base + L::kRawOff + rt.st * L::kRawBytes;
         const uint32_t mine = kv ? e[1] : e[0];
         if (kv == 1) scales(t + 1, e);  // on their way while V is expanded
+        // tokens that no row sees, or scales of NaN, in this tile
+        const bool odd = __any_sync(0xffffffffu, __vcmpeq4(mine, 0xffffffffu) != 0u) || seen0 > 0 || seen1 < kTile;
         if (!wait_or_abort(&s.empty[st.st], st.ph ^ 1, a.status, s.abort_flag)) return;
         uint8_t* dst = s.base + L::kRingOff + st.st * L::kTileBytes + (ch >> 2) * (kTile * 128);
 #pragma unroll 1
@@ -984,14 +983,13 @@ __device__ void expand(const AttendArgs& a, const Shared& s, int tid) {
           const int phys = D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
           uint4 c = *reinterpret_cast<const uint4*>(src + r * D + (phys << 4));
           const uint32_t b = __shfl_sync(0xffffffffu, mine, r >> 2) >> ((r & 3) * 8) & 0xffu;
-          bool drop = edge && (r < seen0 || r >= seen1);
-          if (kv == 1 && b == kNanScale && !drop) {
-            drop = true;
-            *reinterpret_cast<volatile int*>(&u->odd) = 1;
+          uint32_t sc = b * 0x00800080u;  // 2^(b - 127) as a pair of bf16
+          if (odd) {
+            const bool nan = b == kNanScale, drop = r < seen0 || r >= seen1 || (kv == 1 && nan);
+            if (drop) c = make_uint4(0, 0, 0, 0);
+            if (nan || drop) sc = kv == 0 && nan ? 0x7fc07fc0u : 0u;
+            if (kv == 1 && nan && r >= seen0 && r < seen1) *reinterpret_cast<volatile int*>(&u->odd) = 1;
           }
-          if (drop) c = make_uint4(0, 0, 0, 0);
-          // 2^(b - 127) as bf16 (byte 0 or 255, unseen or dropped: times codes 0)
-          const uint32_t sc = b == kNanScale ? (kv ? 0u : 0x7fc07fc0u) : drop ? 0u : b << 7 | b << 23;
           const __nv_bfloat162 sc2 = *reinterpret_cast<const __nv_bfloat162*>(&sc);
           const uint32_t q[4] = {c.x, c.y, c.z, c.w};
           uint32_t o[8];
@@ -1087,10 +1085,10 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
   fence_after();
   const uint32_t tmem = *s.tmem;
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8 ? kFpSoft : kBfSoft));
+    if (kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFpSoft));
     soften<D, kFp8>(a, s, tmem, warp >> 2, threadIdx.x & 127);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8 ? kFpRest : kBfRest));
+    if (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFpRest));
     if (warp == 8) produce<D, kFp8>(a, rg, s, &map_k, &map_v, lane);
     if (warp == 9) multiply<D, kFp8>(a, s, tmem, lane);
     if (warp == 10) load_q<D>(a, s, &map_q, lane);

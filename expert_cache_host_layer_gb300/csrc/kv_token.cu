@@ -71,7 +71,7 @@ struct Layout {
   static constexpr int kMlOff = kRedOff + (kRedBytes > kFacBytes ? kRedBytes : kFacBytes);
   static constexpr int kTotOff = kMlOff + kWarps * 8 * NB * 2 * 4;  // a row's maximum and 1 / sum, of all warps
   static constexpr int kBarOff = kTotOff + 8 * NB * 2 * 4;
-  static constexpr int kSmem = kBarOff + 2 * kStages * 8 + 16 + 1024;
+  static constexpr int kSmem = kBarOff + 2 * kStages * 8 + 16 + 1024;  // ..., abort and odd flags
   static_assert(kStages % kSets == 0, "a set that skipped a turn of a barrier would take it for the next");
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kStages * kStageBytes >= (kMaxSeqs + 1) * 8 + 1024, "the prefix sums fit the ring before it fills");
@@ -194,7 +194,7 @@ struct Warp {
   // One group: tokens j0 .. j0 + 15 at shared addresses kb, vb; ksc, vsc their
   // scale bytes.  full: every row sees all of them.
   __device__ __forceinline__ void group(uint32_t kb, uint32_t vb, const uint8_t* ksc, const uint8_t* vsc, int j0,
-                                        bool full, int m_new, int lane) {
+                                        bool full, int lane) {
     const int g = lane >> 2, c = lane & 3;
     float s[NB][4] = {};
     if (!kFp8) {
@@ -287,76 +287,14 @@ struct Warp {
         }
         pf[nb][i] = transpose8(bits(__floats2bfloat162_rn(w[0], w[1])));
       }
-    // Tokens that no row sees hold anything (a page's unused end): their V is
-    // taken as zero.  Where some rows see a token and others do not (m_new > 1)
-    // and its V is not finite, 0 * V must not reach the others: one product per
-    // row, over the V that it sees, added to it alone.
-    uint32_t keep[2] = {~0u, ~0u};
-    if (!full) {
-      int from = lo[0][0], to = 0;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) to = max(to, hi[nb][j]);
-      from = __shfl_sync(0xffffffffu, from, 0);  // row 0 belongs to the first new token
-      to = max(to, __shfl_xor_sync(0xffffffffu, to, 1));
-      to = max(to, __shfl_xor_sync(0xffffffffu, to, 2));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) keep[i] = keep_mask(i, c, j0, from, to);
-    }
-    if (full) accumulate<true>(vb, pf, keep, false, j0, lane);
-    else accumulate<false>(vb, pf, keep, m_new > 1, j0, lane);
+    accumulate(vb, pf, lane);
   }
-  // Bit mask of the pair of tokens 8 i + tok(2c), tok(2c + 1) within [from, to).
-  __device__ __forceinline__ uint32_t keep_mask(int i, int c, int j0, int from, int to) const {
-    uint32_t k = 0;
+  __device__ __forceinline__ void product(int mb, const uint32_t* v, const uint32_t (*pf)[2]) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int t = j0 + 8 * i + tok<D, kFp8>(2 * c + j);
-      if (t >= from && t < to) k |= 0xffffu << (16 * j);
-    }
-    return k;
+    for (int nb = 0; nb < NB; ++nb) mma_bf16(o[nb][mb], v, pf[nb][0], pf[nb][1]);
   }
-  __device__ __forceinline__ static bool not_finite(uint32_t b) {  // either bf16 half an infinity or a NaN
-    return (b & 0x7f80u) == 0x7f80u || (b & 0x7f800000u) == 0x7f800000u;
-  }
-  // O^T block mb += V^T block (fragment v) P^T
-  template <bool kFull>
-  __device__ __forceinline__ void product(int mb, uint32_t* v, const uint32_t (*pf)[2], const uint32_t* keep, bool split,
-                                          int j0, int lane) {
-    bool bad = false;
-    if (!kFull) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] &= keep[i >> 1];
-        bad |= not_finite(v[i]);
-      }
-    }
-    if (kFull || !split || !__any_sync(0xffffffffu, bad)) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) mma_bf16(o[nb][mb], v, pf[nb][0], pf[nb][1]);
-      return;
-    }
-    const int c = lane & 3;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        for (int src = 0; src < 4; ++src) {  // row 8 nb + 2 src + j
-          const int from = __shfl_sync(0xffffffffu, lo[nb][j], src), to = __shfl_sync(0xffffffffu, hi[nb][j], src);
-          const uint32_t k0 = keep_mask(0, c, j0, from, to), k1 = keep_mask(1, c, j0, from, to);
-          const uint32_t seen[4] = {v[0] & k0, v[1] & k0, v[2] & k1, v[3] & k1};
-          float t[4] = {};
-          mma_bf16(t, seen, pf[nb][0], pf[nb][1]);
-          if (c == src) {
-            o[nb][mb][j] += t[j];
-            o[nb][mb][2 + j] += t[2 + j];
-          }
-        }
-  }
-  template <bool kFull>
-  __device__ __forceinline__ void accumulate(uint32_t vb, const uint32_t (*pf)[2], const uint32_t* keep, bool split,
-                                             int j0, int lane) {
+  // O^T += V^T P^T
+  __device__ __forceinline__ void accumulate(uint32_t vb, const uint32_t (*pf)[2], int lane) {
     const int g = lane >> 2, c = lane & 3;
     if (!kFp8) {
       const int t = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
@@ -364,7 +302,7 @@ struct Warp {
       for (int mb = 0; mb < kMb; ++mb) {
         uint32_t v[4];
         ldsm4t(v, vb + (mb >> 2) * (kTokenTile * 128) + t * 128 + (((2 * (mb & 3) + ch) ^ (t & 7)) << 4));
-        product<kFull>(mb, v, pf, keep, split, j0, lane);
+        product(mb, v, pf);
       }
       return;
     }
@@ -391,13 +329,60 @@ struct Warp {
       const uint32_t b0 = __byte_perm(w[2][k], w[3][k], 0x5140), b1 = __byte_perm(w[2][k], w[3][k], 0x7362);
       uint32_t v[4] = {e4m3x2_to_bf162(a0 & 0xffffu), e4m3x2_to_bf162(a0 >> 16), e4m3x2_to_bf162(b0 & 0xffffu),
                        e4m3x2_to_bf162(b0 >> 16)};
-      product<kFull>(2 * k, v, pf, keep, split, j0, lane);
+      product(2 * k, v, pf);
       uint32_t u[4] = {e4m3x2_to_bf162(a1 & 0xffffu), e4m3x2_to_bf162(a1 >> 16), e4m3x2_to_bf162(b1 & 0xffffu),
                        e4m3x2_to_bf162(b1 >> 16)};
-      product<kFull>(2 * k + 1, u, pf, keep, split, j0, lane);
+      product(2 * k + 1, u, pf);
     }
   }
 };
+
+// A group at the edge of what the rows see, by its warp.  vg: its V in the ring.
+// Tokens [r0, r1) of it are seen by some row; the others hold anything (a page's
+// unused end): their V becomes zero.  Of tokens that some rows see and others do
+// not (outside [a0, a1)), bf16 values that are not finite become zero too, lest 0
+// * V reach the others; the rows that see them add them in the end.  (The
+// quantised cache's codes are finite, and a scale of NaN meets no unseen row's
+// probability.)  Returns whether there were any.
+template <int D, bool kFp8>
+__device__ __noinline__ bool mend(uint8_t* vg, int r0, int r1, int a0, int a1, int lane) {
+  constexpr int kLine = kFp8 ? D : 128, kBoxes = kFp8 ? 1 : D / 64, kPer = kLine / 16;
+  bool odd = false;
+  for (int i = lane; i < kGroup * kPer * kBoxes; i += 32) {
+    const int r = i / kPer % kGroup, box = i / (kPer * kGroup);
+    uint4* at = reinterpret_cast<uint4*>(vg + box * kTokenTile * kLine + r * kLine + i % kPer * 16);
+    if (r < r0 || r >= r1) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+    } else if (!kFp8 && (r < a0 || r >= a1)) {
+      uint4 v = *at;
+      uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // an exponent of all ones carries into the sign's place
+        const uint32_t bad = ((x[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        odd |= bad != 0u;
+        x[k] &= ~((bad & 0x8000u ? 0xffffu : 0u) | (bad & 0x80000000u ? 0xffff0000u : 0u));
+      }
+      *at = v;
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring's next copies come after these writes
+  return __any_sync(0xffffffffu, odd);
+}
+// Sum of the values of tokens [from, to) outside [a0, a1) that are not finite, columns d and d + 1.
+template <int D>
+__device__ __noinline__ float2 not_finite(const AttendArgs& a, int s, int h, int from, int to, int a0, int a1, int d) {
+  float2 sum = make_float2(0.0f, 0.0f);
+  for (int j = from; j < to; ++j) {
+    if (j >= a0 && j < a1) continue;
+    const int page = max(0, load_page(a.p, a.b, s, j / a.p.page_tokens, a.status));
+    const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(
+        static_cast<const __nv_bfloat16*>(a.p.v) +
+        (((long long)page * a.p.num_kv_heads + h) * a.p.page_tokens + j % a.p.page_tokens) * D + d));
+    if (!isfinite(v.x)) sum.x += v.x;
+    if (!isfinite(v.y)) sum.y += v.y;
+  }
+  return sum;
+}
 
 template <int D, bool kFp8, int NB>
 __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
@@ -410,6 +395,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* empty = full + L::kStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + L::kStages);
+  volatile int* odd_flag = abort_flag + 1;  // a mended group of this (sequence, head) had values that are not finite
   long long* s_pre = reinterpret_cast<long long*>(smem);  // in the ring, before it fills
   long long* s_scan = reinterpret_cast<long long*>(smem + L::kRedOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -419,6 +405,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
       dec::mbar_init(&empty[i], kSet);
     }
     *abort_flag = 0;
+    *odd_flag = 0;
     dec::mbar_init_fence();
   }
   dec::pdl_wait_primary();  // the batch, q and the pages may come from the kernel before
@@ -496,10 +483,15 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
         const int j0 = t * kTokenTile + grp * kGroup;
         const bool live = wait_or_abort(&full[st], ph, a.status, abort_flag);
         if (live && j0 < hi && j0 + kGroup > lo) {
-          const uint32_t kb = dec::smem_addr(smem + st * L::kStageBytes) + grp * kGroup * L::kLine;
+          uint8_t* kg = smem + st * L::kStageBytes + grp * kGroup * L::kLine;
           const uint8_t* sc = smem + L::kScaleOff + st * 2 * kTokenTile + grp * kGroup;
-          ws.group(kb, kb + L::kHalfBytes, sc, sc + kTokenTile, j0, j0 >= last.lo && j0 + kGroup <= first.hi, w.q.m,
-                   lane);
+          const bool whole_group = j0 >= last.lo && j0 + kGroup <= first.hi;  // every row sees all of it
+          if (!whole_group) {
+            if (mend<D, kFp8>(kg + L::kHalfBytes, lo - j0, hi - j0, last.lo - j0, first.hi - j0, lane)) *odd_flag = 1;
+            __syncwarp();
+          }
+          const uint32_t kb = dec::smem_addr(kg);
+          ws.group(kb, kb + L::kHalfBytes, sc, sc + kTokenTile, j0, whole_group, lane);
         }
         __syncwarp();
         if (lane == 0) dec::mbar_arrive(&empty[st]);
@@ -526,6 +518,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
           }
         }
       sync();
+      const bool odd = *odd_flag != 0;
       const int rows = min(kRows, w.q.m * a.G);
       const bool whole = w.begins && w.ends;
       const long long slot = 2LL * blockIdx.x + w.begins;
@@ -569,6 +562,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
             }
           }
           sync();
+          if (odd && threadIdx.x == 0) *odd_flag = 0;  // (everyone has read it)
           for (int e = threadIdx.x * 2; e < L::kRedRows * D; e += kConsumers * 2) {
             const int rr = e / D, d = e % D, r = r0 + rr;
             if (r >= rows) continue;
@@ -578,6 +572,13 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
               const float2 y = *reinterpret_cast<const float2*>(&red[(x * L::kRedRows + rr) * L::kRowFloats + d]);
               sum.x += y.x;
               sum.y += y.y;
+            }
+            if (!kFp8 && odd) {
+              const Span v = visible(a, w.q, r / a.G);
+              const float2 add = not_finite<D>(a, w.s, w.h, max(v.lo, w.t0 * kTokenTile), min(v.hi, w.t1 * kTokenTile),
+                                               last.lo, first.hi, d);
+              sum.x += add.x;
+              sum.y += add.y;
             }
             if (whole) {
               const float inv = tot[r].y;
