@@ -15,11 +15,13 @@
 // that took 5 us and a launch; with every part from another CTA, 152 of them,
 // one CTA reads 0.6 MB, some 5 us.)
 //
-// CTA: two producer warps (K, V) and kWarps consumer warps in sets of four.  The
+// CTA: two producer warps (K, V) and kWarps consumer warps in sets.  The
 // producers load a tile as swizzled TMA boxes of as many tokens as a page holds
 // (64 at most: issuing a copy costs some 50 ns, and boxes of 16 tokens kept the
 // consumers waiting) into a ring; the sets take the tiles in turn, a warp a
-// group of 16 tokens.  S^T = K Q^T and O^T += V^T P^T as m16n8k16: tokens
+// group of 16 tokens (with a quantised cache and at most 8 rows, two groups,
+// whose chains of conversions and products interleave: 32.8 -> 31.2 us for
+// eight sequences of 2000-32500 tokens).  S^T = K Q^T and O^T += V^T P^T as m16n8k16: tokens
 // (then head_dim) are the 16 rows, so that 8 attention rows cost one block of
 // columns and not a half-empty block of 16 rows.  Every warp has its own m, l
 // and O; warps meet only at the end of a (sequence, head).  mma.sync is enough
@@ -46,8 +48,6 @@ namespace kv {
 namespace {
 
 constexpr int kGroup = 16;
-constexpr int kSet = 4;  // warps of a set, groups of a tile
-static_assert(kTokenTile == kSet * kGroup, "a group per warp of a set");
 constexpr float kGrow = 8.0f;  // log2 of the growth of a row's maximum that its sums' scale may lag behind
 
 // NB: blocks of 8 rows.  Eight warps: with twelve or sixteen the quantised cache
@@ -55,6 +55,8 @@ constexpr float kGrow = 8.0f;  // log2 of the growth of a row's maximum that its
 template <int D, bool kFp8, int NB>
 struct Layout {
   static constexpr int kWarps = 8;
+  static constexpr int kGroups = kFp8 && NB == 1 ? 2 : 1;          // groups of a warp: independent chains to interleave
+  static constexpr int kSet = kTokenTile / (kGroup * kGroups);     // warps of a set
   static constexpr int kSets = kWarps / kSet;
   static constexpr int kThreads = (kWarps + 2) * 32;
   static constexpr int kLine = kFp8 ? D : 128;                     // bytes of a token's row in a box
@@ -134,7 +136,7 @@ __device__ __forceinline__ int out_col(int mb, int g, int i) {
   return !kFp8 ? 16 * mb + 8 * i + g : (D == 128 ? 16 * ((g >> 1) | ((g & 1) << 2)) : 8 * g) + 2 * mb + i;
 }
 
-template <int D, bool kFp8, int NB>
+template <int D, bool kFp8, int NB, int NG>
 struct Warp {
   static constexpr int kKs = D / 16, kMb = D / 16;
   uint32_t qf[NB][kKs][2];
@@ -191,28 +193,31 @@ struct Warp {
     }
   }
 
-  // One group: tokens j0 .. j0 + 15 at shared addresses kb, vb; ksc, vsc their
-  // scale bytes.  full: every row sees all of them.
+  // NG groups: tokens j0 .. j0 + 16 NG - 1 at shared addresses kb, vb (rows of
+  // kLine bytes); ksc, vsc their scale bytes.  full: every row sees all of them.
   __device__ __forceinline__ void group(uint32_t kb, uint32_t vb, const uint8_t* ksc, const uint8_t* vsc, int j0,
                                         bool full, int lane) {
     const int g = lane >> 2, c = lane & 3;
-    float s[NB][4] = {};
-    if (!kFp8) {
-      const int t = lane & 15, ch = lane >> 4;
+    float s[NG][NB][4] = {};
+    float vs[NG][2];
 #pragma unroll
-      for (int ks = 0; ks < kKs; ++ks) {
-        uint32_t k[4];
-        ldsm4(k, kb + (ks >> 2) * (kTokenTile * 128) + t * 128 + (((2 * (ks & 3) + ch) ^ (t & 7)) << 4));
+    for (int n = 0; n < NG; ++n) {
+      if constexpr (!kFp8) {
+        const int t = 16 * n + (lane & 15), ch = lane >> 4;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma_bf16(s[nb], k, qf[nb][ks][0], qf[nb][ks][1]);
-      }
-    } else {
+        for (int ks = 0; ks < kKs; ++ks) {
+          uint32_t k[4];
+          ldsm4(k, kb + (ks >> 2) * (kTokenTile * 128) + t * 128 + (((2 * (ks & 3) + ch) ^ (t & 7)) << 4));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma_bf16(s[n][nb], k, qf[nb][ks][0], qf[nb][ks][1]);
+        }
+      } else {
 #pragma unroll
       for (int hf = 0; hf < D / 64; ++hf) {
         uint32_t w[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int t = 8 * i + tok<D, kFp8>(g);
+          const int t = 16 * n + 8 * i + tok<D, kFp8>(g);
           const int phys = D == 128 ? (c + 4 * hf) ^ (t & 7) : c ^ ((t >> 1) & 3);
           asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                        : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
@@ -223,42 +228,44 @@ struct Warp {
           const uint32_t f[4] = {bits(e4m3x2_to_half2(w[0][k] & 0xffffu)), bits(e4m3x2_to_half2(w[1][k] & 0xffffu)),
                                  bits(e4m3x2_to_half2(w[0][k] >> 16)), bits(e4m3x2_to_half2(w[1][k] >> 16))};
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_f16(s[nb], f, qf[nb][hf * 4 + k][0], qf[nb][hf * 4 + k][1]);
+          for (int nb = 0; nb < NB; ++nb) mma_f16(s[n][nb], f, qf[nb][hf * 4 + k][0], qf[nb][hf * 4 + k][1]);
         }
       }
-    }
-    // scores in the log2 domain; s[nb][2 i + j]: token tok(g) + 8 i, row 8 nb + 2c + j
-    float vs[2] = {1.0f, 1.0f};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = 8 * i + tok<D, kFp8>(g);
-      float kf = 1.0f;
-      if (kFp8) {
-        kf = scale_of(ksc[t]);
-        vs[i] = scale_of(vsc[t]);
       }
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x = s[nb][2 * i + j] * sc[nb][j];
-          if (kFp8) x *= kf;
-          if (!full && (j0 + t < lo[nb][j] || j0 + t >= hi[nb][j])) x = -INFINITY;
-          s[nb][2 * i + j] = x;
-        }
     }
+    // scores in the log2 domain; s[n][nb][2 i + j]: token 16 n + 8 i + tok(g), row 8 nb + 2c + j
     bool grown = !started;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) grown |= fmaxf(s[nb][j], s[nb][2 + j]) > m[nb][j] + kGrow;
+      for (int i = 0; i < 2; ++i) {
+        const int t = 16 * n + 8 * i + tok<D, kFp8>(g);
+        float kf = 1.0f;
+        vs[n][i] = 1.0f;
+        if (kFp8) {
+          kf = scale_of(ksc[t]);
+          vs[n][i] = scale_of(vsc[t]);
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float x = s[n][nb][2 * i + j] * sc[nb][j];
+            if (kFp8) x *= kf;
+            if (!full && (j0 + t < lo[nb][j] || j0 + t >= hi[nb][j])) x = -INFINITY;
+            s[n][nb][2 * i + j] = x;
+            grown |= x > m[nb][j] + kGrow;
+          }
+      }
     if (__any_sync(0xffffffffu, grown)) {
       started = true;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float top = fmaxf(m[nb][j], fmaxf(s[nb][j], s[nb][2 + j]));
+          float top = m[nb][j];
+#pragma unroll
+          for (int n = 0; n < NG; ++n) top = fmaxf(top, fmaxf(s[n][nb][j], s[n][nb][2 + j]));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -272,32 +279,35 @@ struct Warp {
           }
         }
     }
-    uint32_t pf[NB][2];
+    uint32_t pf[NG][NB][2];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float w[2];
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float x = s[nb][2 * i + j], base = m[nb][j] == -INFINITY ? 0.0f : m[nb][j];
-          w[j] = exp2_approx(x - base);
-          l[nb][j] += w[j];
-          if (kFp8) w[j] = x == -INFINITY ? 0.0f : w[j] * vs[i];  // an unseen token's scale may be NaN
+        for (int i = 0; i < 2; ++i) {
+          float w[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float x = s[n][nb][2 * i + j], base = m[nb][j] == -INFINITY ? 0.0f : m[nb][j];
+            w[j] = exp2_approx(x - base);
+            l[nb][j] += w[j];
+            if (kFp8) w[j] = x == -INFINITY ? 0.0f : w[j] * vs[n][i];  // an unseen token's scale may be NaN
+          }
+          pf[n][nb][i] = transpose8(bits(__floats2bfloat162_rn(w[0], w[1])));
         }
-        pf[nb][i] = transpose8(bits(__floats2bfloat162_rn(w[0], w[1])));
-      }
-    accumulate(vb, pf, lane);
+#pragma unroll
+    for (int n = 0; n < NG; ++n) accumulate(vb, n, pf[n], lane);
   }
   __device__ __forceinline__ void product(int mb, const uint32_t* v, const uint32_t (*pf)[2]) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) mma_bf16(o[nb][mb], v, pf[nb][0], pf[nb][1]);
   }
   // O^T += V^T P^T
-  __device__ __forceinline__ void accumulate(uint32_t vb, const uint32_t (*pf)[2], int lane) {
+  __device__ __forceinline__ void accumulate(uint32_t vb, int n, const uint32_t (*pf)[2], int lane) {
     const int g = lane >> 2, c = lane & 3;
     if (!kFp8) {
-      const int t = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
+      const int t = 16 * n + (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
 #pragma unroll
       for (int mb = 0; mb < kMb; ++mb) {
         uint32_t v[4];
@@ -311,7 +321,7 @@ struct Warp {
     uint32_t w[4][kW];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = 8 * (i >> 1) + tok<D, kFp8>(2 * c + (i & 1));
+      const int t = 16 * n + 8 * (i >> 1) + tok<D, kFp8>(2 * c + (i & 1));
       if (D == 128) {
         const uint32_t at = vb + t * D + ((((g >> 1) | ((g & 1) << 2)) ^ (t & 7)) << 4);
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -344,12 +354,12 @@ struct Warp {
 // * V reach the others; the rows that see them add them in the end.  (The
 // quantised cache's codes are finite, and a scale of NaN meets no unseen row's
 // probability.)  Returns whether there were any.
-template <int D, bool kFp8>
+template <int D, bool kFp8, int kRowsHeld>
 __device__ __noinline__ bool mend(uint8_t* vg, int r0, int r1, int a0, int a1, int lane) {
   constexpr int kLine = kFp8 ? D : 128, kBoxes = kFp8 ? 1 : D / 64, kPer = kLine / 16;
   bool odd = false;
-  for (int i = lane; i < kGroup * kPer * kBoxes; i += 32) {
-    const int r = i / kPer % kGroup, box = i / (kPer * kGroup);
+  for (int i = lane; i < kRowsHeld * kPer * kBoxes; i += 32) {
+    const int r = i / kPer % kRowsHeld, box = i / (kPer * kRowsHeld);
     uint4* at = reinterpret_cast<uint4*>(vg + box * kTokenTile * kLine + r * kLine + i % kPer * 16);
     if (r < r0 || r >= r1) {
       *at = make_uint4(0u, 0u, 0u, 0u);
@@ -402,7 +412,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       dec::mbar_init(&full[i], 2);
-      dec::mbar_init(&empty[i], kSet);
+      dec::mbar_init(&empty[i], L::kSet);
     }
     *abort_flag = 0;
     *odd_flag = 0;
@@ -466,10 +476,10 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
     float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
     float2* tot = reinterpret_cast<float2*>(smem + L::kTotOff);
     auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); };
-    const int set = warp / kSet, grp = warp % kSet;
+    const int set = warp / L::kSet, grp = warp % L::kSet * L::kGroups;
     int it = 0;
     TokenWalk w(a, rg);
-    Warp<D, kFp8, NB> ws;
+    Warp<D, kFp8, NB, L::kGroups> ws;
     while (w.next(a)) {
       ws.begin(a, w.q, w.h, lane);
       const int hi = w.hi, lo = w.lo;
@@ -482,12 +492,12 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
       for (int t = w.t0 + first_turn; t < w.t1; t += L::kSets) {
         const int j0 = t * kTokenTile + grp * kGroup;
         const bool live = wait_or_abort(&full[st], ph, a.status, abort_flag);
-        if (live && j0 < hi && j0 + kGroup > lo) {
+        if (live && j0 < hi && j0 + kGroup * L::kGroups > lo) {
           uint8_t* kg = smem + st * L::kStageBytes + grp * kGroup * L::kLine;
           const uint8_t* sc = smem + L::kScaleOff + st * 2 * kTokenTile + grp * kGroup;
-          const bool whole_group = j0 >= last.lo && j0 + kGroup <= first.hi;  // every row sees all of it
+          const bool whole_group = j0 >= last.lo && j0 + kGroup * L::kGroups <= first.hi;  // every row sees all of it
           if (!whole_group) {
-            if (mend<D, kFp8>(kg + L::kHalfBytes, lo - j0, hi - j0, last.lo - j0, first.hi - j0, lane)) *odd_flag = 1;
+            if (mend<D, kFp8, kGroup * L::kGroups>(kg + L::kHalfBytes, lo - j0, hi - j0, last.lo - j0, first.hi - j0, lane)) *odd_flag = 1;
             __syncwarp();
           }
           const uint32_t kb = dec::smem_addr(kg);
