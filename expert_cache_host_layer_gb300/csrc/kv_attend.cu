@@ -171,21 +171,6 @@ using namespace ft::kv;
 
 namespace {
 
-// The workspace: [counter][desc][part_ml][part_o], each 256-byte aligned, the
-// counters in one place for every shape.
-struct Workspace {
-  uint64_t desc, ml, o, bytes;
-};
-Workspace layout(const ft_kv_pages& p, int grid, int rows) {
-  const uint64_t parts = 2ull * grid * rows;
-  Workspace w;
-  w.desc = (kMostCtas * sizeof(unsigned) + 255) & ~255ull;
-  w.ml = (w.desc + grid * sizeof(int4) + 255) & ~255ull;
-  w.o = (w.ml + parts * 2 * sizeof(float) + 255) & ~255ull;
-  w.bytes = w.o + parts * p.head_dim * sizeof(float);
-  return w;
-}
-
 // Which kernel takes what.  A (sequence, key head) of up to 16 rows is
 // token_kernel's, one of more chunk_kernel's: its tiles have 128 rows whether
 // they are used or not (a batch of 32 decoding sequences beside a chunk, e4m3:
@@ -201,6 +186,26 @@ Split split(const ft_kv_batch& b, int G) {
   if (most <= kTokenRows) return {most <= 8 ? 8 : kTokenRows, true, false};
   if ((long long)b.num_seqs * b.max_q_len <= b.num_tokens || G > kTokenRows) return {0, false, true};  // all as long, or no single token fits
   return {G <= 8 ? 8 : kTokenRows, true, true};
+}
+
+// The workspace: [counter][desc][token_kernel's part_ml, part_o][chunk_kernel's],
+// each 256-byte aligned, the counters in one place for every shape.  The kernels
+// have partial sums of their own: they run side by side.
+struct Workspace {
+  uint64_t desc, ml[2], o[2], bytes;
+};
+Workspace layout(const ft_kv_pages& p, int grid, const Split& sp) {
+  auto up = [](uint64_t x) { return (x + 255) & ~255ull; };
+  Workspace w;
+  w.desc = up(kMostCtas * sizeof(unsigned));
+  w.bytes = up(w.desc + grid * sizeof(int4));
+  for (int k = 0; k < 2; ++k) {
+    const uint64_t parts = (k ? sp.chunk : sp.token) ? 2ull * grid * (k ? kChunkRows : kTokenRows) : 0;
+    w.ml[k] = w.bytes;
+    w.o[k] = up(w.ml[k] + parts * 2 * sizeof(float));
+    w.bytes = up(w.o[k] + parts * p.head_dim * sizeof(float));
+  }
+  return w;
 }
 
 ft_status check_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads) {
@@ -221,7 +226,7 @@ ft_status check_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32
 extern "C" uint64_t ft_kv_attend_workspace(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads) {
   if (check_attend(pages, batch, num_q_heads) != FT_OK) return 0;
   const Split sp = split(*batch, num_q_heads / pages->num_kv_heads);
-  return layout(*pages, std::min(sm_count(), kMostCtas), sp.chunk ? kChunkRows : kTokenRows).bytes;
+  return layout(*pages, std::min(sm_count(), kMostCtas), sp).bytes;
 }
 
 extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads,
@@ -248,7 +253,7 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
     return set_error(FT_ERR_INVALID_ARG, "q's strides must be positive");
   const Split sp = split(*batch, G);
   const int grid = std::min(sm_count(), kMostCtas);
-  const Workspace ws = layout(*pages, grid, sp.chunk ? kChunkRows : kTokenRows);
+  const Workspace ws = layout(*pages, grid, sp);
   if (workspace_bytes < ws.bytes)
     return set_error(FT_ERR_INVALID_ARG, "workspace of %llu bytes: %llu are needed",
                      (unsigned long long)workspace_bytes, (unsigned long long)ws.bytes);
@@ -262,11 +267,16 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.counter = reinterpret_cast<unsigned*>(w);
   a.desc = reinterpret_cast<int4*>(w + ws.desc);
-  a.part_ml = reinterpret_cast<float*>(w + ws.ml);
-  a.part_o = reinterpret_cast<float*>(w + ws.o);
+  auto parts = [&](int k) {
+    a.part_ml = reinterpret_cast<float*>(w + ws.ml[k]);
+    a.part_o = reinterpret_cast<float*>(w + ws.o[k]);
+  };
+  a.beside = sp.token && sp.chunk;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
+  parts(0);
   if (sp.token) e = launch_attend_token(a, s);
+  parts(1);
   if (e == cudaSuccess && sp.chunk) e = launch_attend_chunk(a, s);
   // (a block's rows are used without a gap only while its first sub-tile holds them all)
   if (e == cudaSuccess && sp.chunk) e = launch_combine(a, batch->max_q_len <= a.tps ? (int)rows : kChunkRows, s);

@@ -31,6 +31,7 @@ struct AttendArgs {
   int tps;                // chunk_kernel: new tokens of a sub-tile of 128 rows, 128 / G
   int small;              // sequences of up to so many rows a head are token_kernel's, the others chunk_kernel's
   int grid;               // CTAs of the main kernel
+  bool beside;            // token_kernel and chunk_kernel both run
   int32_t* status;
   // workspace
   unsigned* counter;      // [grid] token_kernel: parts done of what CTA c begins and does not end; 0 between calls
@@ -152,7 +153,14 @@ __device__ __forceinline__ Range cut(const AttendArgs& a, long long* pre, long l
 
 // ---------------------------------------------------------------- token_kernel's items: tiles of a (sequence, head)
 
-constexpr int kPairItems = 4;  // a (sequence, head)'s fixed cost (its rows of q, joining the warps), in tiles
+// A (sequence, head)'s fixed cost (its rows of q, joining the warps and the
+// parts, all of it latency), in tiles: 8 of 32 KB, 12 of the smaller ones.
+// (e4m3, head_dim 128, 4 / 8 / 12 / 20: eight sequences of 2000-32500 tokens 31.5 /
+// 30.7 / 29.6 / 29.0 us, twenty of 200-6500 22.7 / 20.5 / 20.1 / 21.4; bf16,
+// twenty 25.7 / 24.7 / 24.0 / 23.7, 64 of 301-8000 100.9 / 101.3 / 102.0 / 103.6.)
+__device__ __forceinline__ int pair_items(const AttendArgs& a) {
+  return a.p.head_dim == 128 && a.p.kv_dtype == FT_KV_BF16 ? 8 : 12;
+}
 
 __device__ __forceinline__ Span token_tiles(const AttendArgs& a, const Seq& q, Span* seen) {
   seen->lo = visible(a, q, 0).lo;
@@ -162,13 +170,15 @@ __device__ __forceinline__ Span token_tiles(const AttendArgs& a, const Seq& q, S
   t.hi = q.m == 0 ? t.lo : max(t.lo + 1, (seen->hi + kTokenTile - 1) / kTokenTile);  // rows that see nothing: one tile
   return t;
 }
-// Items of one head of a sequence: its tiles, after kPairItems.
-__device__ __forceinline__ int token_items(const Span& t) { return t.hi > t.lo ? t.hi - t.lo + kPairItems : 0; }
+// Items of one head of a sequence: its tiles, after the fixed cost.
+__device__ __forceinline__ int token_items(const AttendArgs& a, const Span& t) {
+  return t.hi > t.lo ? t.hi - t.lo + pair_items(a) : 0;
+}
 __device__ __forceinline__ Range token_range(const AttendArgs& a, long long* pre, long long* scan) {
   return cut(a, pre, scan, [&](int s) {
     if (s == a.b.num_seqs) return 0LL;
     Span seen;
-    return (long long)token_items(token_tiles(a, own_seq<true>(a, s), &seen)) * a.p.num_kv_heads;
+    return (long long)token_items(a, token_tiles(a, own_seq<true>(a, s), &seen)) * a.p.num_kv_heads;
   });
 }
 // The parts of (sequence, head)s in a CTA's range, one after the other.
@@ -195,7 +205,7 @@ struct TokenWalk {
         hi = seen.hi;
         loaded = s;
       }
-      const int items = token_items(tiles);
+      const int items = token_items(a, tiles);
       const long long all = (long long)items * a.p.num_kv_heads;
       if (w - base >= all) {
         base += all;
@@ -205,8 +215,8 @@ struct TokenWalk {
       h = (int)quotient(w - base, items);
       const int rel = (int)(w - base - (long long)h * items), cnt = (int)min((long long)(items - rel), end - w);
       w += cnt;
-      t0 = tiles.lo + max(0, rel - kPairItems);
-      t1 = tiles.lo + max(0, rel + cnt - kPairItems);
+      t0 = tiles.lo + max(0, rel - pair_items(a));
+      t1 = tiles.lo + max(0, rel + cnt - pair_items(a));
       if (t0 == t1) continue;  // only of the fixed cost
       begins = t0 == tiles.lo;
       ends = t1 == tiles.hi;
@@ -214,11 +224,11 @@ struct TokenWalk {
     }
   }
   // first and last CTA of this (sequence, head)
-  __device__ __forceinline__ int first_cta() const {
-    return cta_of(base + (long long)h * token_items(tiles) + kPairItems, total, n);
+  __device__ __forceinline__ int first_cta(const AttendArgs& a) const {
+    return cta_of(base + (long long)h * token_items(a, tiles) + pair_items(a), total, n);
   }
-  __device__ __forceinline__ int last_cta() const {
-    return cta_of(base + (long long)(h + 1) * token_items(tiles) - 1, total, n);
+  __device__ __forceinline__ int last_cta(const AttendArgs& a) const {
+    return cta_of(base + (long long)(h + 1) * token_items(a, tiles) - 1, total, n);
   }
 };
 

@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
       }
       if (whole) continue;
       // the last of the parts joins them
-      const int c0 = w.first_cta(), parts = w.last_cta() - c0 + 1;
+      const int c0 = w.first_cta(a), parts = w.last_cta(a) - c0 + 1;
       __threadfence();
       sync();
       if (threadIdx.x == 0) {
