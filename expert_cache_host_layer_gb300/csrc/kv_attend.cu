@@ -13,96 +13,98 @@ namespace {
 
 // ---------------------------------------------------------------- partial sums
 
-// Block (c, y) joins rows of the row block that CTA c of chunk_kernel began and
-// others went on with: out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, in
-// the order of the tokens.  kOne: a block per row, its eight warps share the
-// parts (few rows of a long sequence, which many CTAs worked on); else a block
-// takes kJoinRows rows, a warp kPer of them at once (many rows, a few parts).
-constexpr int kJoinThreads = 256, kPer = 4, kJoinRows = 8 * kPer;
+// What chunk_kernel has left: the row blocks that CTA c began and others went on
+// with, and whose other parts were not there when it ended,
+//   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,
+// in the order of the tokens.  kOne: block (c, r) joins row r, its eight warps
+// share the parts (few rows of a long sequence, which many CTAs worked on); else
+// block (c, y) joins rows 32 y .. 32 y + 31, a lane a row, a warp an eighth of
+// the columns (many rows, a few parts).  Bound by latency: with nothing left,
+// the rule for long chunks, 2 us; joining every divided block here took 8-12.
+constexpr int kJoinThreads = 256;
 
 template <int D, bool kOne>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int N = D / 32, R = kOne ? 1 : kPer;
-  using Vec = typename std::conditional<N == 4, float4, float2>::type;
-  __shared__ float s_o[kOne ? 8 : 1][D];
-  __shared__ float s_l[8];
   dec::pdl_wait_primary();
-  const int4 u = __ldcg(&a.desc[blockIdx.x]);  // {s, h, row block, last CTA}
+  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.y == 0 && threadIdx.x < 8) a.arrived[c0 * 8 + threadIdx.x] = 0u;
+  const int row = kOne ? (int)blockIdx.y : (int)blockIdx.y * 32 + lane;
+  const int4 u = __ldcg(&a.desc[c0 * 8 + (row >> 5)]);  // {s, h, row block, last CTA}
   if (u.x < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Seq q = load_seq(a.p, a.b, u.x, a.status);
-  const int c0 = blockIdx.x, parts = u.w - c0 + 1;
-  // part i of row r: CTA c0's last slot, then the first slot of each CTA after it
-  auto slot = [&](int i, int r) { return (long long)(2 * (c0 + i) + (i == 0)) * kChunkRows + r; };
-  int row[R], token[R], head[R];
-  float m[R], l[R], acc[R][N];
-  bool any = false;
+  const int parts = u.w - c0 + 1, in_sub = row % kSubRows, ti = in_sub / a.G, head = in_sub - ti * a.G;
+  const int token = (u.z * 2 + row / kSubRows) * a.tps + ti;
+  const bool mine = ti < a.tps && token < q.m;
+  // part i: CTA c0's last slot, then the first slot of each CTA after it
+  auto slot = [&](int i) { return 2LL * (c0 + i) + (i == 0); };
+  auto ml = [&](int i) { return __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot(i) * kChunkRows + row); };
+  if constexpr (kOne) {
+    constexpr int N = D / 32;  // columns of a lane in the end; here lanes 0 .. D / 4 - 1 have four each
+    __shared__ float s_o[8][D];
+    __shared__ float s_l[8];
+    if (!mine) return;  // all of the block
+    float m = -INFINITY, l = 0.0f;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, ml(i).x);
 #pragma unroll
-  for (int k = 0; k < R; ++k) {
-    row[k] = kOne ? blockIdx.y : blockIdx.y * kJoinRows + k * 8 + warp;
-    const int rr = row[k] % kSubRows, ti = rr / a.G;
-    head[k] = rr - ti * a.G;
-    token[k] = (u.z * 2 + row[k] / kSubRows) * a.tps + ti;
-    if (ti >= a.tps || token[k] >= q.m) token[k] = -1;
-    any |= token[k] >= 0;
-    m[k] = -INFINITY;
-    l[k] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[k][i] = 0.0f;
-  }
-  if (!any) return;  // kOne: all of the block; else whole warps
-  for (int i = lane; i < parts; i += 32)
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (token[k] >= 0) m[k] = fmaxf(m[k], __ldcg(&a.part_ml[slot(i, row[k]) * 2]));
-#pragma unroll
-  for (int k = 0; k < R; ++k)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
-  const int per = kOne ? (parts + 7) / 8 : parts, i0 = kOne ? warp * per : 0, i1 = min(parts, i0 + per);
-#pragma unroll 2
-  for (int i = i0; i < i1; ++i) {
-    float2 ml[R];
-    float v[R][N];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      ml[k] = make_float2(-INFINITY, 0.0f);
-      if (token[k] < 0) continue;
-      ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot(i, row[k]));
-      *reinterpret_cast<Vec*>(v[k]) = __ldcg(reinterpret_cast<const Vec*>(a.part_o + slot(i, row[k]) * D) + lane);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.0f : m;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = warp; i < parts; i += 8) {
+      const float2 x = ml(i);
+      const float f = exp2_approx(x.x - base);
+      l = join(l, f, x.y);
+      if (lane < D / 4) {
+        const float4 y = __ldcg(part_at<D>(a, slot(i), row, lane * 4));
+        acc.x = join(acc.x, f, y.x);
+        acc.y = join(acc.y, f, y.y);
+        acc.z = join(acc.z, f, y.z);
+        acc.w = join(acc.w, f, y.w);
+      }
     }
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      if (token[k] < 0) continue;
-      const float f = exp2_approx(ml[k].x - (m[k] == -INFINITY ? 0.0f : m[k]));
-      l[k] += f * ml[k].y;
-#pragma unroll
-      for (int n = 0; n < N; ++n) acc[k][n] += f * v[k][n];
-    }
-  }
-  if (kOne) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) s_o[kOne ? warp : 0][lane * N + i] = acc[0][i];
-    if (lane == 0) s_l[warp] = l[0];
+    if (lane < D / 4) *reinterpret_cast<float4*>(&s_o[warp][lane * 4]) = acc;
+    if (lane == 0) s_l[warp] = l;
     __syncthreads();
     if (warp) return;
-    l[0] = 0.0f;
-    for (int w = 0; w < 8; ++w) l[0] += s_l[w];
+    l = 0.0f;
+    for (int w = 0; w < 8; ++w) l += s_l[w];
+    float o[N] = {};
+    for (int w = 0; w < 8; ++w)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      acc[0][i] = 0.0f;
-      for (int w = 0; w < 8; ++w) acc[0][i] += s_o[kOne ? w : 0][lane * N + i];
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    if (token[k] < 0) continue;
-    const float inv = inverse(l[k]);
-    __nv_bfloat16* out = a.out + out_at(a, q, u.y, token[k], head[k]) + lane * N;
+      for (int i = 0; i < N; ++i) o[i] += s_o[w][lane * N + i];
+    const float inv = inverse(l);
+    __nv_bfloat16* out = a.out + out_at(a, q, u.y, token, head) + lane * N;
 #pragma unroll
     for (int i = 0; i < N; i += 2)
-      *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[k][i] * inv, acc[k][i + 1] * inv);
-    if (lane == 0) write_lse(a, q, u.y, token[k], head[k], m[k], l[k]);
+      *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
+    if (lane == 0) write_lse(a, q, u.y, token, head, m, l);
+  } else {
+    constexpr int N = D / 8;  // columns of a warp
+    if (!mine) return;
+    float m = -INFINITY, l = 0.0f, o[N] = {};
+    for (int i = 0; i < parts; ++i) m = fmaxf(m, ml(i).x);
+    const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const float2 x = ml(i);
+      float4 y[N / 4];
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) y[k] = __ldcg(part_at<D>(a, slot(i), row, warp * N + 4 * k));
+      const float f = exp2_approx(x.x - base);
+      l = join(l, f, x.y);
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        o[4 * k] = join(o[4 * k], f, y[k].x);
+        o[4 * k + 1] = join(o[4 * k + 1], f, y[k].y);
+        o[4 * k + 2] = join(o[4 * k + 2], f, y[k].z);
+        o[4 * k + 3] = join(o[4 * k + 3], f, y[k].w);
+      }
+    }
+    const float inv = inverse(l);
+    __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + out_at(a, q, u.y, token, head) + warp * N);
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) out[k] = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+    if (warp == 0) write_lse(a, q, u.y, token, head, m, l);
   }
 }
 
@@ -119,7 +121,7 @@ int sm_count() {
 
 cudaError_t launch_combine(const AttendArgs& a, int used, cudaStream_t s) {
   const bool one = used <= 64;  // rows enough for a block each without many idle blocks
-  const dim3 grid(a.grid, one ? used : (used + kJoinRows - 1) / kJoinRows);
+  const dim3 grid(a.grid, one ? used : (used + 31) / 32);
   if (a.p.head_dim == 128)
     return one ? launch_dependent(combine_kernel<128, true>, grid, kJoinThreads, 0, s, a)
                : launch_dependent(combine_kernel<128, false>, grid, kJoinThreads, 0, s, a);
@@ -188,17 +190,18 @@ Split split(const ft_kv_batch& b, int G) {
   return {G <= 8 ? 8 : kTokenRows, true, true};
 }
 
-// The workspace: [counter][desc][token_kernel's part_ml, part_o][chunk_kernel's],
+// The workspace: [counter][arrived][desc][token_kernel's part_ml, part_o][chunk_kernel's],
 // each 256-byte aligned, the counters in one place for every shape.  The kernels
 // have partial sums of their own: they run side by side.
 struct Workspace {
-  uint64_t desc, ml[2], o[2], bytes;
+  uint64_t arrived, desc, ml[2], o[2], bytes;
 };
 Workspace layout(const ft_kv_pages& p, int grid, const Split& sp) {
   auto up = [](uint64_t x) { return (x + 255) & ~255ull; };
   Workspace w;
-  w.desc = up(kMostCtas * sizeof(unsigned));
-  w.bytes = up(w.desc + grid * sizeof(int4));
+  w.arrived = up(kMostCtas * sizeof(unsigned));
+  w.desc = up(w.arrived + 8 * kMostCtas * sizeof(unsigned));
+  w.bytes = up(w.desc + 8 * grid * sizeof(int4));
   for (int k = 0; k < 2; ++k) {
     const uint64_t parts = (k ? sp.chunk : sp.token) ? 2ull * grid * (k ? kChunkRows : kTokenRows) : 0;
     w.ml[k] = w.bytes;
@@ -266,6 +269,7 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   if ((st = status_word(&a.status)) != FT_OK) return st;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.counter = reinterpret_cast<unsigned*>(w);
+  a.arrived = reinterpret_cast<unsigned*>(w + ws.arrived);
   a.desc = reinterpret_cast<int4*>(w + ws.desc);
   auto parts = [&](int k) {
     a.part_ml = reinterpret_cast<float*>(w + ws.ml[k]);

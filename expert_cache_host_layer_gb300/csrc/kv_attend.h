@@ -35,10 +35,12 @@ struct AttendArgs {
   int32_t* status;
   // workspace
   unsigned* counter;      // [grid] token_kernel: parts done of what CTA c begins and does not end; 0 between calls
-  int4* desc;             // [grid] chunk_kernel: the (sequence, head, row block) that CTA c begins and does not end: {s, h, row
-                          // block, last CTA}; s = -1: none
+  unsigned* arrived;      // [grid][8] chunk_kernel: parts that others have done of 32 rows of what CTA c begins and does
+                          // not end; 0 between calls
+  int4* desc;             // [grid][8] chunk_kernel: the (sequence, head, row block) whose 32 rows CTA c begins and leaves for
+                          // combine_kernel: {s, h, row block, last CTA}; s = -1: none
   float* part_o;          // [2 grid][rows][D] unnormalised sums: slot 2c of what CTA c finds begun, 2c + 1 of what it
-                          // begins and leaves
+                          // begins and leaves (chunk_kernel: see part_at)
   float* part_ml;         // [2 grid][rows][2] running maximum (log2 domain) and sum
 };
 
@@ -47,6 +49,15 @@ __device__ __forceinline__ float exp2_approx(float x) {  // relative error 2^-22
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// chunk_kernel's partial sums: where columns d .. d + 3 of a row are.  32 rows lie
+// side by side, so that a thread per row writes and reads whole lines.
+template <int D>
+__device__ __forceinline__ float4* part_at(const AttendArgs& a, long long slot, int row, int d) {
+  return reinterpret_cast<float4*>(a.part_o) + ((slot * kChunkRows + (row & ~31)) * (D / 4) + d * 8 + (row & 31));
+}
+// x + f y, rounded twice: whoever joins partial sums gives the same.
+__device__ __forceinline__ float join(float x, float f, float y) { return __fadd_rn(x, __fmul_rn(f, y)); }
 
 // Tokens [lo, hi) that new token i of a sequence sees; lo and hi grow with i.
 struct Span {
