@@ -411,3 +411,23 @@ def test_the_workspace_is_left_as_it_was_found():
     torch.cuda.synchronize()
     ws = paged_kv._workspaces[(0, torch.cuda.current_stream().cuda_stream)]
     assert (ws[:640] == 0).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dim,page,group,q_len,kv_len,window", [
+    (128, 64, 4, [1900], [1900], 0), (64, 16, 1, [700, 1, 650], [900, 80, 4000], 500), (128, 128, 8, [130, 1], [20000, 9], 0)])
+def test_divided_blocks_give_the_same_every_time(fp8, dim, page, group, q_len, kv_len, window):
+    """Row blocks divided between CTAs, joined by whichever kernel comes to it, on a busy and on an idle GPU."""
+    from expert_cache_host_layer_gb300 import paged_kv
+    c = make(q_len, kv_len, 4, group, dim, page, fp8=fp8)
+    first = c.attend(window=window)
+    c.check(*first, window=window, rows=[0, 67, -1])
+    scratch = torch.empty(1 << 27, dtype=torch.uint8, device=DEV)
+    for k in range(6):
+        if k % 2:
+            scratch.fill_(k)  # the L2 cache holds something else
+        again = c.attend(window=window)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    torch.cuda.synchronize()
+    ws = paged_kv._workspaces[(0, torch.cuda.current_stream().cuda_stream)]
+    assert (ws[:640] == 0).all() and (ws[768:768 + 8 * 640] == 0).all()  # both kernels' counters
