@@ -562,6 +562,7 @@ __device__ void multiply(const AttendArgs& a, const Shared& s, uint32_t tmem, in
             if (elect())
               for (int k = k0; k < k1; ++k) mma_ts(O, S + k * 8, vd + k * 128, id_o, k != k0 || live[sub]);
           }
+          if (t == f1[sub] && elect()) commit(&s.ofull[sub]);  // while the other sub-tile goes on
           __syncwarp();
           pp[sub] ^= 1;
           live[sub] = true;
@@ -599,10 +600,6 @@ __device__ void multiply(const AttendArgs& a, const Shared& s, uint32_t tmem, in
         kt.next();
         kt.next();
       }
-    }
-    if (elect()) {
-      if (live[0]) commit(&s.ofull[0]);
-      if (live[1]) commit(&s.ofull[1]);
     }
     units.done(s, lane);
   }
