@@ -18,7 +18,9 @@
 // CTA: two producer warps (K, V) and kWarps consumer warps in sets.  The
 // producers load a tile as swizzled TMA boxes of as many tokens as a page holds
 // (64 at most: issuing a copy costs some 50 ns, and boxes of 16 tokens kept the
-// consumers waiting) into a ring; the sets take the tiles in turn, a warp a
+// consumers waiting) into a ring, several tiles at a time, each by a lane of its
+// own (one after the other they kept the consumers waiting where tiles are small:
+// eight e4m3 sequences of 2000-32500 tokens, head_dim 64, 24.9 -> 22.8 us); the sets take the tiles in turn, a warp a
 // group of 16 tokens (with a quantised cache and at most 8 rows, two groups,
 // whose chains of conversions and products interleave: 32.8 -> 31.2 us for
 // eight sequences of 2000-32500 tokens).  S^T = K Q^T and O^T += V^T P^T as m16n8k16: tokens
@@ -70,6 +72,7 @@ struct Layout {
   static constexpr int kHalfBytes = kTokenTile * kLine * kBoxes;   // a tile's K; its V follows
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kStages = kStageBytes >= 32768 ? 6 : 12;    // a multiple of kSets: a stage is one set's
+  static constexpr int kBurst = kStages / 3;                       // tiles that a producer issues at once
   static constexpr int kRedRows = 4;                               // rows joined across the warps at a time
   static constexpr int kRowFloats = D + 4;
   static constexpr int kScaleOff = kStages * kStageBytes;
@@ -452,24 +455,26 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
         const int row = ahead, te = min(t1, tb + 32 / per);
         ahead = row_of(te);  // on its way while these are issued
         const unsigned live = __ballot_sync(0xffffffffu, row >= 0);
-        for (int t = tb; t < te; ++t, ++it) {
-          const int st = it % L::kStages, l0 = (t - tb) * per;
-          if (!wait_or_abort(&empty[st], ((it / L::kStages) & 1) ^ 1, a.status, abort_flag)) {
-            go = false;
-            break;
-          }
-          if (lane == 0)
+        for (int t = tb; t < te && go;) {
+          const int burst = min(te - t, L::kBurst), mine = lane / per - (t - tb);  // this lane's tile of the burst
+          const bool in = mine >= 0 && mine < burst;
+          const int i = in ? it + mine : it, st = i % L::kStages;
+          go = wait_or_abort(&empty[st], ((i / L::kStages) & 1) ^ 1, a.status, abort_flag);
+          if (!go) break;
+          if (in && lane % per == 0)
             dec::mbar_expect_tx(&full[st],
-                                __popc(live >> l0 & ((1u << per) - 1u)) * br * (L::kLine * L::kBoxes + (kFp8 ? 1 : 0)));
+                                __popc(live >> lane & ((1u << per) - 1u)) * br * (L::kLine * L::kBoxes + (kFp8 ? 1 : 0)));
           __syncwarp();
-          if (lane >= l0 && lane < l0 + per && row >= 0) {
-            const int at = (lane - l0) * br;
+          if (in && row >= 0) {
+            const int at = lane % per * br;
             const uint32_t dst = dec::smem_addr(smem + st * L::kStageBytes) + v * L::kHalfBytes + at * L::kLine;
 #pragma unroll
             for (int c = 0; c < L::kBoxes; ++c) tma_box(dst + c * kTokenTile * 128, map, c * 64, row, &full[st]);
             if (kFp8)
               dec::bulk_g2s(smem + L::kScaleOff + (2 * st + v) * kTokenTile + at, scales + row, br, &full[st]);
           }
+          t += burst;
+          it += burst;
         }
       }
     }
