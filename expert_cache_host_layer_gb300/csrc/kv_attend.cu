@@ -194,7 +194,8 @@ Split split(const ft_kv_batch& b, int G) {
 
 // The workspace: [counter][arrived][desc][token_kernel's part_ml, part_o][chunk_kernel's],
 // each 256-byte aligned, the counters in one place for every shape.  The kernels
-// have partial sums of their own: they run side by side.
+// have partial sums of their own: they run side by side.  (Its size goes by
+// max_q_len and the heads alone, not by the sequences of one step.)
 struct Workspace {
   uint64_t arrived, desc, ml[2], o[2], bytes;
 };
@@ -205,7 +206,7 @@ Workspace layout(const ft_kv_pages& p, int grid, const Split& sp) {
   w.desc = up(w.arrived + 8 * kMostCtas * sizeof(unsigned));
   w.bytes = up(w.desc + 8 * grid * sizeof(int4));
   for (int k = 0; k < 2; ++k) {
-    const uint64_t parts = (k ? sp.chunk : sp.token) ? 2ull * grid * (k ? kChunkRows : kTokenRows) : 0;
+    const uint64_t parts = k == 0 || sp.chunk ? 2ull * grid * (k ? kChunkRows : kTokenRows) : 0;
     w.ml[k] = w.bytes;
     w.o[k] = up(w.ml[k] + parts * 2 * sizeof(float));
     w.bytes = up(w.o[k] + parts * p.head_dim * sizeof(float));

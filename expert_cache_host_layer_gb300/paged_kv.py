@@ -27,6 +27,7 @@ from . import (FT_KV_BF16, FT_KV_FP8E4M3, _check, ft_kv_attend_workspace, ft_kv_
 # and a stream object would cost as much as the GPU's work.
 _lib = library()
 _workspaces: dict = {}  # (device index, stream) -> uint8 tensor
+_outgrown: list = []    # the smaller ones before them, which a captured graph may still use
 
 
 def _need(ok, text, *args):
@@ -171,6 +172,8 @@ class KVPages:
         return self._needs[key]
 
     def _new_workspace(self, s, nbytes, stream):
+        if (self.index, s) in _workspaces:
+            _outgrown.append(_workspaces[(self.index, s)])
         with torch.cuda.device(self.device), torch.cuda.stream(stream):  # reused in this stream's order
             ws = _workspaces[(self.index, s)] = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         return ws

@@ -431,3 +431,40 @@ def test_divided_blocks_give_the_same_every_time(fp8, dim, page, group, q_len, k
     torch.cuda.synchronize()
     ws = paged_kv._workspaces[(0, torch.cuda.current_stream().cuda_stream)]
     assert (ws[:640] == 0).all() and (ws[768:768 + 8 * 640] == 0).all()  # both kernels' counters
+
+
+def test_a_workspace_serves_every_batch_of_its_sizes():
+    """On a new stream: a chunk, then the chunk beside a single token."""
+    side = torch.cuda.Stream()
+    c = make([300], [300], 2, 4, 128, 64)
+    d = make([300, 1], [300, 700], 2, 4, 128, 64)
+    d.pages._needs = c.pages._needs  # as if both steps were of one layer
+    torch.cuda.synchronize()
+    for x in (c, d, c):
+        got = x.attend(stream=side)
+        side.synchronize()
+        x.check(*got, rows=[0, 150, -1])
+
+
+def test_a_captured_call_keeps_its_workspace():
+    """A larger call on the stream leaves the workspace of a graph captured before it alone."""
+    from expert_cache_host_layer_gb300 import paged_kv
+    side = torch.cuda.Stream()
+    c, big = make([1], [20000], 2, 4, 128, 64), make([200], [900], 2, 4, 128, 64)
+    out = torch.empty(1, 8, 128, dtype=torch.bfloat16, device=DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    want = c.attend(stream=side)[0]
+    side.synchronize()
+    key = (0, side.cuda_stream)
+    before = paged_kv._workspaces[key]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        c.pages.attend(c.batch, c.q_dev, out)
+    big.attend(stream=side)
+    side.synchronize()
+    assert paged_kv._workspaces[key] is not before and any(t is before for t in paged_kv._outgrown)
+    out.fill_(7.0)
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
