@@ -54,7 +54,7 @@ constexpr int kSub = kSubRows;
 constexpr int kTile = 128;                    // tokens per tile
 constexpr int kTmemCols = 512;                // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kUnits = 4;                     // ring of row blocks
-constexpr int kBlockItems = 2;                // a block's fixed cost, in tiles, for the cut
+constexpr int kBlockItems = 3;                // a block's fixed cost, in tiles, for the cut
 constexpr float kGrow = 8.0f;                 // log2 of the growth that O's scale may lag behind
 constexpr int kBfThreads = 384, kFpThreads = 640;
 // Registers of the quantised cache's warps (softmax, walker to Q, expanding),
