@@ -19,8 +19,9 @@ namespace {
 // in the order of the tokens.  kOne: block (c, r) joins row r, its eight warps
 // share the parts (few rows of a long sequence, which many CTAs worked on); else
 // block (c, y) joins rows 32 y .. 32 y + 31, a lane a row, a warp an eighth of
-// the columns (many rows, a few parts).  Bound by latency: with nothing left,
-// the rule for long chunks, 2 us; joining every divided block here took 8-12.
+// the columns (many rows, a few parts: three are on their way together).  Bound
+// by latency: joining every divided block here took 8-12 us of a call, what
+// chunk_kernel leaves takes 2-6.
 constexpr int kJoinThreads = 256;
 
 template <int D, bool kOne>
@@ -79,26 +80,41 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
       *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
     if (lane == 0) write_lse(a, q, u.y, token, head, m, l);
   } else {
-    constexpr int N = D / 8;  // columns of a warp
+    constexpr int N = D / 8, kAhead = 3;  // columns of a warp; parts that are on their way together
     if (!mine) return;
+    float2 x[kAhead];
+    float4 y[kAhead][N / 4];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + j < parts) {
+          x[j] = ml(i0 + j);
+#pragma unroll
+          for (int k = 0; k < N / 4; ++k) y[j][k] = __ldcg(part_at<D>(a, slot(i0 + j), row, warp * N + 4 * k));
+        }
+    };
+    load(0);
     float m = -INFINITY, l = 0.0f, o[N] = {};
-    for (int i = 0; i < parts; ++i) m = fmaxf(m, ml(i).x);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (j < parts) m = fmaxf(m, x[j].x);
+    for (int i = kAhead; i < parts; ++i) m = fmaxf(m, ml(i).x);
     const float base = m == -INFINITY ? 0.0f : m;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const float2 x = ml(i);
-      float4 y[N / 4];
+    for (int i0 = 0; i0 < parts; i0 += kAhead) {
+      if (i0) load(i0);
 #pragma unroll
-      for (int k = 0; k < N / 4; ++k) y[k] = __ldcg(part_at<D>(a, slot(i), row, warp * N + 4 * k));
-      const float f = exp2_approx(x.x - base);
-      l = join(l, f, x.y);
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + j < parts) {
+          const float f = exp2_approx(x[j].x - base);
+          l = join(l, f, x[j].y);
 #pragma unroll
-      for (int k = 0; k < N / 4; ++k) {
-        o[4 * k] = join(o[4 * k], f, y[k].x);
-        o[4 * k + 1] = join(o[4 * k + 1], f, y[k].y);
-        o[4 * k + 2] = join(o[4 * k + 2], f, y[k].z);
-        o[4 * k + 3] = join(o[4 * k + 3], f, y[k].w);
-      }
+          for (int k = 0; k < N / 4; ++k) {
+            o[4 * k] = join(o[4 * k], f, y[j][k].x);
+            o[4 * k + 1] = join(o[4 * k + 1], f, y[j][k].y);
+            o[4 * k + 2] = join(o[4 * k + 2], f, y[j][k].z);
+            o[4 * k + 3] = join(o[4 * k + 3], f, y[j][k].w);
+          }
+        }
     }
     const float inv = inverse(l);
     __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + out_at(a, q, u.y, token, head) + warp * N);

@@ -39,11 +39,11 @@
 // Bound: the tensor pipe, 4 D flops per (row, token), if the softmax keeps up: a
 // tile's exponentials take as long as its products (head_dim 128; twice as long
 // with 64).  Measured: a prompt chunk of 16,384 tokens, 16 query heads over 4, bf16,
-// 735-770 us, 1430-1490 TFLOP/s (the clock varies with the power); 2048 e4m3 tokens
-// after 14,336, 229 us, 1120 TFLOP/s (expansion shares the issue slots: 64% used);
-// five chunks of 501-1501 tokens under a window of 1000, 12 heads, head_dim 64, 46.4
-// us, 230 TFLOP/s: 11 tiles a CTA, half of them at an edge, after a start of 4 us (batch, cut, the first
-// block) and 1.5 us for the first tile.
+// 733-815 us, 1350-1500 TFLOP/s (the clock varies with the power); 2048 e4m3 tokens
+// after 14,336, 227 us, 1135 TFLOP/s (expansion shares the issue slots: 64% used);
+// five chunks of 501-1501 tokens under a window of 1000, 12 heads, head_dim 64, 46
+// us, 230 TFLOP/s: 11 tiles a CTA, half of them at an edge, which take twice as
+// long, after a start of 4 us (batch, cut, first block) and 1.5 us for the first tile.
 #include "kv_attend.h"
 
 namespace ft {
@@ -54,7 +54,10 @@ constexpr int kSub = kSubRows;
 constexpr int kTile = 128;                    // tokens per tile
 constexpr int kTmemCols = 512;                // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kUnits = 4;                     // ring of row blocks
-constexpr int kBlockItems = 3;                // a block's fixed cost, in tiles, for the cut
+// A block's fixed cost, in tiles, for the cut.  (2 / 3 / 4: a prompt of 16,384 tokens
+// 752 / 733 / 740-750 us, of 4096 72.6 / 72.6 / 70.4, of 1024 27.1 / 28.7 / 28.6; windows
+// 46.6 / 47 / 49; 8 is slower throughout.)
+constexpr int kBlockItems = 3;
 constexpr float kGrow = 8.0f;                 // log2 of the growth that O's scale may lag behind
 constexpr int kBfThreads = 384, kFpThreads = 640;
 // Registers of the quantised cache's warps (softmax, walker to Q, expanding),
