@@ -222,24 +222,24 @@ struct Warp {
         }
       } else {
 #pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf) {
-        uint32_t w[2][4];
+        for (int hf = 0; hf < D / 64; ++hf) {
+          uint32_t w[2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = 16 * n + 8 * i + tok<D, kFp8>(g);
-          const int phys = D == 128 ? (c + 4 * hf) ^ (t & 7) : c ^ ((t >> 1) & 3);
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
-                       : "r"(kb + t * D + (phys << 4)));
+          for (int i = 0; i < 2; ++i) {
+            const int t = 16 * n + 8 * i + tok<D, kFp8>(g);
+            const int phys = D == 128 ? (c + 4 * hf) ^ (t & 7) : c ^ ((t >> 1) & 3);
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                         : "r"(kb + t * D + (phys << 4)));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t f[4] = {bits(e4m3x2_to_half2(w[0][k] & 0xffffu)), bits(e4m3x2_to_half2(w[1][k] & 0xffffu)),
+                                   bits(e4m3x2_to_half2(w[0][k] >> 16)), bits(e4m3x2_to_half2(w[1][k] >> 16))};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma_f16(s[n][nb], f, qf[nb][hf * 4 + k][0], qf[nb][hf * 4 + k][1]);
+          }
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t f[4] = {bits(e4m3x2_to_half2(w[0][k] & 0xffffu)), bits(e4m3x2_to_half2(w[1][k] & 0xffffu)),
-                                 bits(e4m3x2_to_half2(w[0][k] >> 16)), bits(e4m3x2_to_half2(w[1][k] >> 16))};
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_f16(s[n][nb], f, qf[nb][hf * 4 + k][0], qf[nb][hf * 4 + k][1]);
-        }
-      }
       }
     }
     // scores in the log2 domain; s[n][nb][2 i + j]: token 16 n + 8 i + tok(g), row 8 nb + 2c + j
