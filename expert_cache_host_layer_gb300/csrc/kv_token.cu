@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
 #pragma unroll
         for (int x = 0; x < L::kWarps; ++x) {
           const float2 y = ml[x * kRows + r];
-          if (y.x != -INFINITY) l += y.y * exp2_approx(y.x - mm);
+          l += y.y * (y.x == -INFINITY ? 0.0f : exp2_approx(y.x - mm));  // (only scores of NaN: y.y is NaN, and so is l)
         }
         tot[r] = make_float2(mm, inverse(l));
         if (whole) {

@@ -1,0 +1,51 @@
+"""GPU parity of the key/value cache and its attention where NaN, negative
+positions, strides or capture could go wrong (oracle: fp64; bounds: tests/kv_harness.py)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_kv import DEV, _clean_status, harness, make  # noqa: E402,F401
+
+
+def place(c, s, j):
+    """(page, slot) of token j of sequence s."""
+    return int(c.table[s, j // c.sp.page]), j % c.sp.page
+
+
+def nan_key(c, s, j):
+    """Token j's key becomes NaN throughout."""
+    page, slot = place(c, s, j)
+    if c.sp.fp8:
+        c.pages.k_scale[page, :, slot] = 255
+    else:
+        c.pages.k[page, :, slot] = float("nan")
+    c.vals[0][page, :, slot] = np.nan
+
+
+# ---------------------------------------------------------------- NaN scores
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group", [4, 12])
+@pytest.mark.parametrize("q_len,kv_len,at", [(1, 1, 0), (1, 17, 16), (1, 33, 32), (1, 65, 64), (2, 34, 33),
+                                             (1, 5000, 4999), (40, 40, 39), (40, 129, 128)])
+def test_a_key_of_nan_without_neighbours(fp8, group, q_len, kv_len, at):
+    """The only token that a warp has to do with: out and lse of the rows that see it are NaN."""
+    c = make([q_len], [kv_len], 2, group, 64, 16, fp8)
+    nan_key(c, 0, at)
+    out, lse = c.attend()
+    assert torch.isnan(lse[-1]).all() and torch.isnan(out[-1]).all()
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group,q_len,kv_len", [(4, 1, 1), (4, 1, 40), (8, 2, 700), (4, 1, 20000), (4, 60, 200)])
+def test_a_query_of_nan(fp8, group, q_len, kv_len):
+    """One head's query is NaN: its out and lse are, its neighbours' are not."""
+    c = make([q_len], [kv_len], 2, group, 128, 16, fp8)
+    c.q[-1, 1, 7] = np.nan
+    out, lse = c.attend(q=torch.from_numpy(c.q).bfloat16().to(DEV))
+    assert torch.isnan(lse[-1, 1]) and torch.isnan(out[-1, 1]).all()
+    assert torch.isfinite(lse[-1, 0]) and torch.isfinite(out[-1, 2]).all()
+    c.check(out, lse, rows=[0, 1, -1])
