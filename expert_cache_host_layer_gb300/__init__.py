@@ -25,6 +25,7 @@ FT_OK, FT_ERR_INVALID_ARG, FT_ERR_CUDA, FT_ERR_OOM, FT_ERR_CAPACITY, FT_ERR_STAT
 FT_W_F32, FT_W_BF16, FT_W_FP8E4M3_B128 = 0, 1, 2
 FT_FETCH_COPY_ENGINE, FT_FETCH_SM_PULL = 0, 1
 FT_KV_BF16, FT_KV_FP8E4M3 = 0, 1
+FT_KV_WORKSPACE_ZERO = 8192
 
 
 class FtError(RuntimeError):
@@ -122,6 +123,7 @@ def _load():
         "ft_kv_read": (st, [P, P, P, I64, P, P, P]),
         "ft_kv_attend": (st, [P, P, I32, P, I64, I64, P, I64, I64, P, ctypes.c_float, I32, I32, P, ctypes.c_uint64, P]),
         "ft_kv_attend_workspace": (ctypes.c_uint64, [P, P, I32]),
+        "ft_stream_capture": (ctypes.c_uint64, [P]),
         "ft_kv_status": (st, [P]),
         "ft_status_str": (ctypes.c_char_p, [st]),
         "ft_last_error": (ctypes.c_char_p, []),
@@ -364,6 +366,10 @@ def ft_kv_attend(pages: ft_kv_pages, batch: ft_kv_batch, num_q_heads: int, q: in
 
 def ft_kv_attend_workspace(pages: ft_kv_pages, batch: ft_kv_batch, num_q_heads: int) -> int:
     return int(_lib.ft_kv_attend_workspace(ctypes.addressof(pages), ctypes.addressof(batch), num_q_heads))
+
+
+def ft_stream_capture(stream: int = 0) -> int:
+    return int(_lib.ft_stream_capture(stream or None))
 
 
 def ft_kv_status(stream: int = 0):

@@ -220,6 +220,7 @@ Workspace layout(const ft_kv_pages& p, int grid, const Split& sp) {
   Workspace w;
   w.arrived = up(kMostCtas * sizeof(unsigned));
   w.desc = up(w.arrived + 8 * kMostCtas * sizeof(unsigned));
+  static_assert(9 * kMostCtas * sizeof(unsigned) + 2 * 256 <= FT_KV_WORKSPACE_ZERO, "the counters are zeroed");
   w.bytes = up(w.desc + 8 * grid * sizeof(int4));
   for (int k = 0; k < 2; ++k) {
     const uint64_t parts = k == 0 || sp.chunk ? 2ull * grid * (k ? kChunkRows : kTokenRows) : 0;
@@ -249,6 +250,16 @@ extern "C" uint64_t ft_kv_attend_workspace(const ft_kv_pages* pages, const ft_kv
   if (check_attend(pages, batch, num_q_heads) != FT_OK) return 0;
   const Split sp = split(*batch, num_q_heads / pages->num_kv_heads);
   return layout(*pages, std::min(sm_count(), kMostCtas), sp).bytes;
+}
+
+extern "C" uint64_t ft_stream_capture(void* stream) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &st, &id) != cudaSuccess) {
+    cudaGetLastError();  // (the legacy stream beside another's capture, or no device: not capturing)
+    return 0;
+  }
+  return st == cudaStreamCaptureStatusNone ? 0 : id;
 }
 
 extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads,

@@ -8,9 +8,13 @@
 
 The caller owns every tensor.  ``KVPages.empty`` allocates a layer's pages.
 Work is enqueued on ``stream`` (default: torch's current stream of the cache's
-device); the workspace of ``attend`` is kept per device and stream and grows to
-the largest call, so make one call of a size before capturing it in a graph.
-Device-side errors are reported by ``check`` (see ft_kv_status in include/ft.h,
+device).  ``attend`` needs a workspace that no other call uses at the same time:
+calls outside of a capture share one per stream, which grows to the largest;
+calls captured by ``torch.cuda.graph`` share one that belongs to the graph, so
+that it may be replayed on any stream, in any order, beside anything but itself.
+Whoever captures by other means makes one (``new_workspace``), keeps it as long
+as the graph, and passes it to each captured ``attend``.  Make one call before
+capturing: the first of a kind loads its kernels.  Device-side errors are reported by ``check`` (see ft_kv_status in include/ft.h,
 which also gives the layout and the sequences' description).
 """
 from __future__ import annotations
@@ -19,7 +23,7 @@ import ctypes
 
 import torch
 
-from . import (FT_KV_BF16, FT_KV_FP8E4M3, _check, ft_kv_attend_workspace, ft_kv_batch, ft_kv_pages, ft_kv_status,
+from . import (FT_KV_BF16, FT_KV_FP8E4M3, FT_KV_WORKSPACE_ZERO, _check, ft_kv_attend_workspace, ft_kv_batch, ft_kv_pages, ft_kv_status,
                library)
 
 # The three calls are made once per layer and step, so they go to the library
@@ -27,7 +31,8 @@ from . import (FT_KV_BF16, FT_KV_FP8E4M3, _check, ft_kv_attend_workspace, ft_kv_
 # and a stream object would cost as much as the GPU's work.
 _lib = library()
 _workspaces: dict = {}  # (device index, stream) -> uint8 tensor
-_outgrown: list = []    # the smaller ones before them, which a captured graph may still use
+_outgrown: list = []    # the smaller ones before them (a stream has three at most: sizes go by head_dim and the kernels that may run)
+_captured: dict = {}    # (device index, stream) -> (number, uint8 tensor) of the last capture that the stream was part of
 
 
 def _need(ok, text, *args):
@@ -104,23 +109,31 @@ class KVPages:
 
     def attend(self, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None = None,
                scale: float | None = None, causal: bool = True, window: int = 0,
-               stream: torch.cuda.Stream | None = None):
+               stream: torch.cuda.Stream | None = None, workspace: torch.Tensor | None = None):
         """Attention of the batch's new tokens; q, out: bf16 [num_tokens, q_heads,
         head_dim], lse: f32 [num_tokens, q_heads].  scale defaults to
         1 / sqrt(head_dim); window > 0 keeps that many last tokens, the row's own
-        included."""
+        included.  workspace: the caller's own (see ``new_workspace``)."""
         heads = q.shape[1] if q.dim() == 3 else 0
         rows = (*self._rows(batch, q, heads, "q"), *self._rows(batch, out, heads, "out"))
         if lse is not None:
             _need(lse.dtype == torch.float32 and lse.shape == (batch.num_tokens, heads) and lse.is_contiguous() and
                   lse.get_device() == self.index, "lse is a contiguous float32 [num_tokens, q_heads] tensor")
         s = self._stream(stream)
-        ws = _workspaces.get((self.index, s))
-        if ws is None or ws.numel() < self._need_bytes(batch, heads):
-            ws = self._new_workspace(s, self._need_bytes(batch, heads), stream)
+        if workspace is None:
+            ws = self._workspace(s, self._need_bytes(batch, heads), stream)
+        else:
+            ws = workspace
+            _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.get_device() == self.index,
+                  "workspace is a contiguous uint8 tensor of the cache's device")
         self._call("ft_kv_attend", self.address, batch.address, heads, *rows,
                    lse.data_ptr() if lse is not None else None, self.head_dim ** -0.5 if scale is None else scale, causal,
                    window, ws.data_ptr(), ws.numel(), s)
+
+    def new_workspace(self, batch: KVBatch, q_heads: int, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+        """A workspace for ``attend`` of batches with this one's max_q_len, made on the stream."""
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            return torch.zeros(self._need_bytes(batch, q_heads), dtype=torch.uint8, device=self.device)
 
     def read(self, batch: KVBatch, kv_start: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
              stream: torch.cuda.Stream | None = None):
@@ -171,9 +184,29 @@ class KVPages:
                 self._needs[key] = max(256, ft_kv_attend_workspace(self.c, batch.c, heads))
         return self._needs[key]
 
-    def _new_workspace(self, s, nbytes, stream):
-        if (self.index, s) in _workspaces:
-            _outgrown.append(_workspaces[(self.index, s)])
+    def _workspace(self, s, nbytes, stream):
+        """The one of stream s, or of the capture that it is part of."""
+        # (asking for the capture's number costs more than asking whether the current stream is captured)
+        asks = (stream is not None or torch._C._cuda_getDevice() != self.index or
+                torch._C._cuda_isCurrentStreamCapturing())
+        capture = _lib.ft_stream_capture(s) if asks else 0
+        key = (self.index, s)
+        if capture:
+            of, ws = _captured.get(key, (0, None))
+            if of == capture and ws.numel() >= nbytes:
+                return ws
+        else:
+            ws = _workspaces.get(key)
+            if ws is not None:
+                if ws.numel() >= nbytes:
+                    return ws
+                _outgrown.append(ws)
         with torch.cuda.device(self.device), torch.cuda.stream(stream):  # reused in this stream's order
-            ws = _workspaces[(self.index, s)] = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            ws[:FT_KV_WORKSPACE_ZERO].zero_()
+        # (a capture's lies in its graph's memory, which outlives the tensor: it is let go with the stream's next capture)
+        if capture:
+            _captured[key] = (capture, ws)
+        else:
+            _workspaces[key] = ws
         return ws

@@ -513,15 +513,23 @@ ft_status ft_kv_read(const ft_kv_pages* pages, const ft_kv_batch* batch, const i
  * [num_tokens][num_q_heads] (natural logarithm of the softmax's denominator,
  * scores scaled), or NULL.  Softmax statistics and sums are fp32;
  * probabilities are rounded to bf16 for the product with v.
- * workspace: device, 256-byte aligned, ft_kv_attend_workspace bytes, zero
- * before its first use (each call leaves its counters zero again); calls that
- * follow one another on a stream, of any shape, can share it. */
+ * workspace: device, 256-byte aligned, ft_kv_attend_workspace bytes, the
+ * leading FT_KV_WORKSPACE_ZERO of them zero before its first use (each call
+ * leaves its counters zero again); calls that follow one another on a stream,
+ * of any shape, can share it.  No two calls may use it at the same time: a
+ * captured graph has one of its own, since it may be replayed on any stream. */
+#define FT_KV_WORKSPACE_ZERO 8192
 ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads, const void* q,
                        int64_t q_token_stride, int64_t q_head_stride, void* out, int64_t out_token_stride,
                        int64_t out_head_stride, float* lse, float scale, int32_t causal, int32_t window,
                        void* workspace, uint64_t workspace_bytes, void* stream);
 /* Bytes ft_kv_attend needs for this shape on the current device; 0 for shapes it does not take. */
 uint64_t ft_kv_attend_workspace(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads);
+
+/* The number of the capture that `stream` is part of (one per capture, never
+ * used again), 0 if it is not capturing: what a caller that keeps workspaces
+ * needs to tell a graph's own from the others. */
+uint64_t ft_stream_capture(void* stream);
 
 /* Waits for `stream`, then returns what the ft_kv calls on the current device
  * met since the last ft_kv_status: FT_ERR_INVALID_ARG (device data out of
