@@ -52,8 +52,8 @@ class KVBatch:
         _need(q_start.shape == (S + 1,) and kv_len.dim() == 1 and block_table.dim() == 2 and block_table.shape[0] == S,
               "shapes: q_start [S + 1], kv_len [S], block_table [S, pages]")
         _need(q_start.is_contiguous() and kv_len.is_contiguous(), "q_start and kv_len are contiguous")
-        _need(S <= 1 or (block_table.stride(1) == 1 or block_table.shape[1] == 1) and
-              block_table.stride(0) >= block_table.shape[1], "block_table's rows are contiguous")
+        _need((block_table.stride(1) == 1 or block_table.shape[1] <= 1) and
+              (S <= 1 or block_table.stride(0) >= block_table.shape[1]), "block_table's rows are contiguous")
         _need(q_start.device == kv_len.device == block_table.device, "one device")
         self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table  # keeps them alive
         self.num_seqs, self.num_tokens, self.max_q_len = S, int(num_tokens), int(max_q_len)

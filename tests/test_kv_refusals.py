@@ -6,3 +6,26 @@ ft = pytest.importorskip("expert_cache_host_layer_gb300")
 
 def test_a_stream_that_does_not_capture_has_no_number():
     assert ft.ft_stream_capture(0) == 0
+
+
+def test_a_single_sequences_table_is_a_row_of_consecutive_entries():
+    """A column of a wider table as the table of one sequence: its entries lie a row apart."""
+    torch = pytest.importorskip("torch")
+    from expert_cache_host_layer_gb300.paged_kv import KVBatch
+    i32 = torch.int32
+    wide = torch.arange(40, dtype=i32).view(5, 8)
+    start, n = torch.zeros(2, dtype=i32), torch.zeros(1, dtype=i32)
+    for table in (wide[:, 3:4].T, wide[:1, ::2], wide[0].expand(1, 8)[:, ::3]):
+        with pytest.raises(ValueError, match="rows are contiguous"):
+            KVBatch(start, n, table, 0, 0)
+    # one entry, one row of a wider table, and a row of its own: the row's stride is not used
+    for table in (wide[2:3, 4:5], wide[2:3], wide[4:5, 2:6], wide[:, 3:4].T[:, 1:2], wide[0].expand(1, 8),
+                  torch.empty_strided((1, 4), (1, 1), dtype=i32)):
+        b = KVBatch(start, n, table, 0, 0)
+        assert b.c.block_table == table.data_ptr() and b.c.table_stride == table.shape[1]
+    two = torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32)
+    for table in (wide[0].expand(2, 8), wide[0].as_strided((2, 4), (2, 1))):  # rows that overlap
+        with pytest.raises(ValueError, match="rows are contiguous"):
+            KVBatch(*two, table, 0, 0)
+    b = KVBatch(*two, wide[1:3, 7:8], 0, 0)
+    assert b.c.table_stride == 8
