@@ -6,7 +6,8 @@ j > p - window (window > 0):
 
     out = sum_j softmax_j(scale q.k_j) v_j,    lse = log sum_j exp(scale q.k_j);
 
-a row that sees nothing, or only scores of -inf, gives zeros and lse -inf.
+a row at a negative position sees nothing; a row that sees nothing, or only
+scores of -inf, gives zeros and lse -inf.
 
 The quantised cache holds, per token and head, e4m3 codes of x / 2^k with the
 smallest k >= -110 such that max|x| <= 448 * 2^k (448: the largest e4m3
@@ -63,7 +64,7 @@ def visible(n: int, m: int, causal: bool, window: int) -> np.ndarray:
     """[m, n] mask of what each new token sees."""
     p = np.arange(n - m, n)[:, None]
     j = np.arange(n)[None, :]
-    see = np.ones((m, n), dtype=bool)
+    see = np.broadcast_to(p >= 0, (m, n)).copy()  # a negative position (m > n) sees nothing, causal or not
     if causal:
         see &= j <= p
         if window:

@@ -49,3 +49,19 @@ def test_a_query_of_nan(fp8, group, q_len, kv_len):
     assert torch.isnan(lse[-1, 1]) and torch.isnan(out[-1, 1]).all()
     assert torch.isfinite(lse[-1, 0]) and torch.isfinite(out[-1, 2]).all()
     c.check(out, lse, rows=[0, 1, -1])
+
+
+# ---------------------------------------------------------------- negative positions
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("q_len,kv_len", [([4, 40], [2, 13]), ([200], [60]), ([3], [1]), ([16, 1], [4, 900]),
+                                          ([300], [290]), ([2, 2], [0, 2])])
+def test_negative_positions_see_nothing_without_the_causal_mask(fp8, q_len, kv_len):
+    c = make(q_len, kv_len, 2, 4, 64, 16, fp8)
+    out, lse = c.attend(causal=False)
+    for s, (m, n) in enumerate(zip(q_len, kv_len)):
+        t, none = int(c.q_start[s]), max(0, m - n)
+        assert (out[t:t + none] == 0).all() and torch.isneginf(lse[t:t + none]).all()
+        if n:
+            assert torch.isfinite(lse[t + none:t + m]).all()
+    c.check(out, lse, causal=False)

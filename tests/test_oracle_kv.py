@@ -49,3 +49,8 @@ def test_masks():
     assert kv.visible(2, 3, True, 0).tolist() == [[False, False], [True, False], [True, True]]  # position -1 sees nothing
     out, lse, _, _ = kv.attend(np.ones((3, 1, 4)), np.ones((2, 1, 4)), np.ones((2, 1, 4)), 0.5)
     assert (out[0] == 0).all() and np.isneginf(lse[0]).all() and np.allclose(out[1:], 1)
+
+
+def test_a_negative_position_sees_nothing_without_the_causal_mask():
+    assert kv.visible(2, 3, False, 0).tolist() == [[False, False], [True, True], [True, True]]
+    assert kv.visible(0, 2, False, 0).shape == (2, 0) and kv.visible(3, 2, False, 0).all()
