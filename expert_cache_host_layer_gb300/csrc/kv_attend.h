@@ -66,7 +66,7 @@ struct Span {
 __device__ __forceinline__ Span visible(const AttendArgs& a, const Seq& q, int i) {
   const int pos = q.n - q.m + i;
   Span v;
-  v.hi = pos < 0 ? 0 : a.causal ? min(q.n, pos + 1) : q.n;
+  v.hi = a.causal ? max(0, pos + 1) : q.n & ~(pos >> 31);
   v.lo = a.window ? min(v.hi, max(0, pos - a.window + 1)) : 0;
   return v;
 }
