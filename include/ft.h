@@ -440,7 +440,8 @@ ft_status ft_step_graph_destroy(ft_step_graph* graph);
  * value is a finite bf16 value).  A vector with an infinity or a NaN gets e =
  * 255 and codes 0, and reads as NaN throughout.  A power of two makes
  * x / scale and code * scale exact: the cache rounds each value once, and
- * reading it back in bf16 rounds nothing.
+ * reading it back in bf16 rounds nothing.  (Pages that the caller fills: e is
+ * 17..247 or 255, and a code of NaN is a value of NaN.)
  *
  * Sequences.  Sequence s has q_start[s + 1] - q_start[s] new tokens (0 is
  * fine), rows q_start[s].. of the call's token-major tensors, and kv_len[s]

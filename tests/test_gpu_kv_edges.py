@@ -65,3 +65,35 @@ def test_negative_positions_see_nothing_without_the_causal_mask(fp8, q_len, kv_l
         if n:
             assert torch.isfinite(lse[t + none:t + m]).all()
     c.check(out, lse, causal=False)
+
+
+# ---------------------------------------------------------------- codes of NaN
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("kv_heads,group,q_len,kv_len,at,window", [
+    (2, 4, 60, 200, 170, 0), (2, 4, 60, 200, 30, 150), (2, 8, 300, 300, 129, 0), (1, 8, 2, 200, 199, 0),
+    (1, 8, 2, 200, 40, 159), (1, 2, 4, 90, 87, 0), (2, 4, 150, 600, 20, 0), (2, 1, 1500, 1500, 1400, 0)])
+def test_a_code_of_nan_reaches_only_rows_that_see_it(which, dim, kv_heads, group, q_len, kv_len, at, window):
+    """Codes 0x7f and 0xff in columns 5 and 40 of a token that only some rows see."""
+    c = make([q_len], [kv_len], kv_heads, group, dim, 16, fp8=True)
+    page, slot = place(c, 0, at)
+    t = (c.pages.k, c.pages.v)[which].view(torch.uint8)
+    t[page, :, slot, 5], t[page, :, slot, 40] = 0x7f, 0xff
+    c.vals[which][page, :, slot, 5] = c.vals[which][page, :, slot, 40] = np.nan
+    out, lse = c.attend(window=window)
+    first = at - (kv_len - q_len)
+    rows = {0, q_len - 1, *range(first - 2, first + 3)}
+    if window:
+        last = first + window - 1
+        rows |= set(range(last - 2, last + 3))
+    c.check(out, lse, window=window, rows=sorted(r for r in rows if 0 <= r < q_len))
+
+
+@pytest.mark.parametrize("group,q_len,kv_len", [(4, 1, 70), (8, 2, 300), (4, 50, 133)])
+def test_codes_of_nan_in_places_that_no_sequence_owns(group, q_len, kv_len):
+    c = make([q_len, q_len], [kv_len, kv_len + 9], 2, group, 128, 32, fp8=True, poison=False)
+    free = torch.from_numpy(~c.owned(c.pages.num_pages)).to(DEV)
+    for t in (c.pages.k, c.pages.v):
+        t.view(torch.uint8)[free] = 0x7f
+    c.check(*c.attend())
