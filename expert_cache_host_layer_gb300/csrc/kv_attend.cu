@@ -273,6 +273,8 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
     return set_error(FT_ERR_INVALID_ARG, "window=%d (causal=%d): a window is positive and causal", window, causal);
   if (!(scale == scale)) return set_error(FT_ERR_INVALID_ARG, "scale is NaN");
   if (batch->num_tokens == 0) return FT_OK;
+  if (batch->num_tokens == 1) q_token_stride = out_token_stride = pages->head_dim;  // of single entries: not used
+  if (num_q_heads == 1) q_head_stride = out_head_stride = pages->head_dim;
   if ((st = check_rows("q", q, q_token_stride, q_head_stride)) != FT_OK) return st;
   if ((st = check_rows("out", out, out_token_stride, out_head_stride)) != FT_OK) return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
@@ -282,8 +284,8 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   if (rows > 0x7fffffffLL / 2) return set_error(FT_ERR_UNSUPPORTED, "max_q_len * (num_q_heads / num_kv_heads) is too large");
   if (G > kSubRows)
     return set_error(FT_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads = %d is above %d", G, kSubRows);
-  if (q_token_stride <= 0 || q_head_stride <= 0)
-    return set_error(FT_ERR_INVALID_ARG, "q's strides must be positive");
+  if (q_token_stride <= 0 || q_head_stride <= 0 || out_token_stride <= 0 || out_head_stride <= 0)
+    return set_error(FT_ERR_INVALID_ARG, "q's and out's strides must be positive");
   const Split sp = split(*batch, G);
   const int grid = std::min(sm_count(), kMostCtas);
   const Workspace ws = layout(*pages, grid, sp);

@@ -282,6 +282,8 @@ extern "C" ft_status ft_kv_append(const ft_kv_pages* pages, const ft_kv_batch* b
   ft_status st = check_pages(pages);
   if (st == FT_OK) st = check_batch(pages, batch);
   if (st != FT_OK || batch->num_tokens == 0) return st;
+  if (batch->num_tokens == 1) k_token_stride = v_token_stride = pages->head_dim;  // of single entries: not used
+  if (pages->num_kv_heads == 1) k_head_stride = v_head_stride = pages->head_dim;
   if ((st = check_rows("k", k, k_token_stride, k_head_stride)) != FT_OK) return st;
   if ((st = check_rows("v", v, v_token_stride, v_head_stride)) != FT_OK) return st;
   MoveArgs a{};

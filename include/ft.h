@@ -487,7 +487,8 @@ typedef struct ft_kv_batch {
 /* Writes the batch's new keys and values into their pages.  k, v: device bf16
  * [num_tokens][num_kv_heads][head_dim] with the given strides in elements
  * (views of one projection's output are fine): 16-byte aligned, strides
- * multiples of 8. */
+ * multiples of 8.  (Here and below the stride of a dimension of one entry is not
+ * used.) */
 ft_status ft_kv_append(const ft_kv_pages* pages, const ft_kv_batch* batch, const void* k, int64_t k_token_stride,
                        int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
                        void* stream);

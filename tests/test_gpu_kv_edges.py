@@ -97,3 +97,35 @@ def test_codes_of_nan_in_places_that_no_sequence_owns(group, q_len, kv_len):
     for t in (c.pages.k, c.pages.v):
         t.view(torch.uint8)[free] = 0x7f
     c.check(*c.attend())
+
+
+# ---------------------------------------------------------------- strides
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("q_len,kv_len,group", [([1, 1], [80, 500], 4), ([3, 150], [80, 151], 4), ([70], [333], 1)])
+def test_queries_stored_by_head(fp8, q_len, kv_len, group):
+    """q's head stride is above its token stride."""
+    c = make(q_len, kv_len, 2, group, 128, 16, fp8)
+    by_head = torch.full((c.Hq + 1, c.T, 136), 7.0, dtype=torch.bfloat16, device=DEV)
+    by_head[1:, :, :128] = c.q_dev.transpose(0, 1)
+    c.check(*c.attend(q=by_head[1:, :, :128].transpose(0, 1)))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_strides_of_single_entries(fp8):
+    """One token, one key head: whatever stride a view gives such a dimension, it is not used."""
+    c = make([1], [80], 1, 1, 64, 16, fp8)
+    out = torch.full((1, 1, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    odd = [t.as_strided((1, 1, 64), (s0, s1, 1)) for t, s0, s1 in ((c.q_dev, 3, 0), (out, 0, 5))]
+    _, lse = c.attend(q=odd[0], out=odd[1])
+    c.check(out, lse)
+    x = c.q_dev.as_strided((1, 1, 64), (1, 3, 1))
+    c.pages.append(c.batch, x, x)
+    page, slot = place(c, 0, 79)
+    if not fp8:
+        assert torch.equal(c.pages.k[page, 0, slot], c.q_dev[0, 0]) and torch.equal(c.pages.v[page, 0, slot], c.q_dev[0, 0])
+    else:
+        from oracle import kv as okv
+        codes, e = okv.quantise(c.q[0, 0])
+        assert int(c.pages.v_scale[page, 0, slot]) == int(e)
+        np.testing.assert_array_equal(c.pages.v[page, 0, slot].double().cpu().numpy(), codes)

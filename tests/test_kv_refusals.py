@@ -29,3 +29,27 @@ def test_a_single_sequences_table_is_a_row_of_consecutive_entries():
             KVBatch(*two, table, 0, 0)
     b = KVBatch(*two, wide[1:3, 7:8], 0, 0)
     assert b.c.table_stride == 8
+
+
+def attend(out=8192, heads=8, tokens=5, qt=1024, qh=128, ot=1024, oh=128):
+    """Refused by the strides, or else by the workspace's size: nothing is launched."""
+    p = ft.ft_kv_pages(k=1 << 20, v=1 << 21, k_scale=None, v_scale=None, num_pages=10, num_kv_heads=1, head_dim=128,
+                       page_tokens=64, kv_dtype=ft.FT_KV_BF16)
+    b = ft.ft_kv_batch(q_start=1 << 20, kv_len=1 << 21, block_table=1 << 22, table_stride=4, num_seqs=3,
+                       num_tokens=tokens, max_q_len=2)
+    ft.ft_kv_attend(p, b, heads, 4096, qt, qh, out, ot, oh, None, 0.1, 1, 0, 4096, 0)
+
+
+@pytest.mark.parametrize("kw", [dict(ot=0), dict(oh=0), dict(ot=-1024), dict(oh=-128), dict(qt=0), dict(qh=0),
+                                dict(qt=-1024), dict(qh=-128)])
+def test_strides_of_queries_and_outputs_are_positive(kw):
+    with pytest.raises(ft.FtError, match="strides must be positive") as e:
+        attend(**kw)
+    assert e.value.status == ft.FT_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(tokens=1, qt=0, ot=0), dict(tokens=1, qt=-8, ot=3), dict(heads=1, qh=0, oh=0),
+                                dict(heads=1, tokens=1, qt=1, qh=2, ot=-1, oh=0)])
+def test_strides_of_single_entries_are_not_used(kw):
+    with pytest.raises(ft.FtError, match="are needed"):
+        attend(**kw)
