@@ -244,11 +244,21 @@ ft_status check_attend(const ft_kv_pages* pages, const ft_kv_batch* batch, int32
   return FT_OK;
 }
 
+// What the kernels do not take.
+ft_status check_sizes(const ft_kv_batch* batch, int G) {
+  if ((long long)batch->max_q_len * G > 0x7fffffffLL / 2)
+    return set_error(FT_ERR_UNSUPPORTED, "max_q_len * (num_q_heads / num_kv_heads) is too large");
+  if (G > kSubRows) return set_error(FT_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads = %d is above %d", G, kSubRows);
+  return FT_OK;
+}
+
 }  // namespace
 
 extern "C" uint64_t ft_kv_attend_workspace(const ft_kv_pages* pages, const ft_kv_batch* batch, int32_t num_q_heads) {
   if (check_attend(pages, batch, num_q_heads) != FT_OK) return 0;
-  const Split sp = split(*batch, num_q_heads / pages->num_kv_heads);
+  const int G = num_q_heads / pages->num_kv_heads;
+  if (check_sizes(batch, G) != FT_OK) return 0;
+  const Split sp = split(*batch, G);
   return layout(*pages, std::min(sm_count(), kMostCtas), sp).bytes;
 }
 
@@ -280,10 +290,8 @@ extern "C" ft_status ft_kv_attend(const ft_kv_pages* pages, const ft_kv_batch* b
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return set_error(FT_ERR_INVALID_ARG, "workspace is null or not 256-byte aligned");
   const int G = num_q_heads / pages->num_kv_heads;
+  if ((st = check_sizes(batch, G)) != FT_OK) return st;
   const long long rows = (long long)batch->max_q_len * G;  // of a (sequence, key head), at most
-  if (rows > 0x7fffffffLL / 2) return set_error(FT_ERR_UNSUPPORTED, "max_q_len * (num_q_heads / num_kv_heads) is too large");
-  if (G > kSubRows)
-    return set_error(FT_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads = %d is above %d", G, kSubRows);
   if (q_token_stride <= 0 || q_head_stride <= 0 || out_token_stride <= 0 || out_head_stride <= 0)
     return set_error(FT_ERR_INVALID_ARG, "q's and out's strides must be positive");
   const Split sp = split(*batch, G);

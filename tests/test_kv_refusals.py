@@ -53,3 +53,17 @@ def test_strides_of_queries_and_outputs_are_positive(kw):
 def test_strides_of_single_entries_are_not_used(kw):
     with pytest.raises(ft.FtError, match="are needed"):
         attend(**kw)
+
+
+@pytest.mark.parametrize("heads,most,kv_heads", [(129, 1, 1), (258, 40, 2), (128, 1 << 24, 1), (8, 1 << 30, 2)])
+def test_no_workspace_for_shapes_that_are_refused(heads, most, kv_heads):
+    p = ft.ft_kv_pages(k=1 << 20, v=1 << 21, k_scale=None, v_scale=None, num_pages=10, num_kv_heads=kv_heads, head_dim=128,
+                       page_tokens=64, kv_dtype=ft.FT_KV_BF16)
+    b = ft.ft_kv_batch(q_start=1 << 20, kv_len=1 << 21, block_table=1 << 22, table_stride=4, num_seqs=3, num_tokens=5,
+                       max_q_len=most)
+    assert ft.ft_kv_attend_workspace(p, b, heads) == 0
+    with pytest.raises(ft.FtError) as e:
+        ft.ft_kv_attend(p, b, heads, 4096, 128 * heads, 128, 8192, 128 * heads, 128, None, 0.1, 1, 0, 4096, 1 << 40)
+    assert e.value.status == ft.FT_ERR_UNSUPPORTED
+    b.max_q_len = 1
+    assert (ft.ft_kv_attend_workspace(p, b, 128 * kv_heads) > 0) and ft.ft_kv_attend_workspace(p, b, 0) == 0
