@@ -12,6 +12,9 @@ device).  ``attend`` needs a workspace that no other call uses at the same time:
 calls outside of a capture share one per stream, which grows to the largest;
 calls captured by ``torch.cuda.graph`` share one that belongs to the graph, so
 that it may be replayed on any stream, in any order, beside anything but itself.
+Tensors of a call with ``stream`` are recorded on it, so that dropping them right
+after is fine; waiting for what wrote them, and before what reads its results, is
+the caller's.
 Whoever captures by other means makes one (``new_workspace``), keeps it as long
 as the graph, and passes it to each captured ``attend``.  Make one call before
 capturing: the first of a kind loads its kernels.  Device-side errors are reported by ``check`` (see ft_kv_status in include/ft.h,
@@ -106,6 +109,8 @@ class KVPages:
         """Store the batch's new keys and values, bf16 [num_tokens, kv_heads, head_dim] (strided views are fine)."""
         rows = (*self._rows(batch, k, self.num_kv_heads, "k"), *self._rows(batch, v, self.num_kv_heads, "v"))
         self._call("ft_kv_append", self.address, batch.address, *rows, self._stream(stream))
+        if stream is not None:
+            self._record(stream, batch, k, v)
 
     def attend(self, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None = None,
                scale: float | None = None, causal: bool = True, window: int = 0,
@@ -129,6 +134,8 @@ class KVPages:
         self._call("ft_kv_attend", self.address, batch.address, heads, *rows,
                    lse.data_ptr() if lse is not None else None, self.head_dim ** -0.5 if scale is None else scale, causal,
                    window, ws.data_ptr(), ws.numel(), s)
+        if stream is not None:
+            self._record(stream, batch, q, out, lse, workspace)
 
     def new_workspace(self, batch: KVBatch, q_heads: int, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
         """A workspace for ``attend`` of batches with this one's max_q_len, made on the stream."""
@@ -148,6 +155,8 @@ class KVPages:
         _need(batch.index == self.index, "the batch and the cache are on one device")
         self._call("ft_kv_read", self.address, batch.address, kv_start.data_ptr(), shape[0], k_out.data_ptr(),
                    v_out.data_ptr(), self._stream(stream))
+        if stream is not None:
+            self._record(stream, batch, kv_start, k_out, v_out)
 
     def check(self, stream: torch.cuda.Stream | None = None):
         """Wait for the stream and raise FtError if a call met device data out of range or a timeout."""
@@ -176,6 +185,12 @@ class KVPages:
     def _stream(self, stream):
         # (a Stream object of the current stream takes 2 us to make)
         return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.index)
+
+    def _record(self, stream, batch, *tensors):
+        """Their memory is not given to others before the stream's work so far is done."""
+        for t in (self.k, self.v, self.k_scale, self.v_scale, batch.q_start, batch.kv_len, batch.block_table, *tensors):
+            if t is not None:
+                t.record_stream(stream)
 
     def _need_bytes(self, batch, heads):
         key = (heads, batch.max_q_len)

@@ -124,3 +124,51 @@ def test_a_workspace_of_the_callers_own():
             with pytest.raises(ValueError, match="workspace"):
                 c.pages.attend(c.batch, c.q_dev, out, workspace=bad)
     assert held == (len(paged_kv._captured), len(paged_kv._workspaces))
+
+
+def test_tensors_of_a_call_on_another_stream_may_be_dropped():
+    """The stream is busy when the calls are made; what they read and write is dropped and its memory asked for again."""
+    from expert_cache_host_layer_gb300.paged_kv import KVBatch
+    c = make([3, 60], [400, 90], 2, 8, 128, 16)
+    want, _ = c.attend()
+    k_want, v_want = (torch.empty(490, 2, 128, dtype=torch.bfloat16, device=DEV) for _ in "kv")
+    start = torch.tensor([0, 400, 490], dtype=torch.int32, device=DEV)
+    x = torch.randn(c.T, 2, 128, device=DEV).bfloat16()
+    c.pages.read(c.batch, start, k_want, v_want)  # (before the new tokens are written over)
+    side = torch.cuda.Stream()
+    got, k_out, v_out = torch.empty_like(want), torch.empty_like(k_want), torch.empty_like(v_want)
+    torch.cuda.synchronize()
+    busy = torch.randn(8192, 8192, device=DEV)
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            busy = (busy @ busy).mul_(1e-4)  # some 100 ms
+
+    def batch():
+        return KVBatch(*(t.clone() for t in (c.batch.q_start, c.batch.kv_len, c.batch.block_table)), c.T, 60)
+
+    c.pages.attend(batch(), c.q_dev.clone(), got, stream=side)
+    c.pages.read(batch(), start.clone(), k_out, v_out, stream=side)
+    c.pages.append(batch(), x.clone(), x.clone(), stream=side)
+    grabbed = []
+    for like in (c.batch.q_start, c.batch.kv_len, c.batch.block_table, c.q_dev, x) * 20:
+        grabbed.append(torch.zeros_like(like))  # on this stream, which does not wait
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(k_out, k_want) and torch.equal(v_out, v_want)
+    k_new, v_new = torch.empty_like(k_want), torch.empty_like(v_want)
+    c.pages.read(c.batch, start, k_new, v_new)
+    assert torch.equal(k_new[397:400], x[:3]) and torch.equal(v_new[-60:], x[3:])
+
+
+def test_calls_on_another_stream_can_be_captured():
+    c = make([3, 60], [400, 90], 2, 8, 128, 16)
+    want, _ = c.attend()
+    side, out = torch.cuda.Stream(), torch.empty_like(c.attend()[0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        c.pages.attend(c.batch, c.q_dev, out, stream=side)
+    for _ in range(2):
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
