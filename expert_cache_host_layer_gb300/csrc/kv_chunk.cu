@@ -466,7 +466,8 @@ __device__ void produce(const AttendArgs& a, const Range& rg, const Shared& s, c
     }
   }
   // no copy may still be writing this CTA's shared memory when it exits
-  for (int j = max(0, it - kSlots); j < it; ++j) dec::mbar_wait(&full[j % kSlots], (j / kSlots) & 1, a.status);
+  for (int j = max(0, it - kSlots); j < it; ++j)
+    if (!dec::mbar_wait(&full[j % kSlots], (j / kSlots) & 1, a.status)) break;  // a second has passed: for all of them
 }
 
 // ---------------------------------------------------------------- V at the edge
@@ -632,12 +633,16 @@ template <int D>
 __device__ void load_q(const AttendArgs& a, const Shared& s, const CUtensorMap* map, int lane) {
   const bool flip = a.scale_log2 < 0.0f;  // then Q arrives on `landed` first
   uint32_t ph[2] = {0, 0};
+  bool used[2] = {false, false};
   Units units;
   while (const Unit* u = units.next(a, s)) {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       if (!u->any(sub)) continue;
-      if (!wait_or_abort(&s.qempty[sub], ph[sub] ^ 1, a.status, s.abort_flag)) return;
+      const uint32_t mine = ph[sub];
+      if (!wait_or_abort(&s.qempty[sub], mine ^ 1, a.status, s.abort_flag)) goto out;
+      ph[sub] ^= 1;
+      used[sub] = true;
       uint8_t* Q = s.base + sub * kSub * D * 2;
       uint64_t* bar = flip ? &s.landed[sub] : &s.qfull[sub];
       if (lane == 0) {
@@ -647,7 +652,7 @@ __device__ void load_q(const AttendArgs& a, const Shared& s, const CUtensorMap* 
           tma_box3(dec::smem_addr(Q + c * kSub * 128), map, c * 64, u->h * a.G, u->q0 + (u->rb * 2 + sub) * a.tps, bar);
       }
       if (flip) {
-        if (!wait_or_abort(bar, ph[sub], a.status, s.abort_flag)) return;
+        if (!wait_or_abort(bar, mine, a.status, s.abort_flag)) goto out;
 #pragma unroll 4
         for (int i = lane; i < kSub * D / 8; i += 32) {
           uint4* at = reinterpret_cast<uint4*>(Q) + i;
@@ -659,10 +664,14 @@ __device__ void load_q(const AttendArgs& a, const Shared& s, const CUtensorMap* 
         __syncwarp();
         if (lane == 0) dec::mbar_arrive(&s.qfull[sub]);
       }
-      ph[sub] ^= 1;
     }
     units.done(s, lane);
   }
+out:
+  // no copy may still be writing this CTA's shared memory when it exits (where the CTA aborts, nobody else has waited)
+#pragma unroll
+  for (int sub = 0; sub < 2; ++sub)
+    if (used[sub]) dec::mbar_wait(flip ? &s.landed[sub] : &s.qfull[sub], ph[sub] ^ 1, a.status);
 }
 
 // ---------------------------------------------------------------- softmax
@@ -1166,6 +1175,8 @@ __global__ void __launch_bounds__(kFp8 ? kFpThreads : kBfThreads, 1)
   if (warp < 8) {
     if (kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFpSoft));
     soften<D, kFp8>(a, s, tmem, warp >> 2, threadIdx.x & 127);
+    __syncwarp();
+    st_wait();  // (a CTA that aborts may have stores to TMEM on their way)
   } else if (warp < 12) {
     if (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFpRest));
     if (warp == 8) produce<D, kFp8>(a, rg, s, &map_k, &map_v, lane);

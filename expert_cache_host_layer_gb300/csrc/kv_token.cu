@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(Layout<D, kFp8, NB>::kThreads, 1)
     }
     // no copy may still be writing this CTA's shared memory when it exits
     for (int j = max(0, it - L::kStages); j < it; ++j)
-      dec::mbar_wait(&full[j % L::kStages], (j / L::kStages) & 1, a.status);
+      if (!dec::mbar_wait(&full[j % L::kStages], (j / L::kStages) & 1, a.status)) break;  // a second: long enough for all
   } else {
     // ------------------------------------------------------------ consumers
     float* red = reinterpret_cast<float*>(smem + L::kRedOff);
