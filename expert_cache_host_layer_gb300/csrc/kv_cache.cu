@@ -116,6 +116,10 @@ __device__ __forceinline__ int place_of(const MoveArgs& a, int t) {
   if (kAppend) {
     const Seq q = load_seq(a.p, a.b, s, a.status);
     pos = q.n - q.m + (t - q.q0);
+    if (t < q.q0) {  // rows before q_start[0]: of no sequence, nor of a position that this would give
+      raise(a.status, FT_ERR_INVALID_ARG);
+      return -1;
+    }
     if (t - q.q0 >= q.m || pos < 0) return -1;
   } else {
     const int n = __ldg(&a.b.kv_len[s]);

@@ -451,11 +451,16 @@ ft_status ft_step_graph_destroy(ft_step_graph* graph);
  * whose position is negative (kv_len[s] below its new tokens) is not stored
  * and attends to nothing.
  *
+ * Rows from q_start[num_seqs] on belong to no sequence (a step padded to a fixed
+ * number of rows): they are not stored, and their rows of out and lse are left as
+ * they are.
+ *
  * Device data that is out of range (a page outside [0, num_pages), a kv_len
  * beyond the table, a q_start outside [0, num_tokens], more new tokens than
- * max_q_len) is never followed out of bounds: it sets a sticky word that
- * ft_kv_status reports as FT_ERR_INVALID_ARG, and what the call gives for
- * that sequence is then not defined.
+ * max_q_len; in ft_kv_append also a row before q_start[0], which is not stored)
+ * is never followed out of bounds: it sets a sticky word that ft_kv_status
+ * reports as FT_ERR_INVALID_ARG, and what the call gives for that sequence is
+ * then not defined.
  */
 typedef enum ft_kv_dtype {
   FT_KV_BF16 = 0,

@@ -129,3 +129,44 @@ def test_strides_of_single_entries(fp8):
         codes, e = okv.quantise(c.q[0, 0])
         assert int(c.pages.v_scale[page, 0, slot]) == int(e)
         np.testing.assert_array_equal(c.pages.v[page, 0, slot].double().cpu().numpy(), codes)
+
+
+# ---------------------------------------------------------------- rows of no sequence
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_leaves_rows_before_the_first_sequence_alone(fp8):
+    """q_start[0] = 4: rows 0..3 are nobody's, and no token of the cache changes for them."""
+    from expert_cache_host_layer_gb300 import FT_ERR_INVALID_ARG, FtError
+    from expert_cache_host_layer_gb300.paged_kv import KVBatch
+    c = make([6], [40], 2, 4, 64, 16, fp8, poison=False)
+    before = [t.clone() for t in (c.pages.k.view(torch.uint8), c.pages.v.view(torch.uint8))]
+    b = KVBatch(torch.tensor([4, 6], dtype=torch.int32, device=DEV), c.batch.kv_len, c.batch.block_table, 6, 6)
+    x = torch.ones(6, 2, 64, dtype=torch.bfloat16, device=DEV)
+    c.pages.append(b, x, x)
+    for t, old in zip((c.pages.k, c.pages.v), before):
+        page, slot = place(c, 0, 37)  # the last token that is not new
+        assert torch.equal(t.view(torch.uint8)[page, :, :slot + 1], old[page, :, :slot + 1])
+        assert not torch.equal(t.view(torch.uint8)[page, :, slot + 1], old[page, :, slot + 1])
+    with pytest.raises(FtError) as e:
+        c.pages.check()
+    assert e.value.status == FT_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("q_len,kv_len", [([1, 1], [80, 500]), ([3, 150], [80, 151])])
+def test_rows_after_the_last_sequence_are_left_alone(q_len, kv_len):
+    """A batch padded to a fixed number of rows, as a captured step has it."""
+    from expert_cache_host_layer_gb300.paged_kv import KVBatch
+    c = make(q_len, kv_len, 2, 4, 64, 16)
+    T = c.T + 5
+    b = KVBatch(c.batch.q_start, c.batch.kv_len, c.batch.block_table, T, max(q_len))
+    q = torch.ones(T, c.Hq, 64, dtype=torch.bfloat16, device=DEV)
+    q[:c.T] = c.q_dev
+    out, lse = torch.full_like(q, 7.0), torch.full((T, c.Hq), 7.0, device=DEV)
+    c.pages.attend(b, q, out, lse=lse)
+    assert (out[c.T:] == 7.0).all() and (lse[c.T:] == 7.0).all()
+    c.check(out[:c.T], lse[:c.T], rows=[0, 1, -1])
+    before = c.pages.k.clone()
+    x = torch.ones(T, 2, 64, dtype=torch.bfloat16, device=DEV)
+    c.pages.append(b, x, x)
+    changed = (c.pages.k.view(torch.int16) != before.view(torch.int16)).any(-1).any(1)
+    assert int(changed.sum()) == c.T
