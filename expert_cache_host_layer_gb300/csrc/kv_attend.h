@@ -50,6 +50,15 @@ __device__ __forceinline__ float exp2_approx(float x) {  // relative error 2^-22
   return y;
 }
 
+// A box of a 2-D map at column c0, row c1.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(dec::smem_addr(bar))
+      : "memory");
+}
+
 // chunk_kernel's partial sums: where columns d .. d + 3 of a row are.  32 rows lie
 // side by side, so that a thread per row writes and reads whole lines.
 template <int D>

@@ -152,13 +152,6 @@ __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(dec::smem_addr(bar))
       : "memory");
 }
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(dec::smem_addr(bar))
-      : "memory");
-}
 // kind::f16, fp32 accumulator, both operands bf16, B N-major or not.
 __device__ constexpr uint32_t idesc(int N, bool b_n_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_n_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
@@ -1008,11 +1001,11 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
 
 // Tokens that no row sees become zeros: they may hold anything.  So do the
 // values of a token whose scale is NaN, lest 0 * NaN reach a row that does not
-// see it, and codes of NaN, of tokens that some rows see and
-// others do not; the block's end makes the rows that do NaN there.  (A key of NaN
-// may stay: its scores are hidden, not multiplied.  Looking at the codes of edge
-// tiles costs six chunks of 300 tokens 34.0 -> 34.7 us, a chunk beside 32 decoding
-// sequences 72.8 -> 73.6.)
+// see it, and codes of NaN, of tokens that some rows see and others do not; the
+// block's end makes the rows that do NaN there.  (A key of NaN may stay: its
+// scores are hidden, not multiplied.  Looking at the codes of edge tiles costs six
+// chunks of 300 tokens 34.0 -> 34.7 us, a chunk beside 32 decoding sequences 72.8
+// -> 73.6.)
 template <int D>
 __device__ void expand(const AttendArgs& a, const Shared& s, int tid) {
   using L = Layout<D, true>;

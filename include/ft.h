@@ -519,7 +519,9 @@ ft_status ft_kv_read(const ft_kv_pages* pages, const ft_kv_batch* batch, const i
  * query heads to a key head; the scales 16-byte aligned.  lse: device f32
  * [num_tokens][num_q_heads] (natural logarithm of the softmax's denominator,
  * scores scaled), or NULL.  Softmax statistics and sums are fp32;
- * probabilities are rounded to bf16 for the product with v.
+ * probabilities are rounded to bf16 for the product with v.  (The sums are
+ * divided at their end, and probabilities go up to 2^8 before: values beyond some
+ * 2^120 / kv_len may overflow.)  out does not overlap q or the pages.
  * workspace: device, 256-byte aligned, ft_kv_attend_workspace bytes, the
  * leading FT_KV_WORKSPACE_ZERO of them zero before its first use (each call
  * leaves its counters zero again); calls that follow one another on a stream,
