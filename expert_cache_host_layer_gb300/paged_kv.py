@@ -17,7 +17,9 @@ after is fine; waiting for what wrote them, and before what reads its results, i
 the caller's.
 Whoever captures by other means makes one (``new_workspace``), keeps it as long
 as the graph, and passes it to each captured ``attend``.  Make one call before
-capturing: the first of a kind loads its kernels.  Device-side errors are reported by ``check`` (see ft_kv_status in include/ft.h,
+capturing: the first of a kind loads its kernels.
+
+Device-side errors are reported by ``check`` (see ft_kv_status in include/ft.h,
 which also gives the layout and the sequences' description).
 """
 from __future__ import annotations
@@ -26,16 +28,19 @@ import ctypes
 
 import torch
 
-from . import (FT_KV_BF16, FT_KV_FP8E4M3, FT_KV_WORKSPACE_ZERO, _check, ft_kv_attend_workspace, ft_kv_batch, ft_kv_pages, ft_kv_status,
-               library)
+from . import (FT_KV_BF16, FT_KV_FP8E4M3, FT_KV_WORKSPACE_ZERO, _check, ft_kv_attend_workspace, ft_kv_batch,
+               ft_kv_pages, ft_kv_status, library)
 
 # The three calls are made once per layer and step, so they go to the library
 # directly: at a decode step's sizes the binding's own functions, a device guard
 # and a stream object would cost as much as the GPU's work.
 _lib = library()
 _workspaces: dict = {}  # (device index, stream) -> uint8 tensor
-_outgrown: list = []    # the smaller ones before them (a stream has three at most: sizes go by head_dim and the kernels that may run)
+_outgrown: list = []    # the smaller ones before them: three of a stream at most (sizes go by head_dim and the kernels)
 _captured: dict = {}    # (device index, stream) -> (number, uint8 tensor) of the last capture that the stream was part of
+
+# what torch.cuda.current_device and is_current_stream_capturing ask, once CUDA is initialised
+_device, _capturing = (getattr(torch._C, n, None) for n in ("_cuda_getDevice", "_cuda_isCurrentStreamCapturing"))
 
 
 def _need(ok, text, *args):
@@ -126,7 +131,10 @@ class KVPages:
                   lse.get_device() == self.index, "lse is a contiguous float32 [num_tokens, q_heads] tensor")
         s = self._stream(stream)
         if workspace is None:
-            ws = self._workspace(s, self._need_bytes(batch, heads), stream)
+            ws = _workspaces.get((self.index, s))
+            need = self._needs.get((heads, batch.max_q_len)) or self._need_bytes(batch, heads)
+            if ws is None or ws.numel() < need or stream is not None or _device() != self.index or _capturing():
+                ws = self._workspace(s, need, stream)
         else:
             ws = workspace
             _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.get_device() == self.index,
@@ -174,7 +182,7 @@ class KVPages:
         return t.data_ptr(), s0, s1
 
     def _call(self, name, *args):
-        if torch.cuda.current_device() == self.index:
+        if _device() == self.index:
             st = getattr(_lib, name)(*args)
         else:
             with torch.cuda.device(self.device):
@@ -201,10 +209,7 @@ class KVPages:
 
     def _workspace(self, s, nbytes, stream):
         """The one of stream s, or of the capture that it is part of."""
-        # (asking for the capture's number costs more than asking whether the current stream is captured)
-        asks = (stream is not None or torch._C._cuda_getDevice() != self.index or
-                torch._C._cuda_isCurrentStreamCapturing())
-        capture = _lib.ft_stream_capture(s) if asks else 0
+        capture = _lib.ft_stream_capture(s)
         key = (self.index, s)
         if capture:
             of, ws = _captured.get(key, (0, None))
