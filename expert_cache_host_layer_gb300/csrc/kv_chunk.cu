@@ -662,7 +662,7 @@ __device__ void load_q(const AttendArgs& a, const Shared& s, const CUtensorMap* 
   }
 out:
   // no copy may still be writing this CTA's shared memory when it exits (where the CTA aborts, nobody else has waited)
-#pragma unroll
+#pragma unroll 1
   for (int sub = 0; sub < 2; ++sub)
     if (used[sub]) dec::mbar_wait(flip ? &s.landed[sub] : &s.qfull[sub], ph[sub] ^ 1, a.status);
 }
