@@ -35,6 +35,7 @@ from . import (FT_KV_BF16, FT_KV_FP8E4M3, FT_KV_WORKSPACE_ZERO, _check, ft_kv_at
 # directly: at a decode step's sizes the binding's own functions, a device guard
 # and a stream object would cost as much as the GPU's work.
 _lib = library()
+_append, _attend, _read = _lib.ft_kv_append, _lib.ft_kv_attend, _lib.ft_kv_read
 _workspaces: dict = {}  # (device index, stream) -> uint8 tensor
 _outgrown: list = []    # the smaller ones before them: three of a stream at most (sizes go by head_dim and the kernels)
 _captured: dict = {}    # (device index, stream) -> (number, uint8 tensor) of the last capture that the stream was part of
@@ -93,6 +94,7 @@ class KVPages:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device = k.device
         self.num_pages, self.num_kv_heads, self.page_tokens, self.head_dim = k.shape
+        self.scale = self.head_dim ** -0.5  # of the scores, unless a call gives its own
         self.c = ft_kv_pages(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fp8 else None,
                              v_scale.data_ptr() if fp8 else None, self.num_pages, self.num_kv_heads, self.head_dim,
                              self.page_tokens, FT_KV_FP8E4M3 if fp8 else FT_KV_BF16)
@@ -113,7 +115,7 @@ class KVPages:
     def append(self, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream: torch.cuda.Stream | None = None):
         """Store the batch's new keys and values, bf16 [num_tokens, kv_heads, head_dim] (strided views are fine)."""
         rows = (*self._rows(batch, k, self.num_kv_heads, "k"), *self._rows(batch, v, self.num_kv_heads, "v"))
-        self._call("ft_kv_append", self.address, batch.address, *rows, self._stream(stream))
+        self._call(_append, self.address, batch.address, *rows, self._stream(stream))
         if stream is not None:
             self._record(stream, batch, k, v)
 
@@ -139,8 +141,8 @@ class KVPages:
             ws = workspace
             _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.get_device() == self.index,
                   "workspace is a contiguous uint8 tensor of the cache's device")
-        self._call("ft_kv_attend", self.address, batch.address, heads, *rows,
-                   lse.data_ptr() if lse is not None else None, self.head_dim ** -0.5 if scale is None else scale, causal,
+        self._call(_attend, self.address, batch.address, heads, *rows,
+                   lse.data_ptr() if lse is not None else None, self.scale if scale is None else scale, causal,
                    window, ws.data_ptr(), ws.numel(), s)
         if stream is not None:
             self._record(stream, batch, q, out, lse, workspace)
@@ -161,7 +163,7 @@ class KVPages:
             _need(t.dtype == torch.bfloat16 and t.shape == shape and t.is_contiguous() and t.get_device() == self.index,
                   "k_out and v_out are contiguous bf16 [rows, kv_heads, head_dim] tensors of the cache's device")
         _need(batch.index == self.index, "the batch and the cache are on one device")
-        self._call("ft_kv_read", self.address, batch.address, kv_start.data_ptr(), shape[0], k_out.data_ptr(),
+        self._call(_read, self.address, batch.address, kv_start.data_ptr(), shape[0], k_out.data_ptr(),
                    v_out.data_ptr(), self._stream(stream))
         if stream is not None:
             self._record(stream, batch, kv_start, k_out, v_out)
@@ -181,14 +183,14 @@ class KVPages:
         _need(s2 == 1 or t.numel() == 0, "%s's rows are contiguous", name)
         return t.data_ptr(), s0, s1
 
-    def _call(self, name, *args):
+    def _call(self, fn, *args):
         if _device() == self.index:
-            st = getattr(_lib, name)(*args)
+            st = fn(*args)
         else:
             with torch.cuda.device(self.device):
-                st = getattr(_lib, name)(*args)
+                st = fn(*args)
         if st:
-            _check(st, name)
+            _check(st, fn.__name__)
 
     def _stream(self, stream):
         # (a Stream object of the current stream takes 2 us to make)
