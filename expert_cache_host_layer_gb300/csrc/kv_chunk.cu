@@ -843,7 +843,7 @@ __device__ void soften(const AttendArgs& a, const Shared& s, uint32_t tmem, int 
       if (first) {
         m = top;
         first = false;
-      } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
+      } else if (__any_sync(0xffffffffu, mine && top > m + kGrow)) {  // (a row that is nobody's changes no other's rounding)
         const float mn = fmaxf(m, top), f = top > m ? exp2_approx(m - mn) : 1.0f;
         m = mn;
         l *= f;

@@ -170,3 +170,33 @@ def test_rows_after_the_last_sequence_are_left_alone(q_len, kv_len):
     c.pages.append(b, x, x)
     changed = (c.pages.k.view(torch.int16) != before.view(torch.int16)).any(-1).any(1)
     assert int(changed.sum()) == c.T
+
+
+# ---------------------------------------------------------------- rows of a tile that are nobody's
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scale", [-0.2, 0.2])
+@pytest.mark.parametrize("group,dim", [(5, 128), (3, 128), (7, 64), (12, 128), (100, 64)])
+def test_results_do_not_depend_on_what_ran_before(fp8, scale, group, dim):
+    """128 rows of a tile hold 128 / group tokens' heads and some rows more, which
+    keep what other calls left there: nobody's result may change by a bit for it."""
+    c = make([211], [1417], 3, group, dim, 16, fp8, sharp=0.3)
+    others = [make([300], [600], 3, 4, dim, 16, fp8, sharp=s) for s in (30.0, 300.0, 0.01)]
+    first = c.attend(scale=scale, causal=False)
+    for other in others * 3:
+        other.attend(scale=scale)
+        again = c.attend(scale=scale, causal=False)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group", [1, 3, 8])
+def test_a_sequence_does_not_notice_the_next_ones_queries(fp8, group):
+    """Rows after a sequence's last in its tile are the next one's queries."""
+    c = make([70, 200], [900, 300], 2, group, 64, 16, fp8, sharp=0.3)
+    first = c.attend()
+    for k in (30.0, 300.0, -7.0):
+        q = c.q_dev.clone()
+        q[70:] *= k
+        again = c.attend(q=q)
+        assert torch.equal(first[0][:70], again[0][:70]) and torch.equal(first[1][:70], again[1][:70])
