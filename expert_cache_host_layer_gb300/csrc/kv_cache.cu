@@ -91,7 +91,7 @@ namespace {
 // 21.2 us, 4.8 TB/s, short of the bandwidth for the quantisation's instructions
 // and the few vectors of a block; read of 114,865 tokens x 8 heads 112 us, 6.3 TB/s.
 // bf16, head_dim 64, 14,292 tokens x 5 heads of 37 sequences: append 7.4 us, 5.0
-// TB/s.  One token: 5.5 us, of which the call on the host is 5.)
+// TB/s.  One token: 5.2 us, of which the call on the host is 5.)
 constexpr int kMoveThreads = 256;
 constexpr int kMostTokens = 32;  // of a block
 constexpr int kBatch = 2;

@@ -39,7 +39,7 @@
 // Bound: the tensor pipe, 4 D flops per (row, token), if the softmax keeps up: a
 // tile's exponentials take as long as its products (head_dim 128; twice as long
 // with 64).  Measured: a prompt chunk of 16,384 tokens, 16 query heads over 4, bf16,
-// 733-815 us, 1350-1500 TFLOP/s (the clock varies with the power); 2048 e4m3 tokens
+// 751-815 us, 1350-1465 TFLOP/s (the clock varies with the power); 2048 e4m3 tokens
 // after 14,336, 227 us, 1135 TFLOP/s (expansion shares the issue slots: 64% used);
 // five chunks of 501-1501 tokens under a window of 1000, 12 heads, head_dim 64, 46
 // us, 230 TFLOP/s: 11 tiles a CTA, half of them at an edge, which take twice as

@@ -42,7 +42,7 @@
 // 2^-25 of it.
 //
 // Bound: HBM.  64 bf16 sequences of 301-8000 tokens (head_dim 128, 8 key heads):
-// 99.5 us, 6.3 TB/s.  Where a CTA's share is small its fixed cost shows (batch,
+// 99.9 us, 6.2 TB/s.  Where a CTA's share is small its fixed cost shows (batch,
 // cut, first page and tile 4 us, the end of a sequence and head 3 us), and with
 // codes their expansion: eight e4m3 sequences of 2000-32500 tokens, 4 key heads, 27.5 us, 3.6 TB/s;
 // one bf16 sequence of 1021 tokens 9 us, start and join.
