@@ -26,6 +26,7 @@ FT_W_F32, FT_W_BF16, FT_W_FP8E4M3_B128 = 0, 1, 2
 FT_FETCH_COPY_ENGINE, FT_FETCH_SM_PULL = 0, 1
 FT_KV_BF16, FT_KV_FP8E4M3 = 0, 1
 FT_KV_WORKSPACE_ZERO = 8192
+FT_F32, FT_BF16, FT_FP8E4M3 = 0, 1, 2
 
 
 class FtError(RuntimeError):
@@ -78,6 +79,11 @@ class ft_kv_batch(ctypes.Structure):
                 ("max_q_len", ctypes.c_int32)]
 
 
+class ft_norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int32), ("hidden", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("group", ctypes.c_int32)]
+
+
 # ---------------------------------------------------------------- loading
 
 def _load():
@@ -125,6 +131,7 @@ def _load():
         "ft_kv_attend_workspace": (ctypes.c_uint64, [P, P, I32]),
         "ft_stream_capture": (ctypes.c_uint64, [P]),
         "ft_kv_status": (st, [P]),
+        "ft_add_norm": (st, [P, I64, P, I64, I32, P, I64, I32, P, I64, P, I64, I32, P, P]),
         "ft_status_str": (ctypes.c_char_p, [st]),
         "ft_last_error": (ctypes.c_char_p, []),
     }
@@ -375,6 +382,15 @@ def ft_stream_capture(stream: int = 0) -> int:
 def ft_kv_status(stream: int = 0):
     """Raise FtError if an earlier ft_kv call on this device met bad device data or a timeout (clears it)."""
     _check(_lib.ft_kv_status(stream or None), "ft_kv_status")
+
+
+def ft_add_norm(norm: ft_norm, num_rows: int, x: int, x_stride: int, x_dtype: int, delta: int, delta_stride: int,
+                delta_dtype: int, total: int, total_stride: int, out: int, out_stride: int, out_dtype: int, scales: int,
+                stream: int = 0):
+    st = _lib.ft_add_norm(ctypes.addressof(norm), num_rows, x, x_stride, x_dtype, delta, delta_stride, delta_dtype, total,
+                          total_stride, out, out_stride, out_dtype, scales, stream)
+    if st:
+        _check(st, "ft_add_norm")
 
 
 def ft_status_str(status: int) -> str:

@@ -267,7 +267,6 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.
 
 // ---------------------------------------------------------------- host
 
-int sm_count();  // of the current device
 cudaError_t launch_attend_token(const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_attend_chunk(const AttendArgs& a, cudaStream_t s);
 // Joins the partial sums of chunk_kernel's row blocks that a cut divided;
@@ -291,21 +290,5 @@ static cudaError_t allow_smem(Kernel* kernel, int bytes) {
   if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
   return e;
 }
-// A launch that may begin while the kernel before it on the stream ends (the kernel waits for its end itself).
-template <typename... P, typename... A>
-static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, const A&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace kv
 }  // namespace ft

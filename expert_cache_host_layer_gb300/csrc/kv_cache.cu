@@ -135,18 +135,6 @@ __device__ __forceinline__ int place_of(const MoveArgs& a, int t) {
   return page * a.p.num_kv_heads * a.p.page_tokens + pos % a.p.page_tokens;  // rows are below 2^31
 }
 
-// Scale exponent of a vector: the smallest k >= -110 with amax <= 448 * 2^k,
-// 121 if amax is not finite.  amax = (1 + f) 2^E and 448 = 1.75 * 2^8, so k = E - 8,
-// one more if 1 + f > 1.75.
-__device__ __forceinline__ int scale_exp(float amax) {
-  const uint32_t u = __float_as_uint(amax);
-  if (u >= 0x7f800000u) return 121;
-  const int k = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u);
-  return max(k, kMinScaleExp);
-}
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
 // Eight values of a vector, a lane of its group of kLanes: codes and exponent byte.
 template <int kLanes>
 __device__ __forceinline__ uint2 quantise(uint4 raw, uint32_t* e) {
@@ -159,20 +147,14 @@ __device__ __forceinline__ uint2 quantise(uint4 raw, uint32_t* e) {
   for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
   top = max(top & 0xffff0000u, top << 16);
   const int k = scale_exp(__uint_as_float(top));
-  const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
   float x[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16) * inv;
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * inv;
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
-  if (k >= 120) {  // 256 * 2^120 would not be a bf16 value; k = 121: not finite
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = k > 120 ? 0.0f : fminf(fmaxf(x[i], -240.0f), 240.0f);
-  }
-  *e = k > 120 ? (uint32_t)kNanScale : (uint32_t)(k + 127);
-  return make_uint2(pack_e4m3(x[0], x[1]) | pack_e4m3(x[2], x[3]) << 16,
-                    pack_e4m3(x[4], x[5]) | pack_e4m3(x[6], x[7]) << 16);
+  *e = scale_byte(k);
+  return encode8(x, k);
 }
 // Eight codes times their scale: exact, 4 significant bits.
 __device__ __forceinline__ uint4 dequantise(uint2 c, float scale) {

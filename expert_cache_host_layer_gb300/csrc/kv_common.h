@@ -22,6 +22,22 @@ ft_status check_batch(const ft_kv_pages* p, const ft_kv_batch* b);
 ft_status check_rows(const char* name, const void* ptr, int64_t token_stride, int64_t head_stride);
 // Device address of the current device's sticky status word.
 ft_status status_word(int32_t** out);
+int sm_count();  // of the current device
+// A launch that may begin while the kernel before it on the stream ends (the kernel waits for its end itself).
+template <typename... P, typename... A>
+static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 __device__ __forceinline__ void raise(int32_t* status, int what) { atomicCAS(status, 0, what); }
 
@@ -58,6 +74,33 @@ __device__ __forceinline__ int find_seq(const int32_t* start, int n, int t) {
 }
 // 2^(e - 127) of an exponent byte (255: NaN).  Stored bytes are 17..247 or 255.
 __device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e == kNanScale ? 0x7fc00000u : e << 23); }
+
+
+// Scale exponent of a vector: the smallest k >= -110 with amax <= 448 * 2^k,
+// 121 if amax is not finite.  amax = (1 + f) 2^E and 448 = 1.75 * 2^8, so k = E - 8,
+// one more if 1 + f > 1.75.
+__device__ __forceinline__ int scale_exp(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  if (u >= 0x7f800000u) return 121;
+  const int k = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u);
+  return max(k, kMinScaleExp);
+}
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// Eight values of a vector whose scale exponent is k, as codes.  (x is overwritten.)
+__device__ __forceinline__ uint2 encode8(float* x, int k) {
+  const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= inv;
+  if (k >= 120) {  // 256 * 2^120 would not be a bf16 value; k = 121: not finite
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = k > 120 ? 0.0f : fminf(fmaxf(x[i], -240.0f), 240.0f);
+  }
+  return make_uint2(pack_e4m3(x[0], x[1]) | pack_e4m3(x[2], x[3]) << 16,
+                    pack_e4m3(x[4], x[5]) | pack_e4m3(x[6], x[7]) << 16);
+}
+__device__ __forceinline__ uint32_t scale_byte(int k) { return k > 120 ? (uint32_t)kNanScale : (uint32_t)(k + 127); }
 
 }  // namespace kv
 }  // namespace ft

@@ -546,6 +546,41 @@ uint64_t ft_stream_capture(void* stream);
  * else FT_OK.  Reading clears the word.  Synchronous. */
 ft_status ft_kv_status(void* stream);
 
+/*
+ * What a decoder's layer does beside its products, its attention and its
+ * experts.  Like the ft_kv calls these take no handle: the caller owns every
+ * byte, the structs are host structs read during the call, nothing is allocated
+ * or kept, and the calls can be captured in a CUDA graph.
+ */
+typedef enum ft_dtype { FT_F32 = 0, FT_BF16 = 1, FT_FP8E4M3 = 2 } ft_dtype;
+
+/* A root-mean-square norm. */
+typedef struct ft_norm {
+  const void* weight;   /* device [hidden], 16-byte aligned; NULL: ones */
+  int32_t weight_dtype; /* FT_F32 or FT_BF16 */
+  int32_t hidden;       /* a multiple of 8, 8..16384 */
+  float eps;
+  int32_t group;        /* e4m3 outputs: channels to a scale: 32, 64, 128, or 0: the whole row */
+} ft_norm;
+
+/* The residual's addition and the norm of the sum, row by row:
+ *   r = x + delta,  total = r,  y = r * weight / sqrt(mean(r^2) + eps)
+ * x, delta, total and out are device matrices [num_rows][hidden] whose rows lie
+ * the given number of elements apart (of a single row it is not used): 16-byte
+ * aligned, strides multiples of 8.  x and delta: FT_F32 or FT_BF16, each its
+ * own; delta may be NULL (r = x).  total has x's type and may be NULL, or x or
+ * delta itself; out may be x or delta itself where total is not.  No other
+ * overlap.  r is an fp32 sum, which total rounds and y does not.
+ * out: FT_F32, FT_BF16 or FT_FP8E4M3.  For the last y is given as codes and
+ * fp32 scales, device [num_rows][ceil(hidden / group)] contiguous:
+ *   scale = max|y| / 448 over the group's channels,  code = y / scale to the nearest e4m3 value
+ * (max|r * weight| below 2^-100 counts as that, so that a group of zeros has a
+ * scale too.)  The mean of squares is fp32: magnitudes beyond 2^63 overflow it.
+ * A NaN or infinity in r makes its row, or its group, NaN. */
+ft_status ft_add_norm(const ft_norm* norm, int64_t num_rows, const void* x, int64_t x_stride, int32_t x_dtype,
+                      const void* delta, int64_t delta_stride, int32_t delta_dtype, void* total, int64_t total_stride,
+                      void* out, int64_t out_stride, int32_t out_dtype, float* scales, void* stream);
+
 const char* ft_status_str(ft_status s);
 /* Message of the calling thread's last error ("" if none). */
 const char* ft_last_error(void);
