@@ -84,6 +84,11 @@ class ft_norm(ctypes.Structure):
                 ("eps", ctypes.c_float), ("group", ctypes.c_int32)]
 
 
+class ft_rotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 # ---------------------------------------------------------------- loading
 
 def _load():
@@ -132,6 +137,8 @@ def _load():
         "ft_stream_capture": (ctypes.c_uint64, [P]),
         "ft_kv_status": (st, [P]),
         "ft_add_norm": (st, [P, I64, P, I64, I32, P, I64, I32, P, I64, P, I64, I32, P, P]),
+        "ft_rotate": (st, [P, I32, P, I32, I32, P, I64, I64, P, I64, I64, P]),
+        "ft_kv_append_rotary": (st, [P, P, P, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, P]),
         "ft_status_str": (ctypes.c_char_p, [st]),
         "ft_last_error": (ctypes.c_char_p, []),
     }
@@ -391,6 +398,26 @@ def ft_add_norm(norm: ft_norm, num_rows: int, x: int, x_stride: int, x_dtype: in
                           total_stride, out, out_stride, out_dtype, scales, stream)
     if st:
         _check(st, "ft_add_norm")
+
+
+def ft_rotate(rotary: ft_rotary, num_tokens: int, positions: int, num_heads: int, head_dim: int, x: int,
+              x_token_stride: int, x_head_stride: int, out: int, out_token_stride: int, out_head_stride: int,
+              stream: int = 0):
+    st = _lib.ft_rotate(ctypes.addressof(rotary), num_tokens, positions, num_heads, head_dim, x, x_token_stride,
+                        x_head_stride, out, out_token_stride, out_head_stride, stream)
+    if st:
+        _check(st, "ft_rotate")
+
+
+def ft_kv_append_rotary(pages: ft_kv_pages, batch: ft_kv_batch, rotary: ft_rotary, k: int, k_token_stride: int,
+                        k_head_stride: int, v: int, v_token_stride: int, v_head_stride: int, num_q_heads: int = 0,
+                        q: int = 0, q_token_stride: int = 0, q_head_stride: int = 0, q_out: int = 0,
+                        q_out_token_stride: int = 0, q_out_head_stride: int = 0, stream: int = 0):
+    st = _lib.ft_kv_append_rotary(ctypes.addressof(pages), ctypes.addressof(batch), ctypes.addressof(rotary), k,
+                                  k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, num_q_heads, q,
+                                  q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, stream)
+    if st:
+        _check(st, "ft_kv_append_rotary")
 
 
 def ft_status_str(status: int) -> str:

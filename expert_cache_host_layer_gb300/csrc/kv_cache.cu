@@ -108,28 +108,18 @@ struct MoveArgs {
   int32_t* status;
 };
 
-// Page row of token `t` at head 0 (head h: + h * page_tokens), or -1.
+// Page row of token `t` at head 0 (head h: + h * page_tokens), or a negative number.
 template <bool kAppend>
 __device__ __forceinline__ int place_of(const MoveArgs& a, int t) {
-  const int s = find_seq(kAppend ? a.b.q_start : a.start, a.b.num_seqs, t);
   int pos;
-  if (kAppend) {
-    const Seq q = load_seq(a.p, a.b, s, a.status);
-    pos = q.n - q.m + (t - q.q0);
-    if (t < q.q0) {  // rows before q_start[0]: of no sequence, nor of a position that this would give
-      raise(a.status, FT_ERR_INVALID_ARG);
-      return -1;
-    }
-    if (t - q.q0 >= q.m || pos < 0) return -1;
-  } else {
-    const int n = __ldg(&a.b.kv_len[s]);
-    pos = t - __ldg(&a.start[s]);
-    if (n > a.b.table_stride * a.p.page_tokens) {
-      raise(a.status, FT_ERR_INVALID_ARG);
-      return -1;
-    }
-    if (pos < 0 || pos >= n) return -1;
+  if (kAppend) return new_place(a.p, a.b, t, a.status, &pos);
+  const int s = find_seq(a.start, a.b.num_seqs, t), n = __ldg(&a.b.kv_len[s]);
+  pos = t - __ldg(&a.start[s]);
+  if (n > a.b.table_stride * a.p.page_tokens) {
+    raise(a.status, FT_ERR_INVALID_ARG);
+    return -1;
   }
+  if (pos < 0 || pos >= n) return -1;
   const int page = load_page(a.p, a.b, s, pos / a.p.page_tokens, a.status);
   if (page < 0) return -1;
   return page * a.p.num_kv_heads * a.p.page_tokens + pos % a.p.page_tokens;  // rows are below 2^31

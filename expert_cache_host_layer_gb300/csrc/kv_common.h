@@ -72,6 +72,23 @@ __device__ __forceinline__ int find_seq(const int32_t* start, int n, int t) {
   }
   return lo;
 }
+// Page row of the batch's new token in row t at head 0 (head h: + h * page_tokens), and the
+// token's position; kUnstored: it has a position but no place, kNobodys: it belongs to no sequence.
+constexpr int kUnstored = -1, kNobodys = -2;
+__device__ __forceinline__ int new_place(const ft_kv_pages& p, const ft_kv_batch& b, int t, int32_t* status, int* pos) {
+  const int s = find_seq(b.q_start, b.num_seqs, t);
+  const Seq q = load_seq(p, b, s, status);
+  *pos = q.n - q.m + (t - q.q0);
+  if (t < q.q0) {  // rows before q_start[0]: of no sequence, nor of a position that this would give
+    raise(status, FT_ERR_INVALID_ARG);
+    return kNobodys;
+  }
+  if (t - q.q0 >= q.m) return kNobodys;
+  if (*pos < 0) return kUnstored;
+  const int page = load_page(p, b, s, *pos / p.page_tokens, status);
+  if (page < 0) return kUnstored;
+  return page * p.num_kv_heads * p.page_tokens + *pos % p.page_tokens;  // rows are below 2^31
+}
 // 2^(e - 127) of an exponent byte (255: NaN).  Stored bytes are 17..247 or 255.
 __device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e == kNanScale ? 0x7fc00000u : e << 23); }
 

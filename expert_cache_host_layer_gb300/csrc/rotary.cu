@@ -1,0 +1,287 @@
+// Rotary positions: ft_rotate, and ft_kv_append_rotary, which rotates a
+// batch's new queries, and its new keys on their way into the pages.
+//
+// Pair i of a head's first rot_dim values is turned by position * f_i:
+//   (a, b) -> scale * (a cos - b sin, b cos + a sin)
+// At position 10^6 an fp32 product position * f_i would leave few bits of the
+// turn's fraction, so the frequencies come as 64-bit fixed-point fractions of a
+// turn: position * turns_i mod 2^64 is the turn's fraction, exactly.  The
+// nearest quarter turn comes off in integers too, and the rest, at most an
+// eighth of a turn, becomes a float of 24 bits for sincospif.
+//
+// Values are read and written once: HBM bounds a chunk, the chain of loads
+// (q_start -> kv_len -> page; position -> sine) a decode step.  A block takes
+// `per` consecutive tokens.  Its threads look the places up and form each
+// (token, pair)'s sine and cosine once, for all heads, in shared memory; then a
+// group of head_dim / 16 lanes takes a head of a token at a time.  A lane has 16
+// values of it: both halves of eight pairs (8c.. and rot_dim / 2 + 8c.. where
+// the halves lie apart, 16c.. where pairs are interleaved), so that a pair
+// never leaves its thread, whatever rot_dim is.
+#include <algorithm>
+
+#include "decode_common.h"
+#include "kv_common.h"
+
+namespace ft {
+namespace kv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMostTokens = 32;    // of a block
+constexpr int kTrigFloats = 4096;  // of a block: tokens x rot_dim
+constexpr int kBatch = 2;          // heads a lane has in flight
+constexpr int kMostHeads = 8192;
+constexpr int kMostDim = 512;
+
+struct RotArgs {
+  ft_rotary r;
+  ft_kv_pages p;              // append
+  ft_kv_batch b;
+  const int32_t* positions;   // rotate
+  const __nv_bfloat16* x[3];  // q, k, v
+  int64_t ts[3], hs[3];
+  __nv_bfloat16* out;         // of q
+  int64_t ots, ohs;
+  int rows, per;              // tokens in all, and of a block
+  int Hq, heads, units;       // heads of q, of q, k and v, and lanes to a head
+  uint32_t by_heads;          // floor(2^32 / heads) + 1, 0 for one: v / heads = (v * by_heads) >> 32 for v * heads < 2^32
+  int32_t* status;
+};
+
+__device__ __forceinline__ void unpack8(uint4 r, float* v) { dec::decode_chunk<FT_W_BF16>(r, v); }
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// scale * (cos, sin) of a 64-bit fraction of a turn.
+__device__ __forceinline__ float2 turn(uint64_t fraction, float scale) {
+  const uint32_t f = (uint32_t)(fraction >> 32), quarter = (f + 0x20000000u) >> 30;
+  const int32_t rest = (int32_t)(f - (quarter << 30));  // of a turn of 2^32, within +-2^29
+  float s, c;
+  sincospif((float)rest * 0x1p-31f, &s, &c);
+  s *= scale;
+  c *= scale;
+  const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;  // cos(t + pi / 2) = -sin t, sin(t + pi / 2) = cos t
+  return make_float2(quarter == 1 || quarter == 2 ? -x : x, quarter & 2 ? -y : y);
+}
+
+template <bool kAppend, bool kFp8, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotArgs a) {
+  __shared__ float4 s_trig[kTrigFloats / 4];  // [token][cos 0..3, cos 4..7, sin 0..3, sin 4..7 of a lane's pairs][lane]
+  __shared__ int s_pos[kMostTokens], s_row[kMostTokens];
+  const int rot = a.r.rot_dim, half = rot / 2, lanes = rot / 16;  // lanes: of a head, those with pairs
+  const int t0 = blockIdx.x * a.per, tokens = min(a.per, a.rows - t0), jobs = tokens * a.heads;
+  const int groups = kThreads / a.units, group = threadIdx.x / a.units, c = threadIdx.x - group * a.units;
+  const bool active = group < groups;
+  const int Hk = kAppend ? a.p.num_kv_heads : 0;
+  uint4 x[kBatch][2];
+  int tok[kBatch], head[kBatch];  // head -1: none
+  // where a lane's two vectors lie in a head
+  auto place = [&](bool turned, int* e0, int* e1) {
+    const bool apart = !kInterleaved && turned;
+    *e0 = apart ? 8 * c : 16 * c;
+    *e1 = apart ? half + 8 * c : 16 * c + 8;
+  };
+  auto is_turned = [&](int h) { return c < lanes && (!kAppend || h < a.Hq + Hk); };
+  auto load = [&](int i, int v) {
+    head[i] = -1;
+    if (!active || v >= jobs) return;
+    const int t = a.by_heads ? (int)__umulhi((uint32_t)v, a.by_heads) : v, h = v - t * a.heads;
+    tok[i] = t;
+    head[i] = h;
+    const int which = !kAppend || h < a.Hq ? 0 : h < a.Hq + Hk ? 1 : 2;
+    const __nv_bfloat16* src = a.x[which] + (int64_t)(t0 + t) * a.ts[which] +
+                               (int64_t)(which == 0 ? h : which == 1 ? h - a.Hq : h - a.Hq - Hk) * a.hs[which];
+    int e0, e1;
+    place(is_turned(h), &e0, &e1);
+    x[i][0] = *reinterpret_cast<const uint4*>(src + e0);
+    x[i][1] = *reinterpret_cast<const uint4*>(src + e1);
+  };
+  dec::pdl_wait_primary();
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) load(i, group + i * groups);
+  if (threadIdx.x < tokens) {
+    int pos, row = 0;
+    if (kAppend) row = new_place(a.p, a.b, t0 + threadIdx.x, a.status, &pos);
+    else pos = __ldg(&a.positions[t0 + threadIdx.x]);
+    s_pos[threadIdx.x] = pos;
+    s_row[threadIdx.x] = row;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+    const int t = i / half, pair = i - t * half;
+    const float2 cs = turn((uint64_t)(int64_t)s_pos[t] * __ldg(&a.r.turns[pair]), a.r.scale);
+    float* to = reinterpret_cast<float*>(s_trig) + ((t * 4 + (pair >> 2 & 1)) * lanes + (pair >> 3)) * 4 + (pair & 3);
+    to[0] = cs.x;
+    to[8 * lanes] = cs.y;
+  }
+  __syncthreads();
+  for (int v0 = group; v0 - group < jobs; v0 += kBatch * groups) {  // the whole block together
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = tok[i], h = head[i];
+      float y[2][8];
+      bool turned = false;
+      if (h >= 0) {
+        turned = is_turned(h);
+        unpack8(x[i][0], y[0]);
+        unpack8(x[i][1], y[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e / 8][e % 8] = 0.0f;
+      }
+      if (turned) {
+        const float4* at = s_trig + t * 4 * lanes + c;
+        float cs[8], sn[8];
+        *reinterpret_cast<float4*>(cs) = at[0];
+        *reinterpret_cast<float4*>(cs + 4) = at[lanes];
+        *reinterpret_cast<float4*>(sn) = at[2 * lanes];
+        *reinterpret_cast<float4*>(sn + 4) = at[3 * lanes];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float& p = kInterleaved ? y[e / 4][2 * (e % 4)] : y[0][e];
+          float& q = kInterleaved ? y[e / 4][2 * (e % 4) + 1] : y[1][e];
+          const float u = fmaf(p, cs[e], -(q * sn[e])), w = fmaf(q, cs[e], p * sn[e]);
+          p = u;
+          q = w;
+        }
+      }
+      int e0, e1;
+      place(turned, &e0, &e1);
+      const bool query = !kAppend || h < a.Hq;
+      float top = 0.0f;
+      uint32_t bits = 0;
+      if (kAppend && kFp8) {  // largest magnitude of the head's vector (as bits: NaN above infinity), over its lanes
+#pragma unroll
+        for (int e = 0; e < 16; ++e) bits = max(bits, __float_as_uint(y[e / 8][e % 8]) & 0x7fffffffu);
+        for (int o = a.units / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+        top = __uint_as_float(bits);
+      }
+      if (h >= 0) {
+        const int row = s_row[t];
+        if (query) {
+          if (row != kNobodys) {
+            __nv_bfloat16* dst = a.out + (int64_t)(t0 + t) * a.ots + (int64_t)h * a.ohs;
+            *reinterpret_cast<uint4*>(dst + e0) = pack8(y[0]);
+            *reinterpret_cast<uint4*>(dst + e1) = pack8(y[1]);
+          }
+        } else if (row >= 0) {
+          const bool key = h < a.Hq + Hk;
+          const int64_t at = row + (int64_t)(key ? h - a.Hq : h - a.Hq - Hk) * a.p.page_tokens;
+          void* pages = key ? a.p.k : a.p.v;
+          const int D = a.p.head_dim;
+          if (kFp8) {
+            const int k = scale_exp(top);
+            uint8_t* dst = static_cast<uint8_t*>(pages) + at * D;
+            *reinterpret_cast<uint2*>(dst + e0) = encode8(y[0], k);
+            *reinterpret_cast<uint2*>(dst + e1) = encode8(y[1], k);
+            if (c == 0) (key ? a.p.k_scale : a.p.v_scale)[at] = (uint8_t)scale_byte(k);
+          } else {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(pages) + at * D;
+            *reinterpret_cast<uint4*>(dst + e0) = pack8(y[0]);
+            *reinterpret_cast<uint4*>(dst + e1) = pack8(y[1]);
+          }
+        }
+      }
+      load(i, v0 + (kBatch + i) * groups);
+    }
+  }
+  dec::pdl_launch_dependents();
+}
+
+ft_status check_rotary(const ft_rotary* r, int head_dim) {
+  if (!r) return set_error(FT_ERR_INVALID_ARG, "rotary is null");
+  if (r->rot_dim < 16 || r->rot_dim % 16 || r->rot_dim > head_dim)
+    return set_error(FT_ERR_UNSUPPORTED, "rot_dim=%d is not a multiple of 16 in 16..head_dim=%d", r->rot_dim, head_dim);
+  if (!(r->scale >= -3.0e38f && r->scale <= 3.0e38f)) return set_error(FT_ERR_INVALID_ARG, "the rotary's scale must be finite");
+  if (!r->turns || (reinterpret_cast<uintptr_t>(r->turns) & 7))
+    return set_error(FT_ERR_INVALID_ARG, "turns is null or not 8-byte aligned");
+  return FT_OK;
+}
+
+template <bool kAppend>
+ft_status launch(RotArgs& a, const char* name, bool fp8, cudaStream_t s) {
+  // one wave of eight blocks an SM, while that leaves a block no more tokens than it has room for
+  const int blocks = 8 * sm_count(), most = std::min(kMostTokens, kTrigFloats / a.r.rot_dim);
+  a.per = std::min(most, (int)(((long long)a.rows + blocks - 1) / blocks));
+  a.by_heads = a.heads == 1 ? 0 : (uint32_t)((1ull << 32) / a.heads) + 1;
+  const dim3 grid((unsigned)(((long long)a.rows + a.per - 1) / a.per));
+  auto* kernel = a.r.interleaved ? (fp8 ? rotary_kernel<kAppend, kAppend, true> : rotary_kernel<kAppend, false, true>)
+                                 : (fp8 ? rotary_kernel<kAppend, kAppend, false> : rotary_kernel<kAppend, false, false>);
+  const cudaError_t e = launch_dependent(kernel, grid, kThreads, 0, s, a);
+  if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(e));
+  return FT_OK;
+}
+
+}  // namespace
+}  // namespace kv
+}  // namespace ft
+
+using namespace ft;
+using namespace ft::kv;
+
+extern "C" ft_status ft_rotate(const ft_rotary* rotary, int32_t num_tokens, const int32_t* positions, int32_t num_heads,
+                               int32_t head_dim, const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+                               int64_t out_token_stride, int64_t out_head_stride, void* stream) {
+  if (head_dim < 16 || head_dim % 16 || head_dim > kMostDim)
+    return set_error(FT_ERR_UNSUPPORTED, "head_dim=%d is not a multiple of 16 in 16..%d", head_dim, kMostDim);
+  ft_status st = check_rotary(rotary, head_dim);
+  if (st != FT_OK) return st;
+  if (num_heads < 1 || num_heads > kMostHeads)
+    return set_error(FT_ERR_INVALID_ARG, "num_heads=%d outside 1..%d", num_heads, kMostHeads);
+  if (num_tokens < 0) return set_error(FT_ERR_INVALID_ARG, "num_tokens=%d", num_tokens);
+  if (num_tokens == 0) return FT_OK;
+  if (!positions) return set_error(FT_ERR_INVALID_ARG, "positions is null");
+  if (num_tokens == 1) x_token_stride = out_token_stride = head_dim;  // of single entries: not used
+  if (num_heads == 1) x_head_stride = out_head_stride = head_dim;
+  if ((st = check_rows("x", x, x_token_stride, x_head_stride)) != FT_OK) return st;
+  if ((st = check_rows("out", out, out_token_stride, out_head_stride)) != FT_OK) return st;
+  if (out_token_stride <= 0 || out_head_stride <= 0) return set_error(FT_ERR_INVALID_ARG, "out's strides must be positive");
+  RotArgs a{};
+  a.r = *rotary; a.positions = positions;
+  a.x[0] = static_cast<const __nv_bfloat16*>(x); a.ts[0] = x_token_stride; a.hs[0] = x_head_stride;
+  a.out = static_cast<__nv_bfloat16*>(out); a.ots = out_token_stride; a.ohs = out_head_stride;
+  a.rows = num_tokens; a.Hq = a.heads = num_heads; a.units = head_dim / 16;
+  return launch<false>(a, "rotate", false, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_batch* batch, const ft_rotary* rotary,
+                                         const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                                         int64_t v_token_stride, int64_t v_head_stride, int32_t num_q_heads,
+                                         const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                                         int64_t q_out_token_stride, int64_t q_out_head_stride, void* stream) {
+  ft_status st = check_pages(pages);
+  if (st == FT_OK) st = check_batch(pages, batch);
+  if (st == FT_OK) st = check_rotary(rotary, pages->head_dim);
+  if (st != FT_OK) return st;
+  if (num_q_heads < 0 || num_q_heads > kMostHeads)
+    return set_error(FT_ERR_INVALID_ARG, "num_q_heads=%d outside 0..%d", num_q_heads, kMostHeads);
+  if (batch->num_tokens == 0) return FT_OK;
+  const int D = pages->head_dim;
+  if (batch->num_tokens == 1) k_token_stride = v_token_stride = q_token_stride = q_out_token_stride = D;  // not used
+  if (pages->num_kv_heads == 1) k_head_stride = v_head_stride = D;
+  if (num_q_heads == 1) q_head_stride = q_out_head_stride = D;
+  if ((st = check_rows("k", k, k_token_stride, k_head_stride)) != FT_OK) return st;
+  if ((st = check_rows("v", v, v_token_stride, v_head_stride)) != FT_OK) return st;
+  RotArgs a{};
+  if (num_q_heads > 0) {
+    if ((st = check_rows("q", q, q_token_stride, q_head_stride)) != FT_OK) return st;
+    if ((st = check_rows("q_out", q_out, q_out_token_stride, q_out_head_stride)) != FT_OK) return st;
+    if (q_out_token_stride <= 0 || q_out_head_stride <= 0)
+      return set_error(FT_ERR_INVALID_ARG, "q_out's strides must be positive");
+  }
+  a.r = *rotary; a.p = *pages; a.b = *batch;
+  a.x[0] = static_cast<const __nv_bfloat16*>(q); a.ts[0] = q_token_stride; a.hs[0] = q_head_stride;
+  a.x[1] = static_cast<const __nv_bfloat16*>(k); a.ts[1] = k_token_stride; a.hs[1] = k_head_stride;
+  a.x[2] = static_cast<const __nv_bfloat16*>(v); a.ts[2] = v_token_stride; a.hs[2] = v_head_stride;
+  a.out = static_cast<__nv_bfloat16*>(q_out); a.ots = q_out_token_stride; a.ohs = q_out_head_stride;
+  a.rows = batch->num_tokens; a.Hq = num_q_heads; a.heads = num_q_heads + 2 * pages->num_kv_heads; a.units = D / 16;
+  if ((st = status_word(&a.status)) != FT_OK) return st;
+  return launch<true>(a, "append_rotary", pages->kv_dtype == FT_KV_FP8E4M3, static_cast<cudaStream_t>(stream));
+}

@@ -3,6 +3,7 @@
     pages = KVPages(k, v, k_scale, v_scale)          # once, for the layer's life
     batch = KVBatch(q_start, kv_len, block_table, num_tokens, max_q_len)   # once a step, for every layer
     pages.append(batch, k_new, v_new)                # store the new tokens
+    pages.append(batch, k_new, v_new, rotary=rotary, q=q, q_out=q)   # or: with rotary positions (rotary.py)
     pages.attend(batch, q, out)                      # softmax(q k^T / sqrt(D)) v over their sequences
     pages.read(batch, kv_start, k_out, v_out)        # whole sequences back in bf16
 
@@ -30,12 +31,14 @@ import torch
 
 from . import (FT_KV_BF16, FT_KV_FP8E4M3, FT_KV_WORKSPACE_ZERO, _check, ft_kv_attend_workspace, ft_kv_batch,
                ft_kv_pages, ft_kv_status, library)
+from .rotary import Rotary
 
-# The three calls are made once per layer and step, so they go to the library
+# The calls are made once per layer and step, so they go to the library
 # directly: at a decode step's sizes the binding's own functions, a device guard
 # and a stream object would cost as much as the GPU's work.
 _lib = library()
 _append, _attend, _read = _lib.ft_kv_append, _lib.ft_kv_attend, _lib.ft_kv_read
+_append_rotary = _lib.ft_kv_append_rotary
 _workspaces: dict = {}  # (device index, stream) -> uint8 tensor
 _outgrown: list = []    # the smaller ones before them: three of a stream at most (sizes go by head_dim and the kernels)
 _captured: dict = {}    # (device index, stream) -> (number, uint8 tensor) of the last capture that the stream was part of
@@ -112,12 +115,26 @@ class KVPages:
         return cls(*kv, *sc)
 
     # ---- the calls ---------------------------------------------------------
-    def append(self, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream: torch.cuda.Stream | None = None):
-        """Store the batch's new keys and values, bf16 [num_tokens, kv_heads, head_dim] (strided views are fine)."""
+    def append(self, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream: torch.cuda.Stream | None = None,
+               rotary: Rotary | None = None, q: torch.Tensor | None = None, q_out: torch.Tensor | None = None):
+        """Store the batch's new keys and values, bf16 [num_tokens, kv_heads, head_dim] (strided views are fine).
+        With ``rotary`` the keys are stored rotated to their positions, and the queries q, bf16 [num_tokens, q_heads,
+        head_dim], rotated into q_out (which may be q)."""
         rows = (*self._rows(batch, k, self.num_kv_heads, "k"), *self._rows(batch, v, self.num_kv_heads, "v"))
-        self._call(_append, self.address, batch.address, *rows, self._stream(stream))
+        if rotary is None:
+            _need(q is None and q_out is None, "q and q_out go with rotary")
+            self._call(_append, self.address, batch.address, *rows, self._stream(stream))
+        else:
+            _need((q is None) == (q_out is None), "q goes with q_out")
+            _need(rotary.index == self.index, "the rotary and the cache are on one device")
+            heads, queries = 0, (0, 0, 0, 0, 0, 0)
+            if q is not None:
+                heads = q.shape[1] if q.dim() == 3 else 0
+                queries = (*self._rows(batch, q, heads, "q"), *self._rows(batch, q_out, heads, "q_out"))
+            self._call(_append_rotary, self.address, batch.address, rotary.address, *rows, heads, *queries,
+                       self._stream(stream))
         if stream is not None:
-            self._record(stream, batch, k, v)
+            self._record(stream, batch, k, v, q, q_out, None if rotary is None else rotary.turns)
 
     def attend(self, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None = None,
                scale: float | None = None, causal: bool = True, window: int = 0,

@@ -581,6 +581,43 @@ ft_status ft_add_norm(const ft_norm* norm, int64_t num_rows, const void* x, int6
                       const void* delta, int64_t delta_stride, int32_t delta_dtype, void* total, int64_t total_stride,
                       void* out, int64_t out_stride, int32_t out_dtype, float* scales, void* stream);
 
+/* Rotary positions: pair i of a head's first rot_dim values is turned by the
+ * angle of its token, the rest is left as it is:
+ *   (a, b) -> scale * (a cos - b sin, b cos + a sin),  angle = position * turns[i] / 2^64 turns
+ * Pair i is values (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved.
+ * turns[i] is the fraction of a turn that one position adds, as a 64-bit
+ * fixed-point number (2^64 times frequency / 2 pi, modulo 2^64), so that
+ * position * turns[i] is exact at any position, a negative one among them
+ * (which turns back).  cos and sin are fp32; results are rounded once. */
+typedef struct ft_rotary {
+  const uint64_t* turns; /* device [rot_dim / 2] */
+  int32_t rot_dim;       /* a multiple of 16, 16..head_dim */
+  int32_t interleaved;   /* 0 or 1 */
+  float scale;           /* of cos and sin: 1, or a long-context scaling's factor */
+} ft_rotary;
+
+/* x, out: device bf16 [num_tokens][num_heads][head_dim] with strides in
+ * elements: 16-byte aligned, strides multiples of 8, out's positive; positions:
+ * device int32 [num_tokens].  head_dim: a multiple of 16, at most 512;
+ * num_heads: at most 8192.  out may be x itself (same strides), and does not
+ * overlap it otherwise. */
+ft_status ft_rotate(const ft_rotary* rotary, int32_t num_tokens, const int32_t* positions, int32_t num_heads,
+                    int32_t head_dim, const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+                    int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/* ft_kv_append of the batch's keys after their rotation, at their positions in
+ * their sequences, and the rotation of its queries: q, q_out device bf16
+ * [num_tokens][num_q_heads][head_dim] (num_q_heads 0: none), q_out with positive
+ * strides, q itself or apart from every other tensor.  A rotated key is rounded
+ * once, into the cache's type.  Queries of rows that belong to no sequence are
+ * left as they are in q_out; a row at a negative position is rotated there and
+ * its key not stored. */
+ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_batch* batch, const ft_rotary* rotary, const void* k,
+                              int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                              int64_t v_head_stride, int32_t num_q_heads, const void* q, int64_t q_token_stride,
+                              int64_t q_head_stride, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                              void* stream);
+
 const char* ft_status_str(ft_status s);
 /* Message of the calling thread's last error ("" if none). */
 const char* ft_last_error(void);
