@@ -27,6 +27,7 @@ FT_FETCH_COPY_ENGINE, FT_FETCH_SM_PULL = 0, 1
 FT_KV_BF16, FT_KV_FP8E4M3 = 0, 1
 FT_KV_WORKSPACE_ZERO = 8192
 FT_F32, FT_BF16, FT_FP8E4M3 = 0, 1, 2
+FT_SCORE_SOFTMAX, FT_SCORE_SIGMOID = 0, 1
 
 
 class FtError(RuntimeError):
@@ -89,6 +90,11 @@ class ft_rotary(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class ft_router(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "num_groups", "top_groups", "group_top", "renormalise")] + \
+        [("scale", ctypes.c_float), ("bias", ctypes.c_void_p), ("bias_stride", ctypes.c_int64)]
+
+
 # ---------------------------------------------------------------- loading
 
 def _load():
@@ -107,6 +113,7 @@ def _load():
         "ft_cache_destroy": (st, [P]),
         "ft_cache_resize": (st, [P, P, I64]),
         "ft_route_classify": (st, [P, I32, P, I32, P, P]),
+        "ft_cache_set_router": (st, [P, P]),
         "ft_fetch_misses": (st, [P, I32]),
         "ft_moe_forward": (st, [P, I32, P, I32, P]),
         "ft_synchronize": (st, [P]),
@@ -139,6 +146,7 @@ def _load():
         "ft_add_norm": (st, [P, I64, P, I64, I32, P, I64, I32, P, I64, P, I64, I32, P, P]),
         "ft_rotate": (st, [P, I32, P, I32, I32, P, I64, I64, P, I64, I64, P]),
         "ft_kv_append_rotary": (st, [P, P, P, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, P]),
+        "ft_route": (st, [P, I32, I32, I32, P, I64, I32, P, P, P]),
         "ft_status_str": (ctypes.c_char_p, [st]),
         "ft_last_error": (ctypes.c_char_p, []),
     }
@@ -201,6 +209,10 @@ def ft_cache_resize(cache: int, new_pool: int, new_num_slots: int):
 def ft_route_classify(cache: int, layer: int, logits: int, T: int, topk_idx: int = 0, topk_w: int = 0):
     _check(_lib.ft_route_classify(cache, layer, logits or None, T, topk_idx or None, topk_w or None),
            "ft_route_classify")
+
+
+def ft_cache_set_router(cache: int, router: ft_router | None):
+    _check(_lib.ft_cache_set_router(cache, None if router is None else ctypes.addressof(router)), "ft_cache_set_router")
 
 
 def ft_fetch_misses(cache: int, layer: int):
@@ -418,6 +430,14 @@ def ft_kv_append_rotary(pages: ft_kv_pages, batch: ft_kv_batch, rotary: ft_rotar
                                   q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, stream)
     if st:
         _check(st, "ft_kv_append_rotary")
+
+
+def ft_route(router: ft_router, num_experts: int, top_k: int, num_tokens: int, logits: int, logits_stride: int,
+             logits_dtype: int, topk_idx: int, topk_w: int, stream: int = 0):
+    st = _lib.ft_route(ctypes.addressof(router), num_experts, top_k, num_tokens, logits, logits_stride, logits_dtype,
+                       topk_idx, topk_w, stream)
+    if st:
+        _check(st, "ft_route")
 
 
 def ft_status_str(status: int) -> str:

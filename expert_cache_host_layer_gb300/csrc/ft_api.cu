@@ -31,6 +31,7 @@
 #include <vector>
 
 #include "ft_internal.h"
+#include "route_rule.h"
 #include <nvtx3/nvToolsExt.h>
 
 using namespace ft;
@@ -177,6 +178,8 @@ struct ft_cache {
   int32_t* pf_pos = nullptr;
   int32_t* pf_hist = nullptr;          // [E][chunks of rows]: the row grouping's counts
   unsigned* gbar = nullptr;           // grid-barrier words of the fused FFN kernel
+  ft_router router{};                 // the rule of the choice, if by_rule
+  bool by_rule = false;
   bool fused_ok = true;               // false once the fused FFN kernel reported it cannot run
   // streams and events
   cudaStream_t compute = nullptr;
@@ -788,6 +791,11 @@ ft_status ft_route_classify(ft_cache* c, int32_t layer, const float* logits, int
   a.ring = c->ring_dev;
   a.expert_bytes = (long long)c->eb;
   a.build_rows = (long long)T * c->k <= kMaxExperts;
+  if (c->by_rule) {
+    const bool aligned = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && c->E % 4 == 0;
+    a.by_rule = 1;
+    a.rule = make_rule(c->router, c->E, c->k, c->router.bias ? c->router.bias + layer * c->router.bias_stride : nullptr, aligned);
+  }
   // The route stream starts after everything the caller has enqueued on the
   // compute stream so far: the logits, and in the double-buffered schedule the
   // FFN of event t-2 (whose slots this event may evict).
@@ -808,6 +816,21 @@ ft_status ft_route_classify(ft_cache* c, int32_t layer, const float* logits, int
   return FT_OK;
 }
 
+
+ft_status ft_cache_set_router(ft_cache* c, const ft_router* router) {
+  if (!c) return fail(FT_ERR_INVALID_ARG, "null cache");
+  if (!router) {
+    c->by_rule = false;
+    return FT_OK;
+  }
+  const ft_status st = check_router(router, c->E, c->k);
+  if (st != FT_OK) return st;
+  if (router->bias && (router->bias_stride < 0 || (router->bias_stride > 0 && router->bias_stride < c->E)))
+    return fail(FT_ERR_INVALID_ARG, "bias_stride=%lld is not 0 or %d and more", (long long)router->bias_stride, c->E);
+  c->router = *router;
+  c->by_rule = true;
+  return FT_OK;
+}
 
 ft_status ft_fetch_misses(ft_cache* c, int32_t layer) {
   NvtxRange nv("ft_fetch_misses", layer);

@@ -124,6 +124,17 @@ struct RingEntry {
   int32_t miss_slot[kMaxExperts];
 };
 
+namespace rule {
+// A routing rule (ft_router) as kernels take it (route_rule.h).
+struct Rule {
+  int softmax, groups, top_groups, group_top, renormalise;
+  float scale;
+  const float* bias;  // [E] or null
+  int E, k, lanes, size;  // lanes and experts of a group
+  int vectors;            // rows can be read four logits at a time
+};
+}  // namespace rule
+
 struct RouteArgs {
   const float* logits;
   int T, E, k, layer;  // the event number and the pin flag live in the tables (device state)
@@ -135,6 +146,8 @@ struct RouteArgs {
   RingEntry* ring;     // device address of the event ring (copy-engine mode), or null
   long long expert_bytes;
   int build_rows;      // 1: the kernel groups rows by expert (small T*k)
+  int by_rule;         // 1: picks and gates by `rule`
+  rule::Rule rule;
 };
 
 // Sets the calling thread's ft_last_error() message and returns `s`.

@@ -5,8 +5,6 @@
 
 #include <cuda.h>
 
-#include <atomic>
-
 #include "decode_common.h"
 #include "kv_common.h"
 
@@ -277,18 +275,5 @@ bool pages_map(CUtensorMap* m, const ft_kv_pages& p, const void* base, int box_r
 // q as [token][head][64 of head_dim], boxes of `tokens` x G heads x 128 bytes, swizzled.
 bool queries_map(CUtensorMap* m, const AttendArgs& a, int tokens);
 
-// Raise a kernel's limit of dynamic shared memory, once per device
-// (kId: a number of its own for each kernel of one type.  Static: a process may
-// load two builds of the library, whose kernels are not the same.)
-template <int kId, typename Kernel>
-static cudaError_t allow_smem(Kernel* kernel, int bytes) {
-  static std::atomic<unsigned long long> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
-  return e;
-}
 }  // namespace kv
 }  // namespace ft

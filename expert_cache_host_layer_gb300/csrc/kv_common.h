@@ -2,6 +2,8 @@
 // batch's sequences, and the sticky status word.  Internal to libft.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -23,6 +25,19 @@ ft_status check_rows(const char* name, const void* ptr, int64_t token_stride, in
 // Device address of the current device's sticky status word.
 ft_status status_word(int32_t** out);
 int sm_count();  // of the current device
+// Raise a kernel's limit of dynamic shared memory, once per device
+// (kId: a number of its own for each kernel of one type.  Static: a process may
+// load two builds of the library, whose kernels are not the same.)
+template <int kId, typename Kernel>
+static cudaError_t allow_smem(Kernel* kernel, int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+  return e;
+}
 // A launch that may begin while the kernel before it on the stream ends (the kernel waits for its end itself).
 template <typename... P, typename... A>
 static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, const A&... args) {

@@ -1,0 +1,124 @@
+// ft_route: experts and gates of a batch's tokens by a routing rule
+// (route_rule.h has the rule and how a warp follows it).
+#include <algorithm>
+
+#include "decode_common.h"
+#include "kv_common.h"
+#include "route_rule.h"
+
+namespace ft {
+namespace {
+
+constexpr int kWarps = 4;
+
+struct RouteBatch {
+  rule::Rule r;
+  const void* logits;
+  int64_t stride;
+  int T;
+  int32_t* idx;
+  float* w;
+};
+
+template <int PL, typename T>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteBatch a) {
+  extern __shared__ __align__(16) unsigned char shared[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned char* own = shared + warp * rule::warp_bytes(a.r.E, a.r.bias != nullptr);
+  dec::pdl_wait_primary();
+  for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
+    int e;
+    float w;
+    rule::route_row<PL>(a.r, static_cast<const T*>(a.logits) + t * a.stride, own, &e, &w);
+    if (lane < a.r.k) {
+      a.idx[(int64_t)t * a.r.k + lane] = e;
+      a.w[(int64_t)t * a.r.k + lane] = w;
+    }
+  }
+  dec::pdl_launch_dependents();
+}
+
+template <int PL, typename T>
+cudaError_t launch(const RouteBatch& a, cudaStream_t s) {
+  const int bytes = kWarps * rule::warp_bytes(a.r.E, a.r.bias != nullptr);
+  const cudaError_t e = kv::allow_smem<2 * PL + (sizeof(T) == 2)>(route_kernel<PL, T>, kWarps * rule::warp_bytes(kMaxExperts, true));
+  if (e != cudaSuccess) return e;
+  const int blocks = std::min((a.T + kWarps - 1) / kWarps, 16 * kv::sm_count());
+  return kv::launch_dependent(route_kernel<PL, T>, dim3(blocks), kWarps * 32, bytes, s, a);
+}
+template <typename T>
+cudaError_t launch(const RouteBatch& a, cudaStream_t s) {
+  switch (rule::values_per_lane(a.r.E, a.r.groups)) {
+    case 1: return launch<1, T>(a, s);
+    case 2: return launch<2, T>(a, s);
+    case 4: return launch<4, T>(a, s);
+    case 8: return launch<8, T>(a, s);
+    case 16: return launch<16, T>(a, s);
+    default: return launch<32, T>(a, s);
+  }
+}
+
+}  // namespace
+
+ft_status check_router(const ft_router* r, int E, int k) {
+  if (!r) return set_error(FT_ERR_INVALID_ARG, "router is null");
+  if (E < 1 || E > kMaxExperts) return set_error(FT_ERR_INVALID_ARG, "num_experts=%d outside 1..%d", E, kMaxExperts);
+  if (k < 1 || k > kMaxTopK || k > E) return set_error(FT_ERR_INVALID_ARG, "top_k=%d outside 1..min(num_experts, %d)", k, kMaxTopK);
+  if (r->score != FT_SCORE_SOFTMAX && r->score != FT_SCORE_SIGMOID)
+    return set_error(FT_ERR_INVALID_ARG, "score=%d is not an ft_score", r->score);
+  if (r->num_groups < 1 || r->num_groups > rule::kMostGroups || E % r->num_groups)
+    return set_error(FT_ERR_INVALID_ARG, "num_groups=%d is not a divisor of num_experts=%d in 1..%d", r->num_groups, E, rule::kMostGroups);
+  if (r->top_groups < 1 || r->top_groups > r->num_groups)
+    return set_error(FT_ERR_INVALID_ARG, "top_groups=%d outside 1..num_groups=%d", r->top_groups, r->num_groups);
+  const int size = E / r->num_groups;
+  if (r->group_top < 1 || r->group_top > 2 || (r->num_groups > 1 && r->group_top > size))
+    return set_error(FT_ERR_INVALID_ARG, "group_top=%d is not 1 or 2 experts of a group's %d", r->group_top, size);
+  if (k > r->top_groups * size)
+    return set_error(FT_ERR_INVALID_ARG, "top_k=%d is beyond the %d experts of %d groups", k, r->top_groups * size, r->top_groups);
+  if (rule::values_per_lane(E, r->num_groups) == 0)
+    return set_error(FT_ERR_UNSUPPORTED, "num_experts=%d in %d groups: at most %d", E, r->num_groups,
+                     32 * rule::group_lanes(r->num_groups) * r->num_groups);
+  if (!(r->scale >= -3.0e38f && r->scale <= 3.0e38f)) return set_error(FT_ERR_INVALID_ARG, "the router's scale must be finite");
+  if (reinterpret_cast<uintptr_t>(r->bias) & 3) return set_error(FT_ERR_INVALID_ARG, "bias is not 4-byte aligned");
+  return FT_OK;
+}
+
+rule::Rule make_rule(const ft_router& r, int E, int k, const float* bias, bool aligned_rows) {
+  rule::Rule x{};
+  x.softmax = r.score == FT_SCORE_SOFTMAX;
+  x.groups = r.num_groups; x.top_groups = r.top_groups; x.group_top = r.num_groups > 1 ? r.group_top : 1;
+  x.renormalise = r.renormalise != 0; x.scale = r.scale; x.bias = bias;
+  x.E = E; x.k = k; x.size = E / r.num_groups; x.lanes = rule::group_lanes(r.num_groups);
+  x.vectors = aligned_rows && x.size % 4 == 0;
+  return x;
+}
+
+}  // namespace ft
+
+using namespace ft;
+
+extern "C" ft_status ft_route(const ft_router* router, int32_t num_experts, int32_t top_k, int32_t num_tokens,
+                              const void* logits, int64_t logits_stride, int32_t logits_dtype, int32_t* topk_idx,
+                              float* topk_w, void* stream) {
+  const ft_status st = check_router(router, num_experts, top_k);
+  if (st != FT_OK) return st;
+  if (num_tokens < 0) return set_error(FT_ERR_INVALID_ARG, "num_tokens=%d", num_tokens);
+  if (logits_dtype != FT_F32 && logits_dtype != FT_BF16)
+    return set_error(FT_ERR_INVALID_ARG, "logits_dtype=%d is not FT_F32 or FT_BF16", logits_dtype);
+  if (num_tokens == 0) return FT_OK;
+  const int size = logits_dtype == FT_F32 ? 4 : 2;
+  if (!logits || !topk_idx || !topk_w) return set_error(FT_ERR_INVALID_ARG, "null logits, topk_idx or topk_w");
+  if ((reinterpret_cast<uintptr_t>(logits) & (size - 1)) || ((reinterpret_cast<uintptr_t>(topk_idx) | reinterpret_cast<uintptr_t>(topk_w)) & 3))
+    return set_error(FT_ERR_INVALID_ARG, "logits, topk_idx or topk_w is not aligned to its elements");
+  if (num_tokens == 1) logits_stride = num_experts;  // of a single row: not used
+  if (logits_stride < num_experts)
+    return set_error(FT_ERR_INVALID_ARG, "logits_stride=%lld is below num_experts=%d", (long long)logits_stride, num_experts);
+  RouteBatch a{};
+  const bool aligned = reinterpret_cast<uintptr_t>(logits) % (4 * size) == 0 && (num_tokens == 1 || logits_stride % 4 == 0);
+  a.r = make_rule(*router, num_experts, top_k, router->bias, aligned);
+  a.logits = logits; a.stride = logits_stride; a.T = num_tokens; a.idx = topk_idx; a.w = topk_w;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = size == 4 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s);
+  if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "route launch: %s", cudaGetErrorString(e));
+  return FT_OK;
+}

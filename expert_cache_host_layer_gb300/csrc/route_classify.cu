@@ -6,7 +6,8 @@
 //
 // Phase 1 (all CTAs): one warp per token computes the top-k experts by logit
 // (descending, lower index on ties; NaN ordered as -inf) with k rounds of a
-// warp-wide arg-max, and the gates softmax(selected logits).  Each CTA ORs its
+// warp-wide arg-max, and the gates softmax(selected logits); or both by the
+// cache's routing rule (route_rule.h).  Each CTA ORs its
 // tokens' experts into a shared bit set and counts picks per expert.  With
 // more than one CTA, the CTAs merge both into global scratch (one atomic per
 // non-zero word/count) and the last CTA to finish (atomic ticket) runs phase
@@ -26,6 +27,7 @@
 #include <climits>
 
 #include "ft_internal.h"
+#include "route_rule.h"
 
 namespace ft {
 namespace {
@@ -72,8 +74,58 @@ __device__ __forceinline__ int checked_slot(const Tables& t, int key) {
   return checked_ok(s >= 0 && s < t.num_slots && t.slot_key[s] == key, t.status) ? s : -1;
 }
 
-template <int PL>  // logits per lane: E <= 32 * PL
-__global__ void __launch_bounds__(kThreads) route_classify_kernel(RouteArgs a) {
+// The k largest logits and their softmax: pick and gate j to lane j < k.
+template <int PL>
+__device__ __forceinline__ void default_picks(const float* row, int E, int k, int* pick, float* gate) {
+  const int lane = threadIdx.x & 31;
+  float v[PL];
+#pragma unroll
+  for (int q = 0; q < PL; ++q) {
+    const int e = q * 32 + lane;
+    float x = e < E ? __ldg(row + e) : -INFINITY;
+    v[q] = (x != x) ? -INFINITY : x;  // NaN ordered as -inf
+  }
+  uint32_t taken = 0u;
+  float my_v = -INFINITY;
+  int my_i = 0;
+  for (int j = 0; j < k; ++j) {
+    float bv = -INFINITY;
+    int bi = INT_MAX;
+#pragma unroll
+    for (int q = 0; q < PL; ++q) {
+      const int e = q * 32 + lane;
+      if (e < E && !((taken >> q) & 1u) && better(v[q], e, bv, bi)) {
+        bv = v[q];
+        bi = e;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
+      const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
+      if (better(ov, oi, bv, bi)) {
+        bv = ov;
+        bi = oi;
+      }
+    }
+    if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
+    if (lane == j) {
+      my_v = bv;
+      my_i = bi;
+    }
+  }
+  const float m = __shfl_sync(0xffffffffu, my_v, 0);
+  float ex = lane < k ? expf(my_v - m) : 0.0f;
+  float sum = ex;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  *pick = my_i;
+  *gate = ex / sum;
+}
+
+template <int PL, bool kRule>  // logits per lane: E <= 32 * PL, or as the rule's layout has it
+__global__ void __launch_bounds__(kThreads) route_classify_kernel(const __grid_constant__ RouteArgs a) {
+  extern __shared__ __align__(16) unsigned char s_rule[];  // of each warp, if kRule
   __shared__ uint32_t s_bits[kMaxExperts / 32];
   __shared__ int s_cnt[kMaxExperts];
   __shared__ int s_warp[kWarps];
@@ -115,49 +167,14 @@ __global__ void __launch_bounds__(kThreads) route_classify_kernel(RouteArgs a) {
   // ---------------- phase 1: top-k + gates, one warp per token -------------
   for (int t = blockIdx.x * kWarps + warp; t < T; t += gridDim.x * kWarps) {
     const float* row = a.logits + (long long)t * E;
-    float v[PL];
-#pragma unroll
-    for (int q = 0; q < PL; ++q) {
-      const int e = q * 32 + lane;
-      float x = e < E ? __ldg(row + e) : -INFINITY;
-      v[q] = (x != x) ? -INFINITY : x;  // NaN ordered as -inf
-    }
-    uint32_t taken = 0u;
-    float my_v = -INFINITY;
     int my_i = 0;
-    for (int j = 0; j < k; ++j) {
-      float bv = -INFINITY;
-      int bi = INT_MAX;
-#pragma unroll
-      for (int q = 0; q < PL; ++q) {
-        const int e = q * 32 + lane;
-        if (e < E && !((taken >> q) & 1u) && better(v[q], e, bv, bi)) {
-          bv = v[q];
-          bi = e;
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-        const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-        if (better(ov, oi, bv, bi)) {
-          bv = ov;
-          bi = oi;
-        }
-      }
-      if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
-      if (lane == j) {
-        my_v = bv;
-        my_i = bi;
-      }
+    float w = 0.0f;
+    if (kRule) {
+      rule::route_row<PL>(a.rule, row, s_rule + warp * rule::warp_bytes(E, a.rule.bias != nullptr), &my_i, &w);
+    } else {
+      default_picks<PL>(row, E, k, &my_i, &w);
     }
-    const float m = __shfl_sync(0xffffffffu, my_v, 0);
-    float ex = lane < k ? expf(my_v - m) : 0.0f;
-    float sum = ex;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane < k) {
-      const float w = ex / sum;
       const long long r = (long long)t * k + lane;
       a.plan.topk_idx[r] = my_i;
       a.plan.topk_w[r] = w;
@@ -463,39 +480,50 @@ __global__ void init_tables_kernel(Tables tab, int num_keys) {
 
 }  // namespace
 
+namespace {
+template <typename F>
+cudaError_t each_kernel(F f) {  // f(kernel, values per lane, whether it follows a rule)
+  cudaError_t e = cudaSuccess;
+  auto one = [&](auto* k, int pl, bool by_rule) { if (e == cudaSuccess) e = f(k, pl, by_rule); };
+  one(route_classify_kernel<1, false>, 1, false);
+  one(route_classify_kernel<2, false>, 2, false);
+  one(route_classify_kernel<4, false>, 4, false);
+  one(route_classify_kernel<8, false>, 8, false);
+  one(route_classify_kernel<16, false>, 16, false);
+  one(route_classify_kernel<32, false>, 32, false);
+  one(route_classify_kernel<1, true>, 1, true);
+  one(route_classify_kernel<2, true>, 2, true);
+  one(route_classify_kernel<4, true>, 4, true);
+  one(route_classify_kernel<8, true>, 8, true);
+  one(route_classify_kernel<16, true>, 16, true);
+  one(route_classify_kernel<32, true>, 32, true);
+  return e;
+}
+}  // namespace
+
 cudaError_t prefer_max_shared_route() {
-  const void* fns[] = {reinterpret_cast<const void*>(route_classify_kernel<1>),
-                       reinterpret_cast<const void*>(route_classify_kernel<2>),
-                       reinterpret_cast<const void*>(route_classify_kernel<4>),
-                       reinterpret_cast<const void*>(route_classify_kernel<8>),
-                       reinterpret_cast<const void*>(route_classify_kernel<16>),
-                       reinterpret_cast<const void*>(route_classify_kernel<32>)};
-  for (const void* f : fns) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                               cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return each_kernel([](auto* k, int, bool by_rule) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && by_rule)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * rule::warp_bytes(kMaxExperts, true));
+    return e;
+  });
 }
 
 cudaError_t launch_route_classify(const RouteArgs& a, cudaStream_t s) {
   const int warps_needed = (a.T + kWarps - 1) / kWarps;
   int grid = warps_needed < 1 ? 1 : warps_needed;
   if (grid > 4 * 152) grid = 4 * 152;
-  const int pl = (a.E + 31) / 32;
-  if (pl <= 1)
-    route_classify_kernel<1><<<grid, kThreads, 0, s>>>(a);
-  else if (pl <= 2)
-    route_classify_kernel<2><<<grid, kThreads, 0, s>>>(a);
-  else if (pl <= 4)
-    route_classify_kernel<4><<<grid, kThreads, 0, s>>>(a);
-  else if (pl <= 8)
-    route_classify_kernel<8><<<grid, kThreads, 0, s>>>(a);
-  else if (pl <= 16)
-    route_classify_kernel<16><<<grid, kThreads, 0, s>>>(a);
+  int pl = 1;
+  if (a.by_rule) pl = rule::values_per_lane(a.E, a.rule.groups);
   else
-    route_classify_kernel<32><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+    while (32 * pl < a.E) pl *= 2;
+  const int shared = a.by_rule ? kWarps * rule::warp_bytes(a.E, a.rule.bias != nullptr) : 0;
+  return each_kernel([&](auto* k, int of, bool by_rule) {
+    if (of != pl || by_rule != (a.by_rule != 0)) return cudaSuccess;
+    k<<<grid, kThreads, shared, s>>>(a);
+    return cudaGetLastError();
+  });
 }
 
 cudaError_t launch_init_tables(Tables tab, int num_keys, cudaStream_t s) {

@@ -21,7 +21,7 @@ from . import (FT_FETCH_SM_PULL, FT_W_F32, ft_cache_create, ft_cache_destroy, ft
                ft_host_bank_alloc, ft_host_bank_free,
                ft_cache_resize, ft_expert_bytes, ft_slots_for_budget,
                ft_fetch_misses, ft_get_copy_stream, ft_get_plan, ft_get_stats, ft_get_tables, ft_get_timing,
-               ft_moe_forward, ft_reset_stats, ft_route_classify, ft_step_graph_create, ft_step_graph_destroy,
+               ft_cache_set_router, ft_moe_forward, ft_reset_stats, ft_route_classify, ft_step_graph_create, ft_step_graph_destroy,
                ft_step_graph_launch, ft_step_graph_timing, ft_step_graph_trace, ft_synchronize, ft_timing_enable,
                make_config)
 
@@ -50,6 +50,7 @@ class ExpertCache:
                           bank.numel() * bank.element_size(), self.bank_blobs, max_tokens, fetch_mode, pull_ctas,
                           copy_streams, fetch_warps)
         self.cfg = cfg
+        self.router = None
         self.handle = ft_cache_create(cfg, self.pool.data_ptr(), num_slots, self.stream.cuda_stream)
         self.copy_stream = torch.cuda.ExternalStream(ft_get_copy_stream(self.handle), device=self.device)
 
@@ -89,6 +90,16 @@ class ExpertCache:
         if slots != self.num_slots:
             self.resize(slots, torch.empty(slots * self.eb, dtype=torch.uint8, device=self.device))
         return slots
+
+    def set_router(self, router):
+        """The rule (router.Router; None: the default) of later routing calls and of step graphs created later."""
+        if router is not None and (router.num_experts, router.top_k) != (self.E, self.k):
+            raise ValueError("the router is for %d of %d experts" % (self.k, self.E))
+        if router is not None and router.bias is not None and (router.index != self.pool.get_device() or
+                                                              router.bias.dim() == 2 and router.bias.shape[0] != self.L):
+            raise ValueError("the router's bias is a tensor of the cache's device, [E] or [L, E]")
+        ft_cache_set_router(self.handle, None if router is None else router.c)
+        self.router = router  # keeps the bias
 
     # ---- thin wrappers ---------------------------------------------------
     def route_classify(self, layer, logits: torch.Tensor, topk_idx=None, topk_w=None):
@@ -181,6 +192,7 @@ class StepGraph:
     def __init__(self, cache: ExpertCache, logits, xs, ys, double_buffer=True, timing=False):
         self.cache = cache
         self.logits, self.xs, self.ys = logits, xs, ys  # keep the buffers alive
+        self.router = cache.router                      # (and its bias)
         T = logits[0].shape[0]
         self.handle = ft_step_graph_create(cache.handle, [t.data_ptr() for t in logits], [t.data_ptr() for t in xs],
                                            [t.data_ptr() for t in ys], T, double_buffer, timing)

@@ -219,6 +219,7 @@ ft_status ft_cache_resize(ft_cache* cache, void* new_pool, int64_t new_num_slots
  *   topk_idx device, int32 [T][k] or NULL: experts per token in selection
  *            order (logit descending, lower index first on ties)
  *   topk_w   device, float32 [T][k] or NULL: softmax over the k selected logits
+ * (another rule of choice and gates: ft_cache_set_router)
  * The event number t increments by one per call.  Victims are the least
  * recently used slots excluding this event's hits and the previous event's
  * slots (which the previous layer's FFN may still read).  T may be 0.
@@ -234,6 +235,41 @@ ft_status ft_cache_resize(ft_cache* cache, void* new_pool, int64_t new_num_slots
  */
 ft_status ft_route_classify(ft_cache* cache, int32_t layer, const float* logits, int32_t T, int32_t* topk_idx,
                             float* topk_w);
+
+/* How a layer's tokens choose their experts.  The default of a cache, and what
+ * ft_route does with {FT_SCORE_SOFTMAX, 1, 1, 1, 1, 1.0f, NULL, 0}: the top_k
+ * largest logits, gates their softmax.
+ *   s = softmax(logits) or 1 / (1 + e^-logit);  v = s + bias for the choice alone
+ *   num_groups > 1: the experts of a group are consecutive, and only those of
+ *     the top_groups groups take part whose largest v (group_top 1), or the sum
+ *     of whose two largest (group_top 2), are largest
+ *   the top_k largest v, in that order;  gates s, divided by their sum over the
+ *     picks if renormalise, times scale
+ * Equal values go to the lower group and expert.  The choice is that of exact
+ * arithmetic: logits are compared where their order is that of v, and values
+ * too close for fp32 are compared in fp64.  A NaN logit counts as -inf (and so
+ * does a v of NaN), an infinite one as the largest number; picks without any
+ * score have gate 0. */
+typedef enum ft_score { FT_SCORE_SOFTMAX = 0, FT_SCORE_SIGMOID = 1 } ft_score;
+typedef struct ft_router {
+  int32_t score;       /* ft_score */
+  int32_t num_groups;  /* 1..32, a divisor of the experts' number; at most 32 experts a warp's lane: see ft_route */
+  int32_t top_groups;  /* 1..num_groups, with top_k experts or more */
+  int32_t group_top;   /* 1 or 2 */
+  int32_t renormalise; /* 0 or 1 */
+  float scale;
+  const float* bias;   /* device float32 [num_experts], or NULL */
+  int64_t bias_stride; /* ft_cache_set_router: floats from one layer's bias to the next's (0: one for all) */
+} ft_router;
+
+/*
+ * The rule by which the cache's later ft_route_classify calls, and the step
+ * graphs created later, choose (NULL: the default).  The struct is read during
+ * the call; the bias is read by every later call and graph and stays the
+ * caller's, whose writes to it are ordered like those to the logits.
+ * Errors: FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED (see ft_route).
+ */
+ft_status ft_cache_set_router(ft_cache* cache, const ft_router* router);
 
 /*
  * Copy the layer's misses (from its last ft_route_classify) from the host
@@ -617,6 +653,17 @@ ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_batch* batch
                               int64_t v_head_stride, int32_t num_q_heads, const void* q, int64_t q_token_stride,
                               int64_t q_head_stride, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
                               void* stream);
+
+/* Experts and gates of a batch's tokens by a routing rule (ft_router), without
+ * a cache: for ft_moe_decode_ffn_static, or any other experts.
+ *   logits   device FT_F32 or FT_BF16 [num_tokens][num_experts], rows logits_stride
+ *            elements apart (of a single row it is not used)
+ *   topk_idx device int32 [num_tokens][top_k] in selection order; topk_w device float32, the gates
+ * num_experts 1..1024, top_k 1..min(num_experts, 32).  A group has the largest
+ * power of two of lanes that fits 32 / num_groups, each with 32 experts at most
+ * (FT_ERR_UNSUPPORTED beyond; up to 512 experts always fit). */
+ft_status ft_route(const ft_router* router, int32_t num_experts, int32_t top_k, int32_t num_tokens, const void* logits,
+                   int64_t logits_stride, int32_t logits_dtype, int32_t* topk_idx, float* topk_w, void* stream);
 
 const char* ft_status_str(ft_status s);
 /* Message of the calling thread's last error ("" if none). */

@@ -16,6 +16,8 @@ taken where they are silent:
 """
 from __future__ import annotations
 
+import dataclasses
+
 import numpy as np
 
 
@@ -47,3 +49,57 @@ def route(logits: np.ndarray, k: int):
     """(topk_idx int32 [T,k], gates float64 [T,k]) for router logits [T,E]."""
     idx = topk(logits, k)
     return idx, gates(logits, idx)
+
+
+@dataclasses.dataclass
+class Rule:
+    """A routing rule: scores s = softmax or sigmoid of the logits, the choice by v = s + bias (with groups: among the
+    top_groups groups of consecutive experts whose best v, or sum of the best two, is largest), gates s of the picks,
+    renormalised over them or not, times scale.  Without a bias v has the logits' order.  Equal values go to the lower
+    index; a NaN logit or v is -inf, an infinite one the largest fp32 number; without any score the gates are 0."""
+    score: str = "softmax"
+    bias: np.ndarray | None = None
+    groups: int = 1
+    top_groups: int = 1
+    group_top: int = 1
+    renormalise: bool = True
+    scale: float = 1.0
+
+
+def clean(x):
+    x = np.asarray(x, dtype=np.float64)
+    return np.minimum(np.where(np.isnan(x), -np.inf, x), float(np.finfo(np.float32).max)) + 0.0
+
+
+def route_by(rule: Rule, logits: np.ndarray, k: int):
+    """(topk_idx int32 [T, k], gates float64 [T, k]) by a rule."""
+    x = clean(logits)
+    T, E = x.shape
+    with np.errstate(over="ignore"):
+        if rule.score == "sigmoid":
+            s = 1.0 / (1.0 + np.exp(-x))
+        else:
+            e = np.exp(x - np.maximum(x.max(axis=1, keepdims=True), -1e300))
+            s = np.divide(e, e.sum(axis=1, keepdims=True), out=np.zeros_like(e), where=e.sum(axis=1, keepdims=True) > 0)
+    v = x if rule.bias is None else clean(s + np.asarray(rule.bias, dtype=np.float64))
+    if rule.groups > 1 and rule.top_groups < rule.groups:
+        of = (v if rule.bias is not None or rule.group_top == 1 else s).reshape(T, rule.groups, -1)
+        best = np.sort(of, axis=2)[:, :, ::-1][:, :, :rule.group_top].sum(axis=2)
+        take = selection_order(best)[:, :rule.top_groups]
+        part = np.zeros((T, rule.groups), dtype=bool)
+        np.put_along_axis(part, take, True, axis=1)
+        part = np.repeat(part, E // rule.groups, axis=1)
+    else:
+        part = np.ones((T, E), dtype=bool)
+    idx = np.empty((T, k), dtype=np.int32)
+    for t in range(T):  # those that take part, by (v descending, index ascending)
+        at = np.flatnonzero(part[t])
+        idx[t] = at[np.lexsort((at, -v[t, at]))[:k]]
+    w = np.take_along_axis(s, idx.astype(np.int64), axis=1)
+    if rule.renormalise:
+        l = np.take_along_axis(x, idx.astype(np.int64), axis=1)
+        if rule.score == "softmax":  # the row's denominator cancels, and so may its underflow
+            w = np.exp(l - np.maximum(l.max(axis=1, keepdims=True), -1e300))
+        total = w.sum(axis=1, keepdims=True)
+        w = np.divide(w, total, out=np.zeros_like(w), where=total > 0)
+    return idx, w * rule.scale
