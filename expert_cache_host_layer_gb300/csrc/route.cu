@@ -10,6 +10,7 @@ namespace ft {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kManyRows = 2048;  // from here on four rows go to a warp: below, rows have a warp each at once
 
 struct RouteBatch {
   rule::Rule r;
@@ -20,31 +21,48 @@ struct RouteBatch {
   float* w;
 };
 
-template <int PL, typename T>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteBatch a) {
+template <int PL, typename T, bool kFour>
+__global__ void __launch_bounds__(kWarps * 32, kFour ? 5 : PL <= 8 ? 8 : PL == 16 ? 5 : 3) route_kernel(const __grid_constant__ RouteBatch a) {
   extern __shared__ __align__(16) unsigned char shared[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned char* own = shared + warp * rule::warp_bytes(a.r.E, a.r.bias != nullptr);
+  const bool scored = a.r.bias != nullptr;
+  unsigned char* list = shared + warp * (kFour ? rule::four_bytes(a.r.E, scored) : rule::warp_bytes(a.r.E, scored));
   dec::pdl_wait_primary();
-  for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
-    int e;
-    float w;
-    rule::route_row<PL>(a.r, static_cast<const T*>(a.logits) + t * a.stride, own, &e, &w);
-    if (lane < a.r.k) {
-      a.idx[(int64_t)t * a.r.k + lane] = e;
-      a.w[(int64_t)t * a.r.k + lane] = w;
+  const rule::Lane<PL> own(a.r);
+  const T* logits = static_cast<const T*>(a.logits);
+  if constexpr (kFour) {
+    for (int t = 4 * (blockIdx.x * kWarps + warp); t < a.T; t += 4 * gridDim.x * kWarps)
+      rule::route_four<PL>(a.r, own, logits, a.stride, t, a.T, list, a.idx, a.w);
+  } else {
+    for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
+      int e;
+      float w;
+      rule::route_row<PL>(a.r, own, logits + t * a.stride, list, &e, &w);
+      if (lane < a.r.k) {
+        a.idx[(int64_t)t * a.r.k + lane] = e;
+        a.w[(int64_t)t * a.r.k + lane] = w;
+      }
     }
   }
   dec::pdl_launch_dependents();
 }
 
+template <int PL, typename T, bool kFour>
+cudaError_t launch(const RouteBatch& a, cudaStream_t s) {
+  const bool scored = a.r.bias != nullptr;
+  const int bytes = kWarps * (kFour ? rule::four_bytes(a.r.E, scored) : rule::warp_bytes(a.r.E, scored));
+  const cudaError_t e = kv::allow_smem<4 * PL + 2 * kFour + (sizeof(T) == 2)>(route_kernel<PL, T, kFour>,
+                                                                              kWarps * rule::warp_bytes(kMaxExperts, true));
+  if (e != cudaSuccess) return e;
+  const int rows = kWarps * (kFour ? 4 : 1);
+  const int blocks = std::min((a.T + rows - 1) / rows, (kFour ? 5 : 8) * kv::sm_count());  // one wave
+  return kv::launch_dependent(route_kernel<PL, T, kFour>, dim3(blocks), kWarps * 32, bytes, s, a);
+}
 template <int PL, typename T>
 cudaError_t launch(const RouteBatch& a, cudaStream_t s) {
-  const int bytes = kWarps * rule::warp_bytes(a.r.E, a.r.bias != nullptr);
-  const cudaError_t e = kv::allow_smem<2 * PL + (sizeof(T) == 2)>(route_kernel<PL, T>, kWarps * rule::warp_bytes(kMaxExperts, true));
-  if (e != cudaSuccess) return e;
-  const int blocks = std::min((a.T + kWarps - 1) / kWarps, 16 * kv::sm_count());
-  return kv::launch_dependent(route_kernel<PL, T>, dim3(blocks), kWarps * 32, bytes, s, a);
+  if constexpr (PL <= 8)
+    if (a.T >= kManyRows && a.r.k <= rule::kFew && a.r.groups <= rule::kFew) return launch<PL, T, true>(a, s);
+  return launch<PL, T, false>(a, s);
 }
 template <typename T>
 cudaError_t launch(const RouteBatch& a, cudaStream_t s) {

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) route_classify_kernel(const __grid_c
     int my_i = 0;
     float w = 0.0f;
     if (kRule) {
-      rule::route_row<PL>(a.rule, row, s_rule + warp * rule::warp_bytes(E, a.rule.bias != nullptr), &my_i, &w);
+      rule::route_row<PL>(a.rule, rule::Lane<PL>(a.rule), row, s_rule + warp * rule::warp_bytes(E, a.rule.bias != nullptr), &my_i, &w);
     } else {
       default_picks<PL>(row, E, k, &my_i, &w);
     }

@@ -8,17 +8,18 @@
 //
 // The choice is that of exact arithmetic.  Without a bias v orders as the logit
 // does, and logits are compared as they are.  With one, fp32 values of v are
-// good to `err`: whatever lies within 2 err of another candidate (or, for sums
-// of a group, of the border between taking part and not) is compared again in
-// fp64, for which few rows in a thousand have cause.
+// good to a known error: a pick that has another candidate within twice that
+// (or a group that takes part, one that does not within its own bound) sends the
+// row to a comparison in fp64, for which few rows in a thousand have cause.
 //
 // What bounds it: a row's E logits are read once, but k selections over them
 // are instructions (issue slots on a chunk, their latency for one token).  So
 // the warp does not select k times over E: its lanes' k-th largest maximum,
 // from k warp-wide integer maxima (redux) over one value a lane, bounds the
 // k-th largest value from below; the few values above that bound (9 of 256 for
-// k = 8) go to a list in shared memory, and each finds its rank by comparing
-// itself with the others.
+// k = 8) go to a list in shared memory, and each finds its rank by counting the
+// others above it.  Values that a lane does not have (a ragged group, or a group
+// that takes no part) are NaN, which no comparison holds for.
 #pragma once
 
 #include <cfloat>
@@ -49,10 +50,10 @@ inline int values_per_lane(int E, int groups) {
   }
   return 0;
 }
-// Shared memory of a warp: the list's (value, expert) pairs, their fp64 values where a bias is given, the picks.
-__host__ __device__ __forceinline__ int warp_bytes(int E, bool scored) {
-  return (E + 1) / 2 * 2 * (scored ? 16 : 8) + kMaxTopK * 4;
-}
+// Shared memory of a warp: the list's values (padded to fours with NaN) and experts, fp64 values where a bias is given, the
+// picks.
+__host__ __device__ __forceinline__ int list_room(int E) { return (E + 3) / 4 * 4 + 4; }
+__host__ __device__ __forceinline__ int warp_bytes(int E, bool scored) { return list_room(E) * (scored ? 16 : 8) + kMaxTopK * 4; }
 
 // Floats as unsigned integers of the same order; 0 is below all of them.
 __device__ __forceinline__ uint32_t order(float x) {
@@ -62,8 +63,19 @@ __device__ __forceinline__ uint32_t order(float x) {
 __device__ __forceinline__ float value(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
-// A logit as it counts: NaN as -inf, +inf as the largest number.
-__device__ __forceinline__ float clean(float l) { return l != l ? -INFINITY : fminf(l, FLT_MAX); }
+// A number as it counts: NaN as -inf (fmaxf gives the other operand), +inf as the largest number.
+__device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float logit(const float* row, int e) { return clean(row[e]); }
 __device__ __forceinline__ float logit(const __nv_bfloat16* row, int e) { return clean(__bfloat162float(row[e])); }
 __device__ __forceinline__ void logits4(const float* row, int e, float* l) {
@@ -99,18 +111,29 @@ __device__ __noinline__ Exact make_exact(const Rule r, const T* row, float top) 
   }
   return x;
 }
-// Whether the lane's group takes part, in fp64.
+// Whether the lane's group takes part, in fp64 (of logits where those decide: without a bias, by a group's best).  least: a
+// bound below the fp32 values that may count, as the caller has them (fp64 is slow here: 3000 cycles a sigmoid).
 template <typename T>
-__device__ __noinline__ bool exact_groups(const Rule r, const T* row, float top, int group, int sub) {
+__device__ __noinline__ bool exact_groups(const Rule r, const T* row, float top, float inv_z, int group, int sub, float least) {
   const Exact x = make_exact(r, row, top);
+  const bool logits = !r.bias && r.group_top == 1;
   double a = -INFINITY, b = -INFINITY;
-  if (group < r.groups)
-    for (int i = sub; i < r.size; i += r.lanes) {
-      const int e = group * r.size + i;
-      const double v = x.value(logit(row, e), e);
+  int i = group < r.groups ? sub : r.size;
+  for (;;) {
+    float l = 0.0f;
+    for (; i < r.size; i += r.lanes) {  // the lane's next value that may count
+      l = logit(row, group * r.size + i);
+      const float s = logits ? l : r.softmax ? exp2_approx((l - top) * kLog2e) * inv_z : rcp_approx(1.0f + exp2_approx(-l * kLog2e));
+      if ((r.bias ? s + clean(__ldg(&r.bias[group * r.size + i])) : s) >= least) break;
+    }
+    if (!__any_sync(0xffffffffu, i < r.size)) break;
+    if (i < r.size) {
+      const double v = logits ? (double)l : x.value(l, group * r.size + i);
       b = fmax(b, fmin(a, v));
       a = fmax(a, v);
+      i += r.lanes;
     }
+  }
   for (int o = r.lanes / 2; o > 0; o >>= 1) {
     const double oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
     b = fmax(fmin(a, oa), fmax(b, ob));
@@ -122,54 +145,81 @@ __device__ __noinline__ bool exact_groups(const Rule r, const T* row, float top,
     const double of = __shfl_sync(0xffffffffu, mine, g * r.lanes);
     above += of > mine || (of == mine && g < group);
   }
-  return above < r.top_groups;
+  return group < r.groups && above < r.top_groups;
 }
-// The list's ranks in fp64; picks: the k best.
+// The list's ranks in fp64.
 template <typename T>
-__device__ __noinline__ void exact_ranks(const Rule r, const T* row, float top, const int2* list, double* keys, int n, int* picks) {
-  const Exact x = make_exact(r, row, top);
+__device__ __noinline__ void exact_ranks(const Rule r, const T* row, float top, const int* experts, double* keys, int n, int* picks) {
   const int lane = threadIdx.x & 31;
-  for (int i = lane; i < n; i += 32) keys[i] = x.value(logit(row, list[i].y), list[i].y);
+  const Exact x = make_exact(r, row, top);
+  for (int i = lane; i < n; i += 32) keys[i] = x.value(logit(row, experts[i]), experts[i]);
   __syncwarp();
   for (int i = lane; i < n; i += 32) {
     const double v = keys[i];
-    const int e = list[i].y;
+    const int e = experts[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += keys[j] > v || (keys[j] == v && list[j].y < e);
+    for (int j = 0; j < n; ++j) rank += keys[j] > v || (keys[j] == v && experts[j] < e);
     if (rank < r.k) picks[rank] = e;
   }
 }
+// The rank of (x, e) among a list's values, equal ones by expert.
+__device__ __forceinline__ int rank_of(float x, int e, const float* values, const int* experts, int n) {
+  int rank = 0;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) rank += values[j] > x || (values[j] == x && experts[j] < e);
+  return rank;
+}
+
+// What a lane keeps for every row: its experts' bias (0 without one; NaN: it has no such expert), and where they are.
+template <int PL>
+struct Lane {
+  static constexpr int V = PL < 4 ? PL : 4;
+  float add[PL];
+  int group, sub, expert;  // expert: of value 0
+  __device__ __forceinline__ explicit Lane(const Rule& r) {
+    const int lane = threadIdx.x & 31;
+    group = lane / r.lanes;
+    sub = lane & (r.lanes - 1);
+    expert = group * r.size + sub * V;
+#pragma unroll
+    for (int q = 0; q < PL; ++q) {
+      const bool has = group < r.groups && sub * V + step(r, q) < r.size;
+      add[q] = !has ? NAN : r.bias ? clean(__ldg(&r.bias[expert + step(r, q)])) : 0.0f;
+    }
+  }
+  static __device__ __forceinline__ int step(const Rule& r, int q) { return (q / V) * r.lanes * V + q % V; }
+  __device__ __forceinline__ bool has(int q) const { return add[q] == add[q]; }
+};
 
 // The row's picks in order: expert and gate of pick j to lane j < k.  `shared`:
 // warp_bytes of the warp's own, 16-byte aligned.
 template <int PL, typename T>
-__device__ __forceinline__ void route_row(const Rule& r, const T* row, unsigned char* shared, int* expert, float* gate) {
-  constexpr int V = PL < 4 ? PL : 4;
-  const int lane = threadIdx.x & 31, group = lane / r.lanes, sub = lane & (r.lanes - 1);
+__device__ __forceinline__ void route_row(const Rule& r, const Lane<PL>& own, const T* row, unsigned char* shared, int* expert,
+                                          float* gate) {
+  constexpr int V = Lane<PL>::V;
+  const int lane = threadIdx.x & 31, room = list_room(r.E);
   const bool scored = r.bias != nullptr;
-  int2* list = reinterpret_cast<int2*>(shared);
-  double* keys = reinterpret_cast<double*>(shared + (r.E + 1) / 2 * 16);
-  int* picks = reinterpret_cast<int*>(shared + (r.E + 1) / 2 * 2 * (scored ? 16 : 8));
-  auto in_group = [&](int q) { return (q / V) * r.lanes * V + sub * V + q % V; };
+  float* values = reinterpret_cast<float*>(shared);
+  int* experts = reinterpret_cast<int*>(values + room);
+  double* keys = reinterpret_cast<double*>(experts + room);
+  int* picks = scored ? reinterpret_cast<int*>(keys + room) : experts + room;
 
   float v[PL];
-  bool ok[PL];
 #pragma unroll
-  for (int q = 0; q < PL; ++q) ok[q] = group < r.groups && in_group(q) < r.size;
+  for (int q = 0; q < PL; ++q) v[q] = NAN;
   if (V == 4 && r.vectors) {
 #pragma unroll
     for (int q = 0; q < PL; q += 4)
-      if (ok[q]) logits4(row, group * r.size + in_group(q), &v[q]);
+      if (own.has(q)) logits4(row, own.expert + own.step(r, q), &v[q]);
   } else {
 #pragma unroll
     for (int q = 0; q < PL; ++q)
-      if (ok[q]) v[q] = logit(row, group * r.size + in_group(q));
+      if (own.has(q)) v[q] = logit(row, own.expert + own.step(r, q));
   }
 #pragma unroll
-  for (int q = 0; q < PL; ++q) v[q] = ok[q] ? clean(v[q]) : -INFINITY;
+  for (int q = 0; q < PL; ++q) v[q] = clean(v[q]);  // (-inf where there is none, for now)
 
-  // scores: `largest` of the row's, for the error bound
-  float top = 0.0f, inv_z = 1.0f, largest = 1.0f;
+  float top = 0.0f, inv_z = 1.0f, largest = 1.0f;  // largest: of the row's scores, for the error bound
   if (r.softmax) {
     float m = v[0];
 #pragma unroll
@@ -185,103 +235,135 @@ __device__ __forceinline__ void route_row(const Rule& r, const T* row, unsigned 
       largest = inv_z;
     }
   }
-  auto score = [&](float l) { return r.softmax ? __expf(l - top) * inv_z : __fdividef(1.0f, 1.0f + __expf(-l)); };
+  // exp2 (2^-22) of a rounded argument (1.5 u |l|, at most 0.23 of it left in s (1 - s)), 1 + e (u) and rcp (2^-23) come to
+  // less than 2^-21.5 of a sigmoid; a softmax's denominator may be off by its sum of 32 terms in a lane
+  auto score = [&](float l) {
+    return r.softmax ? exp2_approx((l - top) * kLog2e) * inv_z : rcp_approx(1.0f + exp2_approx(-l * kLog2e));
+  };
+  const float err_score = r.softmax ? largest * 0x1p-18f : 0x1p-21f;
   if (scored) {
+    if (r.softmax) {
 #pragma unroll
-    for (int q = 0; q < PL; ++q) {
-      if (!ok[q]) continue;
-      const float c = score(v[q]) + __ldg(&r.bias[group * r.size + in_group(q)]);
-      v[q] = clean(c);
+      for (int q = 0; q < PL; ++q) v[q] = exp2_approx((v[q] - top) * kLog2e) * inv_z;
+    } else {
+#pragma unroll
+      for (int q = 0; q < PL; ++q) v[q] = rcp_approx(1.0f + exp2_approx(-v[q] * kLog2e));
     }
   }
-  // fp32's error of a score (__expf: 2 ulp and its argument's rounding, sums and quotient the rest), and of the sum with the bias
-  const float err_score = r.softmax ? largest * 0x1p-18f : 0x1p-20f;
-
-  bool part = group < r.groups;
-  if (r.groups > 1 && r.top_groups < r.groups) {
-    float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < PL; ++q) {
-      b = fmaxf(b, fminf(a, v[q]));
-      a = fmaxf(a, v[q]);
-    }
-    for (int o = r.lanes / 2; o > 0; o >>= 1) {
-      const float oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
-      b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-      a = fmaxf(a, oa);
-    }
-    float mine = a;
-    if (r.group_top == 2) mine = scored ? a + b : score(a) + score(b);
-    int above = 0;
-    for (int g = 0; g < r.groups; ++g) {
-      const float of = __shfl_sync(0xffffffffu, mine, g * r.lanes);
-      above += of > mine || (of == mine && g < group);
-    }
-    const bool in = part && above < r.top_groups;
-    const bool mine_is_a_sum = r.group_top == 2;
-    if (scored || mine_is_a_sum) {  // the border between the groups that take part and the others
-      const float worst = value(~__reduce_max_sync(0xffffffffu, in ? ~order(mine) : 0u));
-      const float best = value(__reduce_max_sync(0xffffffffu, part && !in ? order(mine) : 0u));
-      const float size = part ? (scored ? fabsf(a) : 1.0f) + (scored && mine_is_a_sum ? fabsf(b) : 1.0f) : 0.0f;
-      const float err = 2.0f * err_score + 0x1p-22f * value(__reduce_max_sync(0xffffffffu, order(size)));
-      if (worst - best > 2.0f * err) {
-        part = in;
-      } else {
-        const bool in_exactly = exact_groups(r, row, top, group, sub);
-        part = part && in_exactly;
-      }
+  for (int q = 0; q < PL; ++q) v[q] += own.add[q];
+
+  bool part = own.group < r.groups;
+  if (r.top_groups < r.groups) {
+    float a = -INFINITY, b = -INFINITY;
+    if (r.group_top == 1) {
+#pragma unroll
+      for (int q = 0; q < PL; ++q) a = fmaxf(a, v[q]);
+      for (int o = r.lanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     } else {
-      part = in;
+#pragma unroll
+      for (int q = 0; q < PL; ++q) {
+        const float c = fmaxf(v[q], -INFINITY);
+        b = fmaxf(b, fminf(a, c));
+        a = fmaxf(a, c);
+      }
+      for (int o = r.lanes / 2; o > 0; o >>= 1) {
+        const float oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
+        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+        a = fmaxf(a, oa);
+      }
+    }
+    const float mine = r.group_top == 1 ? a : scored ? a + b : score(a) + score(b);
+    // the top_groups largest (fewer rounds than groups; more groups than that if some are equal)
+    uint32_t left = part ? order(mine) : 0u;
+    bool in = false;
+#pragma unroll 1
+    for (int j = 0; j < r.top_groups; ++j) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, left);
+      if (left == m && m != 0u) {
+        in = true;
+        left = 0u;
+      }
+    }
+    bool sure = __popc(__ballot_sync(0xffffffffu, in && own.sub == 0)) == r.top_groups;
+    if (scored || r.group_top == 2) {
+      const float err = 2.0f * err_score + 0x1p-22f * (scored ? fabsf(a) + (r.group_top == 2 ? fabsf(b) : 0.0f) : 2.0f);
+      const uint32_t worst = __reduce_min_sync(0xffffffffu, in ? order(mine - err) : 0xffffffffu);
+      const uint32_t best = __reduce_max_sync(0xffffffffu, part && !in ? order(mine == -INFINITY ? mine : mine + err) : 0u);
+      sure = sure && worst > best;
+    }
+    part = sure ? in : false;
+    if (!sure) {
+      const float by = 2.0f * err_score + 0x1p-21f * fmaxf(fabsf(a), fabsf(b == -INFINITY ? a : b));
+      part = exact_groups(r, row, top, inv_z, own.group, own.sub, scored || r.group_top == 2 ? (r.group_top == 1 ? a : scored ? b : score(b)) - by : a);
     }
   }
 
   // a bound below the k-th largest value: the k-th largest of the lanes' maxima
-  uint32_t u[PL], most = 0;
+  float m = v[0];
 #pragma unroll
-  for (int q = 0; q < PL; ++q) {
-    u[q] = part && ok[q] ? order(v[q]) : 0u;
-    most = max(most, u[q]);
+  for (int q = 1; q < PL; ++q) m = fmaxf(m, v[q]);
+  uint32_t most = part && m == m ? order(m) : 0u;
+  const uint32_t first = __reduce_max_sync(0xffffffffu, most);
+  uint32_t last = first;
+#pragma unroll 2
+  for (int j = 1; j < r.k; ++j) {
+    if (most == last) most = 0u;
+    last = __reduce_max_sync(0xffffffffu, most);
   }
-  uint32_t cut = 0, first = 0;
-  for (int j = 0; j < r.k; ++j) {
-    cut = __reduce_max_sync(0xffffffffu, most);
-    if (j == 0) first = cut;
-    if (most == cut) most = 0;
-  }
-  float near = -1.0f;  // values so close to each other are not told apart
-  if (cut == 0) {      // fewer lanes than picks have any
-    cut = 1;
-    uint32_t size = 0;
+  float cut = -INFINITY, near = 0.0f;  // near: values so close to each other are not told apart
+  if (last != 0u) {
+    cut = value(last);
+    if (scored) {
+      near = 2.0f * err_score + 0x1p-22f * fmaxf(fabsf(value(first)), fabsf(cut));
+      cut -= near;
+    }
+  } else if (scored) {  // fewer lanes than picks have any value: all of them are candidates
+    float size = 0.0f;
 #pragma unroll
-    for (int q = 0; q < PL; ++q) size = max(size, u[q] ? __float_as_uint(value(u[q])) & 0x7fffffffu : 0u);
-    if (scored) near = 2.0f * err_score + 0x1p-21f * __uint_as_float(__reduce_max_sync(0xffffffffu, size));
-  } else if (scored) {
-    near = 2.0f * err_score + 0x1p-21f * fmaxf(fabsf(value(first)), fabsf(value(cut)));
-    cut = order(value(cut) - near);
+    for (int q = 0; q < PL; ++q) size = fmaxf(size, fabsf(v[q]));
+    near = 2.0f * err_score + 0x1p-22f * value(__reduce_max_sync(0xffffffffu, order(size)));
   }
+  if (!part) cut = NAN;
   int n = 0;
 #pragma unroll
   for (int q = 0; q < PL; ++q) {
-    const unsigned m = __ballot_sync(0xffffffffu, u[q] >= cut);
-    if (u[q] >= cut)
-      list[n + __popc(m & ((1u << lane) - 1u))] = make_int2(__float_as_int(value(u[q])), group * r.size + in_group(q));
-    n += __popc(m);
-  }
-  __syncwarp();
-  bool close = false;
-  for (int i = lane; i < n; i += 32) {
-    const int2 own = list[i];
-    const float x = __int_as_float(own.x);
-    int rank = 0;
-    for (int j = 0; j < n; ++j) {
-      const int2 o = list[j];
-      const float y = __int_as_float(o.x);
-      rank += y > x || (y == x && o.y < own.y);
-      close |= fabsf(y - x) <= near && o.y != own.y;
+    const bool in = v[q] >= cut;
+    const unsigned who = __ballot_sync(0xffffffffu, in);
+    if (in) {
+      const int at = n + __popc(who & ((1u << lane) - 1u));
+      values[at] = v[q];
+      experts[at] = own.expert + own.step(r, q);
     }
-    if (rank < r.k) picks[rank] = own.y;
+    n += __popc(who);
   }
-  if (__any_sync(0xffffffffu, close)) exact_ranks(r, row, top, list, keys, n, picks);
+  if (lane < 4) values[n + lane] = NAN;
+  __syncwarp();
+  bool unsure = false;
+  for (int i = lane; i < n; i += 32) {
+    const float x = values[i], lo = x - near, hi = x + near;
+    int above = 0, not_below = 0;
+#pragma unroll 1
+    for (int j = 0; j < n; j += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(values + j);
+      above += (y.x > hi) + (y.y > hi) + (y.z > hi) + (y.w > hi);
+      not_below += (y.x >= lo) + (y.y >= lo) + (y.z >= lo) + (y.w >= lo);
+    }
+    if (above < r.k) {
+      picks[above] = experts[i];
+      unsure |= not_below - above != 1;  // another one beside itself
+    }
+  }
+  if (__any_sync(0xffffffffu, unsure)) {
+    if (scored) {
+      exact_ranks(r, row, top, experts, keys, n, picks);
+    } else {
+      for (int i = lane; i < n; i += 32) {
+        const int rank = rank_of(values[i], experts[i], values, experts, n);
+        if (rank < r.k) picks[rank] = experts[i];
+      }
+    }
+  }
   __syncwarp();
 
   // gates
@@ -289,15 +371,14 @@ __device__ __forceinline__ void route_row(const Rule& r, const T* row, unsigned 
   const float l = lane < r.k ? logit(row, e) : -INFINITY;
   float w = 0.0f;
   if (!r.renormalise) {
-    w = r.softmax ? expf(l - top) * inv_z : 1.0f / (1.0f + expf(-l));
+    w = r.softmax ? expf(l - top) * inv_z : __fdividef(1.0f, 1.0f + expf(-l));
   } else {
     // Factors that all picks share cancel, and with them what might underflow: the softmax's denominator, and e^m of
     // sigmoids whose largest is small (e^l / (1 + e^l) = e^m e^(l - m) / (1 + e^l)).
     const float m = fmaxf(value(__reduce_max_sync(0xffffffffu, order(l))), -FLT_MAX);
     if (r.softmax) w = expf(l - m);
-    else w = m < 0.0f ? expf(l - m) / (1.0f + expf(l)) : 1.0f / (1.0f + expf(-l));
-  }
-  if (r.renormalise) {
+    else if (m < 0.0f) w = __fdividef(expf(l - m), 1.0f + expf(l));
+    else w = __fdividef(1.0f, 1.0f + expf(-l));
     float sum = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -306,6 +387,286 @@ __device__ __forceinline__ void route_row(const Rule& r, const T* row, unsigned 
   *expert = e;
   *gate = w * r.scale;
   __syncwarp();  // the next row's list
+}
+
+
+// ---------------------------------------------------------------- four rows to a warp
+
+// The same for four consecutive rows at a time, for top_k and groups up to
+// eight and up to eight values a lane: what a single row leaves most lanes idle
+// for (the groups' order, the list's ranks, the gates) is done by eight lanes a
+// row for all four, and the rest has four rows' instructions to interleave.  A
+// row with anything out of the ordinary (a comparison that fp32 does not
+// decide, a list that is too long) goes through route_row afterwards.
+constexpr int kFew = 8;
+constexpr int kListRoom = 64;
+struct FourLists {
+  float values[4][kListRoom + 4];
+  int experts[4][kListRoom];
+  int picks[4][kFew];
+};
+__host__ __device__ __forceinline__ int four_bytes(int E, bool scored) {
+  const int one = warp_bytes(E, scored), four = (int)sizeof(FourLists);
+  return one > four ? one : four;
+}
+template <int PL, typename T>
+__device__ __noinline__ void route_again(const Rule r, const T* row, unsigned char* shared, int32_t* idx, float* w) {
+  int e;
+  float g;
+  route_row<PL>(r, Lane<PL>(r), row, shared, &e, &g);
+  if ((threadIdx.x & 31) < r.k) {
+    idx[threadIdx.x & 31] = e;
+    w[threadIdx.x & 31] = g;
+  }
+}
+template <typename X>
+__device__ __forceinline__ X pick4(const X (&x)[4], int j) {
+  return j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3];
+}
+
+// Rows t0 .. t0 + 3 of T, to idx and w.
+template <int PL, typename T>
+__device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, const T* logits, int64_t stride, int t0, int rows,
+                                           unsigned char* shared, int32_t* idx, float* w) {
+  constexpr int V = Lane<PL>::V;
+  const int lane = threadIdx.x & 31, mine_of = lane >> 3, at8 = lane & 7;  // the row and place of the lane where eight lanes have a row
+  const unsigned below = (1u << lane) - 1u;
+  const bool scored = r.bias != nullptr;
+  FourLists& list = *reinterpret_cast<FourLists*>(shared);
+  unsigned again = 0;  // rows to do over
+
+  float v[4][PL];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const T* row = logits + (int64_t)min(t0 + j, rows - 1) * stride;
+#pragma unroll
+    for (int q = 0; q < PL; ++q) v[j][q] = NAN;
+    if (V == 4 && r.vectors) {
+#pragma unroll
+      for (int q = 0; q < PL; q += 4)
+        if (own.has(q)) logits4(row, own.expert + own.step(r, q), &v[j][q]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < PL; ++q)
+        if (own.has(q)) v[j][q] = logit(row, own.expert + own.step(r, q));
+    }
+  }
+  float top[4], inv_z[4], err_score[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+#pragma unroll
+    for (int q = 0; q < PL; ++q) v[j][q] = clean(v[j][q]);
+    top[j] = 0.0f;
+    inv_z[j] = 1.0f;
+    err_score[j] = 0x1p-21f;
+    if (r.softmax) {
+      float m = v[j][0];
+#pragma unroll
+      for (int q = 1; q < PL; ++q) m = fmaxf(m, v[j][q]);
+      top[j] = fmaxf(value(__reduce_max_sync(0xffffffffu, order(m))), -FLT_MAX);
+      if (scored || !r.renormalise) {
+        float z = 0.0f;
+#pragma unroll
+        for (int q = 0; q < PL; ++q) z += expf(v[j][q] - top[j]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        inv_z[j] = z > 0.0f ? 1.0f / z : 0.0f;
+      }
+      err_score[j] = inv_z[j] * 0x1p-18f;
+    }
+  }
+  auto score = [&](float l, float t, float z) {
+    return r.softmax ? exp2_approx((l - t) * kLog2e) * z : rcp_approx(1.0f + exp2_approx(-l * kLog2e));
+  };
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (scored) {
+      if (r.softmax) {
+#pragma unroll
+        for (int q = 0; q < PL; ++q) v[j][q] = exp2_approx((v[j][q] - top[j]) * kLog2e) * inv_z[j];
+      } else {
+#pragma unroll
+        for (int q = 0; q < PL; ++q) v[j][q] = rcp_approx(1.0f + exp2_approx(-v[j][q] * kLog2e));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < PL; ++q) v[j][q] += own.add[q];
+  }
+
+  unsigned parts = 0xffffffffu;  // bit 8 j + g: group g of row j takes part
+  if (r.top_groups < r.groups) {
+    float of[4], err[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a = -INFINITY, b = -INFINITY;
+      if (r.group_top == 1) {
+#pragma unroll
+        for (int q = 0; q < PL; ++q) a = fmaxf(a, v[j][q]);
+        for (int o = r.lanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        of[j] = a;
+        err[j] = scored ? err_score[j] + 0x1p-23f * fabsf(a) : 0.0f;
+      } else {
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+          const float c = fmaxf(v[j][q], -INFINITY);
+          b = fmaxf(b, fminf(a, c));
+          a = fmaxf(a, c);
+        }
+        for (int o = r.lanes / 2; o > 0; o >>= 1) {
+          const float oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
+          b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+          a = fmaxf(a, oa);
+        }
+        of[j] = scored ? a + b : score(a, top[j], inv_z[j]) + score(b, top[j], inv_z[j]);
+        err[j] = 2.0f * err_score[j] + 0x1p-22f * (scored ? fabsf(a) + fabsf(b) : 2.0f);
+      }
+    }
+    // lane 8 j + g: group g of row j
+    float x = NAN, e = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float xj = __shfl_sync(0xffffffffu, of[j], (at8 * r.lanes) & 31), ej = __shfl_sync(0xffffffffu, err[j], (at8 * r.lanes) & 31);
+      if (mine_of == j && at8 < r.groups) {
+        x = xj;
+        e = ej;
+      }
+    }
+    int above = 0;
+#pragma unroll
+    for (int d = 1; d < 8; ++d) {
+      const float y = __shfl_xor_sync(0xffffffffu, x, d);
+      above += y > x || (y == x && (at8 ^ d) < at8);
+    }
+    const bool in = at8 < r.groups && above < r.top_groups;
+    parts = __ballot_sync(0xffffffffu, in);
+    if (scored || r.group_top == 2) {  // the border: a sum that may not be told from another's
+      float worst = in ? x - e : INFINITY, best = !in && x > -INFINITY ? x + e : -INFINITY;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        worst = fminf(worst, __shfl_xor_sync(0xffffffffu, worst, o));
+        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+      }
+      again |= __ballot_sync(0xffffffffu, !(worst > best));  // (eight lanes alike)
+    }
+  }
+
+  // the bound, and the list of what is above it
+  float cut[4], near[4];
+  uint32_t most[4], first[4], last[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float m = v[j][0];
+#pragma unroll
+    for (int q = 1; q < PL; ++q) m = fmaxf(m, v[j][q]);
+    const bool part = own.group < r.groups && (parts >> (8 * j + (own.group & 7)) & 1u);
+    most[j] = part && m == m ? order(m) : 0u;
+    first[j] = last[j] = __reduce_max_sync(0xffffffffu, most[j]);
+    cut[j] = part ? 0.0f : NAN;
+  }
+#pragma unroll 1
+  for (int i = 1; i < r.k; ++i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (most[j] == last[j]) most[j] = 0u;
+      last[j] = __reduce_max_sync(0xffffffffu, most[j]);
+    }
+  }
+  int n[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float least = -INFINITY;
+    near[j] = 0.0f;
+    if (last[j] != 0u) {
+      least = value(last[j]);
+      if (scored) {
+        near[j] = 2.0f * err_score[j] + 0x1p-22f * fmaxf(fabsf(value(first[j])), fabsf(least));
+        least -= near[j];
+      }
+    } else if (scored) {
+      float size = 0.0f;
+#pragma unroll
+      for (int q = 0; q < PL; ++q) size = fmaxf(size, fabsf(v[j][q]));
+      near[j] = 2.0f * err_score[j] + 0x1p-22f * value(__reduce_max_sync(0xffffffffu, order(size)));
+    }
+    cut[j] += least;  // NaN in groups that take no part
+    unsigned mine = 0;
+#pragma unroll
+    for (int q = 0; q < PL; ++q)
+      if (v[j][q] >= cut[j]) mine |= 1u << q;
+    n[j] = 0;
+    for (;;) {  // a value of each lane that has one left
+      const unsigned who = __ballot_sync(0xffffffffu, mine != 0u);
+      if (!who) break;
+      if (mine) {
+        const int q = __ffs(mine) - 1, at = n[j] + __popc(who & below);
+        mine &= mine - 1;
+        if (at < kListRoom) list.experts[j][at] = own.expert + own.step(r, q);
+      }
+      n[j] += __popc(who);
+    }
+    if (n[j] > kListRoom) again |= 0xffu << (8 * j);
+  }
+  __syncwarp();
+
+  // eight lanes a row from here
+  const int t = min(t0 + mine_of, rows - 1), count = min(pick4(n, mine_of), kListRoom);
+  const T* row = logits + (int64_t)t * stride;
+  const float row_top = pick4(top, mine_of), row_z = pick4(inv_z, mine_of), apart = pick4(near, mine_of);
+  float* values = list.values[mine_of];
+  int* experts = list.experts[mine_of];
+  int* picks = list.picks[mine_of];
+  picks[at8] = 0;
+  for (int i = at8; i < count; i += 8) {
+    const int e = experts[i];
+    const float l = logit(row, e);
+    values[i] = scored ? score(l, row_top, row_z) + clean(__ldg(&r.bias[e])) : l;
+  }
+  if (at8 < 4) values[count + at8] = NAN;
+  __syncwarp();
+  bool unsure = false;
+  for (int i = at8; i < count; i += 8) {
+    const float x = values[i], lo = x - apart, hi = x + apart;
+    int above = 0, not_below = 0;
+#pragma unroll 1
+    for (int c = 0; c < count; c += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(values + c);
+      above += (y.x > hi) + (y.y > hi) + (y.z > hi) + (y.w > hi);
+      not_below += (y.x >= lo) + (y.y >= lo) + (y.z >= lo) + (y.w >= lo);
+    }
+    if (above < r.k && not_below - above != 1) {
+      if (scored) unsure = true;
+      else above = rank_of(x, experts[i], values, experts, count);  // equal logits
+    }
+    if (above < r.k) picks[above] = experts[i];
+  }
+  again |= __ballot_sync(0xffffffffu, unsure);
+  __syncwarp();
+  const int e = at8 < r.k ? picks[at8] : 0;
+  const float l = at8 < r.k ? logit(row, e) : -INFINITY;
+  float g = 0.0f;
+  if (!r.renormalise) {
+    g = r.softmax ? expf(l - row_top) * row_z : __fdividef(1.0f, 1.0f + expf(-l));
+  } else {  // (as in route_row)
+    float m = l;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = fmaxf(m, -FLT_MAX);
+    if (r.softmax) g = expf(l - m);
+    else g = m < 0.0f ? __fdividef(expf(l - m), 1.0f + expf(l)) : __fdividef(1.0f, 1.0f + expf(-l));
+    float sum = g;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    g = sum > 0.0f ? g / sum : 0.0f;
+  }
+  if (at8 < r.k && t0 + mine_of < rows) {
+    idx[(int64_t)t * r.k + at8] = e;
+    w[(int64_t)t * r.k + at8] = g * r.scale;
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j)
+    if ((again >> (8 * j) & 0xffu) && t0 + j < rows)
+      route_again<PL>(r, logits + (int64_t)(t0 + j) * stride, shared, idx + (int64_t)(t0 + j) * r.k, w + (int64_t)(t0 + j) * r.k);
 }
 
 }  // namespace rule

@@ -68,7 +68,8 @@ def f32(x):
 
 SHAPES = [(1, 256, 8, 8, 4), (77, 256, 8, 8, 4), (5, 1, 1, 1, 1), (33, 16, 2, 1, 1), (9, 60, 4, 1, 1), (300, 72, 6, 1, 1),
           (40, 160, 6, 8, 3), (21, 60, 7, 4, 2), (13, 1024, 32, 1, 1), (12, 1024, 9, 16, 5), (17, 384, 8, 1, 1), (14, 96, 32, 32, 16),
-          (700, 64, 8, 2, 1), (25, 27, 6, 9, 2), (8, 37, 37 // 2, 1, 1), (6, 640, 3, 5, 1)]
+          (700, 64, 8, 2, 1), (2051, 256, 8, 8, 4), (2050, 72, 6, 1, 1), (3000, 64, 8, 2, 1), (2049, 160, 6, 8, 3), (2500, 16, 2, 1, 1),
+          (2048, 30, 1, 5, 1), (2053, 256, 8, 1, 1), (2500, 128, 16, 1, 1), (2500, 64, 5, 16, 3), (25, 27, 6, 9, 2), (8, 37, 37 // 2, 1, 1), (6, 640, 3, 5, 1)]
 
 
 @pytest.mark.parametrize("T,E,k,groups,top_groups", SHAPES)
@@ -107,15 +108,18 @@ def test_values_that_fp32_cannot_tell_apart(score, E, k, groups):
     rule = Rule(score, f32(0.75 - s[0]), groups, max(1, groups // 2), min(2, groups))
     x = torch.tensor(logits, dtype=torch.float32, device=DEV)
     check(rule, x, k, run(rule, x, k))
+    x = x.repeat(2050, 1)
+    check(rule, x, k, run(rule, x, k))
     # and where only some are: pairs of experts
     rule.bias = f32(np.where(np.arange(E) % 7 == 0, 0.75 - s[0], 0.0))
     check(rule, x, k, run(rule, x, k))
 
 
-def test_rows_with_close_values_among_many():
+@pytest.mark.parametrize("T", [400, 2502])
+def test_rows_with_close_values_among_many(T):
     """Rows of one call with and without such pairs, the pairs at every place of the choice."""
     rng = np.random.default_rng(8)
-    T, E, k = 400, 128, 8
+    E, k = 128, 8
     logits = f32(rng.standard_normal((T, E)))
     b = f32(rng.standard_normal(E) * 0.1)
     s = 1 / (1 + np.exp(-logits))
@@ -135,7 +139,8 @@ def test_rows_with_close_values_among_many():
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("groups,group_top", [(1, 1), (8, 1), (8, 2)])
-def test_equal_logits_and_values_that_are_not_finite(score, bias, groups, group_top):
+@pytest.mark.parametrize("copies", [1, 171])
+def test_equal_logits_and_values_that_are_not_finite(score, bias, groups, group_top, copies):
     E, k = 256, 8
     x = np.round(np.random.default_rng(5).standard_normal((12, E)) * 2) / 2
     x[1] = 0.0
@@ -157,17 +162,22 @@ def test_equal_logits_and_values_that_are_not_finite(score, bias, groups, group_
         b[[4, 90]], b[7], b[8] = np.nan, np.inf, -np.inf
     rule = Rule(score, b, groups, max(1, groups // 2), group_top)
     logits = torch.tensor(x, dtype=torch.float32, device=DEV)
-    check(rule, logits, k, run(rule, logits, k))
+    one = run(rule, logits, k)
+    check(rule, logits, k, one)
+    many = run(rule, logits.repeat(copies, 1), k)  # enough rows for several to a warp
+    assert all(np.array_equal(m, np.tile(o, (copies, 1))) for m, o in zip(many, one))
 
 
 def test_far_biases():
     """Biases of size 30 and of size 1e-6: the order is that of the exact sums."""
     rng = np.random.default_rng(9)
     logits = torch.tensor(rng.standard_normal((200, 256)), dtype=torch.float32, device=DEV)
-    for scale in (30.0, 1e-6, 1e30):
+    many = logits.repeat(11, 1)
+    for scale in (30.0, 1e-6, 1e30, 3e38):
         for groups in (1, 8):
-            rule = Rule("sigmoid", f32(rng.standard_normal(256) * scale), groups, max(1, groups // 2), 2 if groups > 1 else 1)
+            rule = Rule("sigmoid", f32(np.clip(rng.standard_normal(256), -1, 1) * scale), groups, max(1, groups // 2), 2 if groups > 1 else 1)
             check(rule, logits, 8, run(rule, logits, 8))
+            check(rule, many, 8, run(rule, many, 8))
     rule.bias = f32(rng.integers(-2, 3, 256) * 4.0)  # whole steps apart: groups whose best two cancel
     check(rule, logits, 8, run(rule, logits, 8))
 
