@@ -22,11 +22,11 @@ struct RouteBatch {
 };
 
 template <int PL, typename T, bool kFour>
-__global__ void __launch_bounds__(kWarps * 32, kFour ? 5 : PL <= 8 ? 8 : PL == 16 ? 5 : 3) route_kernel(const __grid_constant__ RouteBatch a) {
+__global__ void __launch_bounds__(kWarps * 32, kFour ? 4 : PL <= 8 ? 8 : PL == 16 ? 5 : 3) route_kernel(const __grid_constant__ RouteBatch a) {
   extern __shared__ __align__(16) unsigned char shared[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool scored = a.r.bias != nullptr;
-  unsigned char* list = shared + warp * (kFour ? rule::four_bytes(a.r.E, scored) : rule::warp_bytes(a.r.E, scored));
+  unsigned char* list = shared + warp * (kFour ? (int)sizeof(rule::FourLists<PL>) : rule::warp_bytes(a.r.E, scored));
   dec::pdl_wait_primary();
   const rule::Lane<PL> own(a.r);
   const T* logits = static_cast<const T*>(a.logits);
@@ -50,12 +50,12 @@ __global__ void __launch_bounds__(kWarps * 32, kFour ? 5 : PL <= 8 ? 8 : PL == 1
 template <int PL, typename T, bool kFour>
 cudaError_t launch(const RouteBatch& a, cudaStream_t s) {
   const bool scored = a.r.bias != nullptr;
-  const int bytes = kWarps * (kFour ? rule::four_bytes(a.r.E, scored) : rule::warp_bytes(a.r.E, scored));
+  const int bytes = kWarps * (kFour ? (int)sizeof(rule::FourLists<PL>) : rule::warp_bytes(a.r.E, scored));
   const cudaError_t e = kv::allow_smem<4 * PL + 2 * kFour + (sizeof(T) == 2)>(route_kernel<PL, T, kFour>,
                                                                               kWarps * rule::warp_bytes(kMaxExperts, true));
   if (e != cudaSuccess) return e;
   const int rows = kWarps * (kFour ? 4 : 1);
-  const int blocks = std::min((a.T + rows - 1) / rows, (kFour ? 5 : 8) * kv::sm_count());  // one wave
+  const int blocks = (a.T + rows - 1) / rows;
   return kv::launch_dependent(route_kernel<PL, T, kFour>, dim3(blocks), kWarps * 32, bytes, s, a);
 }
 template <int PL, typename T>

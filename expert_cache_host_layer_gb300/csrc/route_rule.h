@@ -63,6 +63,10 @@ __device__ __forceinline__ uint32_t order(float x) {
 __device__ __forceinline__ float value(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
+__device__ __forceinline__ long long order(double x) {  // (signed: fp64 comparisons are slow here)
+  const long long u = __double_as_longlong(x + 0.0);
+  return u ^ (u >> 63 & 0x7fffffffffffffffll);
+}
 // A number as it counts: NaN as -inf (fmaxf gives the other operand), +inf as the largest number.
 __device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -139,31 +143,33 @@ __device__ __noinline__ bool exact_groups(const Rule r, const T* row, float top,
     b = fmax(fmin(a, oa), fmax(b, ob));
     a = fmax(a, oa);
   }
-  const double mine = r.group_top == 2 ? a + b : a;
+  const long long mine = order(r.group_top == 2 ? a + b : a);
   int above = 0;
   for (int g = 0; g < r.groups; ++g) {
-    const double of = __shfl_sync(0xffffffffu, mine, g * r.lanes);
+    const long long of = __shfl_sync(0xffffffffu, mine, g * r.lanes);
     above += of > mine || (of == mine && g < group);
   }
   return group < r.groups && above < r.top_groups;
 }
-// The list's ranks in fp64.
-template <typename T>
-__device__ __noinline__ void exact_ranks(const Rule r, const T* row, float top, const int* experts, double* keys, int n, int* picks) {
+// The list's ranks in fp64; keys: room for n of them.
+template <typename T, typename I>
+__device__ __noinline__ void exact_ranks(const Rule r, const T* row, float top, const I* experts, long long* keys, int n, int* picks) {
   const int lane = threadIdx.x & 31;
   const Exact x = make_exact(r, row, top);
-  for (int i = lane; i < n; i += 32) keys[i] = x.value(logit(row, experts[i]), experts[i]);
+  for (int i = lane; i < n; i += 32) keys[i] = order(x.value(logit(row, experts[i]), experts[i]));
   __syncwarp();
   for (int i = lane; i < n; i += 32) {
-    const double v = keys[i];
+    const long long v = keys[i];
     const int e = experts[i];
     int rank = 0;
     for (int j = 0; j < n; ++j) rank += keys[j] > v || (keys[j] == v && experts[j] < e);
     if (rank < r.k) picks[rank] = e;
   }
+  __syncwarp();
 }
 // The rank of (x, e) among a list's values, equal ones by expert.
-__device__ __forceinline__ int rank_of(float x, int e, const float* values, const int* experts, int n) {
+template <typename I>
+__device__ __forceinline__ int rank_of(float x, int e, const float* values, const I* experts, int n) {
   int rank = 0;
 #pragma unroll 1
   for (int j = 0; j < n; ++j) rank += values[j] > x || (values[j] == x && experts[j] < e);
@@ -201,7 +207,7 @@ __device__ __forceinline__ void route_row(const Rule& r, const Lane<PL>& own, co
   const bool scored = r.bias != nullptr;
   float* values = reinterpret_cast<float*>(shared);
   int* experts = reinterpret_cast<int*>(values + room);
-  double* keys = reinterpret_cast<double*>(experts + room);
+  long long* keys = reinterpret_cast<long long*>(experts + room);
   int* picks = scored ? reinterpret_cast<int*>(keys + room) : experts + room;
 
   float v[PL];
@@ -273,7 +279,11 @@ __device__ __forceinline__ void route_row(const Rule& r, const Lane<PL>& own, co
         a = fmaxf(a, oa);
       }
     }
-    const float mine = r.group_top == 1 ? a : scored ? a + b : score(a) + score(b);
+    if (r.group_top == 2 && !scored) {
+      a = score(a);
+      b = score(b);
+    }
+    const float mine = r.group_top == 1 ? a : a + b;
     // the top_groups largest (fewer rounds than groups; more groups than that if some are equal)
     uint32_t left = part ? order(mine) : 0u;
     bool in = false;
@@ -287,15 +297,15 @@ __device__ __forceinline__ void route_row(const Rule& r, const Lane<PL>& own, co
     }
     bool sure = __popc(__ballot_sync(0xffffffffu, in && own.sub == 0)) == r.top_groups;
     if (scored || r.group_top == 2) {
-      const float err = 2.0f * err_score + 0x1p-22f * (scored ? fabsf(a) + (r.group_top == 2 ? fabsf(b) : 0.0f) : 2.0f);
+      const float err = r.group_top == 1 ? err_score + 0x1p-23f * fabsf(a) : 2.0f * err_score + 0x1p-22f * (fabsf(a) + fabsf(b));
       const uint32_t worst = __reduce_min_sync(0xffffffffu, in ? order(mine - err) : 0xffffffffu);
       const uint32_t best = __reduce_max_sync(0xffffffffu, part && !in ? order(mine == -INFINITY ? mine : mine + err) : 0u);
       sure = sure && worst > best;
     }
-    part = sure ? in : false;
-    if (!sure) {
-      const float by = 2.0f * err_score + 0x1p-21f * fmaxf(fabsf(a), fabsf(b == -INFINITY ? a : b));
-      part = exact_groups(r, row, top, inv_z, own.group, own.sub, scored || r.group_top == 2 ? (r.group_top == 1 ? a : scored ? b : score(b)) - by : a);
+    part = in;
+    if (!sure) {  // (for logits the bound is their own value)
+      const float off = scored || r.group_top == 2 ? 4.0f * err_score + 0x1p-21f * (fabsf(a) + (r.group_top == 2 ? fabsf(b) : 0.0f)) : 0.0f;
+      part = exact_groups(r, row, top, inv_z, own.group, own.sub, (r.group_top == 1 ? a : b) - off);
     }
   }
 
@@ -395,30 +405,15 @@ __device__ __forceinline__ void route_row(const Rule& r, const Lane<PL>& own, co
 // The same for four consecutive rows at a time, for top_k and groups up to
 // eight and up to eight values a lane: what a single row leaves most lanes idle
 // for (the groups' order, the list's ranks, the gates) is done by eight lanes a
-// row for all four, and the rest has four rows' instructions to interleave.  A
-// row with anything out of the ordinary (a comparison that fp32 does not
-// decide, a list that is too long) goes through route_row afterwards.
+// row for all four, and the rest has four rows' instructions to interleave.
 constexpr int kFew = 8;
-constexpr int kListRoom = 64;
-struct FourLists {
-  float values[4][kListRoom + 4];
-  int experts[4][kListRoom];
+template <int PL>
+struct FourLists {  // room for every value: many may be equal
+  float values[4][32 * PL + 4];
+  long long keys[32 * PL];
   int picks[4][kFew];
+  uint16_t experts[4][32 * PL];
 };
-__host__ __device__ __forceinline__ int four_bytes(int E, bool scored) {
-  const int one = warp_bytes(E, scored), four = (int)sizeof(FourLists);
-  return one > four ? one : four;
-}
-template <int PL, typename T>
-__device__ __noinline__ void route_again(const Rule r, const T* row, unsigned char* shared, int32_t* idx, float* w) {
-  int e;
-  float g;
-  route_row<PL>(r, Lane<PL>(r), row, shared, &e, &g);
-  if ((threadIdx.x & 31) < r.k) {
-    idx[threadIdx.x & 31] = e;
-    w[threadIdx.x & 31] = g;
-  }
-}
 template <typename X>
 __device__ __forceinline__ X pick4(const X (&x)[4], int j) {
   return j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3];
@@ -432,8 +427,7 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
   const int lane = threadIdx.x & 31, mine_of = lane >> 3, at8 = lane & 7;  // the row and place of the lane where eight lanes have a row
   const unsigned below = (1u << lane) - 1u;
   const bool scored = r.bias != nullptr;
-  FourLists& list = *reinterpret_cast<FourLists*>(shared);
-  unsigned again = 0;  // rows to do over
+  FourLists<PL>& list = *reinterpret_cast<FourLists<PL>*>(shared);
 
   float v[4][PL];
 #pragma unroll
@@ -495,7 +489,7 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
 
   unsigned parts = 0xffffffffu;  // bit 8 j + g: group g of row j takes part
   if (r.top_groups < r.groups) {
-    float of[4], err[4];
+    float of[4], err[4], least[4];  // a group's score, its bound, and the least of its values in it
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float a = -INFINITY, b = -INFINITY;
@@ -503,7 +497,7 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
 #pragma unroll
         for (int q = 0; q < PL; ++q) a = fmaxf(a, v[j][q]);
         for (int o = r.lanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        of[j] = a;
+        of[j] = least[j] = a;
         err[j] = scored ? err_score[j] + 0x1p-23f * fabsf(a) : 0.0f;
       } else {
 #pragma unroll
@@ -517,8 +511,13 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
           b = fmaxf(fminf(a, oa), fmaxf(b, ob));
           a = fmaxf(a, oa);
         }
-        of[j] = scored ? a + b : score(a, top[j], inv_z[j]) + score(b, top[j], inv_z[j]);
-        err[j] = 2.0f * err_score[j] + 0x1p-22f * (scored ? fabsf(a) + fabsf(b) : 2.0f);
+        if (!scored) {
+          a = score(a, top[j], inv_z[j]);
+          b = score(b, top[j], inv_z[j]);
+        }
+        of[j] = a + b;
+        least[j] = b;
+        err[j] = 2.0f * err_score[j] + 0x1p-22f * (fabsf(a) + fabsf(b));
       }
     }
     // lane 8 j + g: group g of row j
@@ -546,7 +545,19 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
         worst = fminf(worst, __shfl_xor_sync(0xffffffffu, worst, o));
         best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
       }
-      again |= __ballot_sync(0xffffffffu, !(worst > best));  // (eight lanes alike)
+      const unsigned unsure = __ballot_sync(0xffffffffu, !(worst > best));  // (eight lanes alike)
+      if (unsure) {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          if (!(unsure >> (8 * j) & 1u)) continue;
+          const T* row = logits + (int64_t)min(t0 + j, rows - 1) * stride;
+          const float t = pick4(top, j), z = pick4(inv_z, j), off = 2.0f * pick4(err, j);
+          const bool mine = exact_groups(r, row, t, z, own.group, own.sub, pick4(least, j) - off);
+          unsigned bits = 0;
+          for (int g = 0; g < r.groups; ++g) bits |= (__ballot_sync(0xffffffffu, mine && own.group == g) != 0u) << g;
+          parts = (parts & ~(0xffu << (8 * j))) | bits << (8 * j);
+        }
+      }
     }
   }
 
@@ -600,22 +611,20 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
       if (mine) {
         const int q = __ffs(mine) - 1, at = n[j] + __popc(who & below);
         mine &= mine - 1;
-        if (at < kListRoom) list.experts[j][at] = own.expert + own.step(r, q);
+        list.experts[j][at] = (uint16_t)(own.expert + own.step(r, q));
       }
       n[j] += __popc(who);
     }
-    if (n[j] > kListRoom) again |= 0xffu << (8 * j);
   }
   __syncwarp();
 
   // eight lanes a row from here
-  const int t = min(t0 + mine_of, rows - 1), count = min(pick4(n, mine_of), kListRoom);
+  const int t = min(t0 + mine_of, rows - 1), count = pick4(n, mine_of);
   const T* row = logits + (int64_t)t * stride;
   const float row_top = pick4(top, mine_of), row_z = pick4(inv_z, mine_of), apart = pick4(near, mine_of);
   float* values = list.values[mine_of];
-  int* experts = list.experts[mine_of];
+  const uint16_t* experts = list.experts[mine_of];
   int* picks = list.picks[mine_of];
-  picks[at8] = 0;
   for (int i = at8; i < count; i += 8) {
     const int e = experts[i];
     const float l = logit(row, e);
@@ -639,7 +648,14 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
     }
     if (above < r.k) picks[above] = experts[i];
   }
-  again |= __ballot_sync(0xffffffffu, unsure);
+  const unsigned undecided = __ballot_sync(0xffffffffu, unsure);
+  if (undecided) {
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j)
+      if (undecided >> (8 * j) & 0xffu)
+        exact_ranks(r, logits + (int64_t)min(t0 + j, rows - 1) * stride, pick4(top, j), list.experts[j], list.keys,
+                    pick4(n, j), list.picks[j]);
+  }
   __syncwarp();
   const int e = at8 < r.k ? picks[at8] : 0;
   const float l = at8 < r.k ? logit(row, e) : -INFINITY;
@@ -662,11 +678,7 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
     idx[(int64_t)t * r.k + at8] = e;
     w[(int64_t)t * r.k + at8] = g * r.scale;
   }
-  __syncwarp();
-#pragma unroll 1
-  for (int j = 0; j < 4; ++j)
-    if ((again >> (8 * j) & 0xffu) && t0 + j < rows)
-      route_again<PL>(r, logits + (int64_t)(t0 + j) * stride, shared, idx + (int64_t)(t0 + j) * r.k, w + (int64_t)(t0 + j) * r.k);
+  __syncwarp();  // the next rows' lists
 }
 
 }  // namespace rule
