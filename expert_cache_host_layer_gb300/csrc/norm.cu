@@ -63,14 +63,28 @@ __device__ __forceinline__ void put_bf16(void* base, int64_t at, const float* v)
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at) =
       make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }  // NaN above infinity
+// max(a, |b|), NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
+  return m;
+}
+// 448 / m for m in [2^-100, 2^128), rounded but for an ulp at times: a quotient and its remainder, 2^-16 aside from both
+// so that the reciprocal is a normal number.  (An IEEE division here costs as much as the rest of a group's work.)
+__device__ __forceinline__ float over(float m) {
+  const float d = m * 0x1p-16f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  const float q = 448.0f * 0x1p-16f * r;
+  return fmaf(fmaf(-d, q, 448.0f * 0x1p-16f), r, q);
+}
 
 // A row to a group of `per_row` threads (a power of two, 32 or more), thread t
 // of which holds vectors t, t + per_row, .. of eight values, kVecs of them.
 template <int X, int D, int kVecs>  // types of x and delta (-1: none)
 __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constant__ NormArgs a, int per_row) {
   __shared__ float s_sum[kMostThreads / 32];
-  __shared__ uint32_t s_top[kMostThreads / 32];
+  __shared__ float s_top[kMostThreads / 32];
   const int t = threadIdx.x & (per_row - 1), in_block = threadIdx.x / per_row;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / per_row) + in_block;
   const bool by_row = a.out_dtype == FT_FP8E4M3 && a.group == 0;
@@ -88,17 +102,23 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
     fetch<X>(x[j], a.x, row * a.xs + i);
     if (D >= 0) fetch<D < 0 ? FT_BF16 : D>(d[j], a.delta, row * a.ds + i);
   }
+  const bool w32 = a.w_dtype == FT_F32;
+  if (a.w && w32) {
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    const int i = (j * per_row + t) * 8;
-    if (!ok[j] || !a.w) continue;
-    const uint4* p = static_cast<const uint4*>(a.w) + (a.w_dtype == FT_F32 ? i / 4 : i / 8);
-    w[j].v[0] = __ldg(p);
-    if (a.w_dtype == FT_F32) w[j].v[1] = __ldg(p + 1);
+    for (int j = 0; j < kVecs; ++j) {
+      const uint4* p = static_cast<const uint4*>(a.w) + (j * per_row + t) * 2;
+      if (ok[j]) {
+        w[j].v[0] = __ldg(p);
+        w[j].v[1] = __ldg(p + 1);
+      }
+    }
+  } else if (a.w) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+      if (ok[j]) w[j].v[0] = __ldg(static_cast<const uint4*>(a.w) + j * per_row + t);
   }
   float r[kVecs][8];
-  float sum = 0.0f;
-  uint32_t top = 0;
+  float sum = 0.0f, top = 0.0f;  // top: largest |r w| of a row
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
 #pragma unroll
@@ -118,19 +138,35 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = fmaf(r[j][e], r[j][e], sum);
-    if (a.w) {
+  }
+  if (a.w && w32) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      if (!ok[j]) continue;
       float m[8];
-      if (a.w_dtype == FT_F32) values<FT_F32>(w[j], m);
-      else dec::decode_chunk<FT_W_BF16>(w[j].v[0], m);
+      values<FT_F32>(w[j], m);
 #pragma unroll
       for (int e = 0; e < 8; ++e) r[j][e] *= m[e];
     }
-    if (by_row)
+  } else if (a.w) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, abs_bits(r[j][e]));
+    for (int j = 0; j < kVecs; ++j) {
+      if (!ok[j]) continue;
+      float m[8];
+      dec::decode_chunk<FT_W_BF16>(w[j].v[0], m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[j][e] *= m[e];
+    }
+  }
+  auto warp_top = [](float m) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))); };  // (NaN above infinity)
+  if (by_row) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max_abs(top, r[j][e]);
+    top = warp_top(top);
   }
   sum = dec::warp_sum(sum);
-  if (by_row) top = __reduce_max_sync(0xffffffffu, top);
   if (per_row > 32) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = per_row >> 5, first = in_block * warps;
     if (lane == 0) {
@@ -139,7 +175,7 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
     }
     __syncthreads();
     sum = dec::warp_sum(lane < warps ? s_sum[first + lane] : 0.0f);
-    if (by_row) top = __reduce_max_sync(0xffffffffu, lane < warps ? s_top[first + lane] : 0u);
+    if (by_row) top = warp_top(lane < warps ? s_top[first + lane] : 0.0f);
   }
   const float norm = __frsqrt_rn(sum / (float)a.hidden + a.eps);
   if (a.out_dtype != FT_FP8E4M3) {
@@ -153,25 +189,28 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
       else put_bf16(a.out, at, r[j]);
     }
   } else {
+    const int log_group = __ffs(a.group) - 1;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       const int i = (j * per_row + t) * 8;
       if (!by_row) {  // a group is 4, 8 or 16 lanes; lanes past the row hold zeros
-        top = 0;
+        top = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, abs_bits(r[j][e]));
-        for (int o = a.group / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int e = 0; e < 8; ++e) top = max_abs(top, r[j][e]);
+        for (int o = a.group / 16; o > 0; o >>= 1) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
       if (!ok[j]) continue;
-      const float most = top > 0x7f800000u ? __uint_as_float(top) : fmaxf(__uint_as_float(top), kLeast);
-      const float inv = 448.0f / most;
+      const float most = top == top ? fmaxf(top, kLeast) : top, inv = over(most);
 #pragma unroll
       for (int e = 0; e < 8; ++e) r[j][e] *= inv;
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * a.os + i) =
           make_uint2(kv::pack_e4m3(r[j][0], r[j][1]) | kv::pack_e4m3(r[j][2], r[j][3]) << 16,
                      kv::pack_e4m3(r[j][4], r[j][5]) | kv::pack_e4m3(r[j][6], r[j][7]) << 16);
-      if (by_row ? i == 0 : i % a.group == 0)
-        a.scales[row * a.groups + (by_row ? 0 : i / a.group)] = most * norm / 448.0f;
+      if (by_row) {
+        if (i == 0) a.scales[row] = most * norm * (1.0f / 448.0f);
+      } else if ((i & (a.group - 1)) == 0) {
+        a.scales[row * a.groups + (i >> log_group)] = most * norm * (1.0f / 448.0f);
+      }
     }
   }
   dec::pdl_launch_dependents();
@@ -179,11 +218,11 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
 
 template <int X, int D>
 cudaError_t launch(const NormArgs& a, cudaStream_t s) {
-  // Few rows: as many threads to a row as it has vectors, for the shortest chain.  Many: four vectors to a thread.
+  // Few rows: as many threads to a row as it has vectors, for the shortest chain.  Many: two vectors to a thread.
   const int vecs = a.hidden / 8;
   int per_row = 32;
   const bool many = a.rows >= 4 * kv::sm_count();
-  while (per_row < kMostThreads && per_row * (many ? 4 : 1) < vecs) per_row *= 2;
+  while (per_row < kMostThreads && per_row * (many ? 2 : 1) < vecs) per_row *= 2;
   const int each = (vecs + per_row - 1) / per_row;
   const int threads = per_row < 128 && a.rows > 1 ? 128 : per_row;
   const int64_t blocks = (a.rows + threads / per_row - 1) / (threads / per_row);
