@@ -12,11 +12,13 @@
 // Values are read and written once: HBM bounds a chunk, the chain of loads
 // (q_start -> kv_len -> page; position -> sine) a decode step.  A block takes
 // `per` consecutive tokens.  Its threads look the places up and form each
-// (token, pair)'s sine and cosine once, for all heads, in shared memory; then a
-// group of head_dim / 16 lanes takes a head of a token at a time.  A lane has 16
-// values of it: both halves of eight pairs (8c.. and rot_dim / 2 + 8c.. where
-// the halves lie apart, 16c.. where pairs are interleaved), so that a pair
-// never leaves its thread, whatever rot_dim is.
+// (token, pair)'s sine and cosine once, for all heads, in shared memory.  Then
+// head_dim / 16 lanes have a head each, of one of `step` tokens, and go through
+// the block's tokens: which head it is, whether it is turned and stored, and
+// where, is the same for all of them.  A lane has 16 values of a head: both
+// halves of eight pairs (8c.. and rot_dim / 2 + 8c.. where the halves lie apart,
+// 16c.. where pairs are interleaved), so that a pair never leaves its thread,
+// whatever rot_dim is.
 #include <algorithm>
 
 #include "decode_common.h"
@@ -26,10 +28,10 @@ namespace ft {
 namespace kv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMostThreads = 512;
+constexpr int kThreads = 256;      // of a block, if its heads leave a choice
 constexpr int kMostTokens = 32;    // of a block
 constexpr int kTrigFloats = 4096;  // of a block: tokens x rot_dim
-constexpr int kBatch = 2;          // heads a lane has in flight
 constexpr int kMostHeads = 8192;
 constexpr int kMostDim = 512;
 
@@ -44,11 +46,10 @@ struct RotArgs {
   int64_t ots, ohs;
   int rows, per;              // tokens in all, and of a block
   int Hq, heads, units;       // heads of q, of q, k and v, and lanes to a head
-  uint32_t by_heads;          // floor(2^32 / heads) + 1, 0 for one: v / heads = (v * by_heads) >> 32 for v * heads < 2^32
+  int pass, step;             // heads and tokens that a block's threads have at a time
   int32_t* status;
 };
 
-__device__ __forceinline__ void unpack8(uint4 r, float* v) { dec::decode_chunk<FT_W_BF16>(r, v); }
 __device__ __forceinline__ uint4 pack8(const float* v) {
   uint32_t w[4];
 #pragma unroll
@@ -71,72 +72,63 @@ __device__ __forceinline__ float2 turn(uint64_t fraction, float scale) {
   return make_float2(quarter == 1 || quarter == 2 ? -x : x, quarter & 2 ? -y : y);
 }
 
-template <bool kAppend, bool kFp8, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotArgs a) {
+constexpr int kNone = 0, kBf16 = 1, kFp8 = 2;  // the cache
+
+template <int kCache, bool kInterleaved>
+__global__ void __launch_bounds__(kMostThreads, 2) rotary_kernel(const __grid_constant__ RotArgs a) {
   __shared__ float4 s_trig[kTrigFloats / 4];  // [token][cos 0..3, cos 4..7, sin 0..3, sin 4..7 of a lane's pairs][lane]
   __shared__ int s_pos[kMostTokens], s_row[kMostTokens];
-  const int rot = a.r.rot_dim, half = rot / 2, lanes = rot / 16;  // lanes: of a head, those with pairs
-  const int t0 = blockIdx.x * a.per, tokens = min(a.per, a.rows - t0), jobs = tokens * a.heads;
-  const int groups = kThreads / a.units, group = threadIdx.x / a.units, c = threadIdx.x - group * a.units;
-  const bool active = group < groups;
-  const int Hk = kAppend ? a.p.num_kv_heads : 0;
-  uint4 x[kBatch][2];
-  int tok[kBatch], head[kBatch];  // head -1: none
-  // where a lane's two vectors lie in a head
-  auto place = [&](bool turned, int* e0, int* e1) {
-    const bool apart = !kInterleaved && turned;
-    *e0 = apart ? 8 * c : 16 * c;
-    *e1 = apart ? half + 8 * c : 16 * c + 8;
-  };
-  auto is_turned = [&](int h) { return c < lanes && (!kAppend || h < a.Hq + Hk); };
-  auto load = [&](int i, int v) {
-    head[i] = -1;
-    if (!active || v >= jobs) return;
-    const int t = a.by_heads ? (int)__umulhi((uint32_t)v, a.by_heads) : v, h = v - t * a.heads;
-    tok[i] = t;
-    head[i] = h;
-    const int which = !kAppend || h < a.Hq ? 0 : h < a.Hq + Hk ? 1 : 2;
-    const __nv_bfloat16* src = a.x[which] + (int64_t)(t0 + t) * a.ts[which] +
-                               (int64_t)(which == 0 ? h : which == 1 ? h - a.Hq : h - a.Hq - Hk) * a.hs[which];
-    int e0, e1;
-    place(is_turned(h), &e0, &e1);
-    x[i][0] = *reinterpret_cast<const uint4*>(src + e0);
-    x[i][1] = *reinterpret_cast<const uint4*>(src + e1);
-  };
+  const int half = a.r.rot_dim / 2, lanes = a.r.rot_dim / 16;  // lanes: of a head, those with pairs
+  const int t0 = blockIdx.x * a.per, tokens = min(a.per, a.rows - t0);
+  const int wide = a.pass * a.units, first = threadIdx.x / wide, in_pass = threadIdx.x - first * wide;
+  const int head = in_pass / a.units, c = in_pass - head * a.units;
+  const int Hk = kCache == kNone ? 0 : a.p.num_kv_heads;
   dec::pdl_wait_primary();
-#pragma unroll
-  for (int i = 0; i < kBatch; ++i) load(i, group + i * groups);
-  if (threadIdx.x < tokens) {
-    int pos, row = 0;
-    if (kAppend) row = new_place(a.p, a.b, t0 + threadIdx.x, a.status, &pos);
-    else pos = __ldg(&a.positions[t0 + threadIdx.x]);
-    s_pos[threadIdx.x] = pos;
-    s_row[threadIdx.x] = row;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
-    const int t = i / half, pair = i - t * half;
-    const float2 cs = turn((uint64_t)(int64_t)s_pos[t] * __ldg(&a.r.turns[pair]), a.r.scale);
-    float* to = reinterpret_cast<float*>(s_trig) + ((t * 4 + (pair >> 2 & 1)) * lanes + (pair >> 3)) * 4 + (pair & 3);
-    to[0] = cs.x;
-    to[8 * lanes] = cs.y;
-  }
-  __syncthreads();
-  for (int v0 = group; v0 - group < jobs; v0 += kBatch * groups) {  // the whole block together
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int t = tok[i], h = head[i];
-      float y[2][8];
-      bool turned = false;
-      if (h >= 0) {
-        turned = is_turned(h);
-        unpack8(x[i][0], y[0]);
-        unpack8(x[i][1], y[1]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[e / 8][e % 8] = 0.0f;
+
+  for (int h0 = 0; h0 < a.heads; h0 += a.pass) {  // (one time, but for more heads than a block has threads for)
+    const int h = h0 + head;
+    const bool mine = first < a.step && h < a.heads, query = kCache == kNone || h < a.Hq, key = !query && h < a.Hq + Hk;
+    const bool turned = c < lanes && (query || key);
+    const bool apart = !kInterleaved && turned;
+    const int e0 = apart ? 8 * c : 16 * c, to1 = apart ? half : 8;  // the lane's first vector, and from there to the second
+    const int of = query ? h : key ? h - a.Hq : h - a.Hq - Hk;
+    const int64_t ts = query ? a.ts[0] : key ? a.ts[1] : a.ts[2], hs = query ? a.hs[0] : key ? a.hs[1] : a.hs[2];
+    const __nv_bfloat16* src = (query ? a.x[0] : key ? a.x[1] : a.x[2]) + (t0 + first) * ts + of * hs + e0;
+    __nv_bfloat16* out = a.out + (int64_t)(t0 + first) * a.ots + of * a.ohs + e0;
+    const bool stores = kCache == kFp8 && __any_sync(0xffffffffu, mine && !query);  // of the warp's heads
+    uint4 next[2];
+    auto load = [&](int t) {
+      if (!mine || t >= tokens) return;
+      next[0] = *reinterpret_cast<const uint4*>(src);
+      next[1] = *reinterpret_cast<const uint4*>(src + to1);
+      src += a.step * ts;
+    };
+    load(first);
+    if (h0 == 0) {  // the tokens' places, and their pairs' sines and cosines
+      if (threadIdx.x < tokens) {
+        int pos, row = 0;
+        if (kCache == kNone) pos = __ldg(&a.positions[t0 + threadIdx.x]);
+        else row = new_place(a.p, a.b, t0 + threadIdx.x, a.status, &pos);
+        s_pos[threadIdx.x] = pos;
+        s_row[threadIdx.x] = row;
       }
-      if (turned) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
+        const int t = i / half, pair = i - t * half;
+        const float2 cs = turn((uint64_t)(int64_t)s_pos[t] * __ldg(&a.r.turns[pair]), a.r.scale);
+        float* to = reinterpret_cast<float*>(s_trig) + ((t * 4 + (pair >> 2 & 1)) * lanes + (pair >> 3)) * 4 + (pair & 3);
+        to[0] = cs.x;
+        to[8 * lanes] = cs.y;
+      }
+      __syncthreads();
+    }
+    for (int t = first; t - first < tokens; t += a.step, out += a.step * a.ots) {  // the whole block together
+      const bool live = mine && t < tokens;
+      float y[2][8];
+      dec::decode_chunk<FT_W_BF16>(next[0], y[0]);
+      dec::decode_chunk<FT_W_BF16>(next[1], y[1]);
+      load(t + a.step);
+      if (live && turned) {
         const float4* at = s_trig + t * 4 * lanes + c;
         float cs[8], sn[8];
         *reinterpret_cast<float4*>(cs) = at[0];
@@ -152,44 +144,33 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
           q = w;
         }
       }
-      int e0, e1;
-      place(turned, &e0, &e1);
-      const bool query = !kAppend || h < a.Hq;
-      float top = 0.0f;
       uint32_t bits = 0;
-      if (kAppend && kFp8) {  // largest magnitude of the head's vector (as bits: NaN above infinity), over its lanes
+      if (stores) {  // largest magnitude of the head's vector (as bits: NaN above infinity), over its lanes
 #pragma unroll
         for (int e = 0; e < 16; ++e) bits = max(bits, __float_as_uint(y[e / 8][e % 8]) & 0x7fffffffu);
         for (int o = a.units / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
-        top = __uint_as_float(bits);
       }
-      if (h >= 0) {
-        const int row = s_row[t];
-        if (query) {
-          if (row != kNobodys) {
-            __nv_bfloat16* dst = a.out + (int64_t)(t0 + t) * a.ots + (int64_t)h * a.ohs;
-            *reinterpret_cast<uint4*>(dst + e0) = pack8(y[0]);
-            *reinterpret_cast<uint4*>(dst + e1) = pack8(y[1]);
-          }
-        } else if (row >= 0) {
-          const bool key = h < a.Hq + Hk;
-          const int64_t at = row + (int64_t)(key ? h - a.Hq : h - a.Hq - Hk) * a.p.page_tokens;
-          void* pages = key ? a.p.k : a.p.v;
-          const int D = a.p.head_dim;
-          if (kFp8) {
-            const int k = scale_exp(top);
-            uint8_t* dst = static_cast<uint8_t*>(pages) + at * D;
-            *reinterpret_cast<uint2*>(dst + e0) = encode8(y[0], k);
-            *reinterpret_cast<uint2*>(dst + e1) = encode8(y[1], k);
-            if (c == 0) (key ? a.p.k_scale : a.p.v_scale)[at] = (uint8_t)scale_byte(k);
-          } else {
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(pages) + at * D;
-            *reinterpret_cast<uint4*>(dst + e0) = pack8(y[0]);
-            *reinterpret_cast<uint4*>(dst + e1) = pack8(y[1]);
-          }
+      if (!live) continue;
+      const int row = s_row[t];
+      if (query) {
+        if (row == kNobodys) continue;
+        *reinterpret_cast<uint4*>(out) = pack8(y[0]);
+        *reinterpret_cast<uint4*>(out + to1) = pack8(y[1]);
+      } else if (row >= 0) {
+        const int64_t at = (int64_t)(row + of * a.p.page_tokens);  // rows are below 2^31
+        void* pages = key ? a.p.k : a.p.v;
+        if (kCache == kFp8) {
+          const int k = scale_exp(__uint_as_float(bits));
+          uint8_t* dst = static_cast<uint8_t*>(pages) + at * a.p.head_dim + e0;
+          *reinterpret_cast<uint2*>(dst) = encode8(y[0], k);
+          *reinterpret_cast<uint2*>(dst + to1) = encode8(y[1], k);
+          if (c == 0) (key ? a.p.k_scale : a.p.v_scale)[at] = (uint8_t)scale_byte(k);
+        } else {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(pages) + at * a.p.head_dim + e0;
+          *reinterpret_cast<uint4*>(dst) = pack8(y[0]);
+          *reinterpret_cast<uint4*>(dst + to1) = pack8(y[1]);
         }
       }
-      load(i, v0 + (kBatch + i) * groups);
     }
   }
   dec::pdl_launch_dependents();
@@ -205,16 +186,23 @@ ft_status check_rotary(const ft_rotary* r, int head_dim) {
   return FT_OK;
 }
 
-template <bool kAppend>
-ft_status launch(RotArgs& a, const char* name, bool fp8, cudaStream_t s) {
-  // one wave of eight blocks an SM, while that leaves a block no more tokens than it has room for
-  const int blocks = 8 * sm_count(), most = std::min(kMostTokens, kTrigFloats / a.r.rot_dim);
-  a.per = std::min(most, (int)(((long long)a.rows + blocks - 1) / blocks));
-  a.by_heads = a.heads == 1 ? 0 : (uint32_t)((1ull << 32) / a.heads) + 1;
+ft_status launch(RotArgs& a, const char* name, int cache, cudaStream_t s) {
+  a.heads = a.Hq + (cache == kNone ? 0 : 2 * a.p.num_kv_heads);
+  a.pass = std::min(a.heads, kMostThreads / a.units);
+  const int wide = a.pass * a.units;  // threads of a token
+  const int most = std::min(kMostTokens, kTrigFloats / a.r.rot_dim);
+  a.step = std::min({std::max(1, kThreads / wide), a.rows, most});
+  const int threads = (wide * a.step + 31) / 32 * 32;
+  // one wave (64 registers a thread), while that leaves a block no more tokens than it has room for
+  const int wave = 1024 / threads * sm_count();
+  a.per = std::min(most, (int)(((long long)a.rows + wave - 1) / wave));
+  if (a.per > a.step) a.per = std::min(most, (a.per + a.step - 1) / a.step * a.step);
   const dim3 grid((unsigned)(((long long)a.rows + a.per - 1) / a.per));
-  auto* kernel = a.r.interleaved ? (fp8 ? rotary_kernel<kAppend, kAppend, true> : rotary_kernel<kAppend, false, true>)
-                                 : (fp8 ? rotary_kernel<kAppend, kAppend, false> : rotary_kernel<kAppend, false, false>);
-  const cudaError_t e = launch_dependent(kernel, grid, kThreads, 0, s, a);
+  const bool pairs = a.r.interleaved != 0;
+  auto* kernel = cache == kFp8 ? (pairs ? rotary_kernel<kFp8, true> : rotary_kernel<kFp8, false>)
+                 : cache == kBf16 ? (pairs ? rotary_kernel<kBf16, true> : rotary_kernel<kBf16, false>)
+                                  : (pairs ? rotary_kernel<kNone, true> : rotary_kernel<kNone, false>);
+  const cudaError_t e = launch_dependent(kernel, grid, threads, 0, s, a);
   if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(e));
   return FT_OK;
 }
@@ -247,8 +235,8 @@ extern "C" ft_status ft_rotate(const ft_rotary* rotary, int32_t num_tokens, cons
   a.r = *rotary; a.positions = positions;
   a.x[0] = static_cast<const __nv_bfloat16*>(x); a.ts[0] = x_token_stride; a.hs[0] = x_head_stride;
   a.out = static_cast<__nv_bfloat16*>(out); a.ots = out_token_stride; a.ohs = out_head_stride;
-  a.rows = num_tokens; a.Hq = a.heads = num_heads; a.units = head_dim / 16;
-  return launch<false>(a, "rotate", false, static_cast<cudaStream_t>(stream));
+  a.rows = num_tokens; a.Hq = num_heads; a.units = head_dim / 16;
+  return launch(a, "rotate", kNone, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_batch* batch, const ft_rotary* rotary,
@@ -281,7 +269,7 @@ extern "C" ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_b
   a.x[1] = static_cast<const __nv_bfloat16*>(k); a.ts[1] = k_token_stride; a.hs[1] = k_head_stride;
   a.x[2] = static_cast<const __nv_bfloat16*>(v); a.ts[2] = v_token_stride; a.hs[2] = v_head_stride;
   a.out = static_cast<__nv_bfloat16*>(q_out); a.ots = q_out_token_stride; a.ohs = q_out_head_stride;
-  a.rows = batch->num_tokens; a.Hq = num_q_heads; a.heads = num_q_heads + 2 * pages->num_kv_heads; a.units = D / 16;
+  a.rows = batch->num_tokens; a.Hq = num_q_heads; a.units = D / 16;
   if ((st = status_word(&a.status)) != FT_OK) return st;
-  return launch<true>(a, "append_rotary", pages->kv_dtype == FT_KV_FP8E4M3, static_cast<cudaStream_t>(stream));
+  return launch(a, "append_rotary", pages->kv_dtype == FT_KV_FP8E4M3 ? kFp8 : kBf16, static_cast<cudaStream_t>(stream));
 }
