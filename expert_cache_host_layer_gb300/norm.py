@@ -44,17 +44,15 @@ class RMSNorm:
     def apply(self, x: torch.Tensor, out: torch.Tensor, delta: torch.Tensor | None = None,
               total: torch.Tensor | None = None, scales: torch.Tensor | None = None,
               stream: torch.cuda.Stream | None = None):
-        index = x.get_device()
-        if index < 0 or (self.index is not None and index != self.index):
+        # (called several times a layer: each tensor's attributes are asked for once)
+        index, shape, xt, ot = x.get_device(), x.shape, _DTYPES.get(x.dtype), _OUT.get(out.dtype)
+        if index < 0 or (index != self.index and self.index is not None):
             raise ValueError("x is in the weight's GPU's memory")
-        shape = x.shape
-        xt, ot = _DTYPES.get(x.dtype), _OUT.get(out.dtype)
         if len(shape) != 2 or shape[1] != self.hidden or xt is None:
             raise ValueError(f"x is a bf16 or float32 [rows, {self.hidden}] tensor")
         if ot is None or out.shape != shape or out.get_device() != index:
             raise ValueError("out is a bf16, float32 or float8_e4m3fn tensor of x's shape and device")
-        xs, x1 = x.stride()
-        os, o1 = out.stride()
+        (xs, x1), (os, o1) = x.stride(), out.stride()
         ds = ts = dp = tp = sp = dt = 0
         d1 = t1 = 1
         if delta is not None:
@@ -70,13 +68,13 @@ class RMSNorm:
             tp, (ts, t1) = total.data_ptr(), total.stride()
         if (x1 != 1 or o1 != 1 or d1 != 1 or t1 != 1) and x.numel():
             raise ValueError("rows are contiguous")
-        if (scales is not None) != (ot == FT_FP8E4M3):
-            raise ValueError("scales go with a float8 out, and only with it")
-        if scales is not None:
-            if (scales.dtype != torch.float32 or scales.shape != (shape[0], self.num_scales) or
+        if ot == FT_FP8E4M3:
+            if (scales is None or scales.dtype != torch.float32 or scales.shape != (shape[0], self.num_scales) or
                     not scales.is_contiguous() or scales.get_device() != index):
-                raise ValueError("scales is a contiguous float32 [rows, num_scales] tensor of x's device")
+                raise ValueError("scales go with a float8 out; scales is a contiguous float32 [rows, num_scales] tensor of x's device")
             sp = scales.data_ptr()
+        elif scales is not None:
+            raise ValueError("scales go with a float8 out, and only with it")
         # (a Stream object of the current stream takes 2 us to make)
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
         args = (self.address, shape[0], x.data_ptr(), xs, xt, dp, ds, dt, tp, ts, out.data_ptr(), os, ot, sp, s)

@@ -39,6 +39,8 @@ from .rotary import Rotary
 _lib = library()
 _append, _attend, _read = _lib.ft_kv_append, _lib.ft_kv_attend, _lib.ft_kv_read
 _append_rotary = _lib.ft_kv_append_rotary
+_BF16 = torch.bfloat16
+_NO_QUERIES = (0, 0, 0, 0, 0, 0)
 _workspaces: dict = {}  # (device index, stream) -> uint8 tensor
 _outgrown: list = []    # the smaller ones before them: three of a stream at most (sizes go by head_dim and the kernels)
 _captured: dict = {}    # (device index, stream) -> (number, uint8 tensor) of the last capture that the stream was part of
@@ -120,14 +122,16 @@ class KVPages:
         """Store the batch's new keys and values, bf16 [num_tokens, kv_heads, head_dim] (strided views are fine).
         With ``rotary`` the keys are stored rotated to their positions, and the queries q, bf16 [num_tokens, q_heads,
         head_dim], rotated into q_out (which may be q)."""
-        rows = (*self._rows(batch, k, self.num_kv_heads, "k"), *self._rows(batch, v, self.num_kv_heads, "v"))
+        heads = self.num_kv_heads
+        rows = (*self._rows(batch, k, heads, "k"), *self._rows(batch, v, heads, "v"))
         if rotary is None:
-            _need(q is None and q_out is None, "q and q_out go with rotary")
+            if q is not None or q_out is not None:
+                raise ValueError("q and q_out go with rotary")
             self._call(_append, self.address, batch.address, *rows, self._stream(stream))
         else:
-            _need((q is None) == (q_out is None), "q goes with q_out")
-            _need(rotary.index == self.index, "the rotary and the cache are on one device")
-            heads, queries = 0, (0, 0, 0, 0, 0, 0)
+            if (q is None) != (q_out is None) or rotary.index != self.index:
+                raise ValueError("q goes with q_out, and the rotary is on the cache's device")
+            heads, queries = 0, _NO_QUERIES
             if q is not None:
                 heads = q.shape[1] if q.dim() == 3 else 0
                 queries = (*self._rows(batch, q, heads, "q"), *self._rows(batch, q_out, heads, "q_out"))
@@ -193,11 +197,12 @@ class KVPages:
     # ---- helpers -------------------------------------------------------------
     def _rows(self, batch, t, heads, name):
         """Address and strides of a [num_tokens, heads, head_dim] tensor."""
-        if (t.dtype != torch.bfloat16 or t.shape != (batch.num_tokens, heads, self.head_dim) or
+        if (t.dtype != _BF16 or t.shape != (batch.num_tokens, heads, self.head_dim) or
                 t.get_device() != self.index or batch.index != self.index):
             raise ValueError(f"{name} is a bf16 [num_tokens, heads, {self.head_dim}] tensor of the cache's device")
         s0, s1, s2 = t.stride()
-        _need(s2 == 1 or t.numel() == 0, "%s's rows are contiguous", name)
+        if s2 != 1 and t.numel():
+            raise ValueError(f"{name}'s rows are contiguous")
         return t.data_ptr(), s0, s1
 
     def _call(self, fn, *args):

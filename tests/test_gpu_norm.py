@@ -20,6 +20,7 @@ pytestmark = pytest.mark.gpu
 from oracle import norm as onorm  # noqa: E402
 
 if torch.cuda.is_available():
+    from expert_cache_host_layer_gb300 import FtError
     from expert_cache_host_layer_gb300.norm import RMSNorm
 
 DEV = "cuda:0"
@@ -218,3 +219,15 @@ def test_refusals():
             norm.apply(*args, **kw)
     for n in (0,):
         norm.apply(x[:n], out[:n], delta=delta[:n], total=x[:n])
+
+
+def test_rows_that_are_not_contiguous():
+    """Broadcast and strided columns, of every tensor."""
+    x, out = torch.zeros(4, 64, device=DEV), torch.zeros(4, 64, device=DEV)
+    norm = RMSNorm(64)
+    for bad in (torch.zeros(4, 1, device=DEV).expand(4, 64), torch.zeros(4, 128, device=DEV)[:, ::2], torch.zeros(64, 4, device=DEV).T):
+        for args, kw in (((bad, out), {}), ((x, bad), {}), ((x, out), dict(delta=bad)), ((x, out), dict(delta=x, total=bad))):
+            with pytest.raises(ValueError, match="contiguous"):
+                norm.apply(*args, **kw)
+    with pytest.raises(FtError, match="row stride"):
+        norm.apply(x, out, delta=torch.zeros(1, 64, device=DEV).expand(4, 64))  # a row for all: not taken
