@@ -2,15 +2,16 @@
 cache, and routed experts through the expert cache, layer after layer.
 
     python examples/decoder.py [--streams 4] [--prompt 300] [--steps 32] [--kv fp8|bf16]
+                               [--rotary half|interleaved|none] [--router softmax|sigmoid]
 
 Random weights (synthetic; no checkpoint): the point is the order of the calls.
 
-    layer:  n = norm(x);  q, k, v = n Wqkv            (library products)
-            pages.append(batch, k, v)                 store the new tokens
+    layer:  norm.apply(x, n, delta=y, total=x)        x += y of the layer before, n = the norm of the sum
+            q, k, v = n Wqkv                          (library products)
+            pages.append(batch, k, v, rotary, q, q)   rotate q and k to their positions, store k and v
             pages.attend(batch, q, a)                 attention over their sequences
-            x += a Wo;  n = norm(x)
-            cache.route_classify / fetch_misses / moe_forward   the experts
-            x += y
+            norm.apply(x, n, delta=a Wo, total=x)
+            cache.route_classify / fetch_misses / moe_forward   the experts, chosen by the cache's routing rule: y
 
 A step takes any mix of sequences: whole prompts or chunks of them beside
 sequences that are one token further.  A sequence that has to give up its pages
@@ -31,8 +32,11 @@ if __name__ == "__main__":
     sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from expert_cache_host_layer_gb300 import FT_KV_BF16, FT_KV_FP8E4M3, FT_W_BF16, ft_expert_bytes
+from expert_cache_host_layer_gb300.norm import RMSNorm
 from expert_cache_host_layer_gb300.paged_kv import KVBatch, KVPages
 from expert_cache_host_layer_gb300.pipeline import ExpertCache, pinned_bank
+from expert_cache_host_layer_gb300.rotary import Rotary
+from expert_cache_host_layer_gb300.router import Router
 
 
 @dataclasses.dataclass(frozen=True)
@@ -51,6 +55,8 @@ class Shape:
     slots: int = 64         # of the expert cache: half of the layers' experts
     kv_dtype: int = FT_KV_FP8E4M3
     window: int = 0
+    rotary: str = "none"    # or half, interleaved
+    router: str = "softmax"  # or sigmoid: with a bias for the choice, in the best two of four groups
 
 
 class Decoder:
@@ -76,6 +82,13 @@ class Decoder:
             w[b] = (torch.randn(w.shape[1], generator=gen) * sh.hidden ** -0.5).bfloat16()
         self.experts = ExpertCache(sh.layers, sh.experts, sh.top_k, sh.hidden, sh.inter, FT_W_BF16, sh.slots,
                                    sh.max_tokens, self.bank, device=device)
+        self.norms = [[RMSNorm(sh.hidden) for _ in range(2)] for _ in range(sh.layers)]  # (a model's have weights)
+        self.rotary = None if sh.rotary == "none" else Rotary(sh.head_dim, interleaved=sh.rotary == "interleaved",
+                                                              device=self.dev)
+        if sh.router == "sigmoid":
+            bias = (0.1 * torch.randn(sh.layers, sh.experts, generator=gen)).to(self.dev)
+            self.experts.set_router(Router(sh.experts, sh.top_k, score="sigmoid", bias=bias, groups=4, top_groups=2,
+                                           group_top=2, scale=2.5))
         self.free = list(range(sh.num_pages))
         self.length: dict = {}  # sequence -> tokens in the cache
         self.table: dict = {}   # sequence -> its pages
@@ -107,24 +120,38 @@ class Decoder:
         sh, T = self.sh, batch.num_tokens
         q_wide, k_wide = sh.q_heads * sh.head_dim, sh.kv_heads * sh.head_dim
         a = torch.empty((T, sh.q_heads, sh.head_dim), dtype=torch.bfloat16, device=self.dev)
-        y = torch.empty((T, sh.hidden), dtype=torch.float32, device=self.dev)
+        n, r = torch.empty_like(x), torch.empty_like(x)  # a norm, and the residual
+        y = None
         for l in range(sh.layers):
-            qkv = torch.nn.functional.rms_norm(x, (sh.hidden,)) @ self.wqkv[l]
-            q = qkv[:, :q_wide].view(T, sh.q_heads, sh.head_dim)  # (views: a model's rotation of q and k goes here)
+            before, after = self.norms[l]
+            if y is None:
+                before.apply(x, n)
+            else:
+                before.apply(x, n, delta=y, total=r)
+                x = r
+            qkv = n @ self.wqkv[l]
+            q = qkv[:, :q_wide].view(T, sh.q_heads, sh.head_dim)
             k = qkv[:, q_wide:q_wide + k_wide].view(T, sh.kv_heads, sh.head_dim)
             v = qkv[:, q_wide + k_wide:].view(T, sh.kv_heads, sh.head_dim)
-            self.pages[l].append(batch, k, v)
+            if record is not None:
+                record.append({"x": x.clone(), "n1": n.clone(), "q0": q.clone()})
+            if self.rotary is None:
+                self.pages[l].append(batch, k, v)
+            else:
+                self.pages[l].append(batch, k, v, rotary=self.rotary, q=q, q_out=q)
             self.pages[l].attend(batch, q, a, window=sh.window)
-            x = x + a.view(T, q_wide) @ self.wo[l]
-            n = torch.nn.functional.rms_norm(x, (sh.hidden,))
+            o = a.view(T, q_wide) @ self.wo[l]
+            after.apply(x, n, delta=o, total=r)
+            x = r
             logits = (n @ self.router[l]).float()
+            y = torch.empty((T, sh.hidden), dtype=torch.float32, device=self.dev)
             self.experts.route_classify(l, logits)
             self.experts.fetch_misses(l)
             self.experts.moe_forward(l, n, y)
             if record is not None:
-                record.append({"q": q, "k": k, "v": v, "attention": a.clone(), "n": n, "logits": logits, "y": y.clone()})
-            x = x + y.bfloat16()
-        return x
+                record[-1] |= {"q": q, "k": k, "v": v, "attention": a.clone(), "o": o, "x2": x.clone(), "n": n.clone(),
+                               "logits": logits, "y": y.clone()}
+        return x + y.bfloat16()
 
     # ---- a sequence leaves its pages and comes back -------------------------
     def park(self, s) -> list:
@@ -157,8 +184,10 @@ def main():
     ap.add_argument("--prompt", type=int, default=300, help="tokens of the longest prompt")
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--kv", choices=("fp8", "bf16"), default="fp8")
+    ap.add_argument("--rotary", choices=("half", "interleaved", "none"), default="half")
+    ap.add_argument("--router", choices=("softmax", "sigmoid"), default="softmax")
     a = ap.parse_args()
-    sh = Shape(kv_dtype=FT_KV_FP8E4M3 if a.kv == "fp8" else FT_KV_BF16)
+    sh = Shape(kv_dtype=FT_KV_FP8E4M3 if a.kv == "fp8" else FT_KV_BF16, rotary=a.rotary, router=a.router)
     d = Decoder(sh)
     gen = torch.Generator(device=d.dev).manual_seed(1)
 

@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kMostThreads, 2) rotary_kernel(const __grid_co
     const int e0 = apart ? 8 * c : 16 * c, to1 = apart ? half : 8;  // the lane's first vector, and from there to the second
     const int of = query ? h : key ? h - a.Hq : h - a.Hq - Hk;
     const int64_t ts = query ? a.ts[0] : key ? a.ts[1] : a.ts[2], hs = query ? a.hs[0] : key ? a.hs[1] : a.hs[2];
-    const __nv_bfloat16* src = (query ? a.x[0] : key ? a.x[1] : a.x[2]) + (t0 + first) * ts + of * hs + e0;
-    __nv_bfloat16* out = a.out + (int64_t)(t0 + first) * a.ots + of * a.ohs + e0;
+    const __nv_bfloat16* src = (query ? a.x[0] : key ? a.x[1] : a.x[2]) + ((int64_t)t0 + first) * ts + of * hs + e0;
+    __nv_bfloat16* out = a.out + ((int64_t)t0 + first) * a.ots + of * a.ohs + e0;
     const bool stores = kCache == kFp8 && __any_sync(0xffffffffu, mine && !query);  // of the warp's heads
     uint4 next[2];
     auto load = [&](int t) {

@@ -10,6 +10,7 @@ namespace ft {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kMostRows = 1 << 30;
 constexpr int kManyRows = 2048;  // from here on four rows go to a warp: below, rows have a warp each at once
 
 struct RouteBatch {
@@ -30,11 +31,11 @@ __global__ void __launch_bounds__(kWarps * 32, kFour ? 4 : PL <= 8 ? 8 : PL == 1
   dec::pdl_wait_primary();
   const rule::Lane<PL> own(a.r);
   const T* logits = static_cast<const T*>(a.logits);
-  if constexpr (kFour) {
-    for (int t = 4 * (blockIdx.x * kWarps + warp); t < a.T; t += 4 * gridDim.x * kWarps)
+  const int t = (kFour ? 4 : 1) * (blockIdx.x * kWarps + warp);
+  if (t < a.T) {
+    if constexpr (kFour) {
       rule::route_four<PL>(a.r, own, logits, a.stride, t, a.T, list, a.idx, a.w);
-  } else {
-    for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps) {
+    } else {
       int e;
       float w;
       rule::route_row<PL>(a.r, own, logits + t * a.stride, list, &e, &w);
@@ -120,7 +121,8 @@ extern "C" ft_status ft_route(const ft_router* router, int32_t num_experts, int3
                               float* topk_w, void* stream) {
   const ft_status st = check_router(router, num_experts, top_k);
   if (st != FT_OK) return st;
-  if (num_tokens < 0) return set_error(FT_ERR_INVALID_ARG, "num_tokens=%d", num_tokens);
+  if (num_tokens < 0 || num_tokens > kMostRows)
+    return set_error(FT_ERR_INVALID_ARG, "num_tokens=%d outside 0..%d", num_tokens, kMostRows);
   if (logits_dtype != FT_F32 && logits_dtype != FT_BF16)
     return set_error(FT_ERR_INVALID_ARG, "logits_dtype=%d is not FT_F32 or FT_BF16", logits_dtype);
   if (num_tokens == 0) return FT_OK;

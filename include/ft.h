@@ -659,7 +659,7 @@ ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_batch* batch
  *   logits   device FT_F32 or FT_BF16 [num_tokens][num_experts], rows logits_stride
  *            elements apart (of a single row it is not used)
  *   topk_idx device int32 [num_tokens][top_k] in selection order; topk_w device float32, the gates
- * num_experts 1..1024, top_k 1..min(num_experts, 32).  A group has the largest
+ * num_tokens up to 2^30, num_experts 1..1024, top_k 1..min(num_experts, 32).  A group has the largest
  * power of two of lanes that fits 32 / num_groups, each with 32 experts at most
  * (FT_ERR_UNSUPPORTED beyond; up to 512 experts always fit). */
 ft_status ft_route(const ft_router* router, int32_t num_experts, int32_t top_k, int32_t num_tokens, const void* logits,

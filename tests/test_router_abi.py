@@ -25,7 +25,7 @@ def route(E=64, k=4, T=3, logits=4096, stride=64, dtype=ft.FT_F32, idx=8192, w=1
     (dict(E=4, k=1), "INVALID_ARG", "group_top"), (dict(k=32, top_groups=1), "INVALID_ARG", "beyond the 16 experts"),
     (dict(E=1017, groups=9), "UNSUPPORTED", "at most 576"), (dict(E=1023, groups=31), "UNSUPPORTED", "at most 992"),
     (dict(scale=float("nan")), "INVALID_ARG", "scale"), (dict(bias=16386), "INVALID_ARG", "bias"),
-    (dict(T=-1), "INVALID_ARG", "num_tokens"), (dict(dtype=2), "INVALID_ARG", "logits_dtype"), (dict(logits=None), "INVALID_ARG", "null"),
+    (dict(T=-1), "INVALID_ARG", "num_tokens"), (dict(T=(1 << 30) + 1), "INVALID_ARG", "num_tokens"), (dict(dtype=2), "INVALID_ARG", "logits_dtype"), (dict(logits=None), "INVALID_ARG", "null"),
     (dict(idx=None), "INVALID_ARG", "null"), (dict(w=None), "INVALID_ARG", "null"), (dict(logits=4098), "INVALID_ARG", "aligned"),
     (dict(idx=8194), "INVALID_ARG", "aligned"), (dict(stride=63), "INVALID_ARG", "logits_stride"),
 ])
