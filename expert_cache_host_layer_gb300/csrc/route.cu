@@ -11,7 +11,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMostRows = 1 << 30;
-constexpr int kManyRows = 2048;  // from here on four rows go to a warp: below, rows have a warp each at once
+constexpr int kManyRows = 6144;  // from here on four rows go to a warp
 
 struct RouteBatch {
   rule::Rule r;

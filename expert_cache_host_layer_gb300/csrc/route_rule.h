@@ -26,6 +26,7 @@
 
 #include <cuda_bf16.h>
 
+#include "float_pair.h"
 #include "ft_internal.h"
 
 namespace ft {
@@ -92,13 +93,20 @@ __device__ __forceinline__ void logits4(const __nv_bfloat16* row, int e, float* 
   l[2] = __uint_as_float(v.y << 16); l[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 
-// Scores in fp64, for the comparisons that fp32 does not decide.
+// Scores in fp64 for the comparisons that fp32 does not decide (by pairs of floats as far as those reach: fp64 is slow here).
 struct Exact {
   int softmax;
   const float* bias;
-  double top, inv;  // softmax: largest logit, 1 / sum of e^(l - top)
+  float top;
+  FloatPair inv;  // softmax: 1 / sum of e^(l - top)
   __device__ double value(float l, int e) const {
-    const double s = softmax ? exp((double)l - top) * inv : 1.0 / (1.0 + exp(-(double)l));
+    double s;
+    if (softmax) {
+      const FloatPair x = two_sum(l, -top);
+      s = x.h >= -60.0f ? wide(exp_pair(x) * inv) : exp((double)l - (double)top) * wide(inv);
+    } else {
+      s = fabsf(l) <= 60.0f ? wide(sigmoid_pair(l)) : 1.0 / (1.0 + exp(-(double)l));
+    }
     if (!bias) return s;
     const double v = s + (double)__ldg(&bias[e]);
     return v != v ? -INFINITY : fmin(v, (double)FLT_MAX);
@@ -106,17 +114,20 @@ struct Exact {
 };
 template <typename T>
 __device__ __noinline__ Exact make_exact(const Rule r, const T* row, float top) {
-  Exact x{r.softmax, r.bias, (double)top, 1.0};
+  Exact x{r.softmax, r.bias, top, {1.0f, 0.0f}};
   if (r.softmax) {
-    double z = 0.0;
-    for (int e = threadIdx.x & 31; e < r.E; e += 32) z += exp((double)logit(row, e) - (double)top);
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    x.inv = z > 0.0 ? 1.0 / z : 0.0;
+    FloatPair z{0.0f, 0.0f};
+    for (int e = threadIdx.x & 31; e < r.E; e += 32) {
+      const FloatPair d = two_sum(logit(row, e), -top);
+      if (d.h >= -60.0f) z = z + exp_pair(d);  // (what is left out is below 2^-76 of the sum)
+    }
+    for (int o = 16; o > 0; o >>= 1) z = z + FloatPair{__shfl_xor_sync(0xffffffffu, z.h, o), __shfl_xor_sync(0xffffffffu, z.l, o)};
+    x.inv = z.h > 0.0f ? inverse(z) : FloatPair{0.0f, 0.0f};
   }
   return x;
 }
 // Whether the lane's group takes part, in fp64 (of logits where those decide: without a bias, by a group's best).  least: a
-// bound below the fp32 values that may count, as the caller has them (fp64 is slow here: 3000 cycles a sigmoid).
+// bound below the fp32 values that may count, as the caller has them.
 template <typename T>
 __device__ __noinline__ bool exact_groups(const Rule r, const T* row, float top, float inv_z, int group, int sub, float least) {
   const Exact x = make_exact(r, row, top);
