@@ -28,7 +28,7 @@ namespace ft {
 namespace kv {
 namespace {
 
-constexpr int kMostThreads = 512;
+constexpr int kMostThreads = 384;  // three such blocks an SM: 56 registers a thread
 constexpr int kThreads = 256;      // of a block, if its heads leave a choice
 constexpr int kMostTokens = 32;    // of a block
 constexpr int kTrigFloats = 4096;  // of a block: tokens x rot_dim
@@ -75,7 +75,7 @@ __device__ __forceinline__ float2 turn(uint64_t fraction, float scale) {
 constexpr int kNone = 0, kBf16 = 1, kFp8 = 2;  // the cache
 
 template <int kCache, bool kInterleaved>
-__global__ void __launch_bounds__(kMostThreads, 2) rotary_kernel(const __grid_constant__ RotArgs a) {
+__global__ void __launch_bounds__(kMostThreads, 3) rotary_kernel(const __grid_constant__ RotArgs a) {
   __shared__ float4 s_trig[kTrigFloats / 4];  // [token][cos 0..3, cos 4..7, sin 0..3, sin 4..7 of a lane's pairs][lane]
   __shared__ int s_pos[kMostTokens], s_row[kMostTokens];
   const int half = a.r.rot_dim / 2, lanes = a.r.rot_dim / 16;  // lanes: of a head, those with pairs
@@ -188,13 +188,14 @@ ft_status check_rotary(const ft_rotary* r, int head_dim) {
 
 ft_status launch(RotArgs& a, const char* name, int cache, cudaStream_t s) {
   a.heads = a.Hq + (cache == kNone ? 0 : 2 * a.p.num_kv_heads);
-  a.pass = std::min(a.heads, kMostThreads / a.units);
+  const int fit = kMostThreads / a.units, passes = (a.heads + fit - 1) / fit;
+  a.pass = (a.heads + passes - 1) / passes;
   const int wide = a.pass * a.units;  // threads of a token
   const int most = std::min(kMostTokens, kTrigFloats / a.r.rot_dim);
   a.step = std::min({std::max(1, kThreads / wide), a.rows, most});
   const int threads = (wide * a.step + 31) / 32 * 32;
-  // one wave (64 registers a thread), while that leaves a block no more tokens than it has room for
-  const int wave = 1024 / threads * sm_count();
+  // one wave, while that leaves a block no more tokens than it has room for
+  const int wave = 3 * kMostThreads / threads * sm_count();
   a.per = std::min(most, (int)(((long long)a.rows + wave - 1) / wave));
   if (a.per > a.step) a.per = std::min(most, (a.per + a.step - 1) / a.step * a.step);
   const dim3 grid((unsigned)(((long long)a.rows + a.per - 1) / a.per));
