@@ -81,6 +81,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+template <int PL>
+__device__ __forceinline__ constexpr float softmax_error() { return PL <= 8 ? 0x1p-19f : 0x1p-18f; }  // (see route_row)
 __device__ __forceinline__ float logit(const float* row, int e) { return clean(row[e]); }
 __device__ __forceinline__ float logit(const __nv_bfloat16* row, int e) { return clean(__bfloat162float(row[e])); }
 __device__ __forceinline__ void logits4(const float* row, int e, float* l) {
@@ -178,6 +180,18 @@ __device__ __noinline__ void exact_ranks(const Rule r, const T* row, float top, 
   }
   __syncwarp();
 }
+// bf16 logits, many of which are equal, as keys that order like (value, lower expert first): their 16 bits in order (one more
+// than that takes negative ones, whose low bits are ones, and FLT_MAX, which stands for infinity, to whole steps).
+__device__ __forceinline__ uint32_t rank_key(float l, int e) { return ((order(l) + 1u) & 0xffff0000u) | (0xffffu - (uint32_t)e); }
+__device__ __forceinline__ int count_above(uint32_t x, const float* keys, int n) {
+  int above = 0;
+#pragma unroll 1
+  for (int j = 0; j < n; j += 4) {
+    const uint4 y = *reinterpret_cast<const uint4*>(keys + j);
+    above += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
+  }
+  return above;
+}
 // The rank of (x, e) among a list's values, equal ones by expert.
 template <typename I>
 __device__ __forceinline__ int rank_of(float x, int e, const float* values, const I* experts, int n) {
@@ -215,7 +229,7 @@ __device__ __forceinline__ void route_row(const Rule& r, const Lane<PL>& own, co
                                           float* gate) {
   constexpr int V = Lane<PL>::V;
   const int lane = threadIdx.x & 31, room = list_room(r.E);
-  const bool scored = r.bias != nullptr;
+  const bool scored = r.bias != nullptr, by_key = sizeof(T) == 2 && !scored;
   float* values = reinterpret_cast<float*>(shared);
   int* experts = reinterpret_cast<int*>(values + room);
   long long* keys = reinterpret_cast<long long*>(experts + room);
@@ -252,12 +266,13 @@ __device__ __forceinline__ void route_row(const Rule& r, const Lane<PL>& own, co
       largest = inv_z;
     }
   }
-  // exp2 (2^-22) of a rounded argument (1.5 u |l|, at most 0.23 of it left in s (1 - s)), 1 + e (u) and rcp (2^-23) come to
-  // less than 2^-21.5 of a sigmoid; a softmax's denominator may be off by its sum of 32 terms in a lane
+  // With u = 2^-24: exp2 (4 u) of a rounded argument (1.5 u |l|, at most 0.23 of it left in s (1 - s)), 1 + e (u) and rcp
+  // (2 u) come to less than 2^-21.5 of a sigmoid.  Of a softmax's largest score: 5 u for the same, 4 u for expf, ln E u for
+  // its arguments and PL + 5 u for the sum in the denominator, 2 u for its inverse: 30 u for 8 values a lane, 55 u for 32.
   auto score = [&](float l) {
     return r.softmax ? exp2_approx((l - top) * kLog2e) * inv_z : rcp_approx(1.0f + exp2_approx(-l * kLog2e));
   };
-  const float err_score = r.softmax ? largest * 0x1p-18f : 0x1p-21f;
+  const float err_score = r.softmax ? largest * softmax_error<PL>() : 0x1p-21f;
   if (scored) {
     if (r.softmax) {
 #pragma unroll
@@ -353,15 +368,21 @@ __device__ __forceinline__ void route_row(const Rule& r, const Lane<PL>& own, co
     const unsigned who = __ballot_sync(0xffffffffu, in);
     if (in) {
       const int at = n + __popc(who & ((1u << lane) - 1u));
-      values[at] = v[q];
-      experts[at] = own.expert + own.step(r, q);
+      const int e = own.expert + own.step(r, q);
+      values[at] = by_key ? __uint_as_float(rank_key(v[q], e)) : v[q];
+      experts[at] = e;
     }
     n += __popc(who);
   }
-  if (lane < 4) values[n + lane] = NAN;
+  if (lane < 4) values[n + lane] = by_key ? 0.0f : NAN;
   __syncwarp();
   bool unsure = false;
   for (int i = lane; i < n; i += 32) {
+    if (by_key) {
+      const int above = count_above(__float_as_uint(values[i]), values, n);
+      if (above < r.k) picks[above] = experts[i];
+      continue;
+    }
     const float x = values[i], lo = x - near, hi = x + near;
     int above = 0, not_below = 0;
 #pragma unroll 1
@@ -437,7 +458,7 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
   constexpr int V = Lane<PL>::V;
   const int lane = threadIdx.x & 31, mine_of = lane >> 3, at8 = lane & 7;  // the row and place of the lane where eight lanes have a row
   const unsigned below = (1u << lane) - 1u;
-  const bool scored = r.bias != nullptr;
+  const bool scored = r.bias != nullptr, by_key = sizeof(T) == 2 && !scored;
   FourLists<PL>& list = *reinterpret_cast<FourLists<PL>*>(shared);
 
   float v[4][PL];
@@ -477,7 +498,7 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         inv_z[j] = z > 0.0f ? 1.0f / z : 0.0f;
       }
-      err_score[j] = inv_z[j] * 0x1p-18f;
+      err_score[j] = inv_z[j] * softmax_error<PL>();
     }
   }
   auto score = [&](float l, float t, float z) {
@@ -639,12 +660,17 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
   for (int i = at8; i < count; i += 8) {
     const int e = experts[i];
     const float l = logit(row, e);
-    values[i] = scored ? score(l, row_top, row_z) + clean(__ldg(&r.bias[e])) : l;
+    values[i] = scored ? score(l, row_top, row_z) + clean(__ldg(&r.bias[e])) : by_key ? __uint_as_float(rank_key(l, e)) : l;
   }
-  if (at8 < 4) values[count + at8] = NAN;
+  if (at8 < 4) values[count + at8] = by_key ? 0.0f : NAN;
   __syncwarp();
   bool unsure = false;
   for (int i = at8; i < count; i += 8) {
+    if (by_key) {
+      const int above = count_above(__float_as_uint(values[i]), values, count);
+      if (above < r.k) picks[above] = experts[i];
+      continue;
+    }
     const float x = values[i], lo = x - apart, hi = x + apart;
     int above = 0, not_below = 0;
 #pragma unroll 1
