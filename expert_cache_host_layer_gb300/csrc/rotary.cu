@@ -196,6 +196,7 @@ ft_status launch(RotArgs& a, const char* name, int cache, cudaStream_t s) {
   const int threads = (wide * a.step + 31) / 32 * 32;
   // one wave, while that leaves a block no more tokens than it has room for
   const int wave = 3 * kMostThreads / threads * sm_count();
+  if (wave == 0) return set_error(FT_ERR_CUDA, "%s: no CUDA device", name);
   a.per = std::min(most, (int)(((long long)a.rows + wave - 1) / wave));
   if (a.per > a.step) a.per = std::min(most, (a.per + a.step - 1) / a.step * a.step);
   const dim3 grid((unsigned)(((long long)a.rows + a.per - 1) / a.per));

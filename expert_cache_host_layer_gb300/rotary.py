@@ -31,6 +31,8 @@ def frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", fact
     * "linear": every frequency divided by factor (positions interpolated);
     * "yarn": pairs that turn beta_fast times or more over original_length as they are, those that turn beta_slow times or
       less divided by factor, in between a mix that is linear in the pair's index."""
+    if not base > 0.0:
+        raise ValueError("base is positive")
     freq = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
     if scaling == "none":
         return freq

@@ -76,7 +76,7 @@ def test_frequencies():
         got = frequencies(d, base, "yarn", factor, length)
         assert np.allclose(got, orot.yarn(d, base, factor, length), rtol=1e-12)
         assert got[0] == 1.0 and math.isclose(got[-1], base ** (-(d - 2) / d) / factor, rel_tol=1e-12)
-    for kw, text in ((dict(scaling="cubic"), "scaling"), (dict(scaling="yarn", factor=2.0), "original_length"),
+    for kw, text in ((dict(scaling="cubic"), "scaling"), (dict(base=0.0), "base"), (dict(base=-2.0), "base"), (dict(scaling="yarn", factor=2.0), "original_length"),
                      (dict(scaling="linear", factor=0.5), "factor")):
         with pytest.raises(ValueError, match=text):
             frequencies(64, **kw)
@@ -95,3 +95,15 @@ def test_oracle_pins():
     assert np.allclose(y.ravel(), [-4, 2, -6, -8, 5, 6], atol=1e-14)
     assert np.allclose(orot.rotate(orot.rotate(x, [7], quarter), [-7], quarter), x, atol=1e-13)
     assert orot.reach(-x, quarter).ravel().tolist() == [4, 6, 4, 6, 0, 0]
+
+
+def test_without_a_gpu_calls_report_it():
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is here")
+    for call in (rotate, append, lambda: ft.ft_add_norm(ft.ft_norm(None, 0, 64, 1e-6, 0), 3, 4096, 64, 0, None, 0, 0, None, 0, 8192,
+                                                        64, 0, None),
+                 lambda: ft.ft_route(ft.ft_router(0, 1, 1, 1, 1, 1.0, None, 0), 64, 4, 3, 4096, 64, 0, 8192, 12288)):
+        with pytest.raises(ft.FtError) as e:
+            call()
+        assert e.value.status == ft.FT_ERR_CUDA
