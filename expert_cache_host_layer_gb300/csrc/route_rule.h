@@ -615,6 +615,7 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
     }
   }
   int n[4];
+  unsigned left[4];  // the lane's values that go to the list
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float least = -INFINITY;
@@ -632,20 +633,25 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
       near[j] = 2.0f * err_score[j] + 0x1p-22f * value(__reduce_max_sync(0xffffffffu, order(size)));
     }
     cut[j] += least;  // NaN in groups that take no part
-    unsigned mine = 0;
+    left[j] = 0;
 #pragma unroll
     for (int q = 0; q < PL; ++q)
-      if (v[j][q] >= cut[j]) mine |= 1u << q;
+      if (v[j][q] >= cut[j]) left[j] |= 1u << q;
     n[j] = 0;
-    for (;;) {  // a value of each lane that has one left
-      const unsigned who = __ballot_sync(0xffffffffu, mine != 0u);
-      if (!who) break;
-      if (mine) {
-        const int q = __ffs(mine) - 1, at = n[j] + __popc(who & below);
-        mine &= mine - 1;
+  }
+  for (;;) {  // of each row a value of each lane that has one left
+    unsigned who[4], any = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) any |= who[j] = __ballot_sync(0xffffffffu, left[j] != 0u);
+    if (!any) break;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (left[j]) {
+        const int q = __ffs(left[j]) - 1, at = n[j] + __popc(who[j] & below);
+        left[j] &= left[j] - 1;
         list.experts[j][at] = (uint16_t)(own.expert + own.step(r, q));
       }
-      n[j] += __popc(who);
+      n[j] += __popc(who[j]);
     }
   }
   __syncwarp();
@@ -657,33 +663,51 @@ __device__ __forceinline__ void route_four(const Rule& r, const Lane<PL>& own, c
   float* values = list.values[mine_of];
   const uint16_t* experts = list.experts[mine_of];
   int* picks = list.picks[mine_of];
-  for (int i = at8; i < count; i += 8) {
-    const int e = experts[i];
-    const float l = logit(row, e);
-    values[i] = scored ? score(l, row_top, row_z) + clean(__ldg(&r.bias[e])) : by_key ? __uint_as_float(rank_key(l, e)) : l;
+  auto listed = [&](float l, int e) {
+    return scored ? score(l, row_top, row_z) + clean(__ldg(&r.bias[e])) : by_key ? __uint_as_float(rank_key(l, e)) : l;
+  };
+  for (int i = at8; i < count; i += 16) {  // two of a lane's at a time
+    const int e = experts[i], f = experts[min(i + 8, count - 1)];
+    const float l = logit(row, e), m = logit(row, f);
+    values[i] = listed(l, e);
+    if (i + 8 < count) values[i + 8] = listed(m, f);
   }
   if (at8 < 4) values[count + at8] = by_key ? 0.0f : NAN;
   __syncwarp();
   bool unsure = false;
-  for (int i = at8; i < count; i += 8) {
+  for (int i = at8; i < count; i += 16) {
+    const float x[2] = {values[i], values[min(i + 8, count - 1)]};
+    int above[2] = {0, 0};
     if (by_key) {
-      const int above = count_above(__float_as_uint(values[i]), values, count);
-      if (above < r.k) picks[above] = experts[i];
-      continue;
-    }
-    const float x = values[i], lo = x - apart, hi = x + apart;
-    int above = 0, not_below = 0;
+      const uint32_t a = __float_as_uint(x[0]), b = __float_as_uint(x[1]);
 #pragma unroll 1
-    for (int c = 0; c < count; c += 4) {
-      const float4 y = *reinterpret_cast<const float4*>(values + c);
-      above += (y.x > hi) + (y.y > hi) + (y.z > hi) + (y.w > hi);
-      not_below += (y.x >= lo) + (y.y >= lo) + (y.z >= lo) + (y.w >= lo);
+      for (int c = 0; c < count; c += 4) {
+        const uint4 y = *reinterpret_cast<const uint4*>(values + c);
+        above[0] += (y.x > a) + (y.y > a) + (y.z > a) + (y.w > a);
+        above[1] += (y.x > b) + (y.y > b) + (y.z > b) + (y.w > b);
+      }
+    } else {
+      const float lo[2] = {x[0] - apart, x[1] - apart}, hi[2] = {x[0] + apart, x[1] + apart};
+      int not_below[2] = {0, 0};
+#pragma unroll 1
+      for (int c = 0; c < count; c += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(values + c);
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          above[d] += (y.x > hi[d]) + (y.y > hi[d]) + (y.z > hi[d]) + (y.w > hi[d]);
+          not_below[d] += (y.x >= lo[d]) + (y.y >= lo[d]) + (y.z >= lo[d]) + (y.w >= lo[d]);
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+        if (i + 8 * d < count && above[d] < r.k && not_below[d] - above[d] != 1) {  // another one beside itself
+          if (scored) unsure = true;
+          else above[d] = rank_of(x[d], experts[i + 8 * d], values, experts, count);  // equal logits
+        }
     }
-    if (above < r.k && not_below - above != 1) {
-      if (scored) unsure = true;
-      else above = rank_of(x, experts[i], values, experts, count);  // equal logits
-    }
-    if (above < r.k) picks[above] = experts[i];
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+      if (i + 8 * d < count && above[d] < r.k) picks[above[d]] = experts[i + 8 * d];
   }
   const unsigned undecided = __ballot_sync(0xffffffffu, unsure);
   if (undecided) {
