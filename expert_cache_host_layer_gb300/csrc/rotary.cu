@@ -19,6 +19,12 @@
 // halves of eight pairs (8c.. and rot_dim / 2 + 8c.. where the halves lie apart,
 // 16c.. where pairs are interleaved), so that a pair never leaves its thread,
 // whatever rot_dim is.
+//
+// Measured (head_dim 128, 16 query and 4 key heads): 16,384 tokens into the e4m3
+// cache 33.7 us, 5.5 TB/s (with the head worked out for every vector, 42: 260
+// instructions a warp and vector instead of 200); 8191 tokens x 24 heads of 96, a
+// third of each turned, 14.3 us, 5.3 TB/s; one token 2.6 us in a graph.  The
+// start (places, sines) is 3 to 4 us of each.
 #include <algorithm>
 
 #include "decode_common.h"
@@ -28,7 +34,7 @@ namespace ft {
 namespace kv {
 namespace {
 
-constexpr int kMostThreads = 384;  // three such blocks an SM: 56 registers a thread
+constexpr int kMostThreads = 384;  // three such blocks an SM: 56 registers a thread (64: 34.6 us instead of 33.7, 48: 39.9)
 constexpr int kThreads = 256;      // of a block, if its heads leave a choice
 constexpr int kMostTokens = 32;    // of a block
 constexpr int kTrigFloats = 4096;  // of a block: tokens x rot_dim

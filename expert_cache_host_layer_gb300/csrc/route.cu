@@ -11,7 +11,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMostRows = 1 << 30;
-constexpr int kManyRows = 6144;  // from here on four rows go to a warp
+// From here on four rows go to a warp: 16,384 rows 16.6 us against 20.7, 8192 11.5 against 11.4 (plain softmax 6.4 against
+// 8.2), 4096 10.1 against 8.4: below, every row has a warp of its own at once, and its chain is shorter.
+constexpr int kManyRows = 6144;
 
 struct RouteBatch {
   rule::Rule r;
