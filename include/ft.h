@@ -253,7 +253,7 @@ ft_status ft_route_classify(ft_cache* cache, int32_t layer, const float* logits,
 typedef enum ft_score { FT_SCORE_SOFTMAX = 0, FT_SCORE_SIGMOID = 1 } ft_score;
 typedef struct ft_router {
   int32_t score;       /* ft_score */
-  int32_t num_groups;  /* 1..32, a divisor of the experts' number; at most 32 experts a warp's lane: see ft_route */
+  int32_t num_groups;  /* 1..32, a divisor of the experts' number (above 512 experts see ft_route) */
   int32_t top_groups;  /* 1..num_groups, with top_k experts or more */
   int32_t group_top;   /* 1 or 2 */
   int32_t renormalise; /* 0 or 1 */
@@ -611,8 +611,9 @@ typedef struct ft_norm {
  * fp32 scales, device [num_rows][ceil(hidden / group)] contiguous:
  *   scale = max|y| / 448 over the group's channels,  code = y / scale to the nearest e4m3 value
  * (max|r * weight| below 2^-100 counts as that, so that a group of zeros has a
- * scale too.)  The mean of squares is fp32: magnitudes beyond 2^63 overflow it.
- * A NaN or infinity in r makes its row, or its group, NaN. */
+ * scale too.)  The sum of squares is fp32: magnitudes beyond some 2^57 overflow
+ * it.  A NaN in r makes its row NaN; an infinity makes its own value (of codes: its
+ * group) NaN and the rest of the row 0. */
 ft_status ft_add_norm(const ft_norm* norm, int64_t num_rows, const void* x, int64_t x_stride, int32_t x_dtype,
                       const void* delta, int64_t delta_stride, int32_t delta_dtype, void* total, int64_t total_stride,
                       void* out, int64_t out_stride, int32_t out_dtype, float* scales, void* stream);
