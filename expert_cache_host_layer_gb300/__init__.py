@@ -80,6 +80,9 @@ class ft_kv_batch(ctypes.Structure):
                 ("max_q_len", ctypes.c_int32)]
 
 
+_ROWS = (("", ctypes.c_void_p), ("_token_stride", ctypes.c_int64), ("_head_stride", ctypes.c_int64))
+
+
 class ft_norm(ctypes.Structure):
     _fields_ = [("weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int32), ("hidden", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("group", ctypes.c_int32)]
@@ -93,6 +96,27 @@ class ft_rotary(ctypes.Structure):
 class ft_router(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("score", "num_groups", "top_groups", "group_top", "renormalise")] + \
         [("scale", ctypes.c_float), ("bias", ctypes.c_void_p), ("bias_stride", ctypes.c_int64)]
+
+
+class ft_norm_args(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int64)] + \
+        [f for n in ("x", "delta", "total", "out") for f in ((n, ctypes.c_void_p), (n + "_stride", ctypes.c_int64))] + \
+        [("scales", ctypes.c_void_p)] + [(n, ctypes.c_int32) for n in ("x_dtype", "delta_dtype", "out_dtype")]
+
+
+class ft_rotate_args(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p)] + \
+        [(n + e, t) for n in ("x", "out") for e, t in _ROWS] + [(n, ctypes.c_int32) for n in ("num_tokens", "num_heads", "head_dim")]
+
+
+class ft_append_args(ctypes.Structure):
+    _fields_ = [(n + e, t) for n in ("k", "v", "q", "q_out") for e, t in _ROWS] + [("num_q_heads", ctypes.c_int32)]
+
+
+class ft_route_args(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64), ("topk_idx", ctypes.c_void_p),
+                ("topk_w", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int32) for n in ("logits_dtype", "num_tokens", "num_experts", "top_k")]
 
 
 # ---------------------------------------------------------------- loading
@@ -143,10 +167,10 @@ def _load():
         "ft_kv_attend_workspace": (ctypes.c_uint64, [P, P, I32]),
         "ft_stream_capture": (ctypes.c_uint64, [P]),
         "ft_kv_status": (st, [P]),
-        "ft_add_norm": (st, [P, I64, P, I64, I32, P, I64, I32, P, I64, P, I64, I32, P, P]),
-        "ft_rotate": (st, [P, I32, P, I32, I32, P, I64, I64, P, I64, I64, P]),
-        "ft_kv_append_rotary": (st, [P, P, P, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, P]),
-        "ft_route": (st, [P, I32, I32, I32, P, I64, I32, P, P, P]),
+        "ft_add_norm": (st, [P, P, P]),
+        "ft_rotate": (st, [P, P, P]),
+        "ft_kv_append_rotary": (st, [P, P, P, P, P]),
+        "ft_route": (st, [P, P, P]),
         "ft_status_str": (ctypes.c_char_p, [st]),
         "ft_last_error": (ctypes.c_char_p, []),
     }
@@ -403,41 +427,21 @@ def ft_kv_status(stream: int = 0):
     _check(_lib.ft_kv_status(stream or None), "ft_kv_status")
 
 
-def ft_add_norm(norm: ft_norm, num_rows: int, x: int, x_stride: int, x_dtype: int, delta: int, delta_stride: int,
-                delta_dtype: int, total: int, total_stride: int, out: int, out_stride: int, out_dtype: int, scales: int,
-                stream: int = 0):
-    st = _lib.ft_add_norm(ctypes.addressof(norm), num_rows, x, x_stride, x_dtype, delta, delta_stride, delta_dtype, total,
-                          total_stride, out, out_stride, out_dtype, scales, stream)
-    if st:
-        _check(st, "ft_add_norm")
+def ft_add_norm(norm: ft_norm, args: ft_norm_args, stream: int = 0):
+    _check(_lib.ft_add_norm(ctypes.addressof(norm), ctypes.addressof(args), stream or None), "ft_add_norm")
 
 
-def ft_rotate(rotary: ft_rotary, num_tokens: int, positions: int, num_heads: int, head_dim: int, x: int,
-              x_token_stride: int, x_head_stride: int, out: int, out_token_stride: int, out_head_stride: int,
-              stream: int = 0):
-    st = _lib.ft_rotate(ctypes.addressof(rotary), num_tokens, positions, num_heads, head_dim, x, x_token_stride,
-                        x_head_stride, out, out_token_stride, out_head_stride, stream)
-    if st:
-        _check(st, "ft_rotate")
+def ft_rotate(rotary: ft_rotary, args: ft_rotate_args, stream: int = 0):
+    _check(_lib.ft_rotate(ctypes.addressof(rotary), ctypes.addressof(args), stream or None), "ft_rotate")
 
 
-def ft_kv_append_rotary(pages: ft_kv_pages, batch: ft_kv_batch, rotary: ft_rotary, k: int, k_token_stride: int,
-                        k_head_stride: int, v: int, v_token_stride: int, v_head_stride: int, num_q_heads: int = 0,
-                        q: int = 0, q_token_stride: int = 0, q_head_stride: int = 0, q_out: int = 0,
-                        q_out_token_stride: int = 0, q_out_head_stride: int = 0, stream: int = 0):
-    st = _lib.ft_kv_append_rotary(ctypes.addressof(pages), ctypes.addressof(batch), ctypes.addressof(rotary), k,
-                                  k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, num_q_heads, q,
-                                  q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, stream)
-    if st:
-        _check(st, "ft_kv_append_rotary")
+def ft_kv_append_rotary(pages: ft_kv_pages, batch: ft_kv_batch, rotary: ft_rotary, args: ft_append_args, stream: int = 0):
+    _check(_lib.ft_kv_append_rotary(ctypes.addressof(pages), ctypes.addressof(batch), ctypes.addressof(rotary),
+                                    ctypes.addressof(args), stream or None), "ft_kv_append_rotary")
 
 
-def ft_route(router: ft_router, num_experts: int, top_k: int, num_tokens: int, logits: int, logits_stride: int,
-             logits_dtype: int, topk_idx: int, topk_w: int, stream: int = 0):
-    st = _lib.ft_route(ctypes.addressof(router), num_experts, top_k, num_tokens, logits, logits_stride, logits_dtype,
-                       topk_idx, topk_w, stream)
-    if st:
-        _check(st, "ft_route")
+def ft_route(router: ft_router, args: ft_route_args, stream: int = 0):
+    _check(_lib.ft_route(ctypes.addressof(router), ctypes.addressof(args), stream or None), "ft_route")
 
 
 def ft_status_str(status: int) -> str:

@@ -237,7 +237,7 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
   return kv::launch_dependent(kernel, dim3((unsigned)blocks), threads, 0, s, a, per_row);
 }
 
-ft_status check_matrix(const char* name, const void* p, int64_t stride, int64_t rows, int hidden, int dtype) {
+ft_status check_matrix(const char* name, const void* p, int64_t stride, int64_t rows, int hidden) {
   if (!p) return set_error(FT_ERR_INVALID_ARG, "%s is null", name);
   if ((reinterpret_cast<uintptr_t>(p) & 15) || (stride & 7))
     return set_error(FT_ERR_INVALID_ARG, "%s must be 16-byte aligned with a row stride that is a multiple of 8 elements", name);
@@ -251,47 +251,48 @@ ft_status check_matrix(const char* name, const void* p, int64_t stride, int64_t 
 
 using namespace ft;
 
-extern "C" ft_status ft_add_norm(const ft_norm* norm, int64_t num_rows, const void* x, int64_t x_stride, int32_t x_dtype,
-                                 const void* delta, int64_t delta_stride, int32_t delta_dtype, void* total,
-                                 int64_t total_stride, void* out, int64_t out_stride, int32_t out_dtype, float* scales,
-                                 void* stream) {
-  if (!norm) return set_error(FT_ERR_INVALID_ARG, "norm is null");
+extern "C" ft_status ft_add_norm(const ft_norm* norm, const ft_norm_args* args, void* stream) {
+  if (!norm || !args) return set_error(FT_ERR_INVALID_ARG, "norm or args is null");
+  const ft_norm_args& g = *args;
   const int H = norm->hidden;
   if (H < 8 || H > kMostHidden || H % 8)
     return set_error(FT_ERR_UNSUPPORTED, "hidden=%d is not a multiple of 8 in 8..%d", H, kMostHidden);
   if (!(norm->eps >= 0.0f) || norm->eps > 3.0e38f) return set_error(FT_ERR_INVALID_ARG, "eps must be finite and not negative");
-  if (num_rows < 0 || num_rows > 0x7fffffffLL) return set_error(FT_ERR_INVALID_ARG, "num_rows=%lld outside 0..2^31-1", (long long)num_rows);
+  if (g.num_rows < 0 || g.num_rows > 0x7fffffffLL)
+    return set_error(FT_ERR_INVALID_ARG, "num_rows=%lld outside 0..2^31-1", (long long)g.num_rows);
   if (norm->weight && norm->weight_dtype != FT_F32 && norm->weight_dtype != FT_BF16)
     return set_error(FT_ERR_INVALID_ARG, "weight_dtype=%d is not FT_F32 or FT_BF16", norm->weight_dtype);
   if (reinterpret_cast<uintptr_t>(norm->weight) & 15) return set_error(FT_ERR_INVALID_ARG, "weight is not 16-byte aligned");
-  if (x_dtype != FT_F32 && x_dtype != FT_BF16) return set_error(FT_ERR_INVALID_ARG, "x_dtype=%d is not FT_F32 or FT_BF16", x_dtype);
-  if (delta && delta_dtype != FT_F32 && delta_dtype != FT_BF16)
-    return set_error(FT_ERR_INVALID_ARG, "delta_dtype=%d is not FT_F32 or FT_BF16", delta_dtype);
-  if (total && !delta) return set_error(FT_ERR_INVALID_ARG, "total goes with delta");
-  if (out_dtype != FT_F32 && out_dtype != FT_BF16 && out_dtype != FT_FP8E4M3)
-    return set_error(FT_ERR_INVALID_ARG, "out_dtype=%d is not FT_F32, FT_BF16 or FT_FP8E4M3", out_dtype);
-  const bool fp8 = out_dtype == FT_FP8E4M3;
+  if (g.x_dtype != FT_F32 && g.x_dtype != FT_BF16)
+    return set_error(FT_ERR_INVALID_ARG, "x_dtype=%d is not FT_F32 or FT_BF16", g.x_dtype);
+  if (g.delta && g.delta_dtype != FT_F32 && g.delta_dtype != FT_BF16)
+    return set_error(FT_ERR_INVALID_ARG, "delta_dtype=%d is not FT_F32 or FT_BF16", g.delta_dtype);
+  if (g.total && !g.delta) return set_error(FT_ERR_INVALID_ARG, "total goes with delta");
+  if (g.out_dtype != FT_F32 && g.out_dtype != FT_BF16 && g.out_dtype != FT_FP8E4M3)
+    return set_error(FT_ERR_INVALID_ARG, "out_dtype=%d is not FT_F32, FT_BF16 or FT_FP8E4M3", g.out_dtype);
+  const bool fp8 = g.out_dtype == FT_FP8E4M3;
   if (fp8 && norm->group != 0 && norm->group != 32 && norm->group != 64 && norm->group != 128)
     return set_error(FT_ERR_UNSUPPORTED, "group=%d is not 0, 32, 64 or 128", norm->group);
-  if (num_rows == 0) return FT_OK;
-  if (num_rows == 1) x_stride = delta_stride = total_stride = out_stride = H;  // of a single row: not used
-  ft_status st = check_matrix("x", x, x_stride, num_rows, H, x_dtype);
-  if (st == FT_OK && delta) st = check_matrix("delta", delta, delta_stride, num_rows, H, delta_dtype);
-  if (st == FT_OK && total) st = check_matrix("total", total, total_stride, num_rows, H, x_dtype);
-  if (st == FT_OK) st = check_matrix("out", out, out_stride, num_rows, H, out_dtype);
-  if (st != FT_OK) return st;
-  if (fp8 && (!scales || (reinterpret_cast<uintptr_t>(scales) & 3)))
-    return set_error(FT_ERR_INVALID_ARG, "an e4m3 output needs scales, 4-byte aligned");
+  if (g.num_rows == 0) return FT_OK;
   NormArgs a{};
-  a.x = x; a.delta = delta; a.w = norm->weight; a.total = total; a.out = out; a.scales = scales;
-  a.xs = x_stride; a.ds = delta_stride; a.ts = total_stride; a.os = out_stride; a.rows = num_rows;
-  a.hidden = H; a.w_dtype = norm->weight_dtype; a.out_dtype = out_dtype; a.eps = norm->eps;
+  a.x = g.x; a.delta = g.delta; a.w = norm->weight; a.total = g.total; a.out = g.out; a.scales = g.scales;
+  a.xs = g.x_stride; a.ds = g.delta_stride; a.ts = g.total_stride; a.os = g.out_stride; a.rows = g.num_rows;
+  if (a.rows == 1) a.xs = a.ds = a.ts = a.os = H;  // of a single row: not used
+  ft_status st = check_matrix("x", a.x, a.xs, a.rows, H);
+  if (st == FT_OK && a.delta) st = check_matrix("delta", a.delta, a.ds, a.rows, H);
+  if (st == FT_OK && a.total) st = check_matrix("total", a.total, a.ts, a.rows, H);
+  if (st == FT_OK) st = check_matrix("out", a.out, a.os, a.rows, H);
+  if (st != FT_OK) return st;
+  if (fp8 && (!a.scales || (reinterpret_cast<uintptr_t>(a.scales) & 3)))
+    return set_error(FT_ERR_INVALID_ARG, "an e4m3 output needs scales, 4-byte aligned");
+  a.hidden = H; a.w_dtype = norm->weight_dtype; a.out_dtype = g.out_dtype; a.eps = norm->eps;
   a.group = norm->group;
   a.groups = norm->group ? (H + norm->group - 1) / norm->group : 1;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int d = delta ? delta_dtype : -1;
-  const cudaError_t e = x_dtype == FT_F32 ? (d < 0 ? launch<FT_F32, -1>(a, s) : d == FT_F32 ? launch<FT_F32, FT_F32>(a, s) : launch<FT_F32, FT_BF16>(a, s))
-                                          : (d < 0 ? launch<FT_BF16, -1>(a, s) : d == FT_F32 ? launch<FT_BF16, FT_F32>(a, s) : launch<FT_BF16, FT_BF16>(a, s));
+  const int d = a.delta ? g.delta_dtype : -1;
+  const cudaError_t e = g.x_dtype == FT_F32
+      ? (d < 0 ? launch<FT_F32, -1>(a, s) : d == FT_F32 ? launch<FT_F32, FT_F32>(a, s) : launch<FT_F32, FT_BF16>(a, s))
+      : (d < 0 ? launch<FT_BF16, -1>(a, s) : d == FT_F32 ? launch<FT_BF16, FT_F32>(a, s) : launch<FT_BF16, FT_BF16>(a, s));
   if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "add_norm launch: %s", cudaGetErrorString(e));
   return FT_OK;
 }

@@ -222,62 +222,60 @@ ft_status launch(RotArgs& a, const char* name, int cache, cudaStream_t s) {
 using namespace ft;
 using namespace ft::kv;
 
-extern "C" ft_status ft_rotate(const ft_rotary* rotary, int32_t num_tokens, const int32_t* positions, int32_t num_heads,
-                               int32_t head_dim, const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
-                               int64_t out_token_stride, int64_t out_head_stride, void* stream) {
-  if (head_dim < 16 || head_dim % 16 || head_dim > kMostDim)
-    return set_error(FT_ERR_UNSUPPORTED, "head_dim=%d is not a multiple of 16 in 16..%d", head_dim, kMostDim);
-  ft_status st = check_rotary(rotary, head_dim);
+extern "C" ft_status ft_rotate(const ft_rotary* rotary, const ft_rotate_args* args, void* stream) {
+  if (!args) return set_error(FT_ERR_INVALID_ARG, "args is null");
+  const ft_rotate_args& g = *args;
+  if (g.head_dim < 16 || g.head_dim % 16 || g.head_dim > kMostDim)
+    return set_error(FT_ERR_UNSUPPORTED, "head_dim=%d is not a multiple of 16 in 16..%d", g.head_dim, kMostDim);
+  ft_status st = check_rotary(rotary, g.head_dim);
   if (st != FT_OK) return st;
-  if (num_heads < 1 || num_heads > kMostHeads)
-    return set_error(FT_ERR_INVALID_ARG, "num_heads=%d outside 1..%d", num_heads, kMostHeads);
-  if (num_tokens < 0) return set_error(FT_ERR_INVALID_ARG, "num_tokens=%d", num_tokens);
-  if (num_tokens == 0) return FT_OK;
-  if (!positions) return set_error(FT_ERR_INVALID_ARG, "positions is null");
-  if (num_tokens == 1) x_token_stride = out_token_stride = head_dim;  // of single entries: not used
-  if (num_heads == 1) x_head_stride = out_head_stride = head_dim;
-  if ((st = check_rows("x", x, x_token_stride, x_head_stride)) != FT_OK) return st;
-  if ((st = check_rows("out", out, out_token_stride, out_head_stride)) != FT_OK) return st;
-  if (out_token_stride <= 0 || out_head_stride <= 0) return set_error(FT_ERR_INVALID_ARG, "out's strides must be positive");
+  if (g.num_heads < 1 || g.num_heads > kMostHeads)
+    return set_error(FT_ERR_INVALID_ARG, "num_heads=%d outside 1..%d", g.num_heads, kMostHeads);
+  if (g.num_tokens < 0) return set_error(FT_ERR_INVALID_ARG, "num_tokens=%d", g.num_tokens);
+  if (g.num_tokens == 0) return FT_OK;
+  if (!g.positions) return set_error(FT_ERR_INVALID_ARG, "positions is null");
   RotArgs a{};
-  a.r = *rotary; a.positions = positions;
-  a.x[0] = static_cast<const __nv_bfloat16*>(x); a.ts[0] = x_token_stride; a.hs[0] = x_head_stride;
-  a.out = static_cast<__nv_bfloat16*>(out); a.ots = out_token_stride; a.ohs = out_head_stride;
-  a.rows = num_tokens; a.Hq = num_heads; a.units = head_dim / 16;
+  a.r = *rotary; a.positions = g.positions;
+  a.x[0] = static_cast<const __nv_bfloat16*>(g.x); a.ts[0] = g.x_token_stride; a.hs[0] = g.x_head_stride;
+  a.out = static_cast<__nv_bfloat16*>(g.out); a.ots = g.out_token_stride; a.ohs = g.out_head_stride;
+  if (g.num_tokens == 1) a.ts[0] = a.ots = g.head_dim;  // of single entries: not used
+  if (g.num_heads == 1) a.hs[0] = a.ohs = g.head_dim;
+  if ((st = check_rows("x", a.x[0], a.ts[0], a.hs[0])) != FT_OK) return st;
+  if ((st = check_rows("out", a.out, a.ots, a.ohs)) != FT_OK) return st;
+  if (a.ots <= 0 || a.ohs <= 0) return set_error(FT_ERR_INVALID_ARG, "out's strides must be positive");
+  a.rows = g.num_tokens; a.Hq = g.num_heads; a.units = g.head_dim / 16;
   return launch(a, "rotate", kNone, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_batch* batch, const ft_rotary* rotary,
-                                         const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
-                                         int64_t v_token_stride, int64_t v_head_stride, int32_t num_q_heads,
-                                         const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
-                                         int64_t q_out_token_stride, int64_t q_out_head_stride, void* stream) {
+                                         const ft_append_args* args, void* stream) {
+  if (!args) return set_error(FT_ERR_INVALID_ARG, "args is null");
+  const ft_append_args& g = *args;
   ft_status st = check_pages(pages);
   if (st == FT_OK) st = check_batch(pages, batch);
   if (st == FT_OK) st = check_rotary(rotary, pages->head_dim);
   if (st != FT_OK) return st;
-  if (num_q_heads < 0 || num_q_heads > kMostHeads)
-    return set_error(FT_ERR_INVALID_ARG, "num_q_heads=%d outside 0..%d", num_q_heads, kMostHeads);
+  if (g.num_q_heads < 0 || g.num_q_heads > kMostHeads)
+    return set_error(FT_ERR_INVALID_ARG, "num_q_heads=%d outside 0..%d", g.num_q_heads, kMostHeads);
   if (batch->num_tokens == 0) return FT_OK;
   const int D = pages->head_dim;
-  if (batch->num_tokens == 1) k_token_stride = v_token_stride = q_token_stride = q_out_token_stride = D;  // not used
-  if (pages->num_kv_heads == 1) k_head_stride = v_head_stride = D;
-  if (num_q_heads == 1) q_head_stride = q_out_head_stride = D;
-  if ((st = check_rows("k", k, k_token_stride, k_head_stride)) != FT_OK) return st;
-  if ((st = check_rows("v", v, v_token_stride, v_head_stride)) != FT_OK) return st;
   RotArgs a{};
-  if (num_q_heads > 0) {
-    if ((st = check_rows("q", q, q_token_stride, q_head_stride)) != FT_OK) return st;
-    if ((st = check_rows("q_out", q_out, q_out_token_stride, q_out_head_stride)) != FT_OK) return st;
-    if (q_out_token_stride <= 0 || q_out_head_stride <= 0)
-      return set_error(FT_ERR_INVALID_ARG, "q_out's strides must be positive");
-  }
   a.r = *rotary; a.p = *pages; a.b = *batch;
-  a.x[0] = static_cast<const __nv_bfloat16*>(q); a.ts[0] = q_token_stride; a.hs[0] = q_head_stride;
-  a.x[1] = static_cast<const __nv_bfloat16*>(k); a.ts[1] = k_token_stride; a.hs[1] = k_head_stride;
-  a.x[2] = static_cast<const __nv_bfloat16*>(v); a.ts[2] = v_token_stride; a.hs[2] = v_head_stride;
-  a.out = static_cast<__nv_bfloat16*>(q_out); a.ots = q_out_token_stride; a.ohs = q_out_head_stride;
-  a.rows = batch->num_tokens; a.Hq = num_q_heads; a.units = D / 16;
+  a.x[0] = static_cast<const __nv_bfloat16*>(g.q); a.ts[0] = g.q_token_stride; a.hs[0] = g.q_head_stride;
+  a.x[1] = static_cast<const __nv_bfloat16*>(g.k); a.ts[1] = g.k_token_stride; a.hs[1] = g.k_head_stride;
+  a.x[2] = static_cast<const __nv_bfloat16*>(g.v); a.ts[2] = g.v_token_stride; a.hs[2] = g.v_head_stride;
+  a.out = static_cast<__nv_bfloat16*>(g.q_out); a.ots = g.q_out_token_stride; a.ohs = g.q_out_head_stride;
+  if (batch->num_tokens == 1) a.ts[0] = a.ts[1] = a.ts[2] = a.ots = D;  // of single entries: not used
+  if (pages->num_kv_heads == 1) a.hs[1] = a.hs[2] = D;
+  if (g.num_q_heads == 1) a.hs[0] = a.ohs = D;
+  if ((st = check_rows("k", a.x[1], a.ts[1], a.hs[1])) != FT_OK) return st;
+  if ((st = check_rows("v", a.x[2], a.ts[2], a.hs[2])) != FT_OK) return st;
+  if (g.num_q_heads > 0) {
+    if ((st = check_rows("q", a.x[0], a.ts[0], a.hs[0])) != FT_OK) return st;
+    if ((st = check_rows("q_out", a.out, a.ots, a.ohs)) != FT_OK) return st;
+    if (a.ots <= 0 || a.ohs <= 0) return set_error(FT_ERR_INVALID_ARG, "q_out's strides must be positive");
+  }
+  a.rows = batch->num_tokens; a.Hq = g.num_q_heads; a.units = D / 16;
   if ((st = status_word(&a.status)) != FT_OK) return st;
   return launch(a, "append_rotary", pages->kv_dtype == FT_KV_FP8E4M3 ? kFp8 : kBf16, static_cast<cudaStream_t>(stream));
 }

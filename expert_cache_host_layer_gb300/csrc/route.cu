@@ -118,27 +118,28 @@ rule::Rule make_rule(const ft_router& r, int E, int k, const float* bias, bool a
 
 using namespace ft;
 
-extern "C" ft_status ft_route(const ft_router* router, int32_t num_experts, int32_t top_k, int32_t num_tokens,
-                              const void* logits, int64_t logits_stride, int32_t logits_dtype, int32_t* topk_idx,
-                              float* topk_w, void* stream) {
-  const ft_status st = check_router(router, num_experts, top_k);
+extern "C" ft_status ft_route(const ft_router* router, const ft_route_args* args, void* stream) {
+  if (!args) return set_error(FT_ERR_INVALID_ARG, "args is null");
+  const ft_route_args& g = *args;
+  const ft_status st = check_router(router, g.num_experts, g.top_k);
   if (st != FT_OK) return st;
-  if (num_tokens < 0 || num_tokens > kMostRows)
-    return set_error(FT_ERR_INVALID_ARG, "num_tokens=%d outside 0..%d", num_tokens, kMostRows);
-  if (logits_dtype != FT_F32 && logits_dtype != FT_BF16)
-    return set_error(FT_ERR_INVALID_ARG, "logits_dtype=%d is not FT_F32 or FT_BF16", logits_dtype);
-  if (num_tokens == 0) return FT_OK;
-  const int size = logits_dtype == FT_F32 ? 4 : 2;
-  if (!logits || !topk_idx || !topk_w) return set_error(FT_ERR_INVALID_ARG, "null logits, topk_idx or topk_w");
-  if ((reinterpret_cast<uintptr_t>(logits) & (size - 1)) || ((reinterpret_cast<uintptr_t>(topk_idx) | reinterpret_cast<uintptr_t>(topk_w)) & 3))
+  if (g.num_tokens < 0 || g.num_tokens > kMostRows)
+    return set_error(FT_ERR_INVALID_ARG, "num_tokens=%d outside 0..%d", g.num_tokens, kMostRows);
+  if (g.logits_dtype != FT_F32 && g.logits_dtype != FT_BF16)
+    return set_error(FT_ERR_INVALID_ARG, "logits_dtype=%d is not FT_F32 or FT_BF16", g.logits_dtype);
+  if (g.num_tokens == 0) return FT_OK;
+  const int size = g.logits_dtype == FT_F32 ? 4 : 2;
+  const uintptr_t logits = reinterpret_cast<uintptr_t>(g.logits), outs = reinterpret_cast<uintptr_t>(g.topk_idx) | reinterpret_cast<uintptr_t>(g.topk_w);
+  if (!g.logits || !g.topk_idx || !g.topk_w) return set_error(FT_ERR_INVALID_ARG, "null logits, topk_idx or topk_w");
+  if ((logits & (size - 1)) || (outs & 3))
     return set_error(FT_ERR_INVALID_ARG, "logits, topk_idx or topk_w is not aligned to its elements");
-  if (num_tokens == 1) logits_stride = num_experts;  // of a single row: not used
-  if (logits_stride < num_experts)
-    return set_error(FT_ERR_INVALID_ARG, "logits_stride=%lld is below num_experts=%d", (long long)logits_stride, num_experts);
+  const int64_t stride = g.num_tokens == 1 ? g.num_experts : g.logits_stride;  // (of a single row it is not used)
+  if (stride < g.num_experts)
+    return set_error(FT_ERR_INVALID_ARG, "logits_stride=%lld is below num_experts=%d", (long long)stride, g.num_experts);
   RouteBatch a{};
-  const bool aligned = reinterpret_cast<uintptr_t>(logits) % (4 * size) == 0 && (num_tokens == 1 || logits_stride % 4 == 0);
-  a.r = make_rule(*router, num_experts, top_k, router->bias, aligned);
-  a.logits = logits; a.stride = logits_stride; a.T = num_tokens; a.idx = topk_idx; a.w = topk_w;
+  const bool aligned = logits % (4 * size) == 0 && (g.num_tokens == 1 || stride % 4 == 0);
+  a.r = make_rule(*router, g.num_experts, g.top_k, router->bias, aligned);
+  a.logits = g.logits; a.stride = stride; a.T = g.num_tokens; a.idx = g.topk_idx; a.w = g.topk_w;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = size == 4 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s);
   if (e != cudaSuccess) return set_error(FT_ERR_CUDA, "route launch: %s", cudaGetErrorString(e));

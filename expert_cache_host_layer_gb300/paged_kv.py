@@ -26,6 +26,7 @@ which also gives the layout and the sequences' description).
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -41,6 +42,7 @@ _append, _attend, _read = _lib.ft_kv_append, _lib.ft_kv_attend, _lib.ft_kv_read
 _append_rotary = _lib.ft_kv_append_rotary
 _BF16 = torch.bfloat16
 _NO_QUERIES = (0, 0, 0, 0, 0, 0)
+_append_args = struct.Struct("@PqqPqqPqqPqqi0q").pack  # ft_append_args
 _workspaces: dict = {}  # (device index, stream) -> uint8 tensor
 _outgrown: list = []    # the smaller ones before them: three of a stream at most (sizes go by head_dim and the kernels)
 _captured: dict = {}    # (device index, stream) -> (number, uint8 tensor) of the last capture that the stream was part of
@@ -135,7 +137,7 @@ class KVPages:
             if q is not None:
                 heads = q.shape[1] if q.dim() == 3 else 0
                 queries = (*self._rows(batch, q, heads, "q"), *self._rows(batch, q_out, heads, "q_out"))
-            self._call(_append_rotary, self.address, batch.address, rotary.address, *rows, heads, *queries,
+            self._call(_append_rotary, self.address, batch.address, rotary.address, _append_args(*rows, *queries, heads),
                        self._stream(stream))
         if stream is not None:
             self._record(stream, batch, k, v, q, q_out, None if rotary is None else rotary.turns)

@@ -14,12 +14,14 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
 from . import _check, ft_rotary, library
 
 _rotate = library().ft_rotate
+_pack = struct.Struct("@PPqqPqqiii0q").pack  # ft_rotate_args
 _device = getattr(torch._C, "_cuda_getDevice", None)  # torch.cuda.current_device, once CUDA is initialised
 
 
@@ -99,12 +101,12 @@ class Rotary:
         if (x1 != 1 or o1 != 1) and x.numel():
             raise ValueError("rows are contiguous")
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
-        args = (self.address, T, positions.data_ptr(), heads, dim, x.data_ptr(), xt, xh, out.data_ptr(), ot, oh, s)
+        args = _pack(positions.data_ptr(), x.data_ptr(), xt, xh, out.data_ptr(), ot, oh, T, heads, dim)
         if _device() == index:
-            st = _rotate(*args)
+            st = _rotate(self.address, args, s)
         else:
             with torch.cuda.device(index):
-                st = _rotate(*args)
+                st = _rotate(self.address, args, s)
         if st:
             _check(st, "ft_rotate")
         if stream is not None:

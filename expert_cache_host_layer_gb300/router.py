@@ -12,12 +12,14 @@ not, times ``scale`` (include/ft.h, ft_router, has all of it).
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
 from . import FT_BF16, FT_F32, FT_SCORE_SIGMOID, FT_SCORE_SOFTMAX, _check, ft_router, library
 
 _route = library().ft_route
+_pack = struct.Struct("@PqPPiiii0q").pack  # ft_route_args
 _SCORES = {"softmax": FT_SCORE_SOFTMAX, "sigmoid": FT_SCORE_SIGMOID}
 _DTYPES = {torch.float32: FT_F32, torch.bfloat16: FT_BF16}
 _device = getattr(torch._C, "_cuda_getDevice", None)  # torch.cuda.current_device, once CUDA is initialised
@@ -64,13 +66,12 @@ class Router:
         if one != 1 and self.num_experts > 1 and T:
             raise ValueError("rows are contiguous")
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
-        args = (self.address, self.num_experts, self.top_k, T, logits.data_ptr(), stride, dt, topk_idx.data_ptr(),
-                topk_w.data_ptr(), s)
+        args = _pack(logits.data_ptr(), stride, topk_idx.data_ptr(), topk_w.data_ptr(), dt, T, self.num_experts, self.top_k)
         if _device() == index:
-            st = _route(*args)
+            st = _route(self.address, args, s)
         else:
             with torch.cuda.device(index):
-                st = _route(*args)
+                st = _route(self.address, args, s)
         if st:
             _check(st, "ft_route")
         if stream is not None:

@@ -614,9 +614,22 @@ typedef struct ft_norm {
  * scale too.)  The sum of squares is fp32: magnitudes beyond some 2^57 overflow
  * it.  A NaN in r makes its row NaN; an infinity makes its own value (of codes: its
  * group) NaN and the rest of the row 0. */
-ft_status ft_add_norm(const ft_norm* norm, int64_t num_rows, const void* x, int64_t x_stride, int32_t x_dtype,
-                      const void* delta, int64_t delta_stride, int32_t delta_dtype, void* total, int64_t total_stride,
-                      void* out, int64_t out_stride, int32_t out_dtype, float* scales, void* stream);
+typedef struct ft_norm_args {
+  int64_t num_rows;
+  const void* x;
+  int64_t x_stride;
+  const void* delta;
+  int64_t delta_stride;
+  void* total;
+  int64_t total_stride;
+  void* out;
+  int64_t out_stride;
+  float* scales;       /* FT_FP8E4M3 outputs only */
+  int32_t x_dtype;     /* also total's */
+  int32_t delta_dtype;
+  int32_t out_dtype;
+} ft_norm_args;
+ft_status ft_add_norm(const ft_norm* norm, const ft_norm_args* args, void* stream);
 
 /* Rotary positions: pair i of a head's first rot_dim values is turned by the
  * angle of its token, the rest is left as it is:
@@ -638,22 +651,36 @@ typedef struct ft_rotary {
  * device int32 [num_tokens].  head_dim: a multiple of 16, at most 512;
  * num_heads: at most 8192.  out may be x itself (same strides), and does not
  * overlap it otherwise. */
-ft_status ft_rotate(const ft_rotary* rotary, int32_t num_tokens, const int32_t* positions, int32_t num_heads,
-                    int32_t head_dim, const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
-                    int64_t out_token_stride, int64_t out_head_stride, void* stream);
+typedef struct ft_rotate_args {
+  const int32_t* positions;
+  const void* x;
+  int64_t x_token_stride, x_head_stride;
+  void* out;
+  int64_t out_token_stride, out_head_stride;
+  int32_t num_tokens, num_heads, head_dim;
+} ft_rotate_args;
+ft_status ft_rotate(const ft_rotary* rotary, const ft_rotate_args* args, void* stream);
 
-/* ft_kv_append of the batch's keys after their rotation, at their positions in
- * their sequences, and the rotation of its queries: q, q_out device bf16
- * [num_tokens][num_q_heads][head_dim] (num_q_heads 0: none), q_out with positive
- * strides, q itself or apart from every other tensor.  A rotated key is rounded
- * once, into the cache's type.  Queries of rows that belong to no sequence are
- * left as they are in q_out; a row at a negative position is rotated there and
+/* ft_kv_append of the batch's keys k after their rotation, at their positions in
+ * their sequences, and of its values v, and the rotation of its queries: q, q_out
+ * device bf16 [num_tokens][num_q_heads][head_dim] (num_q_heads 0: none), q_out with
+ * positive strides, q itself or apart from every other tensor.  A rotated key is
+ * rounded once, into the cache's type.  Queries of rows that belong to no sequence
+ * are left as they are in q_out; a row at a negative position is rotated there and
  * its key not stored. */
-ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_batch* batch, const ft_rotary* rotary, const void* k,
-                              int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
-                              int64_t v_head_stride, int32_t num_q_heads, const void* q, int64_t q_token_stride,
-                              int64_t q_head_stride, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
-                              void* stream);
+typedef struct ft_append_args {
+  const void* k;
+  int64_t k_token_stride, k_head_stride;
+  const void* v;
+  int64_t v_token_stride, v_head_stride;
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  void* q_out;
+  int64_t q_out_token_stride, q_out_head_stride;
+  int32_t num_q_heads;
+} ft_append_args;
+ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_batch* batch, const ft_rotary* rotary,
+                              const ft_append_args* args, void* stream);
 
 /* Experts and gates of a batch's tokens by a routing rule (ft_router), without
  * a cache: for ft_moe_decode_ffn_static, or any other experts.
@@ -663,8 +690,14 @@ ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_batch* batch
  * num_tokens up to 2^30, num_experts 1..1024, top_k 1..min(num_experts, 32).  A group has the largest
  * power of two of lanes that fits 32 / num_groups, each with 32 experts at most
  * (FT_ERR_UNSUPPORTED beyond; up to 512 experts always fit). */
-ft_status ft_route(const ft_router* router, int32_t num_experts, int32_t top_k, int32_t num_tokens, const void* logits,
-                   int64_t logits_stride, int32_t logits_dtype, int32_t* topk_idx, float* topk_w, void* stream);
+typedef struct ft_route_args {
+  const void* logits;
+  int64_t logits_stride;
+  int32_t* topk_idx;
+  float* topk_w;
+  int32_t logits_dtype, num_tokens, num_experts, top_k;
+} ft_route_args;
+ft_status ft_route(const ft_router* router, const ft_route_args* args, void* stream);
 
 const char* ft_status_str(ft_status s);
 /* Message of the calling thread's last error ("" if none). */

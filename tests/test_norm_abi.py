@@ -11,8 +11,8 @@ ft = pytest.importorskip("expert_cache_host_layer_gb300")
 
 def call(rows=3, x=4096, xs=64, xt=ft.FT_BF16, delta=8192, ds=64, dt=ft.FT_F32, total=12288, ts=64, out=16384, os=64,
          ot=ft.FT_BF16, scales=None, weight=1 << 20, weight_dtype=ft.FT_BF16, hidden=64, eps=1e-6, group=0):
-    ft.ft_add_norm(ft.ft_norm(weight, weight_dtype, hidden, eps, group), rows, x, xs, xt, delta, ds, dt, total, ts, out, os,
-                   ot, scales)
+    ft.ft_add_norm(ft.ft_norm(weight, weight_dtype, hidden, eps, group),
+                   ft.ft_norm_args(rows, x, xs, delta, ds, total, ts, out, os, scales, xt, dt, ot))
 
 
 @pytest.mark.parametrize("kw,status,text", [
@@ -39,8 +39,22 @@ def test_refusals(kw, status, text):
 
 def test_nothing_to_do_is_not_an_error():
     call(rows=0, x=None, out=None, total=None, delta=None)
-    assert ft.library().ft_add_norm(None, 0, None, 0, 0, None, 0, 0, None, 0, None, 0, 0, None, None) == ft.FT_ERR_INVALID_ARG
-    assert ctypes.sizeof(ft.ft_norm) == 24
+    lib, norm, args = ft.library(), ft.ft_norm(None, 0, 64, 1e-6, 0), ft.ft_norm_args()
+    assert lib.ft_add_norm(None, ctypes.addressof(args), None) == ft.FT_ERR_INVALID_ARG
+    assert lib.ft_add_norm(ctypes.addressof(norm), None, None) == ft.FT_ERR_INVALID_ARG
+    assert ctypes.sizeof(ft.ft_norm) == 24 and ctypes.sizeof(ft.ft_norm_args) == 96
+
+
+def test_packed_arguments_are_the_structures():
+    """What the torch wrappers pack, field by field."""
+    from expert_cache_host_layer_gb300 import norm, paged_kv, rotary, router
+    for pack, cls in ((norm._pack, ft.ft_norm_args), (rotary._pack, ft.ft_rotate_args), (paged_kv._append_args, ft.ft_append_args),
+                      (router._pack, ft.ft_route_args)):
+        n = len(cls._fields_)
+        raw = pack(*range(1, n + 1))
+        assert len(raw) == ctypes.sizeof(cls)
+        c = cls.from_buffer_copy(raw)
+        assert [getattr(c, f) for f, _ in cls._fields_] == list(range(1, n + 1))
 
 
 def test_the_torch_wrapper_refuses_wrong_tensors():

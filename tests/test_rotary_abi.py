@@ -18,12 +18,13 @@ def rotary(**kw):
 
 
 def rotate(r=None, T=3, pos=4096, heads=4, dim=64, x=8192, xt=256, xh=64, out=16384, ot=256, oh=64):
-    ft.ft_rotate(r or rotary(), T, pos, heads, dim, x, xt, xh, out, ot, oh)
+    ft.ft_rotate(r or rotary(), ft.ft_rotate_args(pos, x, xt, xh, out, ot, oh, T, heads, dim))
 
 
 def append(p=None, b=None, r=None, k=4096, kt=256, kh=128, v=8192, vt=256, vh=128, heads=8, q=16384, qt=1024, qh=128, out=32768,
            ot=1024, oh=128):
-    ft.ft_kv_append_rotary(p or pages(), b or batch(), r or rotary(), k, kt, kh, v, vt, vh, heads, q, qt, qh, out, ot, oh)
+    ft.ft_kv_append_rotary(p or pages(), b or batch(), r or rotary(),
+                           ft.ft_append_args(k, kt, kh, v, vt, vh, q, qt, qh, out, ot, oh, heads))
 
 
 BAD = [(dict(turns=None), "INVALID_ARG", "turns"), (dict(turns=(1 << 20) + 4), "INVALID_ARG", "turns"),
@@ -66,6 +67,9 @@ def test_nothing_to_do_is_not_an_error():
     rotate(T=0, pos=None, x=None, out=None)
     append(b=batch(num_tokens=0, max_q_len=0), k=None, v=None, q=None, out=None)
     assert ctypes.sizeof(ft.ft_rotary) == 24
+    lib = ft.library()
+    assert lib.ft_rotate(ctypes.addressof(rotary()), None, None) == ft.FT_ERR_INVALID_ARG
+    assert lib.ft_kv_append_rotary(ctypes.addressof(pages()), ctypes.addressof(batch()), None, None, None) == ft.FT_ERR_INVALID_ARG
 
 
 def test_frequencies():
@@ -101,9 +105,9 @@ def test_without_a_gpu_calls_report_it():
     torch = pytest.importorskip("torch")
     if torch.cuda.is_available():
         pytest.skip("a GPU is here")
-    for call in (rotate, append, lambda: ft.ft_add_norm(ft.ft_norm(None, 0, 64, 1e-6, 0), 3, 4096, 64, 0, None, 0, 0, None, 0, 8192,
-                                                        64, 0, None),
-                 lambda: ft.ft_route(ft.ft_router(0, 1, 1, 1, 1, 1.0, None, 0), 64, 4, 3, 4096, 64, 0, 8192, 12288)):
+    for call in (rotate, append, lambda: ft.ft_add_norm(ft.ft_norm(None, 0, 64, 1e-6, 0),
+                                                        ft.ft_norm_args(3, 4096, 64, None, 0, None, 0, 8192, 64)),
+                 lambda: ft.ft_route(ft.ft_router(0, 1, 1, 1, 1, 1.0, None, 0), ft.ft_route_args(4096, 64, 8192, 12288, 0, 3, 64, 4))):
         with pytest.raises(ft.FtError) as e:
             call()
         assert e.value.status == ft.FT_ERR_CUDA

@@ -12,7 +12,8 @@ ft = pytest.importorskip("expert_cache_host_layer_gb300")
 
 def route(E=64, k=4, T=3, logits=4096, stride=64, dtype=ft.FT_F32, idx=8192, w=12288, score=ft.FT_SCORE_SIGMOID, groups=4,
           top_groups=2, group_top=2, scale=1.0, bias=16384):
-    ft.ft_route(ft.ft_router(score, groups, top_groups, group_top, 1, scale, bias, 0), E, k, T, logits, stride, dtype, idx, w)
+    ft.ft_route(ft.ft_router(score, groups, top_groups, group_top, 1, scale, bias, 0),
+                ft.ft_route_args(logits, stride, idx, w, dtype, T, E, k))
 
 
 @pytest.mark.parametrize("kw,status,text", [
@@ -38,7 +39,9 @@ def test_refusals(kw, status, text):
 def test_nothing_to_do_is_not_an_error():
     route(T=0, logits=None, idx=None, w=None)
     lib = ft.library()
-    assert lib.ft_route(None, 8, 2, 0, None, 8, 0, None, None, None) == ft.FT_ERR_INVALID_ARG
+    args = ft.ft_route_args(None, 8, None, None, 0, 0, 8, 2)
+    assert lib.ft_route(None, ctypes.addressof(args), None) == ft.FT_ERR_INVALID_ARG
+    assert lib.ft_route(ctypes.addressof(ft.ft_router(0, 1, 1, 1, 1, 1.0, None, 0)), None, None) == ft.FT_ERR_INVALID_ARG
     assert lib.ft_cache_set_router(None, None) == ft.FT_ERR_INVALID_ARG
     assert ctypes.sizeof(ft.ft_router) == 40
 
