@@ -14,7 +14,7 @@
 //
 // Measured: 16,384 rows of 2048, bf16 plus fp32 to bf16, 48.7 us, 6.9 TB/s (a copy
 // runs at 6.8); 4099 x 1800, fp32 plus bf16 to e4m3 by groups of 128, 14.9 us, 5.5
-// TB/s, of which 2 are a launch's; one row 1.6 us in a graph, 5.8 with the call on
+// TB/s, of which 2 are a launch's; one row 1.6 us in a graph, 4.7 with the call on
 // the host.
 #include "kv_common.h"
 #include "decode_common.h"
