@@ -23,8 +23,8 @@
 //
 // Measured, 256 experts, k = 8, sigmoid scores, a bias, 4 of 8 groups: one token 3.4
 // us in a graph (5.1 with the call on the host), 16,384 tokens 16.6 us (one row a
-// warp 20.7; k rounds of a warp-wide largest 31.4), of which 2 are rows that fp64
-// decides; plain softmax 10.5 us.
+// warp 20.7; with fp64's own exponentials for close values and IEEE quotients for
+// all 31.4), of which 2 are rows that fp64 decides; plain softmax 10.5 us.
 #pragma once
 
 #include <cfloat>

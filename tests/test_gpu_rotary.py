@@ -215,6 +215,16 @@ def test_append(fp8, D, P, H, Hq, q_len, kv_len):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,Hq,D", [(8, 64, 128), (3, 50, 128), (30, 7, 64), (1, 200, 64)])
+def test_more_heads_than_a_block_has_threads_for(fp8, H, Hq, D):
+    """Several passes over a block's tokens; queries, keys and values in one warp."""
+    for interleaved in (False, True):
+        s = Step([40, 1, 9], [64, 200, 9], H=H, Hq=Hq, D=D, P=32, fp8=fp8, pad=3, seed=H)
+        r = Rotary(48, base=1e4, interleaved=interleaved)
+        s.check(r, s.append(r))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_rows_of_no_sequence_negative_positions_and_no_queries(fp8):
     r = Rotary(64)
     s = Step([3, 4], [10, 2], fp8=fp8, pad=5)  # the second's first two are at positions -2 and -1
