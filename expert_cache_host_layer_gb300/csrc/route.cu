@@ -11,8 +11,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMostRows = 1 << 30;
-// From here on four rows go to a warp: 16,384 rows 16.6 us against 20.7, 8192 11.5 against 11.4 (plain softmax 6.4 against
-// 8.2), 4096 10.1 against 8.4: below, every row has a warp of its own at once, and its chain is shorter.
+// From here on four rows go to a warp: 16,384 rows 15.9 us against 20.7, 8192 11.1 against 11.4 (plain softmax 6.2 against
+// 8.2), 4096 10.1 against 8.6: below, every row has a warp of its own at once, and its chain is shorter.
 constexpr int kManyRows = 6144;
 
 struct RouteBatch {

@@ -22,9 +22,9 @@
 // that takes no part) are NaN, which no comparison holds for.
 //
 // Measured, 256 experts, k = 8, sigmoid scores, a bias, 4 of 8 groups: one token 3.4
-// us in a graph (5.1 with the call on the host), 16,384 tokens 16.6 us (one row a
+// us in a graph (5.1 with the call on the host), 16,384 tokens 15.9 us (one row a
 // warp 20.7; with fp64's own exponentials for close values and IEEE quotients for
-// all 31.4), of which 2 are rows that fp64 decides; plain softmax 10.5 us.
+// all 31.4), of which 2 are rows that fp64 decides; plain softmax 10.1 us.
 #pragma once
 
 #include <cfloat>
@@ -211,20 +211,22 @@ template <int PL>
 struct Lane {
   static constexpr int V = PL < 4 ? PL : 4;
   float add[PL];
+  uint32_t own;            // bit q: it has value q (known before the bias is: the row's loads need not wait for that)
   int group, sub, expert;  // expert: of value 0
   __device__ __forceinline__ explicit Lane(const Rule& r) {
     const int lane = threadIdx.x & 31;
     group = lane / r.lanes;
     sub = lane & (r.lanes - 1);
     expert = group * r.size + sub * V;
+    own = 0;
 #pragma unroll
-    for (int q = 0; q < PL; ++q) {
-      const bool has = group < r.groups && sub * V + step(r, q) < r.size;
-      add[q] = !has ? NAN : r.bias ? clean(__ldg(&r.bias[expert + step(r, q)])) : 0.0f;
-    }
+    for (int q = 0; q < PL; ++q)
+      if (group < r.groups && sub * V + step(r, q) < r.size) own |= 1u << q;
+#pragma unroll
+    for (int q = 0; q < PL; ++q) add[q] = !has(q) ? NAN : r.bias ? clean(__ldg(&r.bias[expert + step(r, q)])) : 0.0f;
   }
   static __device__ __forceinline__ int step(const Rule& r, int q) { return (q / V) * r.lanes * V + q % V; }
-  __device__ __forceinline__ bool has(int q) const { return add[q] == add[q]; }
+  __device__ __forceinline__ bool has(int q) const { return own >> q & 1u; }
 };
 
 // The row's picks in order: expert and gate of pick j to lane j < k.  `shared`:
