@@ -25,6 +25,7 @@
 // plus the tombstones it passes, instead of a pass over all C slots.
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "ft_internal.h"
 #include "route_rule.h"
@@ -123,6 +124,9 @@ __device__ __forceinline__ void default_picks(const float* row, int E, int k, in
   *gate = ex / sum;
 }
 
+struct NoLane {
+  __device__ explicit NoLane(const rule::Rule&) {}
+};
 template <int PL, bool kRule>  // logits per lane: E <= 32 * PL, or as the rule's layout has it
 __global__ void __launch_bounds__(kThreads) route_classify_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ __align__(16) unsigned char s_rule[];  // of each warp, if kRule
@@ -165,12 +169,13 @@ __global__ void __launch_bounds__(kThreads) route_classify_kernel(const __grid_c
   __syncthreads();
 
   // ---------------- phase 1: top-k + gates, one warp per token -------------
+  const typename std::conditional<kRule, rule::Lane<PL>, NoLane>::type own(a.rule);
   for (int t = blockIdx.x * kWarps + warp; t < T; t += gridDim.x * kWarps) {
     const float* row = a.logits + (long long)t * E;
     int my_i = 0;
     float w = 0.0f;
-    if (kRule) {
-      rule::route_row<PL>(a.rule, rule::Lane<PL>(a.rule), row, s_rule + warp * rule::warp_bytes(E, a.rule.bias != nullptr), &my_i, &w);
+    if constexpr (kRule) {
+      rule::route_row<PL>(a.rule, own, row, s_rule + warp * rule::warp_bytes(E, a.rule.bias != nullptr), &my_i, &w);
     } else {
       default_picks<PL>(row, E, k, &my_i, &w);
     }
