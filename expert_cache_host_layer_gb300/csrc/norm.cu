@@ -231,8 +231,7 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
   while (per_row < kMostThreads && per_row * (many ? 2 : 1) < vecs) per_row *= 2;
   const int each = (vecs + per_row - 1) / per_row;
   const int threads = per_row < 128 && a.rows > 1 ? 128 : per_row;
-  const int64_t blocks = (a.rows + threads / per_row - 1) / (threads / per_row);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int64_t blocks = (a.rows + threads / per_row - 1) / (threads / per_row);  // below 2^31, as rows are
   auto* kernel = each <= 1 ? norm_kernel<X, D, 1> : each <= 2 ? norm_kernel<X, D, 2> : norm_kernel<X, D, 4>;
   return kv::launch_dependent(kernel, dim3((unsigned)blocks), threads, 0, s, a, per_row);
 }
