@@ -1,8 +1,9 @@
 // Numbers as the unevaluated sum of two floats, the second at most half an ulp
 // of the first, and e^x, 1 / x and sigmoids of them, good to 2^-45.  (T. J. Dekker,
 // "A floating-point technique for extending the available precision", 1971;
-// D. E. Knuth's two-sum.)  On this GPU fp64 is so slow that a sigmoid takes 3000
-// cycles; this takes some 500.  Internal to libft.
+// D. E. Knuth's two-sum.)  On this GPU fp64 is slow: a warp's sigmoid takes
+// 1600 cycles with its exponential and quotient, 730 with these and one fp64 sum.
+// Internal to libft.
 #pragma once
 
 #include <cuda_runtime.h>
