@@ -21,7 +21,7 @@
 // whatever rot_dim is.
 //
 // Measured (head_dim 128, 16 query and 4 key heads): 16,384 tokens into the e4m3
-// cache 33.7 us, 5.5 TB/s (with the head worked out for every vector, 42: 260
+// cache 32.9 us, 5.6 TB/s (with the head worked out for every vector, 42: 260
 // instructions a warp and vector instead of 200); 8191 tokens x 24 heads of 96, a
 // third of each turned, 14.3 us, 5.3 TB/s; one token 2.6 us in a graph.  The
 // start (places, sines) is 3 to 4 us of each.
@@ -34,7 +34,7 @@ namespace ft {
 namespace kv {
 namespace {
 
-constexpr int kMostThreads = 384;  // three such blocks an SM: 56 registers a thread (64: 34.6 us instead of 33.7, 48: 39.9)
+constexpr int kMostThreads = 384;  // three such blocks an SM: 56 registers a thread (64: 34.6 us where these took 33.7, 48: 39.9)
 constexpr int kThreads = 256;      // of a block, if its heads leave a choice
 constexpr int kMostTokens = 32;    // of a block
 constexpr int kTrigFloats = 4096;  // of a block: tokens x rot_dim
@@ -200,10 +200,13 @@ ft_status launch(RotArgs& a, const char* name, int cache, cudaStream_t s) {
   const int most = std::min(kMostTokens, kTrigFloats / a.r.rot_dim);
   a.step = std::min({std::max(1, kThreads / wide), a.rows, most});
   const int threads = (wide * a.step + 31) / 32 * 32;
-  // one wave, while that leaves a block no more tokens than it has room for
+  // One wave of blocks while they go through less than 18 tokens in turn (8191 x 24 heads in one 14.3 us, in two 14.5; 16,384
+  // x 3 heads in one 10.1, in three 12.1), then as many waves as leave them nine: other blocks' loads fill a block's start
+  // (16,384 x 24 heads in one 33.7 us, in two 32.9, four 33.2).
   const int wave = 3 * kMostThreads / threads * sm_count();
   if (wave == 0) return set_error(FT_ERR_CUDA, "%s: no CUDA device", name);
-  a.per = std::min(most, (int)(((long long)a.rows + wave - 1) / wave));
+  auto tokens_each = [&](long long blocks) { return (int)((a.rows + blocks - 1) / blocks); };
+  a.per = std::min(most, tokens_each((long long)wave * std::max(1, tokens_each(wave) / a.step / 9)));
   if (a.per > a.step) a.per = std::min(most, (a.per + a.step - 1) / a.step * a.step);
   const dim3 grid((unsigned)(((long long)a.rows + a.per - 1) / a.per));
   const bool pairs = a.r.interleaved != 0;
