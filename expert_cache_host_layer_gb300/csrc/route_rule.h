@@ -407,6 +407,7 @@ __device__ __forceinline__ void route_row(const Rule& r, const Lane<PL>& own, co
     if (scored) {
       exact_ranks(r, row, top, experts, keys, n, picks);
     } else {
+      __syncwarp();  // equal logits have all been stored to one place: their own ones come after that
       for (int i = lane; i < n; i += 32) {
         const int rank = rank_of(values[i], experts[i], values, experts, n);
         if (rank < r.k) picks[rank] = experts[i];
