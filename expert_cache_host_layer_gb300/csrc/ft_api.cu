@@ -819,16 +819,24 @@ ft_status ft_route_classify(ft_cache* c, int32_t layer, const float* logits, int
 
 ft_status ft_cache_set_router(ft_cache* c, const ft_router* router) {
   if (!c) return fail(FT_ERR_INVALID_ARG, "null cache");
-  if (!router) {
-    c->by_rule = false;
-    return FT_OK;
+  if (router) {
+    const ft_status st = check_router(router, c->E, c->k);
+    if (st != FT_OK) return st;
+    if (router->bias && (router->bias_stride < 0 || (router->bias_stride > 0 && router->bias_stride < c->E)))
+      return fail(FT_ERR_INVALID_ARG, "bias_stride=%lld is not 0 or %d and more", (long long)router->bias_stride, c->E);
   }
-  const ft_status st = check_router(router, c->E, c->k);
-  if (st != FT_OK) return st;
-  if (router->bias && (router->bias_stride < 0 || (router->bias_stride > 0 && router->bias_stride < c->E)))
-    return fail(FT_ERR_INVALID_ARG, "bias_stride=%lld is not 0 or %d and more", (long long)router->bias_stride, c->E);
-  c->router = *router;
-  c->by_rule = true;
+  if (c->by_rule && c->router.bias) {
+    // The bias until now may still be read on the route stream: what the caller enqueues from here on, which may free or
+    // overwrite it, comes after that.  (A capture that the caller makes has no such reader outside of itself.)
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    CU(cudaStreamIsCapturing(c->compute, &capture));
+    if (capture == cudaStreamCaptureStatusNone) {
+      CU(cudaEventRecord(c->route_join, c->route));
+      CU(cudaStreamWaitEvent(c->compute, c->route_join, 0));
+    }
+  }
+  c->by_rule = router != nullptr;
+  if (router) c->router = *router;
   return FT_OK;
 }
 

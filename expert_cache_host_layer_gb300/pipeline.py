@@ -99,6 +99,9 @@ class ExpertCache:
                                                               router.bias.dim() == 2 and router.bias.shape[0] != self.L):
             raise ValueError("the router's bias is a tensor of the cache's device, [E] or [L, E]")
         ft_cache_set_router(self.handle, None if router is None else router.c)
+        if self.router is not None and self.router.bias is not None:
+            # (its routing is done when the cache's stream gets past here, and its memory may be given to others after that)
+            self.router.bias.record_stream(self.stream)
         self.router = router  # keeps the bias
 
     # ---- thin wrappers ---------------------------------------------------
