@@ -6,11 +6,15 @@
 //   groups: by their best v, or the sum of their best two; the top_groups best take part
 //   the k best v, ties to the lowest expert;  w = s, renormalised over the picks or not, times scale
 //
-// The choice is that of exact arithmetic.  Without a bias v orders as the logit
-// does, and logits are compared as they are.  With one, fp32 values of v are
-// good to a known error: a pick that has another candidate within twice that
-// (or a group that takes part, one that does not within its own bound) sends the
-// row to a comparison in fp64, for which few rows in a thousand have cause.
+// Without a bias v orders as the logit does, and logits are compared as they are.
+// With one (and where a group counts by two) fp32 values of v are good to a known
+// error: a pick that has another candidate within twice that (or a group that
+// takes part, one that does not within its own bound) sends the row to a
+// comparison in fp64, for which few rows in a thousand have cause.  There a score
+// is good to 2^-45 of itself, and its sum with the bias to fp64; values that are
+// the same even so are in the order of their logits, which is right where the
+// biases are equal (scores next to 1, or lost beside a large bias).  Sums of two
+// that are the same are groups in the order of their numbers.
 //
 // What bounds it: a row's E logits are read once, but k selections over them
 // are instructions (issue slots on a chunk, their latency for one token).  So
@@ -115,7 +119,7 @@ struct Exact {
       s = fabsf(l) <= 60.0f ? wide(sigmoid_pair(l)) : 1.0 / (1.0 + exp(-(double)l));
     }
     if (!bias) return s;
-    const double v = s + (double)__ldg(&bias[e]);
+    const double v = __dadd_rn(s, (double)__ldg(&bias[e]));  // (not contracted: the same number wherever it is formed)
     return v != v ? -INFINITY : fmin(v, (double)FLT_MAX);
   }
 };
@@ -162,11 +166,28 @@ __device__ __noinline__ bool exact_groups(const Rule r, const T* row, float top,
     a = fmax(a, oa);
   }
   const long long mine = order(r.group_top == 2 ? a + b : a);
-  int above = 0;
+  int above = 0, same = 0;  // same: of the groups before this one
   for (int g = 0; g < r.groups; ++g) {
     const long long of = __shfl_sync(0xffffffffu, mine, g * r.lanes);
-    above += of > mine || (of == mine && g < group);
+    above += of > mine;
+    same += of == mine && g < group;
   }
+  if (!logits && r.group_top == 1 && __any_sync(0xffffffffu, same && a > -INFINITY)) {  // by their best's logit, largest first
+    float by = -INFINITY;
+    for (int i = group < r.groups ? sub : r.size; i < r.size; i += r.lanes) {
+      const float l = logit(row, group * r.size + i);
+      if (l > by && x.value(l, group * r.size + i) == a) by = l;
+    }
+    for (int o = r.lanes / 2; o > 0; o >>= 1) by = fmaxf(by, __shfl_xor_sync(0xffffffffu, by, o));
+    if (a == -INFINITY) by = 0.0f;  // (nothing to go by)
+    same = 0;
+    for (int g = 0; g < r.groups; ++g) {
+      const long long of = __shfl_sync(0xffffffffu, mine, g * r.lanes);
+      const float key = __shfl_sync(0xffffffffu, by, g * r.lanes);
+      same += of == mine && (key > by || (key == by && g < group));
+    }
+  }
+  above += same;
   return group < r.groups && above < r.top_groups;
 }
 // The list's ranks in fp64; keys: room for n of them.
@@ -179,8 +200,20 @@ __device__ __noinline__ void exact_ranks(const Rule r, const T* row, float top, 
   for (int i = lane; i < n; i += 32) {
     const long long v = keys[i];
     const int e = experts[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += keys[j] > v || (keys[j] == v && experts[j] < e);
+    int rank = 0, same = 0;
+    for (int j = 0; j < n; ++j) {
+      rank += keys[j] > v;
+      same += keys[j] == v;
+    }
+    if (same > 1 && rank < r.k) {  // others than itself: by their logits, largest first (without a value by their numbers)
+      const bool none = v == order(-(double)INFINITY);
+      const float l = logit(row, e);
+      for (int j = 0; j < n; ++j) {
+        if (keys[j] != v) continue;
+        const float of = none ? l : logit(row, experts[j]);
+        rank += of > l || (of == l && experts[j] < e);
+      }
+    }
     if (rank < r.k) picks[rank] = e;
   }
   __syncwarp();

@@ -245,10 +245,13 @@ ft_status ft_route_classify(ft_cache* cache, int32_t layer, const float* logits,
  *     of whose two largest (group_top 2), are largest
  *   the top_k largest v, in that order;  gates s, divided by their sum over the
  *     picks if renormalise, times scale
- * Equal values go to the lower group and expert.  The choice is that of exact
- * arithmetic: logits are compared where their order is that of v, and values
- * too close for fp32 are compared in fp64.  A NaN logit counts as -inf (and so
- * does a v of NaN), an infinite one as the largest number; picks without any
+ * Equal values go to the lower group and expert.  Without a bias logits are
+ * compared, whose order is that of s.  With one, and for sums of two, values too
+ * close for fp32 are compared in fp64, with scores good to 2^-45 of themselves;
+ * values of v that are the same there (scores next to 1, or beside a large bias)
+ * go to the larger logit, which is their exact order where the biases are equal,
+ * and the same sums of two to the lower group.  A NaN logit counts as -inf (and
+ * so does a v of NaN), an infinite one as the largest number; picks without any
  * score have gate 0. */
 typedef enum ft_score { FT_SCORE_SOFTMAX = 0, FT_SCORE_SIGMOID = 1 } ft_score;
 typedef struct ft_router {

@@ -55,7 +55,8 @@ def route(logits: np.ndarray, k: int):
 class Rule:
     """A routing rule: scores s = softmax or sigmoid of the logits, the choice by v = s + bias (with groups: among the
     top_groups groups of consecutive experts whose best v, or sum of the best two, is largest), gates s of the picks,
-    renormalised over them or not, times scale.  Without a bias v has the logits' order.  Equal values go to the lower
+    renormalised over them or not, times scale.  Without a bias v has the logits' order.  Values that fp64 cannot tell
+    apart have the order of their logits (that of exact arithmetic where the biases are equal), equal ones go to the lower
     index; a NaN logit or v is -inf, an infinite one the largest fp32 number; without any score the gates are 0."""
     score: str = "softmax"
     bias: np.ndarray | None = None
@@ -82,19 +83,23 @@ def route_by(rule: Rule, logits: np.ndarray, k: int):
             e = np.exp(x - np.maximum(x.max(axis=1, keepdims=True), -1e300))
             s = np.divide(e, e.sum(axis=1, keepdims=True), out=np.zeros_like(e), where=e.sum(axis=1, keepdims=True) > 0)
     v = x if rule.bias is None else clean(s + np.asarray(rule.bias, dtype=np.float64))
+    tie = np.where(v > -np.inf, x, 0.0)
     if rule.groups > 1 and rule.top_groups < rule.groups:
         of = (v if rule.bias is not None or rule.group_top == 1 else s).reshape(T, rule.groups, -1)
         best = np.sort(of, axis=2)[:, :, ::-1][:, :, :rule.group_top].sum(axis=2)
-        take = selection_order(best)[:, :rule.top_groups]
+        by = np.zeros_like(best)  # a group's best expert's logit
+        if rule.group_top == 1:
+            by = np.where(of == best[:, :, None], tie.reshape(of.shape), -np.inf).max(axis=2)
+        take = np.array([np.lexsort((np.arange(rule.groups), -by[t], -best[t])) for t in range(T)]).reshape(T, rule.groups)[:, :rule.top_groups]
         part = np.zeros((T, rule.groups), dtype=bool)
         np.put_along_axis(part, take, True, axis=1)
         part = np.repeat(part, E // rule.groups, axis=1)
     else:
         part = np.ones((T, E), dtype=bool)
     idx = np.empty((T, k), dtype=np.int32)
-    for t in range(T):  # those that take part, by (v descending, index ascending)
+    for t in range(T):  # those that take part, by (v descending, logit descending, index ascending)
         at = np.flatnonzero(part[t])
-        idx[t] = at[np.lexsort((at, -v[t, at]))[:k]]
+        idx[t] = at[np.lexsort((at, -tie[t, at], -v[t, at]))[:k]]
     w = np.take_along_axis(s, idx.astype(np.int64), axis=1)
     if rule.renormalise:
         l = np.take_along_axis(x, idx.astype(np.int64), axis=1)
