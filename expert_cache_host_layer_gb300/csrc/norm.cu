@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kMostThreads = 512;  // of a row: 128 registers a thread
 constexpr int kMostHidden = kMostThreads * 4 * 8;
+constexpr float kLeastMean = 0x1p-126f;  // the least mean r^2 + eps: its inverse root is a finite number, and zeros times that are zeros
 constexpr float kLeast = 0x1p-100f;  // the least max |r w| that a scale is made of: 448 / it is a finite number
 
 struct NormArgs {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
     sum = dec::warp_sum(lane < warps ? s_sum[first + lane] : 0.0f);
     if (by_row) top = warp_top(lane < warps ? s_top[first + lane] : 0.0f);
   }
-  const float norm = __frsqrt_rn(sum / (float)a.hidden + a.eps);
+  const float norm = __frsqrt_rn(max_abs(kLeastMean, sum / (float)a.hidden + a.eps));
   if (a.out_dtype != FT_FP8E4M3) {
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {

@@ -601,7 +601,7 @@ typedef struct ft_norm {
   const void* weight;   /* device [hidden], 16-byte aligned; NULL: ones */
   int32_t weight_dtype; /* FT_F32 or FT_BF16 */
   int32_t hidden;       /* a multiple of 8, 8..16384 */
-  float eps;
+  float eps;            /* 0 or more, finite */
   int32_t group;        /* e4m3 outputs: channels to a scale: 32, 64, 128, or 0: the whole row */
 } ft_norm;
 
@@ -618,7 +618,9 @@ typedef struct ft_norm {
  *   scale = max|y| / 448 over the group's channels,  code = y / scale to the nearest e4m3 value
  * (max|r * weight| below 2^-100 counts as that, so that a group of zeros has a
  * scale too.)  The sum of squares is fp32: magnitudes beyond some 2^57 overflow
- * it.  A NaN in r makes its row NaN; an infinity makes its own value (of codes: its
+ * it, and mean(r^2) + eps below 2^-126 counts as that, so that with an eps of 0 a
+ * row of zeros is zeros and one of magnitudes below 2^-63 is r * weight * 2^63.
+ * A NaN in r makes its row NaN; an infinity makes its own value (of codes: its
  * group) NaN and the rest of the row 0. */
 typedef struct ft_norm_args {
   int64_t num_rows;
