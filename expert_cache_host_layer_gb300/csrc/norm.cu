@@ -246,6 +246,13 @@ ft_status check_matrix(const char* name, const void* p, int64_t stride, int64_t 
   return FT_OK;
 }
 
+// An output in an input's place: every element has to be where the thread that writes it has read it.
+ft_status check_place(const char* name, const void* p, int dtype, int64_t stride, const char* input, const void* q, int of_dtype,
+                      int64_t of_stride) {
+  if (p != q || (dtype == of_dtype && stride == of_stride)) return FT_OK;
+  return set_error(FT_ERR_INVALID_ARG, "%s may be %s itself only with its type and row stride", name, input);
+}
+
 }  // namespace
 }  // namespace ft
 
@@ -282,7 +289,12 @@ extern "C" ft_status ft_add_norm(const ft_norm* norm, const ft_norm_args* args, 
   if (st == FT_OK && a.delta) st = check_matrix("delta", a.delta, a.ds, a.rows, H);
   if (st == FT_OK && a.total) st = check_matrix("total", a.total, a.ts, a.rows, H);
   if (st == FT_OK) st = check_matrix("out", a.out, a.os, a.rows, H);
+  if (st == FT_OK && a.total) st = check_place("total", a.total, g.x_dtype, a.ts, "x", a.x, g.x_dtype, a.xs);
+  if (st == FT_OK && a.total) st = check_place("total", a.total, g.x_dtype, a.ts, "delta", a.delta, g.delta_dtype, a.ds);
+  if (st == FT_OK) st = check_place("out", a.out, g.out_dtype, a.os, "x", a.x, g.x_dtype, a.xs);
+  if (st == FT_OK && a.delta) st = check_place("out", a.out, g.out_dtype, a.os, "delta", a.delta, g.delta_dtype, a.ds);
   if (st != FT_OK) return st;
+  if (a.total == a.out) return set_error(FT_ERR_INVALID_ARG, "total and out are one matrix");
   if (fp8 && (!a.scales || (reinterpret_cast<uintptr_t>(a.scales) & 3)))
     return set_error(FT_ERR_INVALID_ARG, "an e4m3 output needs scales, 4-byte aligned");
   a.hidden = H; a.w_dtype = norm->weight_dtype; a.out_dtype = g.out_dtype; a.eps = norm->eps;

@@ -611,7 +611,8 @@ typedef struct ft_norm {
  * the given number of elements apart (of a single row it is not used): 16-byte
  * aligned, strides multiples of 8.  x and delta: FT_F32 or FT_BF16, each its
  * own; delta may be NULL (r = x).  total has x's type and may be NULL, or x or
- * delta itself; out may be x or delta itself where total is not.  No other
+ * delta itself; out may be x or delta itself where total is not; either then has
+ * that one's type and stride.  No other
  * overlap.  r is an fp32 sum, which total rounds and y does not.
  * out: FT_F32, FT_BF16 or FT_FP8E4M3.  For the last y is given as codes and
  * fp32 scales, device [num_rows][ceil(hidden / group)] contiguous:
