@@ -192,6 +192,16 @@ ft_status check_rotary(const ft_rotary* r, int head_dim) {
   return FT_OK;
 }
 
+// An output: with positive strides, and where it is its input, with that one's (each value is written where it was read).
+ft_status check_out(const char* name, const RotArgs& a) {
+  const ft_status st = check_rows(name, a.out, a.ots, a.ohs);
+  if (st != FT_OK) return st;
+  if (a.ots <= 0 || a.ohs <= 0) return set_error(FT_ERR_INVALID_ARG, "%s's strides must be positive", name);
+  if (a.out == a.x[0] && (a.ots != a.ts[0] || a.ohs != a.hs[0]))
+    return set_error(FT_ERR_INVALID_ARG, "%s may be its input itself only with its strides", name);
+  return FT_OK;
+}
+
 ft_status launch(RotArgs& a, const char* name, int cache, cudaStream_t s) {
   a.heads = a.Hq + (cache == kNone ? 0 : 2 * a.p.num_kv_heads);
   const int fit = kMostThreads / a.units, passes = (a.heads + fit - 1) / fit;
@@ -244,8 +254,7 @@ extern "C" ft_status ft_rotate(const ft_rotary* rotary, const ft_rotate_args* ar
   if (g.num_tokens == 1) a.ts[0] = a.ots = g.head_dim;  // of single entries: not used
   if (g.num_heads == 1) a.hs[0] = a.ohs = g.head_dim;
   if ((st = check_rows("x", a.x[0], a.ts[0], a.hs[0])) != FT_OK) return st;
-  if ((st = check_rows("out", a.out, a.ots, a.ohs)) != FT_OK) return st;
-  if (a.ots <= 0 || a.ohs <= 0) return set_error(FT_ERR_INVALID_ARG, "out's strides must be positive");
+  if ((st = check_out("out", a)) != FT_OK) return st;
   a.rows = g.num_tokens; a.Hq = g.num_heads; a.units = g.head_dim / 16;
   return launch(a, "rotate", kNone, static_cast<cudaStream_t>(stream));
 }
@@ -275,8 +284,8 @@ extern "C" ft_status ft_kv_append_rotary(const ft_kv_pages* pages, const ft_kv_b
   if ((st = check_rows("v", a.x[2], a.ts[2], a.hs[2])) != FT_OK) return st;
   if (g.num_q_heads > 0) {
     if ((st = check_rows("q", a.x[0], a.ts[0], a.hs[0])) != FT_OK) return st;
-    if ((st = check_rows("q_out", a.out, a.ots, a.ohs)) != FT_OK) return st;
-    if (a.ots <= 0 || a.ohs <= 0) return set_error(FT_ERR_INVALID_ARG, "q_out's strides must be positive");
+    if ((st = check_out("q_out", a)) != FT_OK) return st;
+    if (a.out == a.x[1] || a.out == a.x[2]) return set_error(FT_ERR_INVALID_ARG, "q_out is k or v");
   }
   a.rows = batch->num_tokens; a.Hq = g.num_q_heads; a.units = D / 16;
   if ((st = status_word(&a.status)) != FT_OK) return st;

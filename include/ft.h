@@ -673,7 +673,7 @@ ft_status ft_rotate(const ft_rotary* rotary, const ft_rotate_args* args, void* s
 /* ft_kv_append of the batch's keys k after their rotation, at their positions in
  * their sequences, and of its values v, and the rotation of its queries: q, q_out
  * device bf16 [num_tokens][num_q_heads][head_dim] (num_q_heads 0: none), q_out with
- * positive strides, q itself or apart from every other tensor.  A rotated key is
+ * positive strides, q itself (same strides) or apart from every other tensor.  A rotated key is
  * rounded once, into the cache's type.  Queries of rows that belong to no sequence
  * are left as they are in q_out; a row at a negative position is rotated there and
  * its key not stored. */
