@@ -30,12 +30,14 @@ _device = getattr(torch._C, "_cuda_getDevice", None)  # torch.cuda.current_devic
 
 
 class RMSNorm:
-    """weight: a contiguous bf16 or float32 [hidden] tensor, or None for ones."""
+    """weight: a contiguous bf16 or float32 [hidden] tensor, or None for ones.  The memory that it has now is kept, and read by
+    the calls: values written in place count, ``weight.data = other`` does not reach the norm."""
 
     def __init__(self, hidden: int, weight: torch.Tensor | None = None, eps: float = 1e-6, group: int = 0):
         if weight is not None:
             if weight.shape != (hidden,) or weight.dtype not in _DTYPES or not weight.is_contiguous() or not weight.is_cuda:
                 raise ValueError("weight is a contiguous bf16 or float32 [hidden] tensor in a GPU's memory")
+            weight = weight.detach()  # (the same memory, whatever becomes of the caller's tensor)
         self.hidden, self.weight, self.eps, self.group = hidden, weight, float(eps), group
         self.num_scales = -(-hidden // group) if group else 1
         self.index = None if weight is None else weight.get_device()

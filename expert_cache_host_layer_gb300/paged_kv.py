@@ -58,7 +58,8 @@ def _need(ok, text, *args):
 
 class KVBatch:
     """One step's sequences: int32 device tensors q_start [S + 1], kv_len [S]
-    and block_table [S, pages], and the host's num_tokens and max_q_len."""
+    and block_table [S, pages], and the host's num_tokens and max_q_len.  Later
+    values are written into the tensors; ``kv_len.data = other`` is not one."""
 
     def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor, num_tokens: int,
                  max_q_len: int):
@@ -84,7 +85,8 @@ class KVBatch:
 class KVPages:
     """One layer's cache: k, v [pages, kv_heads, page_tokens, head_dim], bf16 or
     float8_e4m3fn; for the latter k_scale, v_scale [pages, kv_heads,
-    page_tokens] uint8, the exponent bytes of the scales."""
+    page_tokens] uint8, the exponent bytes of the scales.  The memory that the
+    tensors have now is the cache (``k.data = other`` does not reach it)."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
                  v_scale: torch.Tensor | None = None):
@@ -98,7 +100,8 @@ class KVPages:
                 _need(t.dtype == torch.uint8 and t.shape == k.shape[:3] and t.is_contiguous() and t.device == k.device,
                       "scales are contiguous uint8 [pages, kv_heads, page_tokens]")
         _need(k.is_cuda and v.device == k.device, "the pages are in one GPU's memory")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        # (the same memory, whatever becomes of the caller's tensors)
+        self.k, self.v, self.k_scale, self.v_scale = (None if t is None else t.detach() for t in (k, v, k_scale, v_scale))
         self.device = k.device
         self.num_pages, self.num_kv_heads, self.page_tokens, self.head_dim = k.shape
         self.scale = self.head_dim ** -0.5  # of the scores, unless a call gives its own

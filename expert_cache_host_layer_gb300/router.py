@@ -26,8 +26,9 @@ _device = getattr(torch._C, "_cuda_getDevice", None)  # torch.cuda.current_devic
 
 
 class Router:
-    """bias: a contiguous float32 [experts] tensor, or [layers, experts] for a cache whose layers have their own; it is read
-    by the calls and may change between them."""
+    """bias: a contiguous float32 [experts] tensor, or [layers, experts] for a cache whose layers have their own.  The memory
+    that it has now is kept, and read by the calls: values written in place between them count, ``bias.data = other`` does
+    not reach the rule."""
 
     def __init__(self, num_experts: int, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None, groups: int = 1,
                  top_groups: int = 1, group_top: int = 1, renormalise: bool = True, scale: float = 1.0):
@@ -37,6 +38,7 @@ class Router:
             if (bias.dtype != torch.float32 or bias.dim() not in (1, 2) or bias.shape[-1] != num_experts or
                     not bias.is_contiguous() or not bias.is_cuda):
                 raise ValueError("bias is a contiguous float32 [experts] or [layers, experts] tensor in a GPU's memory")
+            bias = bias.detach()  # (the same memory, whatever becomes of the caller's tensor)
         self.num_experts, self.top_k, self.bias = num_experts, top_k, bias
         self.index = None if bias is None else bias.get_device()
         self.c = ft_router(_SCORES[score], groups, top_groups, group_top, int(bool(renormalise)), float(scale),
