@@ -24,7 +24,8 @@
 // cache 32.9 us, 5.6 TB/s (with the head worked out for every vector, 42: 260
 // instructions a warp and vector instead of 200); 8191 tokens x 24 heads of 96, a
 // third of each turned, 14.3 us, 5.3 TB/s; one token 2.6 us in a graph.  The
-// start (places, sines) is 3 to 4 us of each.
+// start (places, sines) is 3 to 4 us of each, and most of a chunk of few heads:
+// 16,384 tokens x 1, 3 and 4 heads 5.7, 7.7 and 9.9 us, their bytes 1.2, 3.7 and 5.0.
 #include <algorithm>
 
 #include "decode_common.h"
@@ -211,8 +212,8 @@ ft_status launch(RotArgs& a, const char* name, int cache, cudaStream_t s) {
   a.step = std::min({std::max(1, kThreads / wide), a.rows, most});
   const int threads = (wide * a.step + 31) / 32 * 32;
   // One wave of blocks while they go through less than 18 tokens in turn (8191 x 24 heads in one 14.3 us, in two 14.5; 16,384
-  // x 3 heads in one 10.1, in three 12.1), then as many waves as leave them nine: other blocks' loads fill a block's start
-  // (16,384 x 24 heads in one 33.7 us, in two 32.9, four 33.2).
+  // x 3 heads in one 7.7, in two 7.9, three 9.0), then as many waves as leave them nine: other blocks' loads fill a block's
+  // start (16,384 x 24 heads in one 33.6 us, in two 32.9, three 32.8, four 33.2).
   const int wave = 3 * kMostThreads / threads * sm_count();
   if (wave == 0) return set_error(FT_ERR_CUDA, "%s: no CUDA device", name);
   auto tokens_each = [&](long long blocks) { return (int)((a.rows + blocks - 1) / blocks); };

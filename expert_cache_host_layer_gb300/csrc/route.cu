@@ -11,8 +11,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMostRows = 1 << 30;
-// From here on four rows go to a warp: 16,384 rows 15.9 us against 20.7, 8192 11.1 against 11.4 (plain softmax 6.2 against
-// 8.2), 4096 10.1 against 8.6: below, every row has a warp of its own at once, and its chain is shorter.
+// From here on four rows go to a warp: 16,384 rows of 256 experts 15.9 us against 20.7, 8192 11.1 against 11.4 (plain softmax
+// 6.2 against 8.2), 4096 10.1 against 8.5: below, every row has a warp of its own at once, and its chain is shorter.  (At the
+// border itself, one row a warp against four: 256 experts 10.7 and 10.8 us, 128 6.5 and 6.2, 64 4.8 and 4.1.)
 constexpr int kManyRows = 6144;
 
 struct RouteBatch {

@@ -17,7 +17,8 @@
 // that are the same are groups in the order of their numbers.
 //
 // What bounds it: a row's E logits are read once, but k selections over them
-// are instructions (issue slots on a chunk, their latency for one token).  So
+// are a chain of dependent instructions, whose latency shows for one token and
+// also on a chunk (16 warps an SM leave half of the issue slots empty).  So
 // the warp does not select k times over E: its lanes' k-th largest maximum,
 // from k warp-wide integer maxima (redux) over one value a lane, bounds the
 // k-th largest value from below; the few values above that bound (9 of 256 for
@@ -453,6 +454,7 @@ __device__ __forceinline__ void route_row(const Rule& r, const Lane<PL>& own, co
   const int e = lane < r.k ? picks[lane] : 0;
   const float l = lane < r.k ? logit(row, e) : -INFINITY;
   float w = 0.0f;
+  // (__fdividef: 2 ulp, as the exponential; 0 for a denominator above 2^126.)
   if (!r.renormalise) {
     w = r.softmax ? expf(l - top) * inv_z : __fdividef(1.0f, 1.0f + expf(-l));
   } else {

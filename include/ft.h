@@ -238,7 +238,8 @@ ft_status ft_route_classify(ft_cache* cache, int32_t layer, const float* logits,
 
 /* How a layer's tokens choose their experts.  The default of a cache, and what
  * ft_route does with {FT_SCORE_SOFTMAX, 1, 1, 1, 1, 1.0f, NULL, 0}: the top_k
- * largest logits, gates their softmax.
+ * largest logits, gates their softmax.  (With an infinite logit among the picks
+ * the default's gates are NaN, a rule's are not.)
  *   s = softmax(logits) or 1 / (1 + e^-logit);  v = s + bias for the choice alone
  *   num_groups > 1: the experts of a group are consecutive, and only those of
  *     the top_groups groups take part whose largest v (group_top 1), or the sum
@@ -252,7 +253,7 @@ ft_status ft_route_classify(ft_cache* cache, int32_t layer, const float* logits,
  * go to the larger logit, which is their exact order where the biases are equal,
  * and the same sums of two to the lower group.  A NaN logit counts as -inf (and
  * so does a v of NaN), an infinite one as the largest number; picks without any
- * score have gate 0. */
+ * score have gate 0, and so may gates below 2^-126. */
 typedef enum ft_score { FT_SCORE_SOFTMAX = 0, FT_SCORE_SIGMOID = 1 } ft_score;
 typedef struct ft_router {
   int32_t score;       /* ft_score */
@@ -612,8 +613,8 @@ typedef struct ft_norm {
  * aligned, strides multiples of 8.  x and delta: FT_F32 or FT_BF16, each its
  * own; delta may be NULL (r = x).  total has x's type and may be NULL, or x or
  * delta itself; out may be x or delta itself where total is not; either then has
- * that one's type and stride.  No other
- * overlap.  r is an fp32 sum, which total rounds and y does not.
+ * that one's type and stride.  No other overlap.  r is an fp32 sum, which total
+ * rounds and y does not.
  * out: FT_F32, FT_BF16 or FT_FP8E4M3.  For the last y is given as codes and
  * fp32 scales, device [num_rows][ceil(hidden / group)] contiguous:
  *   scale = max|y| / 448 over the group's channels,  code = y / scale to the nearest e4m3 value
