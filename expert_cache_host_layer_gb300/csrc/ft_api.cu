@@ -827,7 +827,7 @@ ft_status ft_cache_set_router(ft_cache* c, const ft_router* router) {
   }
   if (c->by_rule && c->router.bias) {
     // The bias until now may still be read on the route stream: what the caller enqueues from here on, which may free or
-    // overwrite it, comes after that.  (A capture that the caller makes has no such reader outside of itself.)
+    // overwrite it, comes after that.  (A stream that the caller captures cannot wait for work outside of its capture.)
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     CU(cudaStreamIsCapturing(c->compute, &capture));
     if (capture == cudaStreamCaptureStatusNone) {

@@ -271,9 +271,9 @@ typedef struct ft_router {
  * graphs created later, choose (NULL: the default).  The struct is read during
  * the call; the bias is read by every later call and graph and stays the
  * caller's, whose writes to it are ordered like those to the logits.  The
- * compute stream waits for the routing enqueued so far that reads the bias of
- * the rule before, so work enqueued there later may free or overwrite that one
- * (unless a step graph has it).
+ * compute stream (unless the caller is capturing it) waits for the routing
+ * enqueued so far that reads the bias of the rule before, so work enqueued there
+ * later may free or overwrite that one, if no step graph has it.
  * Errors: FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED (see ft_route), FT_ERR_CUDA.
  */
 ft_status ft_cache_set_router(ft_cache* cache, const ft_router* router);
